@@ -1,4 +1,5 @@
-"""GB300 OUT_PROD and MUL_MAT_ID_BACK: a thin Python binding of ``liboop.so``.
+"""GB300 OUT_PROD and MUL_MAT_ID_BACK, and the operators of a training step
+around them: a thin Python binding of ``liboop.so``.
 
 The binding only marshals arguments: torch tensors give device pointers, ggml
 ``ne`` and the current stream; every step of the computation runs in the CUDA
@@ -15,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 from . import _build
 
@@ -57,6 +59,7 @@ ERR_DEVICE_TIMEOUT = -9
 ERR_DEVICE = -10
 ERR_PATH = -11
 ERR_SCRATCH_LIMIT = -12
+ERR_VALUE = -13
 
 # (elements, bytes) per block of the quantised types; the plain 16-bit types
 # are tensors of 2-byte elements
@@ -83,6 +86,10 @@ EXPORTS = (
     "oop_mul_mat_back", "oop_mul_mat_back_workspace_size",
     "oop_mul_mat_id_weight_grad", "oop_mul_mat_id_weight_grad_workspace_size",
     "oop_out_prod_batch", "oop_out_prod_batch_max", "oop_lora_backward",
+    "oop_get_rows", "oop_get_rows_back", "oop_get_rows_back_workspace_size",
+    "oop_layer_norm", "oop_layer_norm_back", "oop_layer_norm_back_workspace_size",
+    "oop_dropout", "oop_dropout_back",
+    "oop_preference_loss", "oop_preference_loss_back", "oop_preference_loss_workspace_size",
 )
 
 
@@ -192,6 +199,27 @@ def lib():
             L.oop_lora_backward.restype = ctypes.c_int
             L.oop_lora_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _vp]
+            i, i64, u64, sz, f, d = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint64,
+                                     ctypes.c_size_t, ctypes.c_float, ctypes.c_double)
+            for name, res, args in (
+                    ("oop_get_rows", i, [_vp, i, i64, _vp, _vp, i, i64, _i64p, i64, f, _vp]),
+                    ("oop_get_rows_back_workspace_size", sz, [_i64p, i64]),
+                    ("oop_get_rows_back", i, [_vp, i, i64, _vp, _vp, _i64p, i64, f, i, _vp, sz,
+                                              _vp]),
+                    ("oop_layer_norm", i, [_vp, i, i64, _vp, _vp, i, _vp, i, i64, _vp, _vp, _i64p,
+                                           f, _vp]),
+                    ("oop_layer_norm_back_workspace_size", sz, [_i64p]),
+                    ("oop_layer_norm_back", i, [_vp, i, i64, _vp, i, i64, _vp, _vp, _vp, i, _vp,
+                                                i64, _vp, _vp, _i64p, _vp, sz, _vp]),
+                    ("oop_dropout", i, [_vp, i, i64, _vp, i64, _i64p, d, u64, u64, _vp]),
+                    ("oop_dropout_back", i, [_vp, i, i64, _vp, i64, _i64p, d, u64, u64, _vp]),
+                    ("oop_preference_loss_workspace_size", sz, [_i64p, i64]),
+                    ("oop_preference_loss", i, [_vp, i, i64] + [_vp] * 8 + [_i64p, i64, d, d, _vp,
+                                                                            sz, _vp]),
+                    ("oop_preference_loss_back", i, [_vp, i, i64] + [_vp] * 6 +
+                     [i, i64, _i64p, i64, d, d, _vp])):
+                fn = getattr(L, name)
+                fn.restype, fn.argtypes = res, args
             _lib = L
     return _lib
 
@@ -606,7 +634,7 @@ def set_tc_schedule(mode) -> None:
 
 
 def last_launch_count() -> int:
-    """Kernels the last OUT_PROD / MUL_MAT_ID_BACK call on this thread enqueued."""
+    """Kernels the last compute call on this thread enqueued."""
     return oop_last_launch_count()
 
 
@@ -644,3 +672,385 @@ def out_prod_host(a_host, b_host, a_type=None, ne_a=None, out=None, device_buffe
         raise OopError(rc, "oop_out_prod_host")
     (stream if stream is not None else torch.cuda.current_stream()).synchronize()
     return out
+
+
+# ---------------------------------------------------------------------------
+# the operators of a training step around the products
+# ---------------------------------------------------------------------------
+#
+# Matrices are torch tensors (..., M): any leading shape whose rows lie at one
+# stride (a contiguous tensor, a slice of its rows or of its columns).  Calls
+# run on the current stream; with ``stream`` given, on that one, which then
+# owns what the call allocates.
+
+_DTYPES = None          # torch dtype -> type id
+_Two = ctypes.c_int64 * 2
+
+
+def _plain_type(t, name):
+    global _DTYPES
+    if _DTYPES is None:
+        torch = _torch()
+        _DTYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+    kind = _DTYPES.get(t if not hasattr(t, "dtype") else t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
+    return kind
+
+
+def _matrix(t, name):
+    """(M, T, byte stride of a row) of a CUDA tensor of rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    M, size, numel = shape[-1], t.element_size(), t.numel()
+    if t.is_contiguous():
+        return M, (numel // M if M else shape[:-1].numel()), M * size
+    st = t.stride()
+    if M > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    T, step = 1, None          # the innermost leading stride; the others have to follow from it
+    for n, d in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = d
+        elif d != step * T:
+            raise ValueError(f"the rows of {name} must lie at one stride")
+        T *= n
+    return M, T, (M if step is None else step) * size
+
+
+def _vector(t, name, n, dtype):
+    """The pointer of a contiguous CUDA tensor of n elements (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} {dtype}")
+    return t.data_ptr() if n else None
+
+
+def _output(out, shape, dtype, device, name="out"):
+    """A new tensor, or the caller's if it fits: (tensor, byte stride of a row)."""
+    if out is None:
+        out = _torch().empty(shape, dtype=dtype, device=device)
+        return out, shape[-1] * out.element_size()
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out, _matrix(out, name)[2]
+
+
+def _same_device(*tensors):
+    index = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
+def _on_stream(stream, call, *inputs):
+    """call() with `stream` current; its inputs stay alive until the stream is done with them."""
+    with _torch().cuda.stream(stream):
+        r = call()
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return r
+
+
+def _scratch(nbytes, device, workspace):
+    """(tensor, pointer, bytes) of a workspace of at least nbytes."""
+    if nbytes == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _raw_stream():
+    return _torch().cuda.current_stream().cuda_stream
+
+
+def get_rows(table, ids, scale=1.0, table_type=None, out_dtype=None, out=None, stream=None):
+    """scale * table[ids]: the embeddings of a batch of tokens.
+
+    table: (V, M) float32 / float16 / bfloat16, or uint8 rows of quantised
+    blocks (give ``table_type``); ids: int32, any shape.  Returns
+    (*ids.shape, M) in ``out_dtype`` (default: the table's, float32 for a
+    quantised one).  An id outside the table gives a row of zeros and sets the
+    device status."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: get_rows(table, ids, scale, table_type, out_dtype, out),
+                          table, ids, out)
+    if table.dim() != 2:
+        raise ValueError("table must have two dimensions")
+    if table_type is None:
+        table_type = _plain_type(table, "table")
+    _check_src0(table, table_type, "table")
+    M, V, nb = _matrix(table, "table")
+    if table_type in _BLOCKS:
+        qk, nbytes = _BLOCKS[table_type]
+        if M % nbytes:
+            raise ValueError("the table's rows must be whole blocks")
+        M = M // nbytes * qk
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else \
+            torch.float32 if table_type in _BLOCKS else table.dtype
+    kind = _plain_type(out_dtype, "out")
+    n = ids.numel()
+    pids = _vector(ids, "ids", n, torch.int32)
+    y, nb_y = _output(out, tuple(ids.shape) + (M,) if ids.dim() else (M,), out_dtype, table.device)
+    _same_device(table, ids)
+    rc = lib().oop_get_rows(table.data_ptr(), table_type, nb, pids, y.data_ptr(), kind, nb_y,
+                            _Two(M, V), n, scale, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_get_rows")
+    return y
+
+
+def get_rows_back(dy, ids, n_rows, scale=1.0, out=None, accumulate=False, workspace=None,
+                  stream=None):
+    """The gradient of get_rows with respect to its table: float32 (n_rows, M).
+
+    dy: (*ids.shape, M) float32 or bfloat16; ids: int32.  With ``accumulate``
+    the gradient is added to ``out``; only the rows that occur are touched."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: get_rows_back(dy, ids, n_rows, scale, out, accumulate,
+                                                        workspace), dy, ids, out, workspace)
+    M, T, nb = _matrix(dy, "dy")
+    kind = _plain_type(dy, "dy")
+    pids = _vector(ids, "ids", T, torch.int32)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None and not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    d, _ = _output(out, (n_rows, M), torch.float32, dy.device)
+    _same_device(dy, ids)
+    ne = _Two(M, n_rows)
+    L = lib()
+    ws, pws, nws = _scratch(L.oop_get_rows_back_workspace_size(ne, T), dy.device, workspace)
+    rc = L.oop_get_rows_back(dy.data_ptr(), kind, nb, pids, d.data_ptr(), ne, T, scale,
+                             1 if accumulate else 0, pws, nws, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_get_rows_back")
+    return d
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None, stream=None):
+    """(y, mean, rstd) of layer norm over x's last axis.
+
+    x: (..., M) float32 / float16 / bfloat16; weight, bias: (M,) of one plain
+    type, or None.  y is in ``out_dtype`` (default: x's); mean and rstd are
+    float32 of x's leading shape, as layer_norm_back takes them."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: layer_norm(x, weight, bias, eps, out_dtype, out),
+                          x, weight, bias, out)
+    M, T, nb = _matrix(x, "x")
+    kind = _plain_type(x, "x")
+    w_kind = _param_type(weight, bias)
+    pw = _vector(weight, "weight", M, weight.dtype) if weight is not None else None
+    pb = _vector(bias, "bias", M, bias.dtype) if bias is not None else None
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else x.dtype
+    y, nb_y = _output(out, x.shape, out_dtype, x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _same_device(x, weight, bias)
+    rc = lib().oop_layer_norm(x.data_ptr(), kind, nb, pw, pb, w_kind, y.data_ptr(),
+                              _plain_type(out_dtype, "out"), nb_y, mean.data_ptr(),
+                              rstd.data_ptr(), _Two(M, T), eps, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_layer_norm")
+    return y, mean, rstd
+
+
+def _param_type(weight, bias):
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one type")
+    p = weight if weight is not None else bias
+    return TYPE_F32 if p is None else _plain_type(p, "weight")
+
+
+def layer_norm_back(dy, x, mean, rstd, weight=None, want_dw=True, want_db=True, out=None,
+                    workspace=None, stream=None):
+    """(dx, dw, db) of layer norm from dy and the forward's mean and rstd.
+
+    dy: like x in shape, float32 or bfloat16; dx has dy's type and may be
+    written over it (``out=dy``); dw and db are float32 (M,) or None."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: layer_norm_back(dy, x, mean, rstd, weight, want_dw,
+                                                          want_db, out, workspace),
+                          dy, x, mean, rstd, weight, out, workspace)
+    M, T, nb_x = _matrix(x, "x")
+    kind, d_kind, w_kind = _plain_type(x, "x"), _plain_type(dy, "dy"), _param_type(weight, None)
+    if dy.shape != x.shape:
+        raise ValueError("dy and x must have one shape")
+    nb_dy = _matrix(dy, "dy")[2]
+    pm = _vector(mean, "mean", T, torch.float32)
+    pr = _vector(rstd, "rstd", T, torch.float32)
+    pw = _vector(weight, "weight", M, weight.dtype) if weight is not None else None
+    dx, nb_dx = _output(out, x.shape, dy.dtype, x.device)
+    dw = torch.empty(M, dtype=torch.float32, device=x.device) if want_dw else None
+    db = torch.empty(M, dtype=torch.float32, device=x.device) if want_db else None
+    _same_device(x, dy, mean, rstd, weight)
+    ne = _Two(M, T)
+    L = lib()
+    ws, pws, nws = _scratch(L.oop_layer_norm_back_workspace_size(ne) if want_dw or want_db else 0,
+                            x.device, workspace)
+    rc = L.oop_layer_norm_back(dy.data_ptr(), d_kind, nb_dy, x.data_ptr(), kind, nb_x, pm, pr, pw,
+                               w_kind, dx.data_ptr(), nb_dx, dw.data_ptr() if want_dw else None,
+                               db.data_ptr() if want_db else None, ne, pws, nws, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_layer_norm_back")
+    return dx, dw, db
+
+
+def _drop(fn, where, x, p, seed, offset, out):
+    M, T, nb = _matrix(x, "x")
+    kind = _plain_type(x, "x")
+    y, nb_y = _output(out, x.shape, x.dtype, x.device)
+    _same_device(x)
+    rc = fn(x.data_ptr(), kind, nb, y.data_ptr(), nb_y, _Two(M, T), p,
+            seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, where)
+    return y
+
+
+def dropout(x, p, seed, offset=0, out=None, stream=None):
+    """x with each element dropped with probability p and the others scaled by
+    1 / (1 - p), p rounded to 1/65536.
+
+    The mask is a function of (seed, offset, column, row) and is not stored:
+    dropout_back with the same seed and offset drops the same elements.  x:
+    (..., M) float32 / float16 / bfloat16; ``out=x`` works in place."""
+    if stream is not None:
+        return _on_stream(stream, lambda: dropout(x, p, seed, offset, out), x, out)
+    return _drop(lib().oop_dropout, "oop_dropout", x, p, seed, offset, out)
+
+
+def dropout_back(dy, p, seed, offset=0, out=None, stream=None):
+    """The gradient of dropout: the same elements of dy (float32 or bfloat16)
+    dropped, the others scaled alike."""
+    if stream is not None:
+        return _on_stream(stream, lambda: dropout_back(dy, p, seed, offset, out), dy, out)
+    return _drop(lib().oop_dropout_back, "oop_dropout_back", dy, p, seed, offset, out)
+
+
+class PreferenceLoss(NamedTuple):
+    """What preference_loss returns: float32 tensors on the device."""
+    loss: object        # the mean over the pairs
+    losses: object      # (P,): each pair's
+    ratios: object      # (2P,): sums of logps - ref_logps, the chosen sequences first
+    logps: object       # (T,): log probability of each row's label, 0 where it is not scored
+    lse: object         # (T,): log normaliser of each row, 0 where it is not scored
+
+
+def _pairs(seq):
+    if seq.dim() != 1 or seq.numel() % 2 != 1:
+        raise ValueError("seq must be the 2P + 1 first rows of 2P sequences")
+    return seq.numel() // 2
+
+
+def preference_loss(logits, labels, seq, ref_logps=None, beta=0.1, label_smoothing=0.0,
+                    workspace=None, stream=None):
+    """The loss over preference pairs and its parts, a PreferenceLoss.
+
+    logits: (T, V) rows of all sequences, packed; labels: int32 (T,), negative
+    for rows that are not scored; seq: int32 (2P + 1,), the first row of each
+    sequence and the end, the P chosen sequences before the P rejected ones;
+    ref_logps: float32 (T,), the reference model's logps (see token_logps)."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: preference_loss(logits, labels, seq, ref_logps, beta,
+                                                          label_smoothing, workspace),
+                          logits, labels, seq, ref_logps, workspace)
+    V, T, nb = _matrix(logits, "logits")
+    kind = _plain_type(logits, "logits")
+    P = _pairs(seq)
+    f32, dev = torch.float32, logits.device
+    pl = _vector(labels, "labels", T, torch.int32)
+    ps = _vector(seq, "seq", 2 * P + 1, torch.int32)
+    pr = _vector(ref_logps, "ref_logps", T, f32)
+    r = PreferenceLoss(torch.empty((), dtype=f32, device=dev),
+                       torch.empty(P, dtype=f32, device=dev),
+                       torch.empty(2 * P, dtype=f32, device=dev),
+                       torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev))
+    if P == 0:
+        r.loss.zero_()
+    _same_device(logits, labels, seq, ref_logps)
+    ne = _Two(V, T)
+    L = lib()
+    ws, pws, nws = _scratch(L.oop_preference_loss_workspace_size(ne, P), dev, workspace)
+    rc = L.oop_preference_loss(logits.data_ptr(), kind, nb, pl, ps, pr, r.loss.data_ptr(),
+                               r.losses.data_ptr(), r.ratios.data_ptr(), r.logps.data_ptr(),
+                               r.lse.data_ptr(), ne, P, beta, label_smoothing, pws, nws,
+                               _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_preference_loss")
+    return r
+
+
+def token_logps(logits, labels, workspace=None, stream=None):
+    """(logps, lse) of each row's label: preference_loss without pairs, as the
+    reference model needs it."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: token_logps(logits, labels, workspace), logits, labels,
+                          workspace)
+    V, T, nb = _matrix(logits, "logits")
+    kind = _plain_type(logits, "logits")
+    pl = _vector(labels, "labels", T, torch.int32)
+    logps = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty_like(logps)
+    _same_device(logits, labels)
+    ne = _Two(V, T)
+    L = lib()
+    ws, pws, nws = _scratch(L.oop_preference_loss_workspace_size(ne, 0), logits.device, workspace)
+    rc = L.oop_preference_loss(logits.data_ptr(), kind, nb, pl, None, None, None, None, None,
+                               logps.data_ptr(), lse.data_ptr(), ne, 0, 0.0, 0.0, pws, nws,
+                               _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_preference_loss")
+    return logps, lse
+
+
+def preference_loss_back(logits, labels, seq, lse, ratios, beta=0.1, label_smoothing=0.0,
+                         dloss=None, out_dtype=None, out=None, stream=None):
+    """The gradient of preference_loss's mean with respect to the logits.
+
+    lse and ratios are the forward's; ``dloss``: a float32 CUDA scalar that
+    multiplies the gradient.  Returns (T, V) in ``out_dtype`` (float32 or
+    bfloat16; default: the logits' type, float32 for float16 logits).
+    ``out=logits`` overwrites the logits."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: preference_loss_back(
+            logits, labels, seq, lse, ratios, beta, label_smoothing, dloss, out_dtype, out),
+            logits, labels, seq, lse, ratios, dloss, out)
+    V, T, nb = _matrix(logits, "logits")
+    kind = _plain_type(logits, "logits")
+    P = _pairs(seq)
+    f32 = torch.float32
+    pl = _vector(labels, "labels", T, torch.int32)
+    ps = _vector(seq, "seq", 2 * P + 1, torch.int32)
+    pe = _vector(lse, "lse", T, f32)
+    pr = _vector(ratios, "ratios", 2 * P, f32)
+    pd = _vector(dloss, "dloss", 1, f32)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else f32 if kind == TYPE_F16 else logits.dtype
+    d, nb_d = _output(out, logits.shape, out_dtype, logits.device)
+    _same_device(logits, labels, seq, lse, ratios, dloss)
+    rc = lib().oop_preference_loss_back(logits.data_ptr(), kind, nb, pl, ps, pe, pr, pd,
+                                        d.data_ptr(), _plain_type(out_dtype, "out"), nb_d,
+                                        _Two(V, T), P, beta, label_smoothing, _raw_stream())
+    if rc != OK:
+        raise OopError(rc, "oop_preference_loss_back")
+    return d

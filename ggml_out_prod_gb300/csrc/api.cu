@@ -513,11 +513,12 @@ const char *oop_status_string(int status) {
     case OOP_ERR_ALIGN: return "pointer below its element alignment";
     case OOP_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
     case OOP_ERR_CUDA: return "CUDA runtime error";
-    case OOP_ERR_BAD_ID: return "expert id out of range (slot zeroed)";
+    case OOP_ERR_BAD_ID: return "an id out of range (its slot or row is zeroed or skipped)";
     case OOP_ERR_DEVICE_TIMEOUT: return "a bounded device wait ran out";
     case OOP_ERR_DEVICE: return "current device is not sm_103";
     case OOP_ERR_PATH: return "the requested kernel cannot take this call";
     case OOP_ERR_SCRATCH_LIMIT: return "needs more scratch than the library's fixed device array";
+    case OOP_ERR_VALUE: return "a scalar argument outside its range";
     default: return "unknown status";
     }
 }

@@ -84,12 +84,15 @@ typedef enum {
     OOP_ERR_ALIGN = -5,          /* a pointer below its element's alignment */
     OOP_ERR_WORKSPACE = -6,      /* workspace NULL or smaller than required */
     OOP_ERR_CUDA = -7,           /* a CUDA runtime call or launch failed */
-    OOP_ERR_BAD_ID = -8,         /* device: an expert id outside [0, E) */
+    OOP_ERR_BAD_ID = -8,         /* device: an expert id outside [0, E), a token id or label
+                                    outside the table, or sequence offsets out of order */
     OOP_ERR_DEVICE_TIMEOUT = -9, /* device: a bounded wait ran out */
     OOP_ERR_DEVICE = -10,        /* the current device is not sm_103 */
     OOP_ERR_PATH = -11,          /* oop_out_prod_ex: that kernel cannot take this call */
-    OOP_ERR_SCRATCH_LIMIT = -12  /* oop_out_prod_noalloc: the call needs more scratch
+    OOP_ERR_SCRATCH_LIMIT = -12, /* oop_out_prod_noalloc: the call needs more scratch
                                     than the library's fixed device array holds */
+    OOP_ERR_VALUE = -13          /* a scalar argument outside its range (a probability,
+                                    an epsilon, a smoothing weight; NaN) */
 } oop_status;
 
 /* Kernel selection for oop_out_prod_ex. */
@@ -381,6 +384,158 @@ int oop_mul_mat_id_weight_grad(const float *x, const int32_t *ids, const float *
                                const int64_t ne_x[3], const int64_t ne_dy[3], int64_t n_expert,
                                void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The operators a training step runs between the matrix products above
+ * (no counterpart on the pages but for GET_ROWS_BACK, which "metal: OUT_PROD
+ * runs batched, broadcast and narrow shapes on the GPU" lists among the
+ * training operations left on the CPU).
+ *
+ * A matrix is {M, T}: T rows of M contiguous elements, `nb_...` bytes apart.
+ * Strides are multiples of the element size (OOP_ERR_SHAPE otherwise); an
+ * input's stride may be 0 (one row repeated), an output's rows must not
+ * overlap.  Plain types are F32, F16 and BF16.  A gradient is F32 or BF16:
+ * F16 overflows at 65504, which training gradients pass, and is refused with
+ * OOP_ERR_TYPE.  Every sum, mean and softmax statistic is held in 32 bits or
+ * more and a result is rounded once, to nearest.  Every sum has one order, so
+ * equal calls give equal bits.  16-byte aligned pointers and strides enable
+ * the wide loads.  An output may be its input (equal pointers, types and
+ * strides) where this is said; otherwise outputs must not overlap inputs.
+ */
+
+/*
+ * Embedding lookup: dst[m, t] = scale * table[m, ids[t]].
+ *
+ *   ne_table = {M, V}       table: any oop_type (blocks along m: M % 32 or
+ *                           % 256), rows nb_table bytes apart
+ *   ids: int32 {n_ids}      dst: plain type, {M, n_ids}, OVERWRITTEN
+ *
+ * An id outside [0, V) zeroes its row and records OOP_ERR_BAD_ID in the
+ * device status word.
+ */
+int oop_get_rows(const void *table, int table_type, int64_t nb_table, const int32_t *ids,
+                 void *dst, int dst_type, int64_t nb_dst, const int64_t ne_table[2],
+                 int64_t n_ids, float scale, void *stream);
+
+/*
+ * The gradient of the table (dense, f32, contiguous {M, V}):
+ *
+ *   dtable[m, v] = scale * sum over the t with ids[t] == v of dy[m, t]
+ *
+ * OVERWRITTEN (zero for a row that no id names), or, with accumulate != 0,
+ * added to: then only the named rows are read and written.  dy: F32 or BF16.
+ * An id outside [0, V) takes part in no sum and records OOP_ERR_BAD_ID.
+ * workspace: oop_get_rows_back_workspace_size(...) bytes, 256-byte aligned.
+ */
+size_t oop_get_rows_back_workspace_size(const int64_t ne_table[2], int64_t n_ids);
+
+int oop_get_rows_back(const void *dy, int dy_type, int64_t nb_dy, const int32_t *ids,
+                      float *dtable, const int64_t ne_table[2], int64_t n_ids, float scale,
+                      int accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm over the rows of x {M, T}:
+ *
+ *   y[m, t] = (x[m, t] - mean[t]) * rstd[t] * w[m] + b[m]
+ *   mean[t] = sum_m x / M,  rstd[t] = (sum_m (x - mean)^2 / M + eps)^(-1/2)
+ *
+ * x and y: plain types, y may be x.  w and b {M}: plain, of one type; either
+ * may be NULL (1 and 0).  mean and rstd: f32 {T} or NULL.  eps >= 0, finite
+ * (OOP_ERR_VALUE).  M == 0 with T > 0 is OOP_ERR_SHAPE (the mean of nothing).
+ */
+int oop_layer_norm(const void *x, int x_type, int64_t nb_x, const void *w, const void *b,
+                   int w_type, void *y, int y_type, int64_t nb_y, float *mean, float *rstd,
+                   const int64_t ne[2], float eps, void *stream);
+
+/*
+ * Its backward pass, from the forward's mean and rstd.  With g = dy * w and
+ * xh = (x - mean) * rstd:
+ *
+ *   dx = rstd * (g - sum_m g / M - xh * sum_m (g * xh) / M)
+ *   dw[m] = sum_t dy * xh,   db[m] = sum_t dy
+ *
+ * dy and dx: F32 or BF16, one type; dx may be dy.  dw and db: f32 {M},
+ * OVERWRITTEN; either may be NULL (not computed).  With both NULL no
+ * workspace is needed, else oop_layer_norm_back_workspace_size(...) bytes,
+ * 256-byte aligned.
+ */
+size_t oop_layer_norm_back_workspace_size(const int64_t ne[2]);
+
+int oop_layer_norm_back(const void *dy, int dy_type, int64_t nb_dy, const void *x, int x_type,
+                        int64_t nb_x, const float *mean, const float *rstd, const void *w,
+                        int w_type, void *dx, int64_t nb_dx, float *dw, float *db,
+                        const int64_t ne[2], void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/*
+ * Dropout with a mask that is computed from the position and never stored:
+ *
+ *   y[m, t] = r(m, t) >= D ? x[m, t] * 65536 / (65536 - D) : 0,   D = round(65536 * p)
+ *
+ * r(m, t) is 16 bits of the counter-based generator Philox4x32-10 (Salmon et
+ * al., SC 2011) with key = seed and counter = (m / 8, t, offset low, offset
+ * high): half (m % 8) of its four words, the low half of a word first.  So the
+ * mask depends on seed, offset, m and t alone, not on sizes, strides or
+ * types; use another offset for every call that needs a mask of its own.
+ * p in [0, 1] (OOP_ERR_VALUE), rounded to 1/65536 with the scale to match; p
+ * = 1 zeroes all.  A dropped element is 0 whatever x holds.  y may be x.
+ * oop_dropout_back is the same map on a gradient (F32 or BF16).
+ */
+int oop_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, const int64_t ne[2],
+                double p, uint64_t seed, uint64_t offset, void *stream);
+
+int oop_dropout_back(const void *dy, int type, int64_t nb_dy, void *dx, int64_t nb_dx,
+                     const int64_t ne[2], double p, uint64_t seed, uint64_t offset, void *stream);
+
+/*
+ * A loss over preference pairs, from the logits x {V, T} of all their
+ * sequences' rows, packed.  ne = {V, T}; labels int32 {T}: the token whose
+ * probability row t is scored by, negative for a row that is not scored (a
+ * prompt, padding); its logits are not read.  seq int32 {2 * n_pairs + 1}:
+ * sequence s is rows seq[s] .. seq[s + 1]; sequences 0 .. P-1 are the chosen
+ * ones and P .. 2P-1 the rejected ones of pairs 0 .. P-1.
+ *
+ *   lse[t]    = log sum_v exp(x[v, t]),   logps[t] = x[labels[t], t] - lse[t]
+ *               (both 0 for a row that is not scored)
+ *   ratios[s] = sum over the scored rows of sequence s of logps[t] - ref_logps[t]
+ *   m_i       = beta * (ratios[i] - ratios[P + i])
+ *   losses[i] = -(1 - e) log sigma(m_i) - e log sigma(-m_i),  e = label_smoothing
+ *   loss      = the mean of losses
+ *
+ * x: plain type.  ref_logps f32 {T}: the reference model's logps, read for
+ * scored rows only; NULL for none (0).  A sequence with no scored row has
+ * ratio 0.  n_pairs == 0 computes lse and logps only (the reference model's
+ * pass): seq, loss, losses and ratios are then not used.  beta finite, e in
+ * [0, 1] (OOP_ERR_VALUE).  A label >= V is not scored and records
+ * OOP_ERR_BAD_ID, as do offsets that are out of order or beyond T (they are
+ * clamped).  A -Inf logit has probability 0; a NaN or +Inf logit in a scored
+ * row makes its results non-finite.  workspace:
+ * oop_preference_loss_workspace_size(...) bytes, 256-byte aligned.
+ */
+size_t oop_preference_loss_workspace_size(const int64_t ne[2], int64_t n_pairs);
+
+int oop_preference_loss(const void *logits, int type, int64_t nb, const int32_t *labels,
+                        const int32_t *seq, const float *ref_logps, float *loss, float *losses,
+                        float *ratios, float *logps, float *lse, const int64_t ne[2],
+                        int64_t n_pairs, double beta, double label_smoothing, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of the loss with respect to the logits, from the forward's
+ * lse and ratios:
+ *
+ *   dlogits[v, t] = c_s * (1[v == labels[t]] - exp(x[v, t] - lse[t]))
+ *   c_i = -c_{P+i} = dloss * beta / P * (e * sigma(m_i) - (1 - e) * sigma(-m_i))
+ *
+ * and 0 for a row that is not scored or in no sequence.  dloss: device f32,
+ * the gradient of the mean loss (NULL: 1).  dlogits: F32 or BF16,
+ * OVERWRITTEN; it may be the logits themselves.
+ */
+int oop_preference_loss_back(const void *logits, int type, int64_t nb, const int32_t *labels,
+                             const int32_t *seq, const float *lse, const float *ratios,
+                             const float *dloss, void *dlogits, int d_type, int64_t nb_d,
+                             const int64_t ne[2], int64_t n_pairs, double beta,
+                             double label_smoothing, void *stream);
+
 /* Synchronises `stream`, then returns the current device's status word
  * (OOP_OK, or the first device-side error recorded since it was last
  * cleared); clears it when `clear` is non-zero.  Returns OOP_ERR_CUDA if the
@@ -456,7 +611,7 @@ int oop_out_prod_plan(int a_type, const int64_t ne_a[4], const int64_t ne_b[4], 
  * Returns OOP_OK, or OOP_ERR_PATH for another mode. */
 int oop_debug_set_tc_schedule(int mode);
 
-/* How many kernels the last OUT_PROD or MUL_MAT_ID_BACK call made on this
+/* How many kernels the last compute call made on this
  * host thread enqueued (0 after a rejected call or an empty one; memsets are
  * not kernels).  No counterpart on the pages; for benchmarks that report
  * their launch count. */
