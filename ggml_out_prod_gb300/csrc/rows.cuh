@@ -87,6 +87,121 @@ __device__ __forceinline__ typename Plain<TYPE>::S *row_of(void *p, int64_t nb, 
     return reinterpret_cast<typename Plain<TYPE>::S *>(static_cast<char *>(p) + t * nb);
 }
 
+// ---- vectors --------------------------------------------------------------
+
+// E consecutive elements as they lie in memory: 2 to 16 bytes in one access
+// (E = 1: the element itself).
+template <int BYTES> struct Words;
+template <> struct Words<2> { using T = uint16_t; };
+template <> struct Words<4> { using T = uint32_t; };
+template <> struct Words<8> { using T = uint2; };
+template <> struct Words<16> { using T = uint4; };
+
+template <int TYPE, int E>
+struct Packed {
+    static constexpr int kBytes = E * plain_size(TYPE);
+    typename Words<kBytes>::T raw;
+
+    __device__ __forceinline__ void get(float (&v)[E]) const {
+        using S = typename Plain<TYPE>::S;
+        if constexpr (TYPE == OOP_TYPE_BF16 && E >= 2) {
+            uint32_t w[kBytes / 4];
+            __builtin_memcpy(w, &raw, kBytes);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {      // a bfloat16 is the top half of its float
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            S e[E];
+            __builtin_memcpy(e, &raw, kBytes);
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = to_float(e[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[E]) {
+        if constexpr (TYPE == OOP_TYPE_BF16 && E >= 2) {
+            __nv_bfloat162 e[E / 2];
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) e[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(&raw, e, kBytes);
+        } else if constexpr (TYPE == OOP_TYPE_F16 && E >= 2) {
+            __half2 e[E / 2];
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) e[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            __builtin_memcpy(&raw, e, kBytes);
+        } else {
+            typename Plain<TYPE>::S e[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) e[i] = from_float<TYPE>(v[i]);
+            __builtin_memcpy(&raw, e, kBytes);
+        }
+    }
+};
+
+// Streaming accesses (data read or written once): evicted first.
+template <int TYPE, int E>
+__device__ __forceinline__ Packed<TYPE, E> load_stream(const typename Plain<TYPE>::S *p) {
+    Packed<TYPE, E> r;
+    r.raw = __ldcs(reinterpret_cast<const typename Words<E * plain_size(TYPE)>::T *>(p));
+    return r;
+}
+template <int TYPE, int E>
+__device__ __forceinline__ Packed<TYPE, E> load_packed(const typename Plain<TYPE>::S *p) {
+    Packed<TYPE, E> r;
+    r.raw = *reinterpret_cast<const typename Words<E * plain_size(TYPE)>::T *>(p);
+    return r;
+}
+// E floats as TYPE; more than 16 bytes go in 16-byte pieces.
+template <int TYPE, int E>
+__device__ __forceinline__ void store_stream(typename Plain<TYPE>::S *p, const float (&v)[E]) {
+    if constexpr (E * plain_size(TYPE) > 16) {
+        constexpr int H = 16 / plain_size(TYPE);
+#pragma unroll
+        for (int i = 0; i < E; i += H) {
+            float part[H];
+#pragma unroll
+            for (int j = 0; j < H; ++j) part[j] = v[i + j];
+            store_stream<TYPE, H>(p + i, part);
+        }
+    } else {
+        Packed<TYPE, E> r;
+        r.set(v);
+        __stcs(reinterpret_cast<typename Words<E * plain_size(TYPE)>::T *>(p), r.raw);
+    }
+}
+
+// ---- dependent launches ---------------------------------------------------
+//
+// A kernel launched with launch_dependent may start while the one before it on
+// the stream still runs: as soon as every CTA of that one has called
+// let_next_start (or ended).  wait_previous returns once the previous grid has
+// ended and its writes are visible; nothing that grid writes may be touched
+// before.  A kernel launched plainly waits for everything before it.
+
+__device__ __forceinline__ void let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- reductions (every lane gets the result; fixed order) -----------------
 
 template <class T>

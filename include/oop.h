@@ -406,7 +406,7 @@ int oop_mul_mat_id_weight_grad(const float *x, const int32_t *ids, const float *
  * Embedding lookup: dst[m, t] = scale * table[m, ids[t]].
  *
  *   ne_table = {M, V}       table: any oop_type (blocks along m: M % 32 or
- *                           % 256), rows nb_table bytes apart
+ *                           % 256), rows nb_table bytes apart; M <= 2^20
  *   ids: int32 {n_ids}      dst: plain type, {M, n_ids}, OVERWRITTEN
  *
  * An id outside [0, V) zeroes its row and records OOP_ERR_BAD_ID in the
