@@ -812,6 +812,19 @@ def test_many_rows_past_32_bits(op):
     assert torch.allclose(db.double(), x.sum(0, dtype=torch.float64), atol=0.2)
 
 
+def test_dropout_of_more_groups_than_a_launch(op):
+    """2^31 + 3 rows of one group each: two launches, one mask."""
+    import torch
+    T = 2 ** 31 + 3
+    if torch.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GB of device memory")
+    x = torch.ones((T, 8), dtype=torch.bfloat16, device="cuda")
+    op.dropout(x, 0.5, 3, out=x)
+    assert op.last_launch_count() == 2
+    for t in (0, 1, 2 ** 31 - 1, 2 ** 31, T - 1):
+        assert ((x[t] != 0).cpu().numpy() == _keep_row(t, 8, 0.5, 3)).all()
+
+
 def _keep_row(t, M, p, seed):
     """One row of dropout_keep."""
     drop = int(np.rint(p * 65536))
