@@ -24,11 +24,13 @@ constexpr int kThreads = 256;
 constexpr int64_t kMaxGroups = int64_t(1) << 31;     // of one launch: 32-bit group numbers
 
 struct DropArgs {
-    const void *x;
+    const void *x;               // the launch's first row
     void *y;
     int64_t nb_x, nb_y, M;
     uint32_t t0, rows, groups;   // the launch's rows; groups of 8 columns per row
     uint64_t inverse;            // floor(2^64 / groups) + 1: i / groups = high half of i * inverse
+    uint32_t next_t, next_g;     // kThreads groups on: kThreads / groups rows and the rest
+    bool dense;                  // x's and y's rows follow each other
     uint32_t k0[10], k1[10];     // the key of each round
     uint32_t c2, c3;
     uint32_t drop;               // 0 .. 65536
@@ -72,37 +74,69 @@ __device__ __forceinline__ void place(uint32_t i, const DropArgs &a, uint32_t &t
 }
 
 // A thread takes G groups of 8 columns, whole and aligned (M % 8 == 0): all
-// their loads are in flight while their masks are computed.
+// their loads are in flight while their masks are computed.  The generator
+// bounds this kernel as much as memory does (20 wide multiplies and 20
+// three-way logic operations for 8 elements), so what surrounds it is lean: one
+// division for the G groups, addresses by addition, halves compared in place.
 template <int TYPE, int G>
 __global__ void __launch_bounds__(kThreads) dropout_wide_kernel(const DropArgs a) {
     constexpr int E = 16 / plain_size(TYPE), N = 8 / E;
-    const uint32_t total = a.rows * a.groups;
+    const uint32_t total = a.rows * a.groups, first = blockIdx.x * (G * kThreads) + threadIdx.x;
     uint32_t t[G], g[G];
     Packed<TYPE, E> raw[G][N];
+    place(first, a, t[0], g[0]);
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-        const uint32_t i = (blockIdx.x * G + k) * kThreads + threadIdx.x;
-        place(i, a, t[k], g[k]);
-        if (i < total && a.drop < 65536) {
-            const auto *x = row_of<TYPE>(a.x, a.nb_x, int64_t(a.t0) + t[k]) + int64_t(g[k]) * 8;
-#pragma unroll
-            for (int n = 0; n < N; ++n) raw[k][n] = load_stream<TYPE, E>(x + n * E);
+    for (int k = 1; k < G; ++k) {
+        t[k] = t[k - 1] + a.next_t;
+        g[k] = g[k - 1] + a.next_g;
+        if (g[k] >= a.groups) {
+            g[k] -= a.groups;
+            ++t[k];
         }
     }
+    // byte offsets, of x and of y
+    auto offset = [&](int k, int64_t nb) -> int64_t {
+        if (a.dense) return int64_t(first + k * kThreads) * (8 * plain_size(TYPE));
+        return int64_t(t[k]) * nb + int64_t(g[k]) * (8 * plain_size(TYPE));
+    };
+    if (a.drop < 65536) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            if (first + k * kThreads >= total) break;
+            const char *x = static_cast<const char *>(a.x) + offset(k, a.nb_x);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                raw[k][n] = load_stream<TYPE, E>(reinterpret_cast<const typename Plain<TYPE>::S *>(x) + n * E);
+        }
+    }
+    const uint32_t high = a.drop << 16;              // (drop < 65536)
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-        const uint32_t i = (blockIdx.x * G + k) * kThreads + threadIdx.x;
-        if (i >= total) return;
-        const uint32_t keep = a.drop < 65536 ? keep_bits(g[k], a.t0 + t[k], a) : 0u;
-        auto *y = row_of<TYPE>(a.y, a.nb_y, int64_t(a.t0) + t[k]) + int64_t(g[k]) * 8;
+        if (first + k * kThreads >= total) return;
+        float v[N][E];
+        if (a.drop < 65536) {
+            uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (a.drop > 0) w = philox(g[k], a.t0 + t[k], a);
+            const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float v[E];
-            raw[k][n].get(v);
+            for (int n = 0; n < N; ++n) {
+                raw[k][n].get(v[n]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = (keep >> (n * E + e)) & 1u ? v[e] * a.scale : 0.f;
-            store_stream<TYPE, E>(y + n * E, v);
+                for (int e = 0; e < E; ++e) {
+                    const uint32_t word = r[(n * E + e) / 2], half = (e & 1) ? word : word << 16;
+                    v[n][e] = half >= high ? v[n][e] * a.scale : 0.f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[n][e] = 0.f;
         }
+        char *y = static_cast<char *>(a.y) + offset(k, a.nb_y);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            store_stream<TYPE, E>(reinterpret_cast<typename Plain<TYPE>::S *>(y) + n * E, v[n]);
     }
 }
 
@@ -121,8 +155,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
         uint32_t t, g;
         place(i, a, t, g);
         const int64_t m = int64_t(g) * 8 + lane % 8;
-        at[k] = i < total && m < a.M ? (int64_t(a.t0) + t) * a.nb_y + m * plain_size(TYPE) : -1;
-        if (at[k] >= 0 && a.drop < 65536) raw[k] = row_of<TYPE>(a.x, a.nb_x, int64_t(a.t0) + t)[m];
+        at[k] = i < total && m < a.M ? int64_t(t) * a.nb_y + m * plain_size(TYPE) : -1;
+        if (at[k] >= 0 && a.drop < 65536) raw[k] = row_of<TYPE>(a.x, a.nb_x, t)[m];
     }
     uint32_t t, g, keep = 0;
     place(i0 + lane, a, t, g);
@@ -175,6 +209,9 @@ int run_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, co
     a.M = M;
     a.groups = static_cast<uint32_t>(groups);
     a.inverse = ~uint64_t(0) / a.groups + 1;
+    a.next_t = static_cast<uint32_t>(kThreads / groups);
+    a.next_g = static_cast<uint32_t>(kThreads % groups);
+    a.dense = nb_x == M * size && nb_y == M * size;
     for (int i = 0; i < 10; ++i) {
         a.k0[i] = static_cast<uint32_t>(seed) + static_cast<uint32_t>(i) * 0x9E3779B9u;
         a.k1[i] = static_cast<uint32_t>(seed >> 32) + static_cast<uint32_t>(i) * 0xBB67AE85u;
@@ -190,6 +227,8 @@ int run_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, co
     int launches = 0;
     for (int64_t t0 = 0; t0 < T; t0 += rows, ++launches) {
         a.t0 = static_cast<uint32_t>(t0);
+        a.x = static_cast<const char *>(x) + t0 * nb_x;
+        a.y = static_cast<char *>(y) + t0 * nb_y;
         a.rows = static_cast<uint32_t>(std::min(rows, T - t0));
         if (type == OOP_TYPE_F32) launch_dropout<OOP_TYPE_F32>(a, wide, st);
         else if (type == OOP_TYPE_F16) launch_dropout<OOP_TYPE_F16>(a, wide, st);

@@ -13,21 +13,23 @@
 
 #include "oop_internal.cuh"
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace oop {
 namespace {
 
 constexpr int kThreads = 256;
-// Fewer rows than this: as many threads per row as it has vectors, for latency.
-constexpr int64_t kFewRows = 2048;
-constexpr int64_t kSlices = 152;     // row slices of the weight's gradient: one per SM
+constexpr int64_t kSlices = 152;     // CTAs of the row kernels, one per SM: slices of dw and db
+constexpr int kMaxThreads = 512;     // of a row kernel's CTA: 128 registers each
+constexpr int kSmem = 220 * 1024;    // of a CTA that has an SM to itself
 
 struct NormArgs {
     const void *x, *w, *b;
     void *y;
     float *mean, *rstd;
     int64_t nb_x, nb_y, M, T;
-    int w_type, width;
+    int w_type;
+    int width, groups, stages;       // threads per row, rows at once, rows staged per group
     float eps;
 };
 
@@ -51,82 +53,261 @@ __device__ __forceinline__ void load_params(const void *p, int type, int64_t m0,
     }
 }
 
-// The sum over the `width` threads (a power of two, 32 or more) that share a
-// row; every thread of the CTA calls it.
-__device__ __forceinline__ float row_sum(float v, int width, float *part) {
-    v = warp_sum(v);
-    if (width == 32) return v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = width >> 5;
-    __syncthreads();          // part may still be read by an earlier call
-    if (lane == 0) part[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < warps ? part[(warp & ~(warps - 1)) + lane] : 0.f);
+// A thread's own piece of shared memory, filled behind its back: copies of 4,
+// 8 or 16 bytes, committed row by row.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *p) {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(p) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(p), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `left` (0 .. 3) committed rows are still on their way.
+__device__ __forceinline__ void wait_copies(int left) {
+    if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// `width` threads per row hold it whole: NV vectors of E elements each, every
-// load before the first use, so the mean, the squares and the result read
-// registers.
-template <int XT, int YT, int E, int NV>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
-    __shared__ float part[32];
-    const int lane = static_cast<int>(threadIdx.x) & (a.width - 1);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / a.width) + threadIdx.x / a.width;
-    const bool in = t < a.T;
-    const int M = static_cast<int>(a.M), step = a.width * E;
-    const auto *x = row_of<XT>(a.x, a.nb_x, in ? t : 0);
-    Packed<XT, E> raw[NV];
+// Columns of one thread: 32 where they come in vectors (a row's two reductions
+// and its bookkeeping cost a warp as much as 20 columns do), 16 singles.
+__host__ __device__ constexpr int cols_of(int E) { return E == 1 ? 16 : 32; }
+constexpr int kMaxStages = 4;
+
+// The form of both passes.  `width` threads share a row, 32 columns each; a CTA
+// (one per SM) has `groups` rows in work and goes on to others until none is
+// left, so what belongs to a column (w, b, the sums of dw and db) stays with
+// its thread.  Each thread copies its pieces of the next rows into shared memory
+// while this one is reduced: the loads never wait for a row's sums, and no
+// thread reads what another one copied.  Two columns at a time in packed fp32
+// arithmetic: half the instructions, the same roundings.
+struct Place {
+    int M, threads, width, group, lane, warps, warp0;
+
+    __device__ __forceinline__ Place(int64_t M_, int width_)
+        : M(static_cast<int>(M_)), threads(blockDim.x), width(width_), group(threadIdx.x / width_),
+          lane(threadIdx.x - group * width_), warps(width_ >> 5), warp0(group * (width_ >> 5)) {}
+    // the thread's i-th piece of E columns starts here
+    template <int E>
+    __device__ __forceinline__ int column(int i) const { return (i * width + lane) * E; }
+};
+
+// A thread's columns come in units that are there or not as a whole: a
+// vector of E, or two singles (of which the second may be missing).
+template <int E>
+struct Units {
+    static constexpr int kSize = E == 1 ? 2 : E, kCount = cols_of(E) / kSize, kPairs = kSize / 2;
+    static constexpr int kPieces = kSize / E;        // pieces per unit
+};
+
+// One operand's rows, staged as {stages, columns / E, threads} pieces.
+template <int TYPE, int E>
+struct Staged {
+    using S = typename Plain<TYPE>::S;
+    static constexpr int NV = cols_of(E) / E, kBytes = E * plain_size(TYPE);
+    static constexpr bool kAsync = kBytes >= 4;      // 2-byte pieces are loaded when they are due
+    char *mine;                                      // this thread's piece 0 of stage 0
+    int stage_bytes, piece_bytes;
+
+    __device__ __forceinline__ Staged(char *base, const Place &p)
+        : mine(base + threadIdx.x * kBytes), stage_bytes(p.threads * cols_of(E) * plain_size(TYPE)),
+          piece_bytes(p.threads * kBytes) {}
+    __device__ __forceinline__ void issue(const char *row, int st, const Place &p) const {
+        if constexpr (kAsync) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (in && i * step + lane * E < M) raw[i] = load_stream<XT, E>(x + i * step + lane * E);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (i * step + lane * E >= M) continue;
-        float v[E];
-        raw[i].get(v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += v[e];
-    }
-    const float mean = row_sum(s, a.width, part) / static_cast<float>(M);
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (i * step + lane * E >= M) continue;
-        float v[E];
-        raw[i].get(v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(v[e] - mean, v[e] - mean, s);
-    }
-    const float rstd = 1.f / sqrtf(row_sum(s, a.width, part) / static_cast<float>(M) + a.eps);
-    if (!in) return;
-    auto *y = row_of<YT>(a.y, a.nb_y, t);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int m = i * step + lane * E;
-        if (m >= M) continue;
-        float v[E], p[E];
-        raw[i].get(v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = (v[e] - mean) * rstd;
-        if (a.w) {
-            load_params<E>(a.w, a.w_type, m, p);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= p[e];
+            for (int i = 0; i < NV; ++i)
+                if (p.column<E>(i) < p.M)
+                    copy_async<kBytes>(mine + st * stage_bytes + i * piece_bytes,
+                                       row + p.column<E>(i) * plain_size(TYPE));
         }
-        if (a.b) {
-            load_params<E>(a.b, a.w_type, m, p);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] += p[e];
-        }
-        store_stream<YT, E>(y + m, v);
     }
-    if (lane == 0) {
-        if (a.mean) a.mean[t] = mean;
-        if (a.rstd) a.rstd[t] = rstd;
+    // A row's pieces that were not staged, all at once.
+    __device__ __forceinline__ void load(const char *row, const Place &p, Packed<TYPE, E> (&raw)[NV]) const {
+        if constexpr (!kAsync) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (p.column<E>(i) < p.M)
+                    raw[i] = load_stream<TYPE, E>(reinterpret_cast<const S *>(row) + p.column<E>(i));
+        }
+    }
+    // Unit u as pairs; a missing single is 0.
+    __device__ __forceinline__ void get(int u, int st, const Place &p, const Packed<TYPE, E> (&raw)[NV],
+                                        uint64_t (&v)[Units<E>::kPairs]) const {
+        float f[Units<E>::kSize];
+#pragma unroll
+        for (int k = 0; k < Units<E>::kPieces; ++k) {
+            const int i = u * Units<E>::kPieces + k;
+            Packed<TYPE, E> r = raw[i];
+            if constexpr (kAsync)
+                r.raw = *reinterpret_cast<const decltype(r.raw) *>(mine + st * stage_bytes + i * piece_bytes);
+            float part[E];
+            r.get(part);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[k * E + e] = k == 0 || p.column<E>(i) < p.M ? part[e] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < Units<E>::kPairs; ++j) v[j] = ptx::pack2(f[2 * j], f[2 * j + 1]);
+    }
+};
+
+// Whether unit u's first column is inside the row (and so all of it, but for a
+// second single).
+template <int E>
+__device__ __forceinline__ bool has_unit(int u, const Place &p) {
+    return p.column<E>(u * Units<E>::kPieces) < p.M;
+}
+
+// Unit u of a row of results.
+template <int TYPE, int E>
+__device__ __forceinline__ void put_unit(char *row, int u, const Place &p, const uint64_t (&v)[Units<E>::kPairs]) {
+    auto *out = reinterpret_cast<typename Plain<TYPE>::S *>(row);
+    float f[Units<E>::kSize];
+#pragma unroll
+    for (int j = 0; j < Units<E>::kPairs; ++j) ptx::unpack2(v[j], f[2 * j], f[2 * j + 1]);
+#pragma unroll
+    for (int k = 0; k < Units<E>::kPieces; ++k) {
+        const int m = p.column<E>(u * Units<E>::kPieces + k);
+        float part[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[e] = f[k * E + e];
+        if (k == 0 || m < p.M) store_stream<TYPE, E>(out + m, part);
     }
 }
 
-// Rows that 1024 threads cannot hold: one CTA per row, read three times (the
+// Unit u of w or b (`none` where the pointer is NULL or a single is missing).
+template <int E>
+__device__ __forceinline__ void get_params(const void *q, int type, float none, int u, const Place &p,
+                                           uint64_t (&v)[Units<E>::kPairs]) {
+    float f[Units<E>::kSize];
+#pragma unroll
+    for (int k = 0; k < Units<E>::kPieces; ++k) {
+        const int m = p.column<E>(u * Units<E>::kPieces + k);
+        float part[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[e] = none;
+        if (q && m < p.M) load_params<E>(q, type, m, part);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[k * E + e] = part[e];
+    }
+#pragma unroll
+    for (int j = 0; j < Units<E>::kPairs; ++j) v[j] = ptx::pack2(f[2 * j], f[2 * j + 1]);
+}
+
+__device__ __forceinline__ uint64_t both(float v) { return ptx::pack2(v, v); }
+__device__ __forceinline__ float add_halves(uint64_t v) {
+    float lo, hi;
+    ptx::unpack2(v, lo, hi);
+    return lo + hi;
+}
+
+// One value of each of a row's warps in every lane w < warps of all of them.
+__device__ __forceinline__ float2 exchange(float2 v, const Place &p, float2 *red, int &odd) {
+    float2 *now = red + odd * 32;                    // the other half may still be read
+    if ((threadIdx.x & 31) == 0) now[threadIdx.x >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(p.group + 1), "r"(p.width) : "memory");
+    odd ^= 1;
+    const int lane = threadIdx.x & 31;
+    return lane < p.warps ? now[p.warp0 + lane] : make_float2(0.f, 0.f);
+}
+
+// Mean and squares in one exchange: each warp takes its own mean and the
+// squares about it, and the row's are those of the warps' means and theirs,
+// so nothing cancels whatever the mean (a sum of squares would) and the row is
+// not waited for twice.
+template <int XT, int YT, int E>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormArgs a) {
+    using X = Staged<XT, E>;
+    using U = Units<E>;
+    extern __shared__ __align__(16) char sm[];
+    float2 *red = reinterpret_cast<float2 *>(sm);    // {2, 32}
+    const Place p(a.M, a.width);
+    const X xs(sm + 64 * 8, p);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * a.groups;
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x, *x_next = x;
+    char *y = static_cast<char *>(a.y) + r0 * a.nb_y;
+    int64_t t_next = r0;                             // the next row to copy
+    auto issue = [&](int st) {
+        if (t_next < a.T) xs.issue(x_next, st, p);
+        if (X::kAsync) commit_copies();
+        t_next += step;
+        x_next += step * a.nb_x;
+    };
+    for (int s = 0; s + 1 < a.stages; ++s) issue(s);
+    uint64_t w[U::kCount][U::kPairs], b[U::kCount][U::kPairs];
+#pragma unroll
+    for (int u = 0; u < U::kCount; ++u) {
+        get_params<E>(a.w, a.w_type, 1.f, u, p, w[u]);
+        get_params<E>(a.b, a.w_type, 0.f, u, p, b[u]);
+    }
+    // columns of this warp, and of warp `lane` of the row, and their inverses
+    float own = 0.f, theirs = 0.f;
+#pragma unroll
+    for (int i = 0; i < X::NV; ++i) {
+        const int lane = threadIdx.x & 31;
+        own += max(0, min(32 * E, p.M - (i * p.width + (p.lane & ~31)) * E));
+        if (lane < p.warps) theirs += max(0, min(32 * E, p.M - (i * p.width + lane * 32) * E));
+    }
+    const float each = 1.f / static_cast<float>(p.M), per_own = own > 0.f ? 1.f / own : 0.f;
+    const float per_their = theirs > 0.f ? 1.f / theirs : 0.f;
+    int st = 0, odd = 0;
+    for (int64_t t = r0; t < a.T; t += step) {
+        issue(st == 0 ? a.stages - 1 : st - 1);
+        if (X::kAsync) wait_copies(a.stages - 1);
+        Packed<XT, E> raw[X::NV];
+        xs.load(x, p, raw);
+        uint64_t v[U::kCount][U::kPairs], acc[2] = {0, 0};
+#pragma unroll
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+            xs.get(u, st, p, raw, v[u]);
+#pragma unroll
+            for (int j = 0; j < U::kPairs; ++j) acc[j & 1] = ptx::add2(acc[j & 1], v[u][j]);
+        }
+        float s = warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
+        float mean = s * per_own;
+        acc[0] = acc[1] = 0;
+#pragma unroll
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+#pragma unroll
+            for (int j = 0; j < U::kPairs; ++j) {
+                uint64_t d = ptx::sub2(v[u][j], both(mean));
+                if (E == 1 && p.column<E>(2 * u + 1) >= p.M) d &= 0xffffffffull;    // no second single
+                acc[j & 1] = ptx::fma2(d, d, acc[j & 1]);
+            }
+        }
+        float sq = warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
+        if (p.warps > 1) {
+            const float2 r = exchange(make_float2(s, sq), p, red, odd);
+            mean = warp_sum(r.x) * each;
+            const float d = fmaf(r.x, per_their, theirs > 0.f ? -mean : 0.f);
+            sq = warp_sum(fmaf(theirs * d, d, r.y));
+        }
+        const float rstd = rsqrtf(fmaf(sq, each, a.eps));
+        const uint64_t mean2 = both(mean), rstd2 = both(rstd);
+#pragma unroll
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+#pragma unroll
+            for (int j = 0; j < U::kPairs; ++j)
+                v[u][j] = ptx::fma2(ptx::mul2(ptx::sub2(v[u][j], mean2), rstd2), w[u][j], b[u][j]);
+            put_unit<YT, E>(y, u, p, v[u]);
+        }
+        if (p.lane == 0) {
+            if (a.mean) a.mean[t] = mean;
+            if (a.rstd) a.rstd[t] = rstd;
+        }
+        st = st + 1 == a.stages ? 0 : st + 1;
+        x += step * a.nb_x;
+        y += step * a.nb_y;
+    }
+}
+
+// Rows of more columns than 512 threads hold: one CTA per row, read three times (the
 // second and third time from L2).
 template <int XT, int YT>
 __global__ void __launch_bounds__(kThreads) norm_long_kernel(const NormArgs a) {
@@ -165,163 +346,132 @@ struct NormBackArgs {
     int width, groups, stages;       // threads per row, rows at once, rows staged per group
 };
 
-// A thread's own piece of shared memory, filled behind its back: copies of 4,
-// 8 or 16 bytes, committed row by row.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *smem, const void *p) {
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(p) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(p), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `left` (0 .. 3) committed rows are still on their way.
-__device__ __forceinline__ void wait_copies(int left) {
-    if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+// Where column m's w lies in shared memory: 16 bytes per lane in turn, so that no
+// two lanes of an access meet in a bank.
+template <int E>
+__device__ __forceinline__ int w_slot(int m, int width) {
+    if (E != 8) return m;
+    const int j = m / 8, i = j / width;
+    return ((i * 2 + (m / 4) % 2) * width + j - i * width) * 4 + m % 4;
 }
 
-constexpr int kBackCols = 16;        // columns of one thread
-constexpr int kMaxStages = 4;
-
-// dx, and this CTA's part of dw and db, in one pass.  `width` threads share a
-// row, 16 columns each, and keep the columns' sums in registers over all the
-// rows they meet; a CTA (one per SM) has `groups` such rows in work, and each
-// thread copies its pieces of the next rows into shared memory while this one
-// is reduced, so the loads never wait for the row's two sums.
-template <int XT, int DT, int E, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_back_kernel(const NormBackArgs a) {
-    constexpr int NV = kBackCols / E;
-    constexpr int BX = E * plain_size(XT), BD = E * plain_size(DT);
-    constexpr bool kAsync = BX >= 4 && BD >= 4;      // 2-byte pieces are loaded when they are due
+// dx, and this CTA's part of dw and db, in one pass.
+template <int XT, int DT, int E>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBackArgs a) {
+    using X = Staged<XT, E>;
+    using D = Staged<DT, E>;
+    using U = Units<E>;
+    constexpr bool kAsync = X::kAsync || D::kAsync;
     extern __shared__ __align__(16) char sm[];
     let_next_start();
-    const int M = static_cast<int>(a.M), threads = blockDim.x, tid = threadIdx.x;
+    const Place p(a.M, a.width);
     float *ws = reinterpret_cast<float *>(sm);                       // w as floats
-    float2 *red = reinterpret_cast<float2 *>(sm + ((M + 3) & ~3) * 4);   // {2, 32}
+    float2 *red = reinterpret_cast<float2 *>(sm + p.width * cols_of(E) * 4);    // {2, 32}
     char *ring = reinterpret_cast<char *>(red + 64);
-    const int stage_bytes = threads * NV * (BX + BD);
-    for (int m = tid; m < M; m += threads) ws[m] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
-    __syncthreads();
-
-    const int group = tid / a.width, lane = tid - group * a.width;
-    const int warps = a.width >> 5, warp0 = group * warps;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + group;
+    const X xs(ring, p);
+    const D ds(ring + a.stages * xs.stage_bytes, p);
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
     const int64_t step = static_cast<int64_t>(gridDim.x) * a.groups;
-    auto slot_x = [&](int st, int i) { return ring + st * stage_bytes + (i * threads + tid) * BX; };
-    auto slot_d = [&](int st, int i) {
-        return ring + st * stage_bytes + threads * NV * BX + (i * threads + tid) * BD;
-    };
-    auto issue = [&](int64_t t, int st) {
-        if (kAsync && t < a.T) {
-            const auto *x = row_of<XT>(a.x, a.nb_x, t);
-            const auto *d = row_of<DT>(a.dy, a.nb_dy, t);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int m = (i * a.width + lane) * E;
-                if (m < M) {
-                    if constexpr (kAsync) {
-                        copy_async<BX>(slot_x(st, i), x + m);
-                        copy_async<BD>(slot_d(st, i), d + m);
-                    }
-                }
-            }
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x, *x_next = x;
+    const char *dy = static_cast<const char *>(a.dy) + r0 * a.nb_dy, *dy_next = dy;
+    char *dx = static_cast<char *>(a.dx) + r0 * a.nb_dx;
+    int64_t t_next = r0;
+    auto issue = [&](int st) {
+        if (t_next < a.T) {
+            xs.issue(x_next, st, p);
+            ds.issue(dy_next, st, p);
         }
         if (kAsync) commit_copies();
+        t_next += step;
+        x_next += step * a.nb_x;
+        dy_next += step * a.nb_dy;
     };
-    float dw[NV][E], db[NV][E];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.f;
+    for (int s = 0; s + 1 < a.stages; ++s) issue(s);
+    for (int m = threadIdx.x; m < p.M; m += p.threads)
+        ws[w_slot<E>(m, p.width)] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
+    __syncthreads();
 
-    for (int s = 0; s + 1 < a.stages; ++s) issue(r0 + s * step, s);
+    uint64_t dw[U::kCount][U::kPairs], db[U::kCount][U::kPairs];
+#pragma unroll
+    for (int u = 0; u < U::kCount; ++u)
+#pragma unroll
+        for (int j = 0; j < U::kPairs; ++j) dw[u][j] = db[u][j] = 0;
+    auto get_w = [&](int u, uint64_t (&w)[U::kPairs]) {
+        if constexpr (E == 1) {
+            const int m = p.column<E>(2 * u), n = p.column<E>(2 * u + 1);
+            w[0] = ptx::pack2(ws[m], n < p.M ? ws[n] : 0.f);
+        } else {
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                const float4 q = *reinterpret_cast<const float4 *>(ws + ((u * (E / 4) + h) * p.width + p.lane) * 4);
+                w[2 * h] = ptx::pack2(q.x, q.y);
+                w[2 * h + 1] = ptx::pack2(q.z, q.w);
+            }
+        }
+    };
     float mean_next = 0.f, rstd_next = 0.f;
     if (r0 < a.T) {
         mean_next = a.mean[r0];
         rstd_next = a.rstd[r0];
     }
+    const float each = 1.f / static_cast<float>(p.M);
     int st = 0, odd = 0;
     for (int64_t t = r0; t < a.T; t += step) {
-        const int fill = st == 0 ? a.stages - 1 : st - 1;
-        issue(t + (a.stages - 1) * step, fill);
-        const float mean = mean_next, rstd = rstd_next;
+        issue(st == 0 ? a.stages - 1 : st - 1);
+        const uint64_t mean = both(mean_next), rstd = both(rstd_next);
         if (t + step < a.T) {
             mean_next = a.mean[t + step];
             rstd_next = a.rstd[t + step];
         }
         if (kAsync) wait_copies(a.stages - 1);
-        Packed<XT, E> xr[NV];
-        Packed<DT, E> dr[NV];
-        float2 sum = make_float2(0.f, 0.f);
-        const auto *x = row_of<XT>(a.x, a.nb_x, t);
-        const auto *d = row_of<DT>(a.dy, a.nb_dy, t);
-        if constexpr (!kAsync) {
+        Packed<XT, E> xr[X::NV];
+        Packed<DT, E> dr[D::NV];
+        xs.load(x, p, xr);
+        ds.load(dy, p, dr);
+        uint64_t sg = 0, sgx = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int m = (i * a.width + lane) * E;
-                if (m < M) {
-                    xr[i] = load_stream<XT, E>(x + m);
-                    dr[i] = load_stream<DT, E>(d + m);
-                }
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+            uint64_t w[U::kPairs], d[U::kPairs], xh[U::kPairs];
+            get_w(u, w);
+            xs.get(u, st, p, xr, xh);
+            ds.get(u, st, p, dr, d);
+#pragma unroll
+            for (int j = 0; j < U::kPairs; ++j) {
+                xh[j] = ptx::mul2(ptx::sub2(xh[j], mean), rstd);
+                const uint64_t g = ptx::mul2(d[j], w[j]);
+                sg = ptx::add2(sg, g);
+                sgx = ptx::fma2(g, xh[j], sgx);
+                dw[u][j] = ptx::fma2(d[j], xh[j], dw[u][j]);
+                db[u][j] = ptx::add2(db[u][j], d[j]);
             }
         }
-        auto columns = [&](int i, float (&xh)[E], float (&g)[E], float (&dv)[E], int m) {
-            if constexpr (kAsync) {
-                xr[i].raw = *reinterpret_cast<const decltype(xr[i].raw) *>(slot_x(st, i));
-                dr[i].raw = *reinterpret_cast<const decltype(dr[i].raw) *>(slot_d(st, i));
-            }
-            float w[E];
-            load_params<E>(ws, OOP_TYPE_F32, m, w);
-            xr[i].get(xh);
-            dr[i].get(dv);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                xh[e] = (xh[e] - mean) * rstd;
-                g[e] = dv[e] * w[e];
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int m = (i * a.width + lane) * E;
-            if (m >= M) continue;
-            float xh[E], g[E], dv[E];
-            columns(i, xh, g, dv, m);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                sum.x += g[e];
-                sum.y = fmaf(g[e], xh[e], sum.y);
-                dw[i][e] = fmaf(dv[e], xh[e], dw[i][e]);
-                db[i][e] += dv[e];
-            }
+        float2 sum = make_float2(warp_sum(add_halves(sg)), warp_sum(add_halves(sgx)));
+        if (p.warps > 1) {
+            sum = exchange(sum, p, red, odd);
+            sum = make_float2(warp_sum(sum.x), warp_sum(sum.y));
         }
-        sum.x = warp_sum(sum.x);
-        sum.y = warp_sum(sum.y);
-        if (warps > 1) {
-            float2 *now = red + odd * 32;            // the other half may still be read
-            if ((tid & 31) == 0) now[tid >> 5] = sum;
-            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(a.width) : "memory");
-            sum = (tid & 31) < warps ? now[warp0 + (tid & 31)] : make_float2(0.f, 0.f);
-            sum.x = warp_sum(sum.x);
-            sum.y = warp_sum(sum.y);
-            odd ^= 1;
-        }
-        const float mg = sum.x / static_cast<float>(M), mgx = sum.y / static_cast<float>(M);
-        auto *dx = row_of<DT>(a.dx, a.nb_dx, t);
+        const uint64_t mg = both(sum.x * each), mgx = both(-sum.y * each);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int m = (i * a.width + lane) * E;
-            if (m >= M) continue;
-            float xh[E], g[E], dv[E];
-            columns(i, xh, g, dv, m);
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+            // read again: the registers that would keep g and xh hold dw and db
+            uint64_t w[U::kPairs], xh[U::kPairs], g[U::kPairs];
+            get_w(u, w);
+            xs.get(u, st, p, xr, xh);
+            ds.get(u, st, p, dr, g);
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = rstd * (g[e] - mg - xh[e] * mgx);
-            store_stream<DT, E>(dx + m, g);
+            for (int j = 0; j < U::kPairs; ++j) {
+                xh[j] = ptx::mul2(ptx::sub2(xh[j], mean), rstd);
+                g[j] = ptx::fma2(xh[j], mgx, ptx::mul2(g[j], w[j]));
+                g[j] = ptx::mul2(rstd, ptx::sub2(g[j], mg));
+            }
+            put_unit<DT, E>(dx, u, p, g);
         }
         st = st + 1 == a.stages ? 0 : st + 1;
+        x += step * a.nb_x;
+        dy += step * a.nb_dy;
+        dx += step * a.nb_dx;
     }
     if (!a.part) return;
     // the groups' sums, group after group
@@ -329,25 +479,27 @@ __global__ void __launch_bounds__(THREADS, 1) norm_back_kernel(const NormBackArg
     float *all = reinterpret_cast<float *>(ring);
     for (int k = 0; k < a.groups; ++k) {
         if (a.groups > 1) __syncthreads();
-        if (group != k) continue;
+        if (p.group != k) continue;
         const bool first = k == 0, last = k == a.groups - 1;
-        float *out = a.part + static_cast<int64_t>(blockIdx.x) * M;
+        float *out = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int m = (i * a.width + lane) * E;
-            if (m >= M) continue;
+        for (int u = 0; u < U::kCount; ++u) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float sw = first ? dw[i][e] : all[m + e] + dw[i][e];
-                const float sb = first ? db[i][e] : all[M + m + e] + db[i][e];
-                (last ? out : all)[m + e] = sw;
-                (last ? out + static_cast<int64_t>(gridDim.x) * M : all + M)[m + e] = sb;
+            for (int e = 0; e < U::kSize; ++e) {
+                const int m = E == 1 ? p.column<E>(2 * u + e) : p.column<E>(u) + e;
+                if (m >= p.M) continue;
+                float sw[2], sb[2];
+                ptx::unpack2(dw[u][e / 2], sw[0], sw[1]);
+                ptx::unpack2(db[u][e / 2], sb[0], sb[1]);
+                (last ? out : all)[m] = first ? sw[e & 1] : all[m] + sw[e & 1];
+                (last ? out + static_cast<int64_t>(gridDim.x) * p.M : all + p.M)[m] =
+                    first ? sb[e & 1] : all[p.M + m] + sb[e & 1];
             }
         }
     }
 }
 
-// Rows of more than 16384 columns: dx from one CTA per row, then the columns'
+// Rows of more columns than 512 threads hold: dx from one CTA per row, then the columns'
 // sums.
 template <int XT, int DT>
 __global__ void __launch_bounds__(kThreads) norm_back_row_kernel(const NormBackArgs a) {
@@ -414,29 +566,47 @@ __global__ void __launch_bounds__(kThreads) norm_back_join_kernel(const float *p
 
 int64_t slices_of(int64_t T) { return T < kSlices ? T : kSlices; }
 
-// Vectors a thread of the row kernel holds at most.
-constexpr int kNormVecs = 8, kNormSingles = 16;
+// Threads that share a row.
+int width_of(int64_t M, int cols) { return static_cast<int>((M + 32 * cols - 1) / (32 * cols)) * 32; }
+
+// Shares a CTA among rows: width, groups and stages of the row kernels, with
+// `fixed` bytes of shared memory besides the staged rows and `bytes` of them per
+// column.  As many rows at once as fit, twice if they can be (one in
+// work, one on its way), but no CTA with many rows while others have none.
+// Named barriers 1 .. 15 are the groups' (a warp that has a row alone needs none).
+template <class Args>
+void share_cta(Args &a, int cols, int fixed, int bytes) {
+    a.width = width_of(a.M, cols);
+    const int slots = (kSmem - fixed) / (a.width * cols * bytes);
+    a.groups = static_cast<int>(std::min<int64_t>({kMaxThreads / a.width, a.width == 32 ? 16 : 15,
+                                                   std::max(1, slots / 2), (a.T + kSlices - 1) / kSlices}));
+    a.stages = std::max(1, std::min(kMaxStages, slots / a.groups));
+}
+
+template <int XT, int YT, int E>
+cudaError_t launch_norm_kernel(NormArgs a, cudaStream_t st) {
+    share_cta(a, cols_of(E), 64 * 8, plain_size(XT));
+    const int threads = a.width * a.groups;
+    const int smem = 64 * 8 + a.stages * threads * cols_of(E) * plain_size(XT);
+    const auto kern = norm_kernel<XT, YT, E>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(std::min(kSlices, (a.T + a.groups - 1) / a.groups)), threads, smem, st>>>(a);
+    return cudaGetLastError();
+}
 
 template <int XT, int YT>
-void launch_norm(NormArgs a, bool wide, cudaStream_t st) {
+cudaError_t launch_norm(const NormArgs &a, bool wide, cudaStream_t st) {
     // 16 bytes of the narrower type, so that neither side moves less
     constexpr int E = plain_size(XT) == 2 && plain_size(YT) == 2 ? 8 : 4;
-    const int64_t units = wide ? a.M / E : a.M;
-    const int64_t most = wide ? kNormVecs : kNormSingles;
-    if (units > 1024 * most) {
-        norm_long_kernel<XT, YT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
-        return;
-    }
-    a.width = 32;
-    while (a.width < 1024 && (units > a.width * most || (a.T < kFewRows && units > a.width))) a.width *= 2;
-    const int threads = std::max(a.width, 128);
-    const unsigned grid = static_cast<unsigned>((a.T + threads / a.width - 1) / (threads / a.width));
-    if (wide) norm_kernel<XT, YT, E, kNormVecs><<<grid, threads, 0, st>>>(a);
-    else norm_kernel<XT, YT, 1, kNormSingles><<<grid, threads, 0, st>>>(a);
+    if (wide && a.M <= kMaxThreads * cols_of(E)) return launch_norm_kernel<XT, YT, E>(a, st);
+    if (!wide && a.M <= kMaxThreads * cols_of(1)) return launch_norm_kernel<XT, YT, 1>(a, st);
+    norm_long_kernel<XT, YT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <int XT>
-void launch_norm(const NormArgs &a, int yt, bool wide, cudaStream_t st) {
+cudaError_t launch_norm(const NormArgs &a, int yt, bool wide, cudaStream_t st) {
     switch (yt) {
     case OOP_TYPE_F32: return launch_norm<XT, OOP_TYPE_F32>(a, wide, st);
     case OOP_TYPE_F16: return launch_norm<XT, OOP_TYPE_F16>(a, wide, st);
@@ -452,38 +622,27 @@ cudaError_t join_slices(const NormBackArgs &a, int slices, cudaStream_t st) {
 
 template <int XT, int DT, int E>
 cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
-    constexpr int bytes = kBackCols * (plain_size(XT) + plain_size(DT));
-    constexpr bool async = E * plain_size(XT) >= 4 && E * plain_size(DT) >= 4;
-    constexpr int most = async ? 1024 : 512;     // threads of a CTA
-    a.width = static_cast<int>((a.M + 32 * kBackCols - 1) / (32 * kBackCols)) * 32;
-    const int fixed = static_cast<int>((a.M + 3) / 4 * 16) + 64 * 8;
-    const int slots = (220 * 1024 - fixed) / (a.width * bytes);      // rows that fit on chip
-    // as many rows at once as fit, twice if they can be (one in work, one on its
-    // way), but no CTA with many rows while others have none; named barriers
-    // 1 .. 15 are theirs (a warp that has a row alone needs none)
-    a.groups = static_cast<int>(std::min<int64_t>({most / a.width, a.width == 32 ? 16 : 15,
-                                                   std::max(1, slots / 2), (a.T + kSlices - 1) / kSlices}));
+    constexpr int bytes = plain_size(XT) + plain_size(DT), cols = cols_of(E);
+    const int fixed = width_of(a.M, cols) * cols * 4 + 64 * 8;
+    share_cta(a, cols, fixed, bytes);
     const int threads = a.width * a.groups;
     const int slices = static_cast<int>(std::min(kSlices, (a.T + a.groups - 1) / a.groups));
-    a.stages = std::max(1, std::min(kMaxStages, slots / a.groups));
-    const int ring = std::max(a.stages * threads * bytes, a.groups > 1 ? static_cast<int>(a.M) * 8 : 0);
-    const auto kern = norm_back_kernel<XT, DT, E, most>;
+    const int ring = std::max(a.stages * threads * cols * bytes, a.groups > 1 ? static_cast<int>(a.M) * 8 : 0);
+    const auto kern = norm_back_kernel<XT, DT, E>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + ring);
     if (e != cudaSuccess) return e;
     kern<<<slices, threads, fixed + ring, st>>>(a);
-    if (!a.part) return cudaGetLastError();
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : join_slices<XT, DT>(a, slices, st);
+    if (e != cudaSuccess || !a.part) return e;
+    return join_slices<XT, DT>(a, slices, st);
 }
 
 template <int XT, int DT>
 cudaError_t launch_back(const NormBackArgs &a, bool wide, cudaStream_t st) {
     constexpr int E = plain_size(XT) == 2 && plain_size(DT) == 2 ? 8 : 4;
-    const bool single = !wide && (plain_size(XT) == 2 || plain_size(DT) == 2);
-    if (a.M <= (single ? 512 : 1024) * kBackCols) {
-        g_kernel_launches = a.part ? 2 : 1;
-        return wide ? launch_back_kernel<XT, DT, E>(a, st) : launch_back_kernel<XT, DT, 1>(a, st);
-    }
+    g_kernel_launches = a.part ? 2 : 1;
+    if (wide && a.M <= kMaxThreads * cols_of(E)) return launch_back_kernel<XT, DT, E>(a, st);
+    if (!wide && a.M <= kMaxThreads * cols_of(1)) return launch_back_kernel<XT, DT, 1>(a, st);
     norm_back_row_kernel<XT, DT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
     g_kernel_launches = a.part ? 3 : 1;
     if (!a.part) return cudaGetLastError();
@@ -530,14 +689,13 @@ int oop_layer_norm(const void *x, int x_type, int64_t nb_x, const void *w, const
         return OOP_ERR_ALIGN;
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
-    const NormArgs a = {x, w, b, y, mean, rstd, nb_x, nb_y, M, T, w_type, 0, eps};
+    const NormArgs a = {x, w, b, y, mean, rstd, nb_x, nb_y, M, T, w_type, 0, 0, 0, eps};
     const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && is_aligned(w, 16) &&
                       is_aligned(b, 16) && nb_x % 16 == 0 && nb_y % 16 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (x_type == OOP_TYPE_F32) launch_norm<OOP_TYPE_F32>(a, y_type, wide, st);
-    else if (x_type == OOP_TYPE_F16) launch_norm<OOP_TYPE_F16>(a, y_type, wide, st);
-    else launch_norm<OOP_TYPE_BF16>(a, y_type, wide, st);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = x_type == OOP_TYPE_F32   ? launch_norm<OOP_TYPE_F32>(a, y_type, wide, st)
+                          : x_type == OOP_TYPE_F16 ? launch_norm<OOP_TYPE_F16>(a, y_type, wide, st)
+                                                   : launch_norm<OOP_TYPE_BF16>(a, y_type, wide, st);
     if (e == cudaSuccess) g_kernel_launches = 1;
     return cuda_status(e);
 }
