@@ -29,15 +29,23 @@ struct NormArgs {
     float *mean, *rstd;
     int64_t nb_x, nb_y, M, T;
     int w_type;
-    int width, groups, stages;       // threads per row, rows at once, rows staged per group
+    int width, pieces, groups;       // threads per row, pieces of a thread, rows at once
     float eps;
 };
 
-// Column m0 .. m0 + E - 1 of a parameter of a run-time type (E = 1, or 16-byte
-// aligned rows and m0 % E == 0).
+// Column m0 .. m0 + E - 1 of a parameter of a run-time type (E = 1, or a 32-byte
+// aligned parameter and m0 % E == 0).
 template <int E>
 __device__ __forceinline__ void load_params(const void *p, int type, int64_t m0, float (&v)[E]) {
-    if (type == OOP_TYPE_F32) {
+    if (type == OOP_TYPE_F32 && E == 8) {
+        // one 32-byte access: as two of 16 bytes, a warp's lanes would lie 32
+        // bytes apart in each and take twice the cache's bandwidth
+        const float *q = static_cast<const float *>(p) + m0;
+        asm("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=f"(v[0]), "=f"(v[1 % E]), "=f"(v[2 % E]), "=f"(v[3 % E]), "=f"(v[4 % E]), "=f"(v[5 % E]),
+              "=f"(v[6 % E]), "=f"(v[7 % E])
+            : "l"(q));
+    } else if (type == OOP_TYPE_F32) {
         constexpr int H = E < 4 ? E : 4;
 #pragma unroll
         for (int i = 0; i < E; i += H) {
@@ -77,10 +85,9 @@ __device__ __forceinline__ void wait_copies(int left) {
 __host__ __device__ constexpr int cols_of(int E) { return E == 1 ? 16 : 32; }
 constexpr int kMaxStages = 4;
 
-// The form of both passes.  `width` threads share a row, 32 columns each; a CTA
-// (one per SM) has `groups` rows in work and goes on to others until none is
-// left, so what belongs to a column (w, b, the sums of dw and db) stays with
-// its thread.  Each thread copies its pieces of the next rows into shared memory
+// The backward pass.  `width` threads share a row, 32 columns each; a CTA (one
+// per SM) has `groups` rows in work and goes on to others until none is left, so
+// the sums of a column stay with its thread.  Each thread copies its pieces of the next rows into shared memory
 // while this one is reduced: the loads never wait for a row's sums, and no
 // thread reads what another one copied.  Two columns at a time in packed fp32
 // arithmetic: half the instructions, the same roundings.
@@ -177,25 +184,6 @@ __device__ __forceinline__ void put_unit(char *row, int u, const Place &p, const
     }
 }
 
-// Unit u of w or b (`none` where the pointer is NULL or a single is missing).
-template <int E>
-__device__ __forceinline__ void get_params(const void *q, int type, float none, int u, const Place &p,
-                                           uint64_t (&v)[Units<E>::kPairs]) {
-    float f[Units<E>::kSize];
-#pragma unroll
-    for (int k = 0; k < Units<E>::kPieces; ++k) {
-        const int m = p.column<E>(u * Units<E>::kPieces + k);
-        float part[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) part[e] = none;
-        if (q && m < p.M) load_params<E>(q, type, m, part);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[k * E + e] = part[e];
-    }
-#pragma unroll
-    for (int j = 0; j < Units<E>::kPairs; ++j) v[j] = ptx::pack2(f[2 * j], f[2 * j + 1]);
-}
-
 __device__ __forceinline__ uint64_t both(float v) { return ptx::pack2(v, v); }
 __device__ __forceinline__ float add_halves(uint64_t v) {
     float lo, hi;
@@ -213,102 +201,223 @@ __device__ __forceinline__ float2 exchange(float2 v, const Place &p, float2 *red
     return lane < p.warps ? now[p.warp0 + lane] : make_float2(0.f, 0.f);
 }
 
-// Mean and squares in one exchange: each warp takes its own mean and the
-// squares about it, and the row's are those of the warps' means and theirs,
-// so nothing cancels whatever the mean (a sum of squares would) and the row is
-// not waited for twice.
-template <int XT, int YT, int E>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormArgs a) {
-    using X = Staged<XT, E>;
-    using U = Units<E>;
-    extern __shared__ __align__(16) char sm[];
-    float2 *red = reinterpret_cast<float2 *>(sm);    // {2, 32}
-    const Place p(a.M, a.width);
-    const X xs(sm + 64 * 8, p);
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * a.groups;
-    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x, *x_next = x;
-    char *y = static_cast<char *>(a.y) + r0 * a.nb_y;
-    int64_t t_next = r0;                             // the next row to copy
-    auto issue = [&](int st) {
-        if (t_next < a.T) xs.issue(x_next, st, p);
-        if (X::kAsync) commit_copies();
-        t_next += step;
-        x_next += step * a.nb_x;
-    };
-    for (int s = 0; s + 1 < a.stages; ++s) issue(s);
-    uint64_t w[U::kCount][U::kPairs], b[U::kCount][U::kPairs];
-#pragma unroll
-    for (int u = 0; u < U::kCount; ++u) {
-        get_params<E>(a.w, a.w_type, 1.f, u, p, w[u]);
-        get_params<E>(a.b, a.w_type, 0.f, u, p, b[u]);
+// Where column m's w lies in shared memory: 16 bytes per lane in turn, so that no
+// two lanes of an access meet in a bank.
+template <int E>
+__device__ __forceinline__ int w_slot(int m, int width) {
+    if (E != 8) return m;
+    const int j = m / 8, i = j / width;
+    return ((i * 2 + (m / 4) % 2) * width + j - i * width) * 4 + m % 4;
+}
+
+// A row held in registers by `width` threads, n pieces of E columns each (of at
+// most NV).  FULL: every lane has n whole pieces.
+template <int XT, int E, int NV, bool FULL>
+struct HeldRow {
+    Packed<XT, E> raw[NV];
+
+    static __device__ __forceinline__ bool has(int i, const Place &p) {
+        return FULL ? true : p.column<E>(i) < p.M;
     }
-    // columns of this warp, and of warp `lane` of the row, and their inverses
-    float own = 0.f, theirs = 0.f;
+    // f(i, values) for each of the thread's pieces.
+    template <class F>
+    __device__ __forceinline__ void each(int n, const Place &p, F f) const {
 #pragma unroll
-    for (int i = 0; i < X::NV; ++i) {
-        const int lane = threadIdx.x & 31;
-        own += max(0, min(32 * E, p.M - (i * p.width + (p.lane & ~31)) * E));
-        if (lane < p.warps) theirs += max(0, min(32 * E, p.M - (i * p.width + lane * 32) * E));
-    }
-    const float each = 1.f / static_cast<float>(p.M), per_own = own > 0.f ? 1.f / own : 0.f;
-    const float per_their = theirs > 0.f ? 1.f / theirs : 0.f;
-    int st = 0, odd = 0;
-    for (int64_t t = r0; t < a.T; t += step) {
-        issue(st == 0 ? a.stages - 1 : st - 1);
-        if (X::kAsync) wait_copies(a.stages - 1);
-        Packed<XT, E> raw[X::NV];
-        xs.load(x, p, raw);
-        uint64_t v[U::kCount][U::kPairs], acc[2] = {0, 0};
-#pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
-            if (!has_unit<E>(u, p)) continue;
-            xs.get(u, st, p, raw, v[u]);
-#pragma unroll
-            for (int j = 0; j < U::kPairs; ++j) acc[j & 1] = ptx::add2(acc[j & 1], v[u][j]);
+        for (int i = 0; i < NV; ++i) {
+            if (i >= n) break;
+            float v[E];
+            raw[i].get(v);
+            if (has(i, p)) f(i, v);
         }
-        float s = warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
-        float mean = s * per_own;
-        acc[0] = acc[1] = 0;
+    }
+    __device__ __forceinline__ float sum(int n, const Place &p) const {
+        if constexpr (E == 1) {
+            float s = 0.f;
+            each(n, p, [&](int, const float (&v)[E]) { s += v[0]; });
+            return warp_sum(s);
+        } else {
+            uint64_t acc[2] = {0, 0};
+            each(n, p, [&](int, const float (&v)[E]) {
 #pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
-            if (!has_unit<E>(u, p)) continue;
+                for (int e = 0; e < E; e += 2)
+                    acc[(e / 2) & 1] = ptx::add2(acc[(e / 2) & 1], ptx::pack2(v[e], v[e + 1]));
+            });
+            return warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
+        }
+    }
+    __device__ __forceinline__ float squares(int n, const Place &p, float mean) const {
+        if constexpr (E == 1) {
+            float s = 0.f;
+            each(n, p, [&](int, const float (&v)[E]) { s = fmaf(v[0] - mean, v[0] - mean, s); });
+            return warp_sum(s);
+        } else {
+            uint64_t acc[2] = {0, 0};
+            const uint64_t m2 = both(mean);
+            each(n, p, [&](int, const float (&v)[E]) {
 #pragma unroll
-            for (int j = 0; j < U::kPairs; ++j) {
-                uint64_t d = ptx::sub2(v[u][j], both(mean));
-                if (E == 1 && p.column<E>(2 * u + 1) >= p.M) d &= 0xffffffffull;    // no second single
-                acc[j & 1] = ptx::fma2(d, d, acc[j & 1]);
+                for (int e = 0; e < E; e += 2) {
+                    const uint64_t d = ptx::sub2(ptx::pack2(v[e], v[e + 1]), m2);
+                    acc[(e / 2) & 1] = ptx::fma2(d, d, acc[(e / 2) & 1]);
+                }
+            });
+            return warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
+        }
+    }
+};
+
+// Columns of warp k of a row.
+template <int E, bool FULL>
+__device__ __forceinline__ float warp_columns(int k, int n, const Place &p) {
+    if (FULL) return static_cast<float>(n * 32 * E);
+    int c = 0;
+    for (int i = 0; i < n; ++i) c += max(0, min(32 * E, p.M - (i * p.width + k * 32) * E));
+    return static_cast<float>(c);
+}
+
+// (mean, rstd) of a row.  Rows that several warps share exchange once: each warp
+// takes its own mean and the squares about it, and the row's are those of the
+// warps' means and theirs, so nothing cancels whatever the mean (a sum of
+// squares would).  `meet` is the barrier of the row's warps.
+template <int XT, int E, int NV, bool FULL, class Meet>
+__device__ __forceinline__ float2 moments(const HeldRow<XT, E, NV, FULL> &row, int n, const Place &p, float eps,
+                                          float own, float theirs, float2 *red, Meet meet) {
+    const float s = row.sum(n, p);
+    float mean = own > 0.f ? s / own : 0.f;
+    float sq = row.squares(n, p, mean);
+    if (p.warps > 1) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) red[threadIdx.x >> 5] = make_float2(s, sq);
+        meet();
+        const float2 r = lane < p.warps ? red[p.warp0 + lane] : make_float2(0.f, 0.f);
+        mean = warp_sum(r.x) / static_cast<float>(p.M);
+        const float d = theirs > 0.f ? r.x / theirs - mean : 0.f;
+        sq = warp_sum(fmaf(theirs * d, d, r.y));
+    }
+    return make_float2(mean, rsqrtf(sq / static_cast<float>(p.M) + eps));
+}
+
+// The forward pass of few rows, and of rows that come in singles: a row per
+// `width` threads, every load before the first use.
+template <int XT, int YT, int E, int NV, bool FULL>
+__global__ void __launch_bounds__(NV > 4 ? 512 : 1024) norm_kernel(const NormArgs a) {
+    __shared__ float2 red[32];
+    const Place p(a.M, a.width);
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / a.width) + p.group;
+    const bool in = t < a.T;
+    if (!in && p.warps == 1) return;
+    const auto *x = row_of<XT>(a.x, a.nb_x, in ? t : 0) + p.lane * E;
+    const int step = p.width * E, n = a.pieces, lane = threadIdx.x & 31;
+    HeldRow<XT, E, NV, FULL> row;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i >= n) break;
+        if (row.has(i, p)) row.raw[i] = load_stream<XT, E>(x + i * step);
+    }
+    const float own = warp_columns<E, FULL>(p.lane >> 5, n, p);
+    const float theirs = lane < p.warps ? warp_columns<E, FULL>(lane, n, p) : 0.f;
+    const float2 mr = moments(row, n, p, a.eps, own, theirs, red, [] { __syncthreads(); });
+    if (!in) return;
+    auto *y = row_of<YT>(a.y, a.nb_y, t) + p.lane * E;
+    row.each(n, p, [&](int i, float (&v)[E]) {
+        float q[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = (v[e] - mr.x) * mr.y;
+        if (a.w) {
+            load_params<E>(a.w, a.w_type, p.column<E>(i), q);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= q[e];
+        }
+        if (a.b) {
+            load_params<E>(a.b, a.w_type, p.column<E>(i), q);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] += q[e];
+        }
+        store_stream<YT, E>(y + i * step, v);
+    });
+    if (p.lane == 0) {
+        if (a.mean) a.mean[t] = mr.x;
+        if (a.rstd) a.rstd[t] = mr.y;
+    }
+}
+
+// The forward pass of many rows.  One CTA per SM keeps w and b in shared memory
+// and takes row after row; a warp has as much of a row as its registers hold (20
+// vectors a lane), so that a reduction is paid for by up to 160 columns a lane
+// and most rows need no barrier.  A lane copies its pieces of its next row to
+// shared memory from when it has taken the current one into registers: there is
+// always a row per warp on its way.
+template <int XT, int YT, int E, int NV, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_many_kernel(const NormArgs a) {
+    constexpr int kBytes = E * plain_size(XT);
+    extern __shared__ __align__(16) char sm[];
+    const Place p(a.M, a.width);
+    float2 *red = reinterpret_cast<float2 *>(sm);                    // {2, 16}
+    float *ws = reinterpret_cast<float *>(sm + 256), *bs = ws + a.pieces * a.width * E;
+    char *mine = reinterpret_cast<char *>(bs + a.pieces * a.width * E) + threadIdx.x * kBytes;
+    const int n = a.pieces, lane = threadIdx.x & 31, piece = p.threads * kBytes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * a.groups;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x + p.lane * kBytes;
+    char *y = static_cast<char *>(a.y) + r0 * a.nb_y + p.lane * (E * plain_size(YT));
+    auto issue = [&](int64_t t) {
+        if (t < a.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i >= n) break;
+                if (HeldRow<XT, E, NV, FULL>::has(i, p))
+                    copy_async<kBytes>(mine + i * piece, x + i * (p.width * kBytes));
             }
         }
-        float sq = warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
-        if (p.warps > 1) {
-            const float2 r = exchange(make_float2(s, sq), p, red, odd);
-            mean = warp_sum(r.x) * each;
-            const float d = fmaf(r.x, per_their, theirs > 0.f ? -mean : 0.f);
-            sq = warp_sum(fmaf(theirs * d, d, r.y));
-        }
-        const float rstd = rsqrtf(fmaf(sq, each, a.eps));
-        const uint64_t mean2 = both(mean), rstd2 = both(rstd);
-#pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
-            if (!has_unit<E>(u, p)) continue;
-#pragma unroll
-            for (int j = 0; j < U::kPairs; ++j)
-                v[u][j] = ptx::fma2(ptx::mul2(ptx::sub2(v[u][j], mean2), rstd2), w[u][j], b[u][j]);
-            put_unit<YT, E>(y, u, p, v[u]);
-        }
-        if (p.lane == 0) {
-            if (a.mean) a.mean[t] = mean;
-            if (a.rstd) a.rstd[t] = rstd;
-        }
-        st = st + 1 == a.stages ? 0 : st + 1;
+        commit_copies();
         x += step * a.nb_x;
+    };
+    issue(r0);
+    for (int m = threadIdx.x; m < p.M; m += p.threads) {
+        ws[w_slot<E>(m, p.width)] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
+        bs[w_slot<E>(m, p.width)] = a.b ? load_any(a.b, a.w_type, m) : 0.f;
+    }
+    __syncthreads();
+    const float own = warp_columns<E, FULL>(p.lane >> 5, n, p);
+    const float theirs = lane < p.warps ? warp_columns<E, FULL>(lane, n, p) : 0.f;
+    int odd = 0;
+    for (int64_t t = r0; t < a.T; t += step) {
+        wait_copies(0);
+        HeldRow<XT, E, NV, FULL> row;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i >= n) break;
+            row.raw[i].raw = *reinterpret_cast<const decltype(row.raw[i].raw) *>(mine + i * piece);
+        }
+        issue(t + step);
+        const float2 mr = moments(row, n, p, a.eps, own, theirs, red + odd, [&] {
+            asm volatile("bar.sync %0, %1;" ::"r"(p.group + 1), "r"(p.width) : "memory");
+        });
+        odd ^= 16;                                   // the other half may still be read
+        const uint64_t mean = both(mr.x), rstd = both(mr.y);
+        row.each(n, p, [&](int i, float (&v)[E]) {
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                const int at = ((i * (E / 4) + h) * p.width + p.lane) * 4;
+                const float4 w = *reinterpret_cast<const float4 *>(ws + at);
+                const float4 b = *reinterpret_cast<const float4 *>(bs + at);
+                uint64_t lo = ptx::pack2(v[4 * h], v[4 * h + 1]), hi = ptx::pack2(v[4 * h + 2], v[4 * h + 3]);
+                lo = ptx::fma2(ptx::mul2(ptx::sub2(lo, mean), rstd), ptx::pack2(w.x, w.y), ptx::pack2(b.x, b.y));
+                hi = ptx::fma2(ptx::mul2(ptx::sub2(hi, mean), rstd), ptx::pack2(w.z, w.w), ptx::pack2(b.z, b.w));
+                ptx::unpack2(lo, v[4 * h], v[4 * h + 1]);
+                ptx::unpack2(hi, v[4 * h + 2], v[4 * h + 3]);
+            }
+            store_stream<YT, E>(reinterpret_cast<typename Plain<YT>::S *>(y) + i * (p.width * E), v);
+        });
+        if (p.lane == 0) {
+            if (a.mean) a.mean[t] = mr.x;
+            if (a.rstd) a.rstd[t] = mr.y;
+        }
         y += step * a.nb_y;
     }
 }
 
-// Rows of more columns than 512 threads hold: one CTA per row, read three times (the
-// second and third time from L2).
+// Rows that fit neither: one CTA per row, read three times (the second and third
+// time from L2).
 template <int XT, int YT>
 __global__ void __launch_bounds__(kThreads) norm_long_kernel(const NormArgs a) {
     __shared__ float part[32];
@@ -345,15 +454,6 @@ struct NormBackArgs {
     int w_type;
     int width, groups, stages;       // threads per row, rows at once, rows staged per group
 };
-
-// Where column m's w lies in shared memory: 16 bytes per lane in turn, so that no
-// two lanes of an access meet in a bank.
-template <int E>
-__device__ __forceinline__ int w_slot(int m, int width) {
-    if (E != 8) return m;
-    const int j = m / 8, i = j / width;
-    return ((i * 2 + (m / 4) % 2) * width + j - i * width) * 4 + m % 4;
-}
 
 // dx, and this CTA's part of dw and db, in one pass.
 template <int XT, int DT, int E>
@@ -583,24 +683,57 @@ void share_cta(Args &a, int cols, int fixed, int bytes) {
     a.stages = std::max(1, std::min(kMaxStages, slots / a.groups));
 }
 
-template <int XT, int YT, int E>
-cudaError_t launch_norm_kernel(NormArgs a, cudaStream_t st) {
-    share_cta(a, cols_of(E), 64 * 8, plain_size(XT));
-    const int threads = a.width * a.groups;
-    const int smem = 64 * 8 + a.stages * threads * cols_of(E) * plain_size(XT);
-    const auto kern = norm_kernel<XT, YT, E>;
+template <int XT, int YT, int E, int NV>
+cudaError_t launch_norm_few(const NormArgs &a, cudaStream_t st) {
+    const int threads = std::max(a.width, 128 / a.width * a.width);
+    const int64_t rows = threads / a.width;
+    const auto kern = int64_t(a.pieces) * a.width * E == a.M ? norm_kernel<XT, YT, E, NV, true>
+                                                             : norm_kernel<XT, YT, E, NV, false>;
+    kern<<<static_cast<unsigned>((a.T + rows - 1) / rows), threads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int XT, int YT, int E, int NV>
+cudaError_t launch_norm_many(const NormArgs &a, int fixed, cudaStream_t st) {
+    const auto kern = int64_t(a.pieces) * a.width * E == a.M ? norm_many_kernel<XT, YT, E, NV, true>
+                                                             : norm_many_kernel<XT, YT, E, NV, false>;
+    const int threads = a.width * a.groups, smem = fixed + threads * a.pieces * E * plain_size(XT);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(std::min(kSlices, (a.T + a.groups - 1) / a.groups)), threads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
+// Fewer rows than the SMs have warps for are spread over more threads each, for
+// latency.
+constexpr int64_t kFewRows = 152 * 8;
+
 template <int XT, int YT>
-cudaError_t launch_norm(const NormArgs &a, bool wide, cudaStream_t st) {
+cudaError_t launch_norm(NormArgs a, bool wide, cudaStream_t st) {
     // 16 bytes of the narrower type, so that neither side moves less
     constexpr int E = plain_size(XT) == 2 && plain_size(YT) == 2 ? 8 : 4;
-    if (wide && a.M <= kMaxThreads * cols_of(E)) return launch_norm_kernel<XT, YT, E>(a, st);
-    if (!wide && a.M <= kMaxThreads * cols_of(1)) return launch_norm_kernel<XT, YT, 1>(a, st);
+    const int64_t units = wide ? a.M / E : a.M;
+    // threads per row: the fewest that hold it in so many pieces, in whole warps
+    auto fits = [&](int pieces, int threads) {
+        const int64_t width = (units + 32 * pieces - 1) / (32 * pieces) * 32;
+        if (width > threads) return false;
+        a.width = static_cast<int>(width);
+        a.pieces = static_cast<int>((units + width - 1) / width);
+        return true;
+    };
+    if (wide) {
+        if (a.T < kFewRows && fits(4, 1024)) return launch_norm_few<XT, YT, E, 4>(a, st);
+        if (fits(20, kMaxThreads)) {
+            const int row = a.pieces * a.width * E, fixed = 256 + 2 * row * 4;
+            a.groups = std::min({kMaxThreads / a.width, a.width == 32 ? 16 : 15,
+                                 (kSmem - fixed) / (row * plain_size(XT))});
+            if (a.groups > 0 && a.pieces <= 10) return launch_norm_many<XT, YT, E, 10>(a, fixed, st);
+            if (a.groups > 0) return launch_norm_many<XT, YT, E, 20>(a, fixed, st);
+        }
+    } else {
+        if (a.T < kFewRows && fits(4, 1024)) return launch_norm_few<XT, YT, 1, 4>(a, st);
+        if (fits(32, 512)) return launch_norm_few<XT, YT, 1, 32>(a, st);
+    }
     norm_long_kernel<XT, YT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
@@ -690,8 +823,8 @@ int oop_layer_norm(const void *x, int x_type, int64_t nb_x, const void *w, const
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     const NormArgs a = {x, w, b, y, mean, rstd, nb_x, nb_y, M, T, w_type, 0, 0, 0, eps};
-    const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && is_aligned(w, 16) &&
-                      is_aligned(b, 16) && nb_x % 16 == 0 && nb_y % 16 == 0;
+    const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && is_aligned(w, 32) &&
+                      is_aligned(b, 32) && nb_x % 16 == 0 && nb_y % 16 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = x_type == OOP_TYPE_F32   ? launch_norm<OOP_TYPE_F32>(a, y_type, wide, st)
                           : x_type == OOP_TYPE_F16 ? launch_norm<OOP_TYPE_F16>(a, y_type, wide, st)

@@ -139,11 +139,18 @@ struct Packed {
     }
 };
 
-// Streaming accesses (data read or written once): evicted first.
+// Streaming accesses (data read or written once): evicted first, and
+// 16-byte loads leave L1 to what is read again (parameters).  Volatile: an
+// output may lie over the input, so no load may be repeated later.
 template <int TYPE, int E>
 __device__ __forceinline__ Packed<TYPE, E> load_stream(const typename Plain<TYPE>::S *p) {
     Packed<TYPE, E> r;
-    r.raw = __ldcs(reinterpret_cast<const typename Words<E * plain_size(TYPE)>::T *>(p));
+    if constexpr (E * plain_size(TYPE) == 16)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.raw.x), "=r"(r.raw.y), "=r"(r.raw.z), "=r"(r.raw.w)
+                     : "l"(p));
+    else
+        r.raw = __ldcs(reinterpret_cast<const typename Words<E * plain_size(TYPE)>::T *>(p));
     return r;
 }
 template <int TYPE, int E>
