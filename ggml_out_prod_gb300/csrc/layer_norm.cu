@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kSlices = 152;     // CTAs of the row kernels, one per SM: slices of dw and db
+static_assert(kSlices % (kThreads / 32) == 0);
 constexpr int kMaxThreads = 512;     // of a row kernel's CTA: 128 registers each
 constexpr int kSmem = 220 * 1024;    // of a CTA that has an SM to itself
 
@@ -122,13 +123,14 @@ struct Staged {
     __device__ __forceinline__ Staged(char *base, const Place &p)
         : mine(base + threadIdx.x * kBytes), stage_bytes(p.threads * cols_of(E) * plain_size(TYPE)),
           piece_bytes(p.threads * kBytes) {}
+    // (row: the address of the thread's first piece)
     __device__ __forceinline__ void issue(const char *row, int st, const Place &p) const {
         if constexpr (kAsync) {
+            char *to = mine + st * stage_bytes;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (p.column<E>(i) < p.M)
-                    copy_async<kBytes>(mine + st * stage_bytes + i * piece_bytes,
-                                       row + p.column<E>(i) * plain_size(TYPE));
+                    copy_async<kBytes>(to + i * piece_bytes, row + i * (p.width * kBytes));
         }
     }
     // A row's pieces that were not staged, all at once.
@@ -137,7 +139,7 @@ struct Staged {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (p.column<E>(i) < p.M)
-                    raw[i] = load_stream<TYPE, E>(reinterpret_cast<const S *>(row) + p.column<E>(i));
+                    raw[i] = load_stream<TYPE, E>(reinterpret_cast<const S *>(row + i * (p.width * kBytes)));
         }
     }
     // Unit u as pairs; a missing single is 0.
@@ -167,7 +169,7 @@ __device__ __forceinline__ bool has_unit(int u, const Place &p) {
     return p.column<E>(u * Units<E>::kPieces) < p.M;
 }
 
-// Unit u of a row of results.
+// Unit u of a row of results (row: the address of the thread's first piece).
 template <int TYPE, int E>
 __device__ __forceinline__ void put_unit(char *row, int u, const Place &p, const uint64_t (&v)[Units<E>::kPairs]) {
     auto *out = reinterpret_cast<typename Plain<TYPE>::S *>(row);
@@ -176,11 +178,11 @@ __device__ __forceinline__ void put_unit(char *row, int u, const Place &p, const
     for (int j = 0; j < Units<E>::kPairs; ++j) ptx::unpack2(v[j], f[2 * j], f[2 * j + 1]);
 #pragma unroll
     for (int k = 0; k < Units<E>::kPieces; ++k) {
-        const int m = p.column<E>(u * Units<E>::kPieces + k);
+        const int i = u * Units<E>::kPieces + k;
         float part[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) part[e] = f[k * E + e];
-        if (k == 0 || m < p.M) store_stream<TYPE, E>(out + m, part);
+        if (k == 0 || p.column<E>(i) < p.M) store_stream<TYPE, E>(out + i * (p.width * E), part);
     }
 }
 
@@ -199,6 +201,18 @@ __device__ __forceinline__ float2 exchange(float2 v, const Place &p, float2 *red
     odd ^= 1;
     const int lane = threadIdx.x & 31;
     return lane < p.warps ? now[p.warp0 + lane] : make_float2(0.f, 0.f);
+}
+
+// 2 * N floats, 16-byte aligned.
+template <int N>
+__device__ __forceinline__ void put_floats(float *out, const uint64_t (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; j += 2) {
+        float4 q;
+        ptx::unpack2(v[j], q.x, q.y);
+        ptx::unpack2(v[j + 1], q.z, q.w);
+        *reinterpret_cast<float4 *>(out + 2 * j) = q;
+    }
 }
 
 // Where column m's w lies in shared memory: 16 bytes per lane in turn, so that no
@@ -455,7 +469,9 @@ struct NormBackArgs {
     int width, groups, stages;       // threads per row, rows at once, rows staged per group
 };
 
-// dx, and this CTA's part of dw and db, in one pass.
+// dx, and this CTA's part of dw and db, in one pass.  (A variant without the
+// checks for a missing unit, for rows that fill every lane, keeps more of a row
+// in flight than 128 registers hold, and is 35% slower.)
 template <int XT, int DT, int E>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBackArgs a) {
     using X = Staged<XT, E>;
@@ -470,21 +486,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     char *ring = reinterpret_cast<char *>(red + 64);
     const X xs(ring, p);
     const D ds(ring + a.stages * xs.stage_bytes, p);
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * a.groups;
-    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x, *x_next = x;
-    const char *dy = static_cast<const char *>(a.dy) + r0 * a.nb_dy, *dy_next = dy;
-    char *dx = static_cast<char *>(a.dx) + r0 * a.nb_dx;
-    int64_t t_next = r0;
+    const unsigned step = gridDim.x * a.groups, T = static_cast<unsigned>(a.T);
+    const unsigned r0 = blockIdx.x * a.groups + p.group;
+    // addresses of the thread's first piece; all advance by `step` rows
+    const int64_t up_x = step * a.nb_x, up_dy = step * a.nb_dy, up_dx = step * a.nb_dx;
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x + p.lane * X::kBytes, *x_next = x;
+    const char *dy = static_cast<const char *>(a.dy) + r0 * a.nb_dy + p.lane * D::kBytes, *dy_next = dy;
+    char *dx = static_cast<char *>(a.dx) + r0 * a.nb_dx + p.lane * D::kBytes;
+    const float *mean_at = a.mean + r0, *rstd_at = a.rstd + r0;
+    unsigned t_next = r0;                            // (T <= 2^31, step <= 2432: no overflow)
     auto issue = [&](int st) {
-        if (t_next < a.T) {
+        if (t_next < T) {
             xs.issue(x_next, st, p);
             ds.issue(dy_next, st, p);
         }
         if (kAsync) commit_copies();
         t_next += step;
-        x_next += step * a.nb_x;
-        dy_next += step * a.nb_dy;
+        x_next += up_x;
+        dy_next += up_dy;
     };
     for (int s = 0; s + 1 < a.stages; ++s) issue(s);
     for (int m = threadIdx.x; m < p.M; m += p.threads)
@@ -510,18 +529,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         }
     };
     float mean_next = 0.f, rstd_next = 0.f;
-    if (r0 < a.T) {
-        mean_next = a.mean[r0];
-        rstd_next = a.rstd[r0];
+    if (r0 < T) {
+        mean_next = *mean_at;
+        rstd_next = *rstd_at;
     }
     const float each = 1.f / static_cast<float>(p.M);
     int st = 0, odd = 0;
-    for (int64_t t = r0; t < a.T; t += step) {
+    for (unsigned t = r0; t < T; t += step) {
         issue(st == 0 ? a.stages - 1 : st - 1);
         const uint64_t mean = both(mean_next), rstd = both(rstd_next);
-        if (t + step < a.T) {
-            mean_next = a.mean[t + step];
-            rstd_next = a.rstd[t + step];
+        mean_at += step;
+        rstd_at += step;
+        if (t + step < T) {
+            mean_next = *mean_at;
+            rstd_next = *rstd_at;
         }
         if (kAsync) wait_copies(a.stages - 1);
         Packed<XT, E> xr[X::NV];
@@ -551,7 +572,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             sum = exchange(sum, p, red, odd);
             sum = make_float2(warp_sum(sum.x), warp_sum(sum.y));
         }
-        const uint64_t mg = both(sum.x * each), mgx = both(-sum.y * each);
+        float r, unused;
+        ptx::unpack2(rstd, r, unused);
+        // dx = g * rstd + (x - mean) * slope + level
+        const uint64_t slope = both(-r * r * (sum.y * each)), level = both(-r * (sum.x * each));
 #pragma unroll
         for (int u = 0; u < U::kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
@@ -562,38 +586,53 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             ds.get(u, st, p, dr, g);
 #pragma unroll
             for (int j = 0; j < U::kPairs; ++j) {
-                xh[j] = ptx::mul2(ptx::sub2(xh[j], mean), rstd);
-                g[j] = ptx::fma2(xh[j], mgx, ptx::mul2(g[j], w[j]));
-                g[j] = ptx::mul2(rstd, ptx::sub2(g[j], mg));
+                const uint64_t rest = ptx::fma2(ptx::sub2(xh[j], mean), slope, level);
+                g[j] = ptx::fma2(ptx::mul2(g[j], w[j]), rstd, rest);
             }
             put_unit<DT, E>(dx, u, p, g);
         }
         st = st + 1 == a.stages ? 0 : st + 1;
-        x += step * a.nb_x;
-        dy += step * a.nb_dy;
-        dx += step * a.nb_dx;
+        x += up_x;
+        dy += up_dy;
+        dx += up_dx;
     }
     if (!a.part) return;
-    // the groups' sums, group after group
+    // the groups' sums, group after group: through shared memory in the threads'
+    // own order, from the last one to the workspace
     if (kAsync) wait_copies(0);
-    float *all = reinterpret_cast<float *>(ring);
+    uint64_t *all = reinterpret_cast<uint64_t *>(ring) + p.lane;     // {pairs, width}
+    constexpr int kAll = U::kCount * U::kPairs;
     for (int k = 0; k < a.groups; ++k) {
         if (a.groups > 1) __syncthreads();
         if (p.group != k) continue;
-        const bool first = k == 0, last = k == a.groups - 1;
-        float *out = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
 #pragma unroll
         for (int u = 0; u < U::kCount; ++u) {
 #pragma unroll
-            for (int e = 0; e < U::kSize; ++e) {
-                const int m = E == 1 ? p.column<E>(2 * u + e) : p.column<E>(u) + e;
-                if (m >= p.M) continue;
-                float sw[2], sb[2];
-                ptx::unpack2(dw[u][e / 2], sw[0], sw[1]);
-                ptx::unpack2(db[u][e / 2], sb[0], sb[1]);
-                (last ? out : all)[m] = first ? sw[e & 1] : all[m] + sw[e & 1];
-                (last ? out + static_cast<int64_t>(gridDim.x) * p.M : all + p.M)[m] =
-                    first ? sb[e & 1] : all[p.M + m] + sb[e & 1];
+            for (int j = 0; j < U::kPairs; ++j) {
+                const int at = (u * U::kPairs + j) * p.width;
+                if (k > 0) {
+                    dw[u][j] = ptx::add2(all[at], dw[u][j]);
+                    db[u][j] = ptx::add2(all[kAll * p.width + at], db[u][j]);
+                }
+                if (k + 1 < a.groups) {
+                    all[at] = dw[u][j];
+                    all[kAll * p.width + at] = db[u][j];
+                }
+            }
+        }
+        if (k + 1 < a.groups) continue;
+        float *out_w = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
+        float *out_b = out_w + static_cast<int64_t>(gridDim.x) * p.M;
+        // (16-byte stores where the parts' rows allow them)
+#pragma unroll
+        for (int u = 0; u < U::kCount; ++u) {
+            if (!has_unit<E>(u, p)) continue;
+            if (E > 1) {
+                put_floats<U::kPairs>(out_w + p.column<E>(u), dw[u]);
+                put_floats<U::kPairs>(out_b + p.column<E>(u), db[u]);
+            } else {
+                put_unit<OOP_TYPE_F32, E>(reinterpret_cast<char *>(out_w + p.lane), u, p, dw[u]);
+                put_unit<OOP_TYPE_F32, E>(reinterpret_cast<char *>(out_b + p.lane), u, p, db[u]);
             }
         }
     }
@@ -652,10 +691,15 @@ __global__ void __launch_bounds__(kThreads) norm_back_join_kernel(const float *p
     if (!out) return;
     part += static_cast<int64_t>(blockIdx.y) * slices * M + m;
     float s = 0.f;
-    if (m < M) {
-#pragma unroll 20
-        for (int k = warp; k < slices; k += kThreads / 32) s += __ldcg(part + k * M);
+    constexpr int kMost = static_cast<int>(kSlices) / (kThreads / 32);
+    float v[kMost];                                  // every load before the first sum
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const int k = warp + j * (kThreads / 32);
+        v[j] = m < M && k < slices ? __ldcg(part + k * M) : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) s += v[j];
     sums[warp][lane] = s;
     __syncthreads();
     if (warp > 0 || m >= M) return;
@@ -760,7 +804,7 @@ cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
     share_cta(a, cols, fixed, bytes);
     const int threads = a.width * a.groups;
     const int slices = static_cast<int>(std::min(kSlices, (a.T + a.groups - 1) / a.groups));
-    const int ring = std::max(a.stages * threads * cols * bytes, a.groups > 1 ? static_cast<int>(a.M) * 8 : 0);
+    const int ring = std::max(a.stages * threads * cols * bytes, a.groups > 1 ? a.width * cols * 8 : 0);
     const auto kern = norm_back_kernel<XT, DT, E>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + ring);
     if (e != cudaSuccess) return e;
