@@ -683,16 +683,37 @@ def out_prod_host(a_host, b_host, a_type=None, ne_a=None, out=None, device_buffe
 # run on the current stream; with ``stream`` given, on that one, which then
 # owns what the call allocates.
 
-_DTYPES = None          # torch dtype -> type id
 _Two = ctypes.c_int64 * 2
 
 
-def _plain_type(t, name):
-    global _DTYPES
-    if _DTYPES is None:
+class _Runtime:
+    """What every call below needs, looked up once: on this host a small call's
+    time is its lookups and allocations."""
+
+    def __init__(self):
         torch = _torch()
-        _DTYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
-    kind = _DTYPES.get(t if not hasattr(t, "dtype") else t.dtype)
+        self.lib = lib()
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.f32, self.i32, self.u8 = torch.float32, torch.int32, torch.uint8
+        self.types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+        self.device = torch.cuda.current_device
+        # the current stream's handle by device index takes 0.1 us, the Stream object 3 us
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_runtime = None
+
+
+def _rt():
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
+
+
+def _plain_type(dtype, name):
+    kind = _rt().types.get(dtype)
     if kind is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16")
     return kind
@@ -735,18 +756,21 @@ def _vector(t, name, n, dtype):
 def _output(out, shape, dtype, device, name="out"):
     """A new tensor, or the caller's if it fits: (tensor, byte stride of a row)."""
     if out is None:
-        out = _torch().empty(shape, dtype=dtype, device=device)
+        out = _rt().empty(shape, dtype=dtype, device=device)
         return out, shape[-1] * out.element_size()
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
     return out, _matrix(out, name)[2]
 
 
-def _same_device(*tensors):
-    index = _torch().cuda.current_device()
+def _current_stream(*tensors):
+    """The current stream's handle, after checking that every tensor is on its device."""
+    rt = _rt()
+    index = rt.device()
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("every tensor must be on the current CUDA device")
+    return rt.stream(index)
 
 
 def _on_stream(stream, call, *inputs):
@@ -764,24 +788,10 @@ def _scratch(nbytes, device, workspace):
     if nbytes == 0:
         return None, None, 0
     if workspace is None:
-        workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+        workspace = _rt().empty(nbytes, dtype=_rt().u8, device=device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-_stream_of = None
-
-
-def _raw_stream():
-    """The current stream's handle.  torch's own lookup by device index takes
-    0.1 us, the Stream object 3 us: as much as the rest of a small call."""
-    global _stream_of
-    torch = _torch()
-    if _stream_of is None:
-        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _stream_of(torch.cuda.current_device())
 
 
 def get_rows(table, ids, scale=1.0, table_type=None, out_dtype=None, out=None, stream=None):
@@ -792,14 +802,14 @@ def get_rows(table, ids, scale=1.0, table_type=None, out_dtype=None, out=None, s
     (*ids.shape, M) in ``out_dtype`` (default: the table's, float32 for a
     quantised one).  An id outside the table gives a row of zeros and sets the
     device status."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: get_rows(table, ids, scale, table_type, out_dtype, out),
                           table, ids, out)
     if table.dim() != 2:
         raise ValueError("table must have two dimensions")
     if table_type is None:
-        table_type = _plain_type(table, "table")
+        table_type = _plain_type(table.dtype, "table")
     _check_src0(table, table_type, "table")
     M, V, nb = _matrix(table, "table")
     if table_type in _BLOCKS:
@@ -809,14 +819,13 @@ def get_rows(table, ids, scale=1.0, table_type=None, out_dtype=None, out=None, s
         M = M // nbytes * qk
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else \
-            torch.float32 if table_type in _BLOCKS else table.dtype
+            rt.f32 if table_type in _BLOCKS else table.dtype
     kind = _plain_type(out_dtype, "out")
     n = ids.numel()
-    pids = _vector(ids, "ids", n, torch.int32)
+    pids = _vector(ids, "ids", n, rt.i32)
     y, nb_y = _output(out, tuple(ids.shape) + (M,) if ids.dim() else (M,), out_dtype, table.device)
-    _same_device(table, ids)
-    rc = lib().oop_get_rows(table.data_ptr(), table_type, nb, pids, y.data_ptr(), kind, nb_y,
-                            _Two(M, V), n, scale, _raw_stream())
+    rc = rt.lib.oop_get_rows(table.data_ptr(), table_type, nb, pids, y.data_ptr(), kind, nb_y,
+                                _Two(M, V), n, scale, _current_stream(table, ids))
     if rc != OK:
         raise OopError(rc, "oop_get_rows")
     return y
@@ -828,24 +837,24 @@ def get_rows_back(dy, ids, n_rows, scale=1.0, out=None, accumulate=False, worksp
 
     dy: (*ids.shape, M) float32 or bfloat16; ids: int32.  With ``accumulate``
     the gradient is added to ``out``; only the rows that occur are touched."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: get_rows_back(dy, ids, n_rows, scale, out, accumulate,
                                                         workspace), dy, ids, out, workspace)
     M, T, nb = _matrix(dy, "dy")
-    kind = _plain_type(dy, "dy")
-    pids = _vector(ids, "ids", T, torch.int32)
+    kind = _plain_type(dy.dtype, "dy")
+    pids = _vector(ids, "ids", T, rt.i32)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is not None and not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    d, _ = _output(out, (n_rows, M), torch.float32, dy.device)
-    _same_device(dy, ids)
+    d, _ = _output(out, (n_rows, M), rt.f32, dy.device)
+    st = _current_stream(dy, ids)
     ne = _Two(M, n_rows)
-    L = lib()
+    L = rt.lib
     ws, pws, nws = _scratch(L.oop_get_rows_back_workspace_size(ne, T), dy.device, workspace)
     rc = L.oop_get_rows_back(dy.data_ptr(), kind, nb, pids, d.data_ptr(), ne, T, scale,
-                             1 if accumulate else 0, pws, nws, _raw_stream())
+                             1 if accumulate else 0, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_get_rows_back")
     return d
@@ -857,24 +866,24 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, out=None, st
     x: (..., M) float32 / float16 / bfloat16; weight, bias: (M,) of one plain
     type, or None.  y is in ``out_dtype`` (default: x's); mean and rstd are
     float32 of x's leading shape, as layer_norm_back takes them."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: layer_norm(x, weight, bias, eps, out_dtype, out),
                           x, weight, bias, out)
     M, T, nb = _matrix(x, "x")
-    kind = _plain_type(x, "x")
+    kind = _plain_type(x.dtype, "x")
     w_kind = _param_type(weight, bias)
     pw = _vector(weight, "weight", M, weight.dtype) if weight is not None else None
     pb = _vector(bias, "bias", M, bias.dtype) if bias is not None else None
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else x.dtype
     y, nb_y = _output(out, x.shape, out_dtype, x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
-    _same_device(x, weight, bias)
-    rc = lib().oop_layer_norm(x.data_ptr(), kind, nb, pw, pb, w_kind, y.data_ptr(),
-                              _plain_type(out_dtype, "out"), nb_y, mean.data_ptr(),
-                              rstd.data_ptr(), _Two(M, T), eps, _raw_stream())
+    mean = rt.empty(x.shape[:-1], dtype=rt.f32, device=x.device)
+    rstd = rt.empty_like(mean)
+    rc = rt.lib.oop_layer_norm(x.data_ptr(), kind, nb, pw, pb, w_kind, y.data_ptr(),
+                                  _plain_type(out_dtype, "out"), nb_y, mean.data_ptr(),
+                                  rstd.data_ptr(), _Two(M, T), eps,
+                                  _current_stream(x, weight, bias))
     if rc != OK:
         raise OopError(rc, "oop_layer_norm")
     return y, mean, rstd
@@ -884,7 +893,7 @@ def _param_type(weight, bias):
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have one type")
     p = weight if weight is not None else bias
-    return TYPE_F32 if p is None else _plain_type(p, "weight")
+    return TYPE_F32 if p is None else _plain_type(p.dtype, "weight")
 
 
 def layer_norm_back(dy, x, mean, rstd, weight=None, want_dw=True, want_db=True, out=None,
@@ -893,30 +902,30 @@ def layer_norm_back(dy, x, mean, rstd, weight=None, want_dw=True, want_db=True, 
 
     dy: like x in shape, float32 or bfloat16; dx has dy's type and may be
     written over it (``out=dy``); dw and db are float32 (M,) or None."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: layer_norm_back(dy, x, mean, rstd, weight, want_dw,
                                                           want_db, out, workspace),
                           dy, x, mean, rstd, weight, out, workspace)
     M, T, nb_x = _matrix(x, "x")
-    kind, d_kind, w_kind = _plain_type(x, "x"), _plain_type(dy, "dy"), _param_type(weight, None)
+    kind, d_kind, w_kind = _plain_type(x.dtype, "x"), _plain_type(dy.dtype, "dy"), _param_type(weight, None)
     if dy.shape != x.shape:
         raise ValueError("dy and x must have one shape")
     nb_dy = _matrix(dy, "dy")[2]
-    pm = _vector(mean, "mean", T, torch.float32)
-    pr = _vector(rstd, "rstd", T, torch.float32)
+    pm = _vector(mean, "mean", T, rt.f32)
+    pr = _vector(rstd, "rstd", T, rt.f32)
     pw = _vector(weight, "weight", M, weight.dtype) if weight is not None else None
     dx, nb_dx = _output(out, x.shape, dy.dtype, x.device)
-    dw = torch.empty(M, dtype=torch.float32, device=x.device) if want_dw else None
-    db = torch.empty(M, dtype=torch.float32, device=x.device) if want_db else None
-    _same_device(x, dy, mean, rstd, weight)
+    dw = rt.empty(M, dtype=rt.f32, device=x.device) if want_dw else None
+    db = rt.empty(M, dtype=rt.f32, device=x.device) if want_db else None
+    st = _current_stream(x, dy, mean, rstd, weight)
     ne = _Two(M, T)
-    L = lib()
+    L = rt.lib
     ws, pws, nws = _scratch(L.oop_layer_norm_back_workspace_size(ne) if want_dw or want_db else 0,
                             x.device, workspace)
     rc = L.oop_layer_norm_back(dy.data_ptr(), d_kind, nb_dy, x.data_ptr(), kind, nb_x, pm, pr, pw,
                                w_kind, dx.data_ptr(), nb_dx, dw.data_ptr() if want_dw else None,
-                               db.data_ptr() if want_db else None, ne, pws, nws, _raw_stream())
+                               db.data_ptr() if want_db else None, ne, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_layer_norm_back")
     return dx, dw, db
@@ -924,11 +933,10 @@ def layer_norm_back(dy, x, mean, rstd, weight=None, want_dw=True, want_db=True, 
 
 def _drop(fn, where, x, p, seed, offset, out):
     M, T, nb = _matrix(x, "x")
-    kind = _plain_type(x, "x")
+    kind = _plain_type(x.dtype, "x")
     y, nb_y = _output(out, x.shape, x.dtype, x.device)
-    _same_device(x)
     rc = fn(x.data_ptr(), kind, nb, y.data_ptr(), nb_y, _Two(M, T), p,
-            seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _raw_stream())
+            seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, _current_stream(x))
     if rc != OK:
         raise OopError(rc, where)
     return y
@@ -943,7 +951,7 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
     (..., M) float32 / float16 / bfloat16; ``out=x`` works in place."""
     if stream is not None:
         return _on_stream(stream, lambda: dropout(x, p, seed, offset, out), x, out)
-    return _drop(lib().oop_dropout, "oop_dropout", x, p, seed, offset, out)
+    return _drop(_rt().lib.oop_dropout, "oop_dropout", x, p, seed, offset, out)
 
 
 def dropout_back(dy, p, seed, offset=0, out=None, stream=None):
@@ -951,7 +959,7 @@ def dropout_back(dy, p, seed, offset=0, out=None, stream=None):
     dropped, the others scaled alike."""
     if stream is not None:
         return _on_stream(stream, lambda: dropout_back(dy, p, seed, offset, out), dy, out)
-    return _drop(lib().oop_dropout_back, "oop_dropout_back", dy, p, seed, offset, out)
+    return _drop(_rt().lib.oop_dropout_back, "oop_dropout_back", dy, p, seed, offset, out)
 
 
 class PreferenceLoss(NamedTuple):
@@ -977,32 +985,31 @@ def preference_loss(logits, labels, seq, ref_logps=None, beta=0.1, label_smoothi
     for rows that are not scored; seq: int32 (2P + 1,), the first row of each
     sequence and the end, the P chosen sequences before the P rejected ones;
     ref_logps: float32 (T,), the reference model's logps (see token_logps)."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: preference_loss(logits, labels, seq, ref_logps, beta,
                                                           label_smoothing, workspace),
                           logits, labels, seq, ref_logps, workspace)
     V, T, nb = _matrix(logits, "logits")
-    kind = _plain_type(logits, "logits")
+    kind = _plain_type(logits.dtype, "logits")
     P = _pairs(seq)
-    f32, dev = torch.float32, logits.device
-    pl = _vector(labels, "labels", T, torch.int32)
-    ps = _vector(seq, "seq", 2 * P + 1, torch.int32)
+    dev = logits.device
+    empty, f32 = rt.empty, rt.f32
+    pl = _vector(labels, "labels", T, rt.i32)
+    ps = _vector(seq, "seq", 2 * P + 1, rt.i32)
     pr = _vector(ref_logps, "ref_logps", T, f32)
-    r = PreferenceLoss(torch.empty((), dtype=f32, device=dev),
-                       torch.empty(P, dtype=f32, device=dev),
-                       torch.empty(2 * P, dtype=f32, device=dev),
-                       torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev))
+    logps = empty(T, dtype=f32, device=dev)
+    r = PreferenceLoss(empty((), dtype=f32, device=dev), empty(P, dtype=f32, device=dev),
+                       empty(2 * P, dtype=f32, device=dev), logps, rt.empty_like(logps))
     if P == 0:
         r.loss.zero_()
-    _same_device(logits, labels, seq, ref_logps)
+    st = _current_stream(logits, labels, seq, ref_logps)
     ne = _Two(V, T)
-    L = lib()
+    L = rt.lib
     ws, pws, nws = _scratch(L.oop_preference_loss_workspace_size(ne, P), dev, workspace)
     rc = L.oop_preference_loss(logits.data_ptr(), kind, nb, pl, ps, pr, r.loss.data_ptr(),
                                r.losses.data_ptr(), r.ratios.data_ptr(), r.logps.data_ptr(),
-                               r.lse.data_ptr(), ne, P, beta, label_smoothing, pws, nws,
-                               _raw_stream())
+                               r.lse.data_ptr(), ne, P, beta, label_smoothing, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_preference_loss")
     return r
@@ -1011,22 +1018,21 @@ def preference_loss(logits, labels, seq, ref_logps=None, beta=0.1, label_smoothi
 def token_logps(logits, labels, workspace=None, stream=None):
     """(logps, lse) of each row's label: preference_loss without pairs, as the
     reference model needs it."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: token_logps(logits, labels, workspace), logits, labels,
                           workspace)
     V, T, nb = _matrix(logits, "logits")
-    kind = _plain_type(logits, "logits")
-    pl = _vector(labels, "labels", T, torch.int32)
-    logps = torch.empty(T, dtype=torch.float32, device=logits.device)
-    lse = torch.empty_like(logps)
-    _same_device(logits, labels)
+    kind = _plain_type(logits.dtype, "logits")
+    pl = _vector(labels, "labels", T, rt.i32)
+    logps = rt.empty(T, dtype=rt.f32, device=logits.device)
+    lse = rt.empty_like(logps)
+    st = _current_stream(logits, labels)
     ne = _Two(V, T)
-    L = lib()
+    L = rt.lib
     ws, pws, nws = _scratch(L.oop_preference_loss_workspace_size(ne, 0), logits.device, workspace)
     rc = L.oop_preference_loss(logits.data_ptr(), kind, nb, pl, None, None, None, None, None,
-                               logps.data_ptr(), lse.data_ptr(), ne, 0, 0.0, 0.0, pws, nws,
-                               _raw_stream())
+                               logps.data_ptr(), lse.data_ptr(), ne, 0, 0.0, 0.0, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_preference_loss")
     return logps, lse
@@ -1040,27 +1046,27 @@ def preference_loss_back(logits, labels, seq, lse, ratios, beta=0.1, label_smoot
     multiplies the gradient.  Returns (T, V) in ``out_dtype`` (float32 or
     bfloat16; default: the logits' type, float32 for float16 logits).
     ``out=logits`` overwrites the logits."""
-    torch = _torch()
+    rt = _rt()
     if stream is not None:
         return _on_stream(stream, lambda: preference_loss_back(
             logits, labels, seq, lse, ratios, beta, label_smoothing, dloss, out_dtype, out),
             logits, labels, seq, lse, ratios, dloss, out)
     V, T, nb = _matrix(logits, "logits")
-    kind = _plain_type(logits, "logits")
+    kind = _plain_type(logits.dtype, "logits")
     P = _pairs(seq)
-    f32 = torch.float32
-    pl = _vector(labels, "labels", T, torch.int32)
-    ps = _vector(seq, "seq", 2 * P + 1, torch.int32)
+    f32 = rt.f32
+    pl = _vector(labels, "labels", T, rt.i32)
+    ps = _vector(seq, "seq", 2 * P + 1, rt.i32)
     pe = _vector(lse, "lse", T, f32)
     pr = _vector(ratios, "ratios", 2 * P, f32)
     pd = _vector(dloss, "dloss", 1, f32)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else f32 if kind == TYPE_F16 else logits.dtype
     d, nb_d = _output(out, logits.shape, out_dtype, logits.device)
-    _same_device(logits, labels, seq, lse, ratios, dloss)
-    rc = lib().oop_preference_loss_back(logits.data_ptr(), kind, nb, pl, ps, pe, pr, pd,
-                                        d.data_ptr(), _plain_type(out_dtype, "out"), nb_d,
-                                        _Two(V, T), P, beta, label_smoothing, _raw_stream())
+    rc = rt.lib.oop_preference_loss_back(
+        logits.data_ptr(), kind, nb, pl, ps, pe, pr, pd, d.data_ptr(),
+        _plain_type(out_dtype, "out"), nb_d, _Two(V, T), P, beta, label_smoothing,
+        _current_stream(logits, labels, seq, lse, ratios, dloss))
     if rc != OK:
         raise OopError(rc, "oop_preference_loss_back")
     return d

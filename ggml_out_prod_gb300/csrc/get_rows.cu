@@ -86,6 +86,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 9;                        // of the id, sorted in one pass
 constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kRanked = 1024;                      // tokens sorted by counting: an eighth per CTA, 8 threads each
+static_assert(kRanked / kSortCluster * 8 <= kSortThreads);
 constexpr int kSortSmem = (kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
 
 struct SortPlan {
@@ -148,7 +150,26 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a) {
     const int64_t w0 = min(c1, c0 + per_warp * warp), w1 = min(c1, w0 + per_warp);
     if (rank == 0 && tid == 0) *a.n_crossing = 0;
 
-    for (int pass = 0; pass < a.passes; ++pass) {
+    if (a.T <= kRanked) {
+        // few enough to count, for each, the items before it: 8 threads per item
+        for (int64_t i = tid; i < a.T; i += kSortThreads) {
+            const int32_t id = a.ids[i];
+            const bool ok = id >= 0 && id < a.V;
+            sm[i] = ok ? static_cast<uint32_t>(id) : static_cast<uint32_t>(a.V);
+            if (!ok && rank == 0) record_status(a.status, OOP_ERR_BAD_ID);
+        }
+        __syncthreads();
+        const int T = static_cast<int>(a.T), i = static_cast<int>(c0) + tid / 8;
+        const bool in = i < static_cast<int>(c1);
+        const uint32_t key = in ? sm[i] : 0;
+        uint32_t before = 0;
+        for (int j = tid % 8; j < T && in; j += 8) before += sm[j] < key || (sm[j] == key && j < i);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        if (in && tid % 8 == 0) __stcg(a.buf[0] + before, make_uint2(key, static_cast<uint32_t>(i)));
+        cluster.sync();
+    }
+    for (int pass = 0; pass < a.passes && a.T > kRanked; ++pass) {
         // the last pass writes buf[0]
         const bool to_first = ((a.passes - pass) & 1) != 0;
         uint2 *out = to_first ? a.buf[0] : a.buf[1];
@@ -196,8 +217,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a) {
         }
         if (lane == 31) part[warp] = scan;
         __syncthreads();
-        uint32_t lower = 0;
-        for (int w = 0; w < warp; ++w) lower += part[w];
+        const uint32_t lower = warp_sum(lane < warp ? part[lane] : 0u);
         if (tid < bins) base[tid] = lower + scan - all + before;
         __syncthreads();
         for (int64_t i0 = w0; i0 < w1; i0 += 32) {
@@ -227,14 +247,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortArgs a) {
         const uint32_t key = __ldcg(list + p1 - 1).x;
         if (key == static_cast<uint32_t>(a.V) || __ldcg(list + p1).x != key) continue;
         if (p0 > 0 && __ldcg(list + p0).x == key && __ldcg(list + p0 - 1).x == key) continue;
-        int64_t lo = p1 + 1, hi = a.T;             // the run's end: the first item beyond key
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (__ldcg(list + mid).x <= key) lo = mid + 1;
-            else hi = mid;
+        // the last chunk that begins with key: doubling steps, then halving ones
+        // (most runs cross one boundary, and every load is a round trip)
+        int64_t last = c + 1, reach = 1;
+        while (last + reach < chunks && __ldcg(list + (last + reach) * kChunk).x == key) {
+            last += reach;
+            reach *= 2;
         }
+        for (; reach > 0; reach /= 2)
+            if (last + reach < chunks && __ldcg(list + (last + reach) * kChunk).x == key) last += reach;
         a.crossing[atomicAdd(a.n_crossing, 1)] =
-            make_uint2(static_cast<uint32_t>(c), static_cast<uint32_t>((lo - 1) / kChunk));
+            make_uint2(static_cast<uint32_t>(c), static_cast<uint32_t>(last));
     }
 }
 
@@ -337,11 +360,18 @@ __global__ void __launch_bounds__(kJoinLanes *kJoinGroups) join_rows_kernel(cons
         float acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (m < a.M) {
-#pragma unroll 8
-            for (int64_t k = k0; k < k1; ++k) {
+        constexpr int kBatch = 8;                  // parts in flight
+        for (int64_t k = k0; k < k1 && m < a.M; k += kBatch) {
+            Packed<OOP_TYPE_F32, E> raw[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (k + j < k1)
+                    raw[j] = load_packed<OOP_TYPE_F32, E>((k + j == first ? a.tail : a.head) + (k + j) * a.M + m);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (k + j >= k1) break;
                 float v[E];
-                load_packed<OOP_TYPE_F32, E>((k == first ? a.tail : a.head) + k * a.M + m).get(v);
+                raw[j].get(v);
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] += v[e];
             }
@@ -546,8 +576,7 @@ int oop_get_rows_back(const void *dy, int dy_type, int64_t nb_dy, const int32_t 
                    {reinterpret_cast<uint2 *>(ws + w.buf[0]), reinterpret_cast<uint2 *>(ws + w.buf[1])},
                    reinterpret_cast<uint2 *>(ws + w.crossing), reinterpret_cast<int *>(ws + w.count),
                    n_ids, V, plan.bits, plan.passes, status};
-    cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortSmem);
+    cudaError_t e = allow_smem<sort_kernel>();
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSortCluster);

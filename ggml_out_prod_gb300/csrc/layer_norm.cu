@@ -313,7 +313,7 @@ __device__ __forceinline__ float2 moments(const HeldRow<XT, E, NV, FULL> &row, i
 // The forward pass of few rows, and of rows that come in singles: a row per
 // `width` threads, every load before the first use.
 template <int XT, int YT, int E, int NV, bool FULL>
-__global__ void __launch_bounds__(NV > 4 ? 512 : 1024) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(NV > 16 ? 512 : 1024) norm_kernel(const NormArgs a) {
     __shared__ float2 red[32];
     const Place p(a.M, a.width);
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / a.width) + p.group;
@@ -332,22 +332,35 @@ __global__ void __launch_bounds__(NV > 4 ? 512 : 1024) norm_kernel(const NormArg
     const float2 mr = moments(row, n, p, a.eps, own, theirs, red, [] { __syncthreads(); });
     if (!in) return;
     auto *y = row_of<YT>(a.y, a.nb_y, t) + p.lane * E;
-    row.each(n, p, [&](int i, float (&v)[E]) {
-        float q[E];
+    // parameters a few pieces ahead of their use: singly, each would be a wait
+    constexpr int kAhead = E == 1 ? (NV < 8 ? NV : 8) : 2;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = (v[e] - mr.x) * mr.y;
-        if (a.w) {
-            load_params<E>(a.w, a.w_type, p.column<E>(i), q);
+    for (int i0 = 0; i0 < NV; i0 += kAhead) {
+        if (i0 >= n) break;
+        float w[kAhead][E], b[kAhead][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] *= q[e];
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                w[j][e] = 1.f;
+                b[j][e] = 0.f;
+            }
+            if (i >= n || !row.has(i, p)) continue;
+            if (a.w) load_params<E>(a.w, a.w_type, p.column<E>(i), w[j]);
+            if (a.b) load_params<E>(a.b, a.w_type, p.column<E>(i), b[j]);
         }
-        if (a.b) {
-            load_params<E>(a.b, a.w_type, p.column<E>(i), q);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] += q[e];
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i >= n || !row.has(i, p)) continue;
+            float v[E];
+            row.raw[i].get(v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mr.x) * mr.y, w[j][e], b[j][e]);
+            store_stream<YT, E>(y + i * step, v);
         }
-        store_stream<YT, E>(y + i * step, v);
-    });
+    }
     if (p.lane == 0) {
         if (a.mean) a.mean[t] = mr.x;
         if (a.rstd) a.rstd[t] = mr.y;
@@ -737,15 +750,20 @@ cudaError_t launch_norm_few(const NormArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <int XT, int YT, int E, int NV, bool FULL>
+cudaError_t launch_norm_many(const NormArgs &a, int fixed, cudaStream_t st) {
+    const int threads = a.width * a.groups, smem = fixed + threads * a.pieces * E * plain_size(XT);
+    const cudaError_t e = allow_smem<norm_many_kernel<XT, YT, E, NV, FULL>>();
+    if (e != cudaSuccess) return e;
+    norm_many_kernel<XT, YT, E, NV, FULL>
+        <<<static_cast<unsigned>(std::min(kSlices, (a.T + a.groups - 1) / a.groups)), threads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <int XT, int YT, int E, int NV>
 cudaError_t launch_norm_many(const NormArgs &a, int fixed, cudaStream_t st) {
-    const auto kern = int64_t(a.pieces) * a.width * E == a.M ? norm_many_kernel<XT, YT, E, NV, true>
-                                                             : norm_many_kernel<XT, YT, E, NV, false>;
-    const int threads = a.width * a.groups, smem = fixed + threads * a.pieces * E * plain_size(XT);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(std::min(kSlices, (a.T + a.groups - 1) / a.groups)), threads, smem, st>>>(a);
-    return cudaGetLastError();
+    return int64_t(a.pieces) * a.width * E == a.M ? launch_norm_many<XT, YT, E, NV, true>(a, fixed, st)
+                                                  : launch_norm_many<XT, YT, E, NV, false>(a, fixed, st);
 }
 
 // Fewer rows than the SMs have warps for are spread over more threads each, for
@@ -775,7 +793,7 @@ cudaError_t launch_norm(NormArgs a, bool wide, cudaStream_t st) {
             if (a.groups > 0) return launch_norm_many<XT, YT, E, 20>(a, fixed, st);
         }
     } else {
-        if (a.T < kFewRows && fits(4, 1024)) return launch_norm_few<XT, YT, 1, 4>(a, st);
+        if (a.T < kFewRows && fits(16, 1024)) return launch_norm_few<XT, YT, 1, 16>(a, st);
         if (fits(32, 512)) return launch_norm_few<XT, YT, 1, 32>(a, st);
     }
     norm_long_kernel<XT, YT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
@@ -805,10 +823,9 @@ cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
     const int threads = a.width * a.groups;
     const int slices = static_cast<int>(std::min(kSlices, (a.T + a.groups - 1) / a.groups));
     const int ring = std::max(a.stages * threads * cols * bytes, a.groups > 1 ? a.width * cols * 8 : 0);
-    const auto kern = norm_back_kernel<XT, DT, E>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + ring);
+    cudaError_t e = allow_smem<norm_back_kernel<XT, DT, E>>();
     if (e != cudaSuccess) return e;
-    kern<<<slices, threads, fixed + ring, st>>>(a);
+    norm_back_kernel<XT, DT, E><<<slices, threads, fixed + ring, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.part) return e;
     return join_slices<XT, DT>(a, slices, st);

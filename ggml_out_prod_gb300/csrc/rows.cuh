@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "oop_internal.cuh"
@@ -176,6 +177,31 @@ __device__ __forceinline__ void store_stream(typename Plain<TYPE>::S *p, const f
         r.set(v);
         __stcs(reinterpret_cast<typename Words<E * plain_size(TYPE)>::T *>(p), r.raw);
     }
+}
+
+// ---- launches -------------------------------------------------------------
+
+// Lets KERNEL be launched with all the dynamic shared memory a CTA can have.  The
+// call costs about a microsecond, so it is made once per device (two threads
+// that race make it twice, with the same value).
+constexpr int kMostSmem = 227 * 1024;
+
+template <auto KERNEL>
+cudaError_t allow_smem() {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevices;
+    if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes attr = {};
+    e = cudaFuncGetAttributes(&attr, KERNEL);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMostSmem - static_cast<int>(attr.sharedSizeBytes));
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 // ---- dependent launches ---------------------------------------------------
