@@ -44,10 +44,12 @@ __host__ __device__ constexpr int64_t step_elems(int size) {
 int64_t steps_of(int64_t V, int size) {
     return std::max<int64_t>(1, (V + 16 / size - 1 + step_elems(size) - 1) / step_elems(size));
 }
-// CTAs of a row: as few as still give every SM several waves of CTAs, since a
+// CTAs of a row: as few as still give every SM two waves of its four, since a
 // CTA keeps the next step's loads in flight through the current one but not
-// through its start and end.
-constexpr int64_t kWantCtas = 152 * 4 * 8;
+// through its start and end.  (Gradient, bf16, 2300 rows of 32825: 47 us with two
+// waves, 52 with four, 61 with eight; forward, f32, 2000 rows of 50257: 57, 56
+// and 58.)
+constexpr int64_t kWantCtas = 152 * 4 * 2;
 int64_t pieces_of(int64_t V, int64_t T, int size) {
     const int64_t steps = steps_of(V, size);
     const int64_t per = std::max<int64_t>(1, steps * T / kWantCtas);
@@ -379,18 +381,40 @@ struct LossBackArgs {
     const float *lse, *ratios, *dloss;
     void *dx;
     int64_t nb_x, nb_dx, V, T, P, pieces;
-    double beta, smoothing;
+    double beta, smoothing, scale;                // scale: beta / P
     int *status;
 };
 
-// d(loss) / d(logp) of a row of sequence s.
+// d(loss) / d(logp) of a row of sequence s.  In 64 bits, so that a small
+// difference of the two terms keeps its digits, but in as few of this GPU's slow
+// 64-bit operations as that takes: one exponential (the Taylor series to the 8th
+// power on [-0.35, 0.35], off by 2e-10) and one reciprocal (a 32-bit one and a
+// Newton step) give both sigma(m) and sigma(-m).
 __device__ __forceinline__ float slope_of(const LossBackArgs &a, int64_t s) {
     const int64_t i = s < a.P ? s : s - a.P;
-    const double m = a.beta * (static_cast<double>(a.ratios[i]) - a.ratios[a.P + i]);
-    const double e = a.smoothing;
+    const double m = a.beta * (static_cast<double>(a.ratios[i]) - a.ratios[a.P + i]), size = fabs(m);
+    double t = size;                              // exp(-|m|); NaN stays NaN
+    if (size < 700.0) {
+        const int k = __float2int_rn(static_cast<float>(size) * kLog2e);
+        const double r = fma(static_cast<double>(k), 0.69314718055994530942, -size);
+        t = 1.0 / 40320.0;
+        t = fma(t, r, 1.0 / 5040.0);
+        t = fma(t, r, 1.0 / 720.0);
+        t = fma(t, r, 1.0 / 120.0);
+        t = fma(t, r, 1.0 / 24.0);
+        t = fma(t, r, 1.0 / 6.0);
+        t = fma(t, r, 0.5);
+        t = fma(t, r, 1.0);
+        t = fma(t, r, 1.0) * __longlong_as_double(static_cast<long long>(1023 - k) << 52);
+    } else if (size >= 700.0) {
+        t = 0.0;
+    }
+    const double both = 1.0 + t;
+    const double guess = 1.f / static_cast<float>(both);
+    const double large = guess * fma(-both, guess, 2.0), small = t * large;    // sigma(|m|), sigma(-|m|)
+    const double pos = m < 0.0 ? small : large, neg = m < 0.0 ? large : small;
     const double up = a.dloss ? static_cast<double>(*a.dloss) : 1.0;
-    const double c = up * a.beta / static_cast<double>(a.P) *
-                     (e / (1.0 + exp(-m)) - (1.0 - e) / (1.0 + exp(m)));
+    const double c = up * a.scale * (a.smoothing * pos - (1.0 - a.smoothing) * neg);
     return static_cast<float>(s < a.P ? c : -c);
 }
 
@@ -599,7 +623,8 @@ int oop_preference_loss_back(const void *logits, int type, int64_t nb, const int
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const LossBackArgs a = {logits, labels, seq, lse, ratios, dloss, dlogits, nb, nb_d, V, T,
-                            n_pairs, pieces_of(V, T, size), beta, label_smoothing, status};
+                            n_pairs, pieces_of(V, T, size), beta, label_smoothing,
+                            n_pairs > 0 ? beta / static_cast<double>(n_pairs) : 0.0, status};
     void (*kern)(LossBackArgs) = nullptr;
     const bool f32 = d_type == OOP_TYPE_F32;
     switch (type) {
