@@ -27,7 +27,7 @@ struct DropArgs {
     const void *x;               // the launch's first row
     void *y;
     int64_t nb_x, nb_y, M;
-    uint32_t t0, rows, groups;   // the launch's rows; groups of 8 columns per row
+    uint32_t t0, rows, groups;   // the launch's rows; units of a row: groups of 8 columns, or spans of 256
     uint64_t inverse;            // floor(2^64 / groups) + 1: i / groups = high half of i * inverse
     uint32_t next_t, next_g;     // kThreads groups on: kThreads / groups rows and the rest
     bool dense;                  // x's and y's rows follow each other
@@ -66,8 +66,8 @@ __device__ __forceinline__ uint32_t keep_bits(uint32_t g, uint32_t t, const Drop
     return keep;
 }
 
-// Group i of the launch: row and group of the row (i < 2^31 and groups < 2^32,
-// so the truncated product is exact; one group per row needs no division).
+// Unit i of the launch: row and unit of the row (i <= 2^31 and groups < 2^32, so
+// the truncated product is exact; one unit per row needs no division).
 __device__ __forceinline__ void place(uint32_t i, const DropArgs &a, uint32_t &t, uint32_t &g) {
     t = a.groups == 1 ? i : static_cast<uint32_t>(__umul64hi(i, a.inverse));
     g = i - t * a.groups;
@@ -140,46 +140,51 @@ __global__ void __launch_bounds__(kThreads) dropout_wide_kernel(const DropArgs a
     }
 }
 
-// Rows of any alignment: a lane computes the mask of one group; then the warp
-// goes over its 32 groups four at a time, a lane per element, so that
-// neighbouring lanes touch neighbouring elements.
-template <int TYPE>
+// Rows of any alignment.  A warp takes 256 columns of a row: each lane computes
+// the mask of one of their 32 groups, then the lanes go over the columns side by
+// side, E (1 or 2, as the rows' alignment allows) each, and fetch the bits from
+// the lane that has them.
+constexpr int kSpan = 256;
+
+template <int TYPE, int E>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
-    const uint32_t total = a.rows * a.groups, lane = threadIdx.x & 31;
-    const uint32_t i0 = blockIdx.x * kThreads + (threadIdx.x & ~31u);     // the warp's first group
-    typename Plain<TYPE>::S raw[8];
-    int64_t at[8];
+    constexpr int N = kSpan / (32 * E);
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);    // the warp's span
+    uint32_t t, span;
+    place(i, a, t, span);
+    if (t >= a.rows) return;
+    const int64_t m0 = int64_t(span) * kSpan + lane * E;
+    const auto *x = row_of<TYPE>(a.x, a.nb_x, t) + m0;
+    auto *y = row_of<TYPE>(a.y, a.nb_y, t) + m0;
+    const int left = static_cast<int>(min(a.M - m0, int64_t(kSpan)));        // columns from this lane's first
+    Packed<TYPE, E> raw[N];
+    if (a.drop < 65536) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t i = i0 + 4 * k + lane / 8;
-        uint32_t t, g;
-        place(i, a, t, g);
-        const int64_t m = int64_t(g) * 8 + lane % 8;
-        at[k] = i < total && m < a.M ? int64_t(t) * a.nb_y + m * plain_size(TYPE) : -1;
-        if (at[k] >= 0 && a.drop < 65536) raw[k] = row_of<TYPE>(a.x, a.nb_x, t)[m];
+        for (int k = 0; k < N; ++k)
+            if (k * 32 * E < left) raw[k] = load_stream<TYPE, E>(x + k * 32 * E);
     }
-    uint32_t t, g, keep = 0;
-    place(i0 + lane, a, t, g);
-    if (a.drop < 65536) keep = keep_bits(g, a.t0 + t, a);
+    const uint32_t keep = a.drop < 65536 ? keep_bits(span * 32 + lane, a.t0 + t, a) : 0u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t bits = __shfl_sync(0xffffffffu, keep, 4 * k + lane / 8);
-        if (at[k] < 0) continue;
-        const float v = (bits >> (lane % 8)) & 1u ? to_float(raw[k]) * a.scale : 0.f;
-        *reinterpret_cast<typename Plain<TYPE>::S *>(static_cast<char *>(a.y) + at[k]) = from_float<TYPE>(v);
+    for (int k = 0; k < N; ++k) {
+        const uint32_t bits = __shfl_sync(0xffffffffu, keep, (k * 32 + lane) * E / 8) >> (lane * E % 8);
+        if (k * 32 * E >= left) continue;
+        float v[E];
+        raw[k].get(v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = (bits >> e) & 1u ? v[e] * a.scale : 0.f;
+        store_stream<TYPE, E>(y + k * 32 * E, v);
     }
 }
 
 template <int TYPE>
-void launch_dropout(const DropArgs &a, bool wide, cudaStream_t st) {
+void launch_dropout(const DropArgs &a, int e, cudaStream_t st) {
     constexpr int G = TYPE == OOP_TYPE_F32 ? 2 : 4;        // 64 bytes per thread
     const int64_t total = int64_t(a.rows) * a.groups;
-    if (wide)
-        dropout_wide_kernel<TYPE, G>
-            <<<static_cast<unsigned>((total + G * kThreads - 1) / (G * kThreads)), kThreads, 0, st>>>(a);
-    else
-        dropout_kernel<TYPE>
-            <<<static_cast<unsigned>((total + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+    auto grid = [](int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); };
+    if (e == 8) dropout_wide_kernel<TYPE, G><<<grid(total, G * kThreads), kThreads, 0, st>>>(a);
+    else if (e == 2) dropout_kernel<TYPE, 2><<<grid(total, kThreads / 32), kThreads, 0, st>>>(a);
+    else dropout_kernel<TYPE, 1><<<grid(total, kThreads / 32), kThreads, 0, st>>>(a);
 }
 
 int run_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, const int64_t ne[2],
@@ -201,16 +206,22 @@ int run_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, co
     if ((rc = check_pointer(y, size)) != OOP_OK) return rc;
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
+    // elements of one access: 16 bytes and whole groups, two, or one
+    auto fits = [&](int e, int bytes) {
+        return M % e == 0 && is_aligned(x, bytes) && is_aligned(y, bytes) && nb_x % bytes == 0 &&
+               nb_y % bytes == 0;
+    };
+    const int e = fits(8, 16) ? 8 : fits(2, 2 * size) ? 2 : 1;
     DropArgs a = {};
     a.x = x;
     a.y = y;
     a.nb_x = nb_x;
     a.nb_y = nb_y;
     a.M = M;
-    a.groups = static_cast<uint32_t>(groups);
+    a.groups = static_cast<uint32_t>(e == 8 ? groups : (M + kSpan - 1) / kSpan);
     a.inverse = ~uint64_t(0) / a.groups + 1;
-    a.next_t = static_cast<uint32_t>(kThreads / groups);
-    a.next_g = static_cast<uint32_t>(kThreads % groups);
+    a.next_t = kThreads / a.groups;
+    a.next_g = kThreads % a.groups;
     a.dense = nb_x == M * size && nb_y == M * size;
     for (int i = 0; i < 10; ++i) {
         a.k0[i] = static_cast<uint32_t>(seed) + static_cast<uint32_t>(i) * 0x9E3779B9u;
@@ -220,21 +231,19 @@ int run_dropout(const void *x, int type, int64_t nb_x, void *y, int64_t nb_y, co
     a.c3 = static_cast<uint32_t>(offset >> 32);
     a.drop = static_cast<uint32_t>(std::nearbyint(p * 65536.0));
     a.scale = a.drop < 65536 ? static_cast<float>(65536.0 / (65536 - a.drop)) : 0.f;
-    const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && nb_x % 16 == 0 &&
-                      nb_y % 16 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t rows = std::min(T, kMaxGroups / groups);
+    const int64_t rows = std::min(T, kMaxGroups / a.groups);
     int launches = 0;
     for (int64_t t0 = 0; t0 < T; t0 += rows, ++launches) {
         a.t0 = static_cast<uint32_t>(t0);
         a.x = static_cast<const char *>(x) + t0 * nb_x;
         a.y = static_cast<char *>(y) + t0 * nb_y;
         a.rows = static_cast<uint32_t>(std::min(rows, T - t0));
-        if (type == OOP_TYPE_F32) launch_dropout<OOP_TYPE_F32>(a, wide, st);
-        else if (type == OOP_TYPE_F16) launch_dropout<OOP_TYPE_F16>(a, wide, st);
-        else launch_dropout<OOP_TYPE_BF16>(a, wide, st);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_status(e);
+        if (type == OOP_TYPE_F32) launch_dropout<OOP_TYPE_F32>(a, e, st);
+        else if (type == OOP_TYPE_F16) launch_dropout<OOP_TYPE_F16>(a, e, st);
+        else launch_dropout<OOP_TYPE_BF16>(a, e, st);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return cuda_status(err);
     }
     g_kernel_launches = launches;
     return OOP_OK;

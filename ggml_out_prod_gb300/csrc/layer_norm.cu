@@ -81,9 +81,9 @@ __device__ __forceinline__ void wait_copies(int left) {
     else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// Columns of one thread: 32 where they come in vectors (a row's two reductions
-// and its bookkeeping cost a warp as much as 20 columns do), 16 singles.
-__host__ __device__ constexpr int cols_of(int E) { return E == 1 ? 16 : 32; }
+// Columns of one thread in the backward pass: a row's two reductions and its
+// bookkeeping cost a warp as much as 20 columns do.
+constexpr int kCols = 32;
 constexpr int kMaxStages = 4;
 
 // The backward pass.  `width` threads share a row, 32 columns each; a CTA (one
@@ -94,71 +94,119 @@ constexpr int kMaxStages = 4;
 // arithmetic: half the instructions, the same roundings.
 struct Place {
     int M, threads, width, group, lane, warps, warp0;
+    int full, rest;                  // singles: every lane has `full` of them, `rest` lanes one more
 
     __device__ __forceinline__ Place(int64_t M_, int width_)
         : M(static_cast<int>(M_)), threads(blockDim.x), width(width_), group(threadIdx.x / width_),
-          lane(threadIdx.x - group * width_), warps(width_ >> 5), warp0(group * (width_ >> 5)) {}
+          lane(threadIdx.x - group * width_), warps(width_ >> 5), warp0(group * (width_ >> 5)),
+          full(M / width_), rest(M - full * width_) {}
     // the thread's i-th piece of E columns starts here
     template <int E>
     __device__ __forceinline__ int column(int i) const { return (i * width + lane) * E; }
+    // whether it lies in the row
+    template <int E>
+    __device__ __forceinline__ bool has(int i) const {
+        return E == 1 ? i < full || (i == full && lane < rest) : column<E>(i) < M;
+    }
 };
 
 // A thread's columns come in units that are there or not as a whole: a
 // vector of E, or two singles (of which the second may be missing).
 template <int E>
 struct Units {
-    static constexpr int kSize = E == 1 ? 2 : E, kCount = cols_of(E) / kSize, kPairs = kSize / 2;
+    static constexpr int kSize = E == 1 ? 2 : E, kPairs = kSize / 2;
     static constexpr int kPieces = kSize / E;        // pieces per unit
 };
 
-// One operand's rows, staged as {stages, columns / E, threads} pieces.
+// Where a matrix lies: rows are copied by the 16 bytes, and those at a row's ends
+// may hold a neighbour's elements, but nothing before the first row or behind
+// the last one is touched.
+struct Extent {
+    const char *begin, *end;
+    __device__ __forceinline__ Extent(const void *p, int64_t nb, int64_t T, int64_t row_bytes)
+        : begin(static_cast<const char *>(p)), end(begin + (T - 1) * nb + row_bytes) {}
+};
+
+// Bytes of a row of singles in shared memory: the 16-byte pieces it may touch.
+__host__ __device__ constexpr int row_room(int64_t M, int size) {
+    return static_cast<int>((M * size + 15 + 15) / 16 * 16);
+}
+
+// Copies a row as it lies, from the 16-byte boundary at or below its start, by
+// `width` threads; element m is then at (row & 15) + m * size.
+template <int TYPE>
+__device__ __forceinline__ void copy_row(char *to, const char *row, int64_t row_bytes, const Extent &all, int lane,
+                                         int width) {
+    using S = typename Plain<TYPE>::S;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+    const char *from = row - off;
+    const int n = static_cast<int>((off + row_bytes + 15) / 16);
+    for (int c = lane; c < n; c += width) {
+        const char *p = from + c * 16;
+        if (p >= all.begin && p + 16 <= all.end) {
+            copy_async<16>(to + c * 16, p);
+        } else {                                     // the matrix's first or last elements
+            for (int k = 0; k < 16; k += sizeof(S))
+                if (p + k >= row && p + k < row + row_bytes)
+                    *reinterpret_cast<S *>(to + c * 16 + k) = *reinterpret_cast<const S *>(p + k);
+        }
+    }
+}
+
+// One operand's rows, staged as {stages, columns / E, threads} pieces, each read
+// by the thread that copied it; or (E = 1) as {stages} whole rows of one group,
+// read by all its threads.
 template <int TYPE, int E>
 struct Staged {
-    using S = typename Plain<TYPE>::S;
-    static constexpr int NV = cols_of(E) / E, kBytes = E * plain_size(TYPE);
-    static constexpr bool kAsync = kBytes >= 4;      // 2-byte pieces are loaded when they are due
+    static constexpr int kBytes = E * plain_size(TYPE);
     char *mine;                                      // this thread's piece 0 of stage 0
     int stage_bytes, piece_bytes;
 
-    __device__ __forceinline__ Staged(char *base, const Place &p)
-        : mine(base + threadIdx.x * kBytes), stage_bytes(p.threads * cols_of(E) * plain_size(TYPE)),
+    __device__ __forceinline__ Staged(char *base, const Place &p, const void *, int64_t, int64_t, int)
+        : mine(base + threadIdx.x * kBytes), stage_bytes(p.threads * kCols * plain_size(TYPE)),
           piece_bytes(p.threads * kBytes) {}
-    // (row: the address of the thread's first piece)
+    // bytes of all stages
+    __device__ __forceinline__ int room(const Place &, int stages) const { return stages * stage_bytes; }
     __device__ __forceinline__ void issue(const char *row, int st, const Place &p) const {
-        if constexpr (kAsync) {
-            char *to = mine + st * stage_bytes;
+        char *to = mine + st * stage_bytes;
+        row += p.lane * kBytes;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (p.column<E>(i) < p.M)
-                    copy_async<kBytes>(to + i * piece_bytes, row + i * (p.width * kBytes));
-        }
+        for (int i = 0; i < kCols / E; ++i)
+            if (p.column<E>(i) < p.M) copy_async<kBytes>(to + i * piece_bytes, row + i * (p.width * kBytes));
     }
-    // A row's pieces that were not staged, all at once.
-    __device__ __forceinline__ void load(const char *row, const Place &p, Packed<TYPE, E> (&raw)[NV]) const {
-        if constexpr (!kAsync) {
+    // Unit u as pairs.
+    __device__ __forceinline__ void get(int u, int st, const char *, const Place &, uint64_t (&v)[E / 2]) const {
+        Packed<TYPE, E> r;
+        r.raw = *reinterpret_cast<const decltype(r.raw) *>(mine + st * stage_bytes + u * piece_bytes);
+        float f[E];
+        r.get(f);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (p.column<E>(i) < p.M)
-                    raw[i] = load_stream<TYPE, E>(reinterpret_cast<const S *>(row + i * (p.width * kBytes)));
-        }
+        for (int j = 0; j < E / 2; ++j) v[j] = ptx::pack2(f[2 * j], f[2 * j + 1]);
     }
-    // Unit u as pairs; a missing single is 0.
-    __device__ __forceinline__ void get(int u, int st, const Place &p, const Packed<TYPE, E> (&raw)[NV],
-                                        uint64_t (&v)[Units<E>::kPairs]) const {
-        float f[Units<E>::kSize];
-#pragma unroll
-        for (int k = 0; k < Units<E>::kPieces; ++k) {
-            const int i = u * Units<E>::kPieces + k;
-            Packed<TYPE, E> r = raw[i];
-            if constexpr (kAsync)
-                r.raw = *reinterpret_cast<const decltype(r.raw) *>(mine + st * stage_bytes + i * piece_bytes);
-            float part[E];
-            r.get(part);
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[k * E + e] = k == 0 || p.column<E>(i) < p.M ? part[e] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < Units<E>::kPairs; ++j) v[j] = ptx::pack2(f[2 * j], f[2 * j + 1]);
+};
+
+template <int TYPE>
+struct Staged<TYPE, 1> {
+    static constexpr int kBytes = plain_size(TYPE);
+    char *rows;                                      // this group's
+    int stage_bytes, row_bytes;
+    Extent all;
+
+    __device__ __forceinline__ Staged(char *base, const Place &p, const void *x, int64_t nb, int64_t T, int stages)
+        : rows(base + p.group * stages * row_room(p.M, kBytes)), stage_bytes(row_room(p.M, kBytes)),
+          row_bytes(p.M * kBytes), all(x, nb, T, row_bytes) {}
+    __device__ __forceinline__ int room(const Place &p, int stages) const {
+        return (p.threads / p.width) * stages * stage_bytes;
+    }
+    __device__ __forceinline__ void issue(const char *row, int st, const Place &p) const {
+        copy_row<TYPE>(rows + st * stage_bytes, row, row_bytes, all, p.lane, p.width);
+    }
+    // Unit u as a pair; a missing second single is 0.
+    __device__ __forceinline__ void get(int u, int st, const char *row, const Place &p, uint64_t (&v)[1]) const {
+        const auto *q = reinterpret_cast<const typename Plain<TYPE>::S *>(
+            rows + st * stage_bytes + (reinterpret_cast<uintptr_t>(row) & 15));
+        const int m = p.column<1>(2 * u), n = p.column<1>(2 * u + 1);
+        v[0] = ptx::pack2(to_float(q[m]), p.has<1>(2 * u + 1) ? to_float(q[n]) : 0.f);
     }
 };
 
@@ -166,7 +214,7 @@ struct Staged {
 // second single).
 template <int E>
 __device__ __forceinline__ bool has_unit(int u, const Place &p) {
-    return p.column<E>(u * Units<E>::kPieces) < p.M;
+    return p.has<E>(u * Units<E>::kPieces);
 }
 
 // Unit u of a row of results (row: the address of the thread's first piece).
@@ -182,7 +230,7 @@ __device__ __forceinline__ void put_unit(char *row, int u, const Place &p, const
         float part[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) part[e] = f[k * E + e];
-        if (k == 0 || p.column<E>(i) < p.M) store_stream<TYPE, E>(out + i * (p.width * E), part);
+        if (k == 0 || p.has<E>(i)) store_stream<TYPE, E>(out + i * (p.width * E), part);
     }
 }
 
@@ -443,6 +491,97 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_many_kernel(const NormArg
     }
 }
 
+// The forward pass of many rows that are not aligned.  As above, but a row is
+// copied as it lies, by all of its threads together, and they read it from
+// shared memory element by element, neighbouring lanes neighbouring elements:
+// alignment then costs nothing but narrow reads and stores.
+template <int XT, int YT>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_odd_kernel(const NormArgs a) {
+    using SX = typename Plain<XT>::S;
+    extern __shared__ __align__(16) char sm[];
+    const Place p(a.M, a.width);
+    const int room = row_room(p.M, sizeof(SX)), lane = threadIdx.x & 31;
+    float2 *red = reinterpret_cast<float2 *>(sm);                    // {2, 16}
+    char *rows = sm + 256 + p.group * 2 * room;
+    float *ws = reinterpret_cast<float *>(sm + 256 + a.groups * 2 * room), *bs = ws + p.M;
+    const unsigned step = gridDim.x * a.groups, T = static_cast<unsigned>(a.T);
+    const unsigned r0 = blockIdx.x * a.groups + p.group;
+    const int64_t up_x = step * a.nb_x, up_y = step * a.nb_y, row_bytes = a.M * int64_t(sizeof(SX));
+    const Extent all(a.x, a.nb_x, a.T, row_bytes);
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x;
+    char *y = static_cast<char *>(a.y) + r0 * a.nb_y;
+    auto meet = [&] {
+        if (p.warps > 1) asm volatile("bar.sync %0, %1;" ::"r"(p.group + 1), "r"(p.width) : "memory");
+        else __syncwarp();
+    };
+    if (r0 < T) copy_row<XT>(rows, x, row_bytes, all, p.lane, p.width);
+    commit_copies();
+    for (int m = threadIdx.x; m < p.M; m += p.threads) {
+        ws[m] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
+        bs[m] = a.b ? load_any(a.b, a.w_type, m) : 0.f;
+    }
+    __syncthreads();
+    // columns of this warp, and of warp `lane` of the row: every width-th 32
+    auto columns = [&](int k) {
+        int c = 0;
+        for (int m = k * 32; m < p.M; m += p.width) c += min(32, p.M - m);
+        return static_cast<float>(c);
+    };
+    const float own = columns(p.lane >> 5), theirs = lane < p.warps ? columns(lane) : 0.f;
+    int st = 0;
+    for (unsigned t = r0; t < T; t += step, st ^= 1) {
+        wait_copies(0);
+        meet();                                      // the row is there, the one before it done with
+        const SX *v = reinterpret_cast<const SX *>(rows + st * room + (reinterpret_cast<uintptr_t>(x) & 15));
+        x += up_x;
+        if (t + step < T) copy_row<XT>(rows + (st ^ 1) * room, x, row_bytes, all, p.lane, p.width);
+        commit_copies();
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        int m = p.lane;
+        for (; m + 3 * p.width < p.M; m += 4 * p.width)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += to_float(v[m + j * p.width]);
+        for (; m < p.M; m += p.width) s[0] += to_float(v[m]);
+        const float sum = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+        float mean = own > 0.f ? sum / own : 0.f;
+        s[0] = s[1] = s[2] = s[3] = 0.f;
+        for (m = p.lane; m + 3 * p.width < p.M; m += 4 * p.width)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float d = to_float(v[m + j * p.width]) - mean;
+                s[j] = fmaf(d, d, s[j]);
+            }
+        for (; m < p.M; m += p.width) {
+            const float d = to_float(v[m]) - mean;
+            s[0] = fmaf(d, d, s[0]);
+        }
+        float sq = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+        if (p.warps > 1) {
+            float2 *now = red + st * 16;             // the other half may still be read
+            if (lane == 0) now[threadIdx.x >> 5] = make_float2(sum, sq);
+            meet();
+            const float2 r = lane < p.warps ? now[p.warp0 + lane] : make_float2(0.f, 0.f);
+            mean = warp_sum(r.x) / static_cast<float>(p.M);
+            const float d = theirs > 0.f ? r.x / theirs - mean : 0.f;
+            sq = warp_sum(fmaf(theirs * d, d, r.y));
+        }
+        const float rstd = rsqrtf(sq / static_cast<float>(p.M) + a.eps);
+        auto *out = reinterpret_cast<typename Plain<YT>::S *>(y);
+        for (m = p.lane; m + 3 * p.width < p.M; m += 4 * p.width)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = m + j * p.width;
+                __stcs(out + k, from_float<YT>(fmaf((to_float(v[k]) - mean) * rstd, ws[k], bs[k])));
+            }
+        for (; m < p.M; m += p.width) __stcs(out + m, from_float<YT>(fmaf((to_float(v[m]) - mean) * rstd, ws[m], bs[m])));
+        if (p.lane == 0) {
+            if (a.mean) a.mean[t] = mean;
+            if (a.rstd) a.rstd[t] = rstd;
+        }
+        y += up_y;
+    }
+}
+
 // Rows that fit neither: one CTA per row, read three times (the second and third
 // time from L2).
 template <int XT, int YT>
@@ -485,26 +624,26 @@ struct NormBackArgs {
 // dx, and this CTA's part of dw and db, in one pass.  (A variant without the
 // checks for a missing unit, for rows that fill every lane, keeps more of a row
 // in flight than 128 registers hold, and is 35% slower.)
-template <int XT, int DT, int E>
+template <int XT, int DT, int E, int COLS>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBackArgs a) {
     using X = Staged<XT, E>;
     using D = Staged<DT, E>;
     using U = Units<E>;
-    constexpr bool kAsync = X::kAsync || D::kAsync;
+    constexpr int kCount = COLS / U::kSize;
     extern __shared__ __align__(16) char sm[];
     let_next_start();
     const Place p(a.M, a.width);
     float *ws = reinterpret_cast<float *>(sm);                       // w as floats
-    float2 *red = reinterpret_cast<float2 *>(sm + p.width * cols_of(E) * 4);    // {2, 32}
+    float2 *red = reinterpret_cast<float2 *>(sm + p.width * COLS * 4);    // {2, 32}
     char *ring = reinterpret_cast<char *>(red + 64);
-    const X xs(ring, p);
-    const D ds(ring + a.stages * xs.stage_bytes, p);
+    const X xs(ring, p, a.x, a.nb_x, a.T, a.stages);
+    const D ds(ring + xs.room(p, a.stages), p, a.dy, a.nb_dy, a.T, a.stages);
     const unsigned step = gridDim.x * a.groups, T = static_cast<unsigned>(a.T);
     const unsigned r0 = blockIdx.x * a.groups + p.group;
-    // addresses of the thread's first piece; all advance by `step` rows
+    // rows; all advance by `step`
     const int64_t up_x = step * a.nb_x, up_dy = step * a.nb_dy, up_dx = step * a.nb_dx;
-    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x + p.lane * X::kBytes, *x_next = x;
-    const char *dy = static_cast<const char *>(a.dy) + r0 * a.nb_dy + p.lane * D::kBytes, *dy_next = dy;
+    const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x, *x_next = x;
+    const char *dy = static_cast<const char *>(a.dy) + r0 * a.nb_dy, *dy_next = dy;
     char *dx = static_cast<char *>(a.dx) + r0 * a.nb_dx + p.lane * D::kBytes;
     const float *mean_at = a.mean + r0, *rstd_at = a.rstd + r0;
     unsigned t_next = r0;                            // (T <= 2^31, step <= 2432: no overflow)
@@ -513,7 +652,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             xs.issue(x_next, st, p);
             ds.issue(dy_next, st, p);
         }
-        if (kAsync) commit_copies();
+        commit_copies();
         t_next += step;
         x_next += up_x;
         dy_next += up_dy;
@@ -523,15 +662,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         ws[w_slot<E>(m, p.width)] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
     __syncthreads();
 
-    uint64_t dw[U::kCount][U::kPairs], db[U::kCount][U::kPairs];
+    uint64_t dw[kCount][U::kPairs], db[kCount][U::kPairs];
 #pragma unroll
-    for (int u = 0; u < U::kCount; ++u)
+    for (int u = 0; u < kCount; ++u)
 #pragma unroll
         for (int j = 0; j < U::kPairs; ++j) dw[u][j] = db[u][j] = 0;
     auto get_w = [&](int u, uint64_t (&w)[U::kPairs]) {
         if constexpr (E == 1) {
             const int m = p.column<E>(2 * u), n = p.column<E>(2 * u + 1);
-            w[0] = ptx::pack2(ws[m], n < p.M ? ws[n] : 0.f);
+            w[0] = ptx::pack2(ws[m], p.has<E>(2 * u + 1) ? ws[n] : 0.f);
         } else {
 #pragma unroll
             for (int h = 0; h < E / 4; ++h) {
@@ -549,7 +688,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     const float each = 1.f / static_cast<float>(p.M);
     int st = 0, odd = 0;
     for (unsigned t = r0; t < T; t += step) {
-        issue(st == 0 ? a.stages - 1 : st - 1);
+        if (E > 1) {
+            issue(st == 0 ? a.stages - 1 : st - 1);
+            wait_copies(a.stages - 1);
+        } else {
+            // every thread's copies of this row have to be there, and every thread
+            // be done with the row before it, which the next copies overwrite
+            wait_copies(a.stages - 2);
+            if (p.warps > 1) asm volatile("bar.sync %0, %1;" ::"r"(p.group + 1), "r"(p.width) : "memory");
+            else __syncwarp();
+            issue(st == 0 ? a.stages - 1 : st - 1);
+        }
         const uint64_t mean = both(mean_next), rstd = both(rstd_next);
         mean_at += step;
         rstd_at += step;
@@ -557,19 +706,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             mean_next = *mean_at;
             rstd_next = *rstd_at;
         }
-        if (kAsync) wait_copies(a.stages - 1);
-        Packed<XT, E> xr[X::NV];
-        Packed<DT, E> dr[D::NV];
-        xs.load(x, p, xr);
-        ds.load(dy, p, dr);
         uint64_t sg = 0, sgx = 0;
 #pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
+        for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
             uint64_t w[U::kPairs], d[U::kPairs], xh[U::kPairs];
             get_w(u, w);
-            xs.get(u, st, p, xr, xh);
-            ds.get(u, st, p, dr, d);
+            xs.get(u, st, x, p, xh);
+            ds.get(u, st, dy, p, d);
 #pragma unroll
             for (int j = 0; j < U::kPairs; ++j) {
                 xh[j] = ptx::mul2(ptx::sub2(xh[j], mean), rstd);
@@ -590,13 +734,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         // dx = g * rstd + (x - mean) * slope + level
         const uint64_t slope = both(-r * r * (sum.y * each)), level = both(-r * (sum.x * each));
 #pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
+        for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
             // read again: the registers that would keep g and xh hold dw and db
             uint64_t w[U::kPairs], xh[U::kPairs], g[U::kPairs];
             get_w(u, w);
-            xs.get(u, st, p, xr, xh);
-            ds.get(u, st, p, dr, g);
+            xs.get(u, st, x, p, xh);
+            ds.get(u, st, dy, p, g);
 #pragma unroll
             for (int j = 0; j < U::kPairs; ++j) {
                 const uint64_t rest = ptx::fma2(ptx::sub2(xh[j], mean), slope, level);
@@ -610,35 +754,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         dx += up_dx;
     }
     if (!a.part) return;
-    // the groups' sums, group after group: through shared memory in the threads'
-    // own order, from the last one to the workspace
-    if (kAsync) wait_copies(0);
-    uint64_t *all = reinterpret_cast<uint64_t *>(ring) + p.lane;     // {pairs, width}
-    constexpr int kAll = U::kCount * U::kPairs;
-    for (int k = 0; k < a.groups; ++k) {
-        if (a.groups > 1) __syncthreads();
-        if (p.group != k) continue;
+    float *out_w = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
+    float *out_b = out_w + static_cast<int64_t>(gridDim.x) * p.M;
+    if (a.groups == 1) {
 #pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
-#pragma unroll
-            for (int j = 0; j < U::kPairs; ++j) {
-                const int at = (u * U::kPairs + j) * p.width;
-                if (k > 0) {
-                    dw[u][j] = ptx::add2(all[at], dw[u][j]);
-                    db[u][j] = ptx::add2(all[kAll * p.width + at], db[u][j]);
-                }
-                if (k + 1 < a.groups) {
-                    all[at] = dw[u][j];
-                    all[kAll * p.width + at] = db[u][j];
-                }
-            }
-        }
-        if (k + 1 < a.groups) continue;
-        float *out_w = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
-        float *out_b = out_w + static_cast<int64_t>(gridDim.x) * p.M;
-        // (16-byte stores where the parts' rows allow them)
-#pragma unroll
-        for (int u = 0; u < U::kCount; ++u) {
+        for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
             if (E > 1) {
                 put_floats<U::kPairs>(out_w + p.column<E>(u), dw[u]);
@@ -648,6 +768,35 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
                 put_unit<OOP_TYPE_F32, E>(reinterpret_cast<char *>(out_b + p.lane), u, p, db[u]);
             }
         }
+        return;
+    }
+    // the groups' sums in shared memory ({groups, 2, pairs, width}), then every group
+    // adds up a share of the pairs over all groups, in order
+    wait_copies(0);
+    __syncthreads();
+    constexpr int kAll = kCount * U::kPairs;
+    uint64_t *all = reinterpret_cast<uint64_t *>(ring) + p.lane;
+    const int of_group = 2 * kAll * p.width;
+#pragma unroll
+    for (int u = 0; u < kCount; ++u) {
+#pragma unroll
+        for (int j = 0; j < U::kPairs; ++j) {
+            all[p.group * of_group + (u * U::kPairs + j) * p.width] = dw[u][j];
+            all[p.group * of_group + (kAll + u * U::kPairs + j) * p.width] = db[u][j];
+        }
+    }
+    __syncthreads();
+    for (int k = p.group; k < 2 * kAll; k += a.groups) {
+        uint64_t sum = all[k * p.width];
+        for (int g = 1; g < a.groups; ++g) sum = ptx::add2(sum, all[g * of_group + k * p.width]);
+        float *out = k < kAll ? out_w : out_b;
+        const int u = k % kAll / U::kPairs, j = k % U::kPairs;
+        const int m = E == 1 ? p.column<E>(2 * u) : p.column<E>(u) + 2 * j;
+        const int n = E == 1 ? p.column<E>(2 * u + 1) : m + 1;
+        float lo, hi;
+        ptx::unpack2(sum, lo, hi);
+        if (m < p.M) out[m] = lo;
+        if (n < p.M) out[n] = hi;
     }
 }
 
@@ -721,20 +870,19 @@ __global__ void __launch_bounds__(kThreads) norm_back_join_kernel(const float *p
     out[m] = s;
 }
 
-int64_t slices_of(int64_t T) { return T < kSlices ? T : kSlices; }
-
 // Threads that share a row.
 int width_of(int64_t M, int cols) { return static_cast<int>((M + 32 * cols - 1) / (32 * cols)) * 32; }
 
-// Shares a CTA among rows: width, groups and stages of the row kernels, with
-// `fixed` bytes of shared memory besides the staged rows and `bytes` of them per
-// column.  As many rows at once as fit, twice if they can be (one in
-// work, one on its way), but no CTA with many rows while others have none.
-// Named barriers 1 .. 15 are the groups' (a warp that has a row alone needs none).
-template <class Args>
-void share_cta(Args &a, int cols, int fixed, int bytes) {
+int64_t slices_of(int64_t T) { return T < kSlices ? T : kSlices; }
+
+// Shares a CTA among rows: width, groups and stages of the backward kernel, with
+// `fixed` bytes of shared memory besides the staged rows of `row_bytes` each.  As
+// many rows at once as fit, twice if they can be (one in work, one on its way),
+// but no CTA with many rows while others have none.  Named barriers 1 .. 15 are
+// the groups' (a warp that has a row alone needs none).
+void share_cta(NormBackArgs &a, int cols, int fixed, int row_bytes) {
     a.width = width_of(a.M, cols);
-    const int slots = (kSmem - fixed) / (a.width * cols * bytes);
+    const int slots = (kSmem - fixed) / row_bytes;
     a.groups = static_cast<int>(std::min<int64_t>({kMaxThreads / a.width, a.width == 32 ? 16 : 15,
                                                    std::max(1, slots / 2), (a.T + kSlices - 1) / kSlices}));
     a.stages = std::max(1, std::min(kMaxStages, slots / a.groups));
@@ -794,7 +942,20 @@ cudaError_t launch_norm(NormArgs a, bool wide, cudaStream_t st) {
         }
     } else {
         if (a.T < kFewRows && fits(16, 1024)) return launch_norm_few<XT, YT, 1, 16>(a, st);
-        if (fits(32, 512)) return launch_norm_few<XT, YT, 1, 32>(a, st);
+        // as many rows as fit twice, and as many threads for each as that leaves
+        const int64_t room = row_room(a.M, plain_size(XT)), fixed = 256 + a.M * 8;
+        if (a.M <= 128 * kMaxThreads && fixed + 2 * room <= kSmem) {
+            a.width = width_of(a.M, 128);
+            a.groups = static_cast<int>(std::min<int64_t>({kMaxThreads / a.width, a.width == 32 ? 16 : 15,
+                                                           (kSmem - fixed) / (2 * room)}));
+            if (a.groups < 16) a.width = std::max(a.width, kMaxThreads / a.groups / 32 * 32);
+            const cudaError_t e = allow_smem<norm_odd_kernel<XT, YT>>();
+            if (e != cudaSuccess) return e;
+            norm_odd_kernel<XT, YT>
+                <<<static_cast<unsigned>(std::min(kSlices, (a.T + a.groups - 1) / a.groups)), a.width * a.groups,
+                   fixed + a.groups * 2 * room, st>>>(a);
+            return cudaGetLastError();
+        }
     }
     norm_long_kernel<XT, YT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
     return cudaGetLastError();
@@ -815,17 +976,20 @@ cudaError_t join_slices(const NormBackArgs &a, int slices, cudaStream_t st) {
                             kThreads, 0, st, a.part, slices, a.M, a.dw, a.db);
 }
 
-template <int XT, int DT, int E>
+// cudaErrorNotSupported: no room for two stages of a row of singles.
+template <int XT, int DT, int E, int COLS>
 cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
-    constexpr int bytes = plain_size(XT) + plain_size(DT), cols = cols_of(E);
-    const int fixed = width_of(a.M, cols) * cols * 4 + 64 * 8;
-    share_cta(a, cols, fixed, bytes);
+    const int width = width_of(a.M, COLS), fixed = width * COLS * 4 + 64 * 8;
+    const int row = E == 1 ? row_room(a.M, plain_size(XT)) + row_room(a.M, plain_size(DT))
+                           : width * COLS * (plain_size(XT) + plain_size(DT));
+    share_cta(a, COLS, fixed, row);
+    if (E == 1 && (a.stages < 2 || fixed + a.groups * 2 * row > kSmem)) return cudaErrorNotSupported;
     const int threads = a.width * a.groups;
     const int slices = static_cast<int>(std::min(kSlices, (a.T + a.groups - 1) / a.groups));
-    const int ring = std::max(a.stages * threads * cols * bytes, a.groups > 1 ? a.width * cols * 8 : 0);
-    cudaError_t e = allow_smem<norm_back_kernel<XT, DT, E>>();
+    const int ring = std::max(a.stages * a.groups * row, a.groups > 1 ? threads * COLS * 8 : 0);
+    cudaError_t e = allow_smem<norm_back_kernel<XT, DT, E, COLS>>();
     if (e != cudaSuccess) return e;
-    norm_back_kernel<XT, DT, E><<<slices, threads, fixed + ring, st>>>(a);
+    norm_back_kernel<XT, DT, E, COLS><<<slices, threads, fixed + ring, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.part) return e;
     return join_slices<XT, DT>(a, slices, st);
@@ -834,9 +998,16 @@ cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
 template <int XT, int DT>
 cudaError_t launch_back(const NormBackArgs &a, bool wide, cudaStream_t st) {
     constexpr int E = plain_size(XT) == 2 && plain_size(DT) == 2 ? 8 : 4;
-    g_kernel_launches = a.part ? 2 : 1;
-    if (wide && a.M <= kMaxThreads * cols_of(E)) return launch_back_kernel<XT, DT, E>(a, st);
-    if (!wide && a.M <= kMaxThreads * cols_of(1)) return launch_back_kernel<XT, DT, 1>(a, st);
+    if (a.M <= kMaxThreads * kCols) {
+        g_kernel_launches = a.part ? 2 : 1;
+        // singles: half the columns per thread while two rows' threads fit (bf16, 4096
+        // rows of 2050: 33 us against 41; of 4097, where they do not: 70 against 61)
+        const bool half = 2 * width_of(a.M, kCols / 2) <= kMaxThreads;
+        const cudaError_t e = wide   ? launch_back_kernel<XT, DT, E, kCols>(a, st)
+                              : half ? launch_back_kernel<XT, DT, 1, kCols / 2>(a, st)
+                                     : launch_back_kernel<XT, DT, 1, kCols>(a, st);
+        if (e != cudaErrorNotSupported) return e;
+    }
     norm_back_row_kernel<XT, DT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
     g_kernel_launches = a.part ? 3 : 1;
     if (!a.part) return cudaGetLastError();
