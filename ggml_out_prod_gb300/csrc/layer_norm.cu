@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     constexpr int kCount = COLS / U::kSize;
     extern __shared__ __align__(16) char sm[];
     let_next_start();
-    const Place p(a.M, a.width);
+    const Place place(a.M, a.width), &p = place;
     float *ws = reinterpret_cast<float *>(sm);                       // w as floats
     float2 *red = reinterpret_cast<float2 *>(sm + p.width * COLS * 4);    // {2, 32}
     char *ring = reinterpret_cast<char *>(red + 64);
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     for (int u = 0; u < kCount; ++u)
 #pragma unroll
         for (int j = 0; j < U::kPairs; ++j) dw[u][j] = db[u][j] = 0;
-    auto get_w = [&](int u, uint64_t (&w)[U::kPairs]) {
+    auto get_w = [&](int u, const Place &p, uint64_t (&w)[U::kPairs]) {
         if constexpr (E == 1) {
             const int m = p.column<E>(2 * u), n = p.column<E>(2 * u + 1);
             w[0] = ptx::pack2(ws[m], p.has<E>(2 * u + 1) ? ws[n] : 0.f);
@@ -699,6 +699,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             else __syncwarp();
             issue(st == 0 ? a.stages - 1 : st - 1);
         }
+        // the places of up to 24 singles are cheaper to find again for every row
+        // than to keep in registers
+        Place p = place;
+        if (E == 1) asm volatile("" : "+r"(p.width));
         const uint64_t mean = both(mean_next), rstd = both(rstd_next);
         mean_at += step;
         rstd_at += step;
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
             uint64_t w[U::kPairs], d[U::kPairs], xh[U::kPairs];
-            get_w(u, w);
+            get_w(u, p, w);
             xs.get(u, st, x, p, xh);
             ds.get(u, st, dy, p, d);
 #pragma unroll
@@ -738,7 +742,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
             if (!has_unit<E>(u, p)) continue;
             // read again: the registers that would keep g and xh hold dw and db
             uint64_t w[U::kPairs], xh[U::kPairs], g[U::kPairs];
-            get_w(u, w);
+            get_w(u, p, w);
             xs.get(u, st, x, p, xh);
             ds.get(u, st, dy, p, g);
 #pragma unroll
@@ -756,17 +760,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     if (!a.part) return;
     float *out_w = a.part + static_cast<int64_t>(blockIdx.x) * p.M;
     float *out_b = out_w + static_cast<int64_t>(gridDim.x) * p.M;
-    if (a.groups == 1) {
+    if (E > 1 && a.groups == 1) {
 #pragma unroll
         for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
-            if (E > 1) {
-                put_floats<U::kPairs>(out_w + p.column<E>(u), dw[u]);
-                put_floats<U::kPairs>(out_b + p.column<E>(u), db[u]);
-            } else {
-                put_unit<OOP_TYPE_F32, E>(reinterpret_cast<char *>(out_w + p.lane), u, p, dw[u]);
-                put_unit<OOP_TYPE_F32, E>(reinterpret_cast<char *>(out_b + p.lane), u, p, db[u]);
-            }
+            put_floats<U::kPairs>(out_w + p.column<E>(u), dw[u]);
+            put_floats<U::kPairs>(out_b + p.column<E>(u), db[u]);
         }
         return;
     }
@@ -986,7 +985,7 @@ cudaError_t launch_back_kernel(NormBackArgs a, cudaStream_t st) {
     if (E == 1 && (a.stages < 2 || fixed + a.groups * 2 * row > kSmem)) return cudaErrorNotSupported;
     const int threads = a.width * a.groups;
     const int slices = static_cast<int>(std::min(kSlices, (a.T + a.groups - 1) / a.groups));
-    const int ring = std::max(a.stages * a.groups * row, a.groups > 1 ? threads * COLS * 8 : 0);
+    const int ring = std::max(a.stages * a.groups * row, a.groups > 1 || E == 1 ? threads * COLS * 8 : 0);
     cudaError_t e = allow_smem<norm_back_kernel<XT, DT, E, COLS>>();
     if (e != cudaSuccess) return e;
     norm_back_kernel<XT, DT, E, COLS><<<slices, threads, fixed + ring, st>>>(a);
@@ -1000,12 +999,12 @@ cudaError_t launch_back(const NormBackArgs &a, bool wide, cudaStream_t st) {
     constexpr int E = plain_size(XT) == 2 && plain_size(DT) == 2 ? 8 : 4;
     if (a.M <= kMaxThreads * kCols) {
         g_kernel_launches = a.part ? 2 : 1;
-        // singles: half the columns per thread while two rows' threads fit (bf16, 4096
-        // rows of 2050: 33 us against 41; of 4097, where they do not: 70 against 61)
+        // singles: half the columns per thread while two rows' threads fit, then three
+        // quarters (bf16, 4096 rows of 4097: 55 us; half, with one row at a time, 70)
         const bool half = 2 * width_of(a.M, kCols / 2) <= kMaxThreads;
         const cudaError_t e = wide   ? launch_back_kernel<XT, DT, E, kCols>(a, st)
                               : half ? launch_back_kernel<XT, DT, 1, kCols / 2>(a, st)
-                                     : launch_back_kernel<XT, DT, 1, kCols>(a, st);
+                                     : launch_back_kernel<XT, DT, 1, kCols * 3 / 4>(a, st);
         if (e != cudaErrorNotSupported) return e;
     }
     norm_back_row_kernel<XT, DT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
