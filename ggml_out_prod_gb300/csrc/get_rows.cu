@@ -341,52 +341,67 @@ __global__ void __launch_bounds__(kSumThreads) sum_rows_kernel(const SumArgs a) 
     }
 }
 
-// A CTA takes 64 * E columns of every gridDim.x-th run that crosses chunks; its
-// four groups of 64 threads take a quarter of the run's parts each.
-constexpr int kJoinLanes = 64, kJoinGroups = 4;
+// A CTA takes 256 columns of every gridDim.x-th run that crosses chunks; its four
+// groups of 64 threads take a quarter of the run's parts each, N pieces of E
+// columns per thread.
+constexpr int kJoinLanes = 64, kJoinGroups = 4, kJoinCols = 256;
 
 template <int E>
 __global__ void __launch_bounds__(kJoinLanes *kJoinGroups) join_rows_kernel(const SumArgs a) {
-    __shared__ float part[kJoinGroups][kJoinLanes * E];
+    constexpr int N = kJoinCols / (kJoinLanes * E);
+    __shared__ float part[kJoinGroups][kJoinCols];
     wait_previous();
     const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
-    const int64_t m = (static_cast<int64_t>(blockIdx.y) * kJoinLanes + lane) * E;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kJoinCols + lane * E;
     const int n = *a.n_crossing;
     for (int r = blockIdx.x; r < n; r += gridDim.x) {
         const int64_t first = a.crossing[r].x, last = a.crossing[r].y;
+        const uint32_t key = a.items[first * kChunk + kChunk - 1].x;
         const int64_t parts = last - first + 1;    // tail[first], head[first + 1 .. last]
         const int64_t k0 = first + parts * group / kJoinGroups;
         const int64_t k1 = first + parts * (group + 1) / kJoinGroups;
-        float acc[E];
+        float acc[N][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        constexpr int kBatch = 8;                  // parts in flight
-        for (int64_t k = k0; k < k1 && m < a.M; k += kBatch) {
-            Packed<OOP_TYPE_F32, E> raw[kBatch];
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+        constexpr int kBatch = 4;                  // parts in flight
+        for (int64_t k = k0; k < k1; k += kBatch) {
+            Packed<OOP_TYPE_F32, E> raw[kBatch][N];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                if (k + j < k1)
-                    raw[j] = load_packed<OOP_TYPE_F32, E>((k + j == first ? a.tail : a.head) + (k + j) * a.M + m);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int64_t m = m0 + i * (kJoinLanes * E);
+                    raw[j][i].raw = {};
+                    if (k + j < k1 && m < a.M)
+                        raw[j][i] = load_packed<OOP_TYPE_F32, E>((k + j == first ? a.tail : a.head) + (k + j) * a.M + m);
+                }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (k + j >= k1) break;
-                float v[E];
-                raw[j].get(v);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += v[e];
+                for (int i = 0; i < N; ++i) {
+                    float v[E];
+                    raw[j][i].get(v);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[i][e] += v[e];
+                }
             }
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) part[group][lane * E + e] = acc[e];
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) part[group][(i * kJoinLanes + lane) * E + e] = acc[i][e];
         __syncthreads();
-        if (group == 0 && m < a.M) {
-            const uint32_t key = a.items[first * kChunk + kChunk - 1].x;
+        // a quarter of the columns for every group
+        const int at = threadIdx.x;                // (kJoinCols threads)
+        float sum = part[0][at];
 #pragma unroll
-            for (int g = 1; g < kJoinGroups; ++g)
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += part[g][lane * E + e];
-            put_row<E>(a.dw + static_cast<int64_t>(key) * a.M + m, acc, a.scale, a.accumulate);
-        }
+        for (int g = 1; g < kJoinGroups; ++g) sum += part[g][at];
+        const int64_t m = static_cast<int64_t>(blockIdx.y) * kJoinCols + at;
+        const float one[1] = {sum};
+        if (m < a.M) put_row<1>(a.dw + static_cast<int64_t>(key) * a.M + m, one, a.scale, a.accumulate);
         __syncthreads();
     }
 }
@@ -422,7 +437,7 @@ cudaError_t launch_sums(const SumArgs &a, cudaStream_t st) {
     constexpr int J = E > 4 ? 4 : E;
     return launch_dependent(join_rows_kernel<J>,
                             dim3(static_cast<unsigned>(std::min<int64_t>(chunks - 1, 256)),
-                                 static_cast<unsigned>(ceil_div(a.M, kJoinLanes * J))),
+                                 static_cast<unsigned>(ceil_div(a.M, kJoinCols))),
                             kJoinLanes * kJoinGroups, 0, st, a);
 }
 
