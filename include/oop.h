@@ -397,7 +397,8 @@ int oop_mul_mat_id_weight_grad(const float *x, const int32_t *ids, const float *
  * F16 overflows at 65504, which training gradients pass, and is refused with
  * OOP_ERR_TYPE.  Every sum, mean and softmax statistic is held in 32 bits or
  * more and a result is rounded once, to nearest.  Every sum has one order, so
- * equal calls give equal bits.  16-byte aligned pointers and strides enable
+ * equal calls give equal bits.  Up to 15 bytes beside a row of an input, between
+ * its first row and the end of its last, may be read and are not used.  16-byte aligned pointers and strides enable
  * the wide loads.  An output may be its input (equal pointers, types and
  * strides) where this is said; otherwise outputs must not overlap inputs.
  */

@@ -98,6 +98,20 @@ def test_get_rows_plain(op, kind, out, M, V, T):
     _close(y, want, (U + UOUT[out]) * np.abs(want) + FLOOR[out], "get_rows")
 
 
+@pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("M", [7, 96, 1026, 2304])
+def test_get_rows_of_many_tokens(op, kind, out, M):
+    """Several tokens per CTA, the last of them fewer; ids outside among them."""
+    import torch
+    T, V = 2051, 301
+    table, values = _rand(M, (V, M), kind)
+    ids = np.random.default_rng(T).integers(-1, V + 1, T).astype(np.int32)
+    y = op.get_rows(table, torch.from_numpy(ids).cuda(), scale=0.75, out_dtype=_dt(out))
+    assert op.device_status(clear=True) == op.ERR_BAD_ID
+    want = tr.get_rows(values, ids, 0.75)
+    _close(y, want, (U + UOUT[out]) * np.abs(want) + FLOOR[out], "get_rows")
+
+
 @pytest.mark.parametrize("kind", QUANTS)
 @pytest.mark.parametrize("blocks", [1, 3, 10])
 def test_get_rows_quantised(op, kind, blocks):
@@ -241,6 +255,38 @@ def _norm_tolerance(x, w, b, eps, mean, rstd, y, out):
 WIDTHS = [1, 2, 7, 8, 33, 64, 127, 256, 513, 1000, 2560, 2561, 4096, 5120, 8200, 9728, 16384, 17408]
 
 
+@pytest.mark.parametrize("T,M", [(1300, 333), (1300, 1001), (2500, 2560), (1217, 4100), (1250, 9000), (1216, 17409),
+                                 (1300, 64)])
+@pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "bf16")])
+def test_layer_norm_of_many_rows(op, T, M, kind, out):
+    """More rows than the SMs have warps for: the forms that go from row to row,
+    aligned and not."""
+    x, xv = _rand(M, (T, M), kind, 1.5, 0.4)
+    w, wv = _rand(1, (M,), "f32", 0.3, 1.0)
+    b, bv = _rand(2, (M,), "f32", 0.2)
+    y, mean, rstd = op.layer_norm(x, w, b, eps=1e-5, out_dtype=_dt(out))
+    want, m, r = tr.layer_norm(xv, wv, bv, 1e-5)
+    tol = _norm_tolerance(xv, wv, bv, 1e-5, m, r, want, out)
+    for got, w_, t_, what in zip((y, mean, rstd), (want, m, r), tol, ("y", "mean", "rstd")):
+        _close(got, w_, t_, f"layer_norm {what} M={M} T={T}")
+
+
+@pytest.mark.parametrize("how", ["pad", "offset", "wide"])
+def test_layer_norm_of_many_strided_rows_in_place(op, how):
+    """The same at other strides, written over the input: what lies between the
+    rows (NaN) is neither used nor written."""
+    import torch
+    x, xv = _rand(5, (1500, 520), "bf16")
+    want, m, r = tr.layer_norm(xv, None, None, 1e-5)
+    tol = _norm_tolerance(xv, None, None, 1e-5, m, r, want, "bf16")[0]
+    xs = _strided(x, how)
+    y = op.layer_norm(xs)[0]
+    _close(y, want, tol, "strided")
+    assert torch.equal(op.layer_norm(xs, out=xs)[0], y)
+    if xs._base is not None:
+        assert int(torch.isnan(xs._base).sum()) == xs._base.numel() - x.numel()
+
+
 @pytest.mark.parametrize("M", WIDTHS)
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
 def test_layer_norm(op, M, kind):
@@ -321,7 +367,7 @@ def _back_tolerance(dy, x, mean, rstd, w, dx, out):
     return d, (c + 6) * U * np.abs(dy * xh).sum(0), c * U * np.abs(dy).sum(0)
 
 
-@pytest.mark.parametrize("M", WIDTHS + [20001, 40000])
+@pytest.mark.parametrize("M", WIDTHS + [4099, 8195, 12289, 13001, 15361, 20001, 40000])
 @pytest.mark.parametrize("kind,grad", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "bf16"),
                                        ("bf16", "f32")])
 def test_layer_norm_back(op, M, kind, grad):
@@ -364,6 +410,26 @@ def test_layer_norm_back_strides(op, how, kind):
     assert none[1] is None and none[2] is None and torch.equal(none[0], dx)
     over = op.layer_norm_back(ds, x, mean, rstd, out=ds)[0]      # written over dy
     assert over.data_ptr() == ds.data_ptr() and torch.equal(over, dx)
+
+
+@pytest.mark.parametrize("T,M,kind,grad", [(4001, 333, "bf16", "bf16"), (3000, 1024, "bf16", "bf16"),
+                                           (2000, 1025, "f32", "f32"), (1500, 4099, "f16", "f32"), (1000, 5120, "f32", "bf16"),
+                                           (900, 9000, "bf16", "bf16"), (5000, 17, "f32", "f32")])
+def test_layer_norm_back_rows_in_turn(op, T, M, kind, grad):
+    """Every thread group takes several rows; written over dy as well."""
+    import torch
+    x, xv = _rand(M + T, (T, M), kind, 1.5, 0.4)
+    dy, dv = _rand(M + T + 1, (T, M), grad, 2.0)
+    w, wv = _rand(1, (M,), "bf16", 0.3, 1.0)
+    _, mean, rstd = op.layer_norm(x, eps=1e-2)
+    mv, rv = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    got = op.layer_norm_back(dy, x, mean, rstd, w)
+    want = tr.layer_norm_back(dv, xv, mv, rv, wv)
+    tol = _back_tolerance(dv, xv, mv, rv, wv, want[0], grad)
+    for g, w_, t_, what in zip(got, want, tol, ("dx", "dw", "db")):
+        _close(g, w_, t_, f"layer_norm_back {what} M={M} T={T}")
+    over = op.layer_norm_back(dy, x, mean, rstd, w, out=dy)
+    assert all(torch.equal(p, q) for p, q in zip(got, over))
 
 
 def test_layer_norm_back_many_rows(op):
@@ -411,7 +477,8 @@ def test_layer_norm_gradient_by_differences(op):
 # ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("T,M", [(1, 1), (3, 7), (2, 8), (5, 64), (17, 129), (4, 1000), (9, 264), (2, 2561)])
+@pytest.mark.parametrize("T,M", [(1, 1), (3, 7), (2, 8), (5, 64), (17, 129), (4, 1000), (9, 264), (2, 2561), (3, 1002), (40, 30),
+                                 (1, 258)])
 @pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0])
 def test_dropout(op, kind, T, M, p):
     seed, offset = 0xFEDCBA9876543210, 0x8000000000000005
@@ -651,6 +718,18 @@ def test_preference_rows_outside_every_sequence(op):
     d = op.preference_loss_back(x, tl, ts, r.lse, r.ratios, beta=0.4)
     _check_backward(op, d, xv, labels, seq, r.lse, r.ratios, 0.4, 0.0, "f32")
     assert (d[:2] == 0).all() and (d[9:] == 0).all() and (r.lse != 0).all()
+
+
+@pytest.mark.parametrize("kind,V", [("bf16", 20001), ("f32", 9000)])
+def test_preference_many_rows(op, kind, V):
+    """Enough rows that a CTA takes several steps of one."""
+    import torch
+    x, xv, labels, seq, ref, (tl, ts, tr_) = _pairs(63, [400, 333, 420, 411], V, kind, scored=0.6)
+    r = op.preference_loss(x, tl, ts, tr_, beta=0.05)
+    _check_forward(op, r, xv, labels, seq, ref, 0.05, 0.0)
+    d = op.preference_loss_back(x, tl, ts, r.lse, r.ratios, beta=0.05)
+    _check_backward(op, d, xv, labels, seq, r.lse, r.ratios, 0.05, 0.0, kind)
+    assert torch.equal(op.preference_loss_back(x, tl, ts, r.lse, r.ratios, beta=0.05, out=x), d)
 
 
 def test_preference_many_pairs(op):
