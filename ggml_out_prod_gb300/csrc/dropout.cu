@@ -78,8 +78,12 @@ __device__ __forceinline__ void place(uint32_t i, const DropArgs &a, uint32_t &t
 // bounds this kernel as much as memory does (20 wide multiplies and 20
 // three-way logic operations for 8 elements), so what surrounds it is lean: one
 // division for the G groups, addresses by addition, halves compared in place.
+//
+// bf16, 16384 x 9728: 103 us, 6.2 TB/s (91% of the measured copy rate), with 8 CTAs
+// per SM; with the 5 that an unbounded register count leaves, 113 to 115 us.  64
+// bytes per thread: the same there, 5.4 us against 4.2 for f32, 512 x 2560.
 template <int TYPE, int G>
-__global__ void __launch_bounds__(kThreads) dropout_wide_kernel(const DropArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) dropout_wide_kernel(const DropArgs a) {
     constexpr int E = 16 / plain_size(TYPE), N = 8 / E;
     const uint32_t total = a.rows * a.groups, first = blockIdx.x * (G * kThreads) + threadIdx.x;
     uint32_t t[G], g[G];
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
 
 template <int TYPE>
 void launch_dropout(const DropArgs &a, int e, cudaStream_t st) {
-    constexpr int G = TYPE == OOP_TYPE_F32 ? 2 : 4;        // 64 bytes per thread
+    constexpr int G = TYPE == OOP_TYPE_F32 ? 1 : 2;        // 32 bytes per thread
     const int64_t total = int64_t(a.rows) * a.groups;
     auto grid = [](int64_t n, int64_t per) { return static_cast<unsigned>((n + per - 1) / per); };
     if (e == 8) dropout_wide_kernel<TYPE, G><<<grid(total, G * kThreads), kThreads, 0, st>>>(a);

@@ -22,9 +22,12 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A CTA takes R tokens and kThreads * E columns of their rows; every load is
-// issued before the first store, so a CTA waits for memory twice (the ids,
-// then all of its rows).
+// Bound by memory: a row is read and written once.  A CTA takes R tokens and
+// kThreads * E columns of their rows; every load is issued before the first
+// store, so a CTA waits for memory twice (the ids, then all of its rows).  bf16,
+// 16384 tokens x 4096: 33 us, 8.1 TB/s of rows, of which the frequent ones come
+// from L2 (one token per CTA and scalar loads: 92 us); q8_0, 8192 x 4096 to f32:
+// 34.5 us, 73% of the measured copy rate, decoding four elements per thread.
 template <int TYPE, int OUT, int E, int R>
 __global__ void __launch_bounds__(kThreads) get_rows_kernel(const void *table, int64_t nb_table,
                                                             const int32_t *ids, void *dst,
@@ -79,7 +82,12 @@ __global__ void __launch_bounds__(kThreads) get_rows_kernel(const void *table, i
 // spread like any other: a CTA adds up the rows of its chunk, run by run,
 // writes the sum of a run that lies inside it to the table and the sum of a
 // run that crosses its ends to the workspace, where a last launch joins the
-// parts of each such run in a fixed order.
+// parts of each such run in a fixed order.  Each launch is on its way while the
+// one before drains.
+//
+// f32, 8192 tokens x 2560 into 50257 rows: 97 us, 91% of the measured copy rate;
+// the zeros take 68 us (the sort's 14 hidden behind them), the sums 24 and the
+// join 6.  Where there are few zeros to write, the sort is the longest part.
 
 constexpr int kSortCluster = 8;
 constexpr int kSortThreads = 1024;
