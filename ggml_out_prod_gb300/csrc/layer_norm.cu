@@ -629,7 +629,7 @@ struct NormBackArgs {
 // in packed fp32 arithmetic: half the instructions, the same roundings.
 //
 // bf16, 16384 x 5120: 90 us, 5.6 TB/s (82% of the measured copy rate); a main pass of
-// 84 us in which the 15 warps that the registers allow issue in 44% of the
+// 84 us in which the 15 warps that the registers allow issue in 50% of the
 // cycles, waiting for shared memory and for the row's two sums, and 4 us for the
 // sum of the CTAs' parts.  16 columns per thread (20 warps, w and the row in
 // registers): 138 us, the reductions then are most of the work.  (A variant without the
