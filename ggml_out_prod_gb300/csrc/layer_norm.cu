@@ -262,13 +262,37 @@ __device__ __forceinline__ void put_floats(float *out, const uint64_t (&v)[N]) {
     }
 }
 
-// Where column m's w lies in shared memory: 16 bytes per lane in turn, so that no
-// two lanes of an access meet in a bank.
+// w or b (`none` where NULL) to shared memory as floats, by the whole CTA: in the
+// order in which a row's threads read it, 16 bytes per lane in turn, so that no two
+// lanes of an access meet in a bank.  The loads go out four at a time, since the
+// first row waits for them.
 template <int E>
-__device__ __forceinline__ int w_slot(int m, int width) {
-    if (E != 8) return m;
-    const int j = m / 8, i = j / width;
-    return ((i * 2 + (m / 4) % 2) * width + j - i * width) * 4 + m % 4;
+__device__ __forceinline__ void stage_params(float *to, const void *q, int type, float none, int M, int width) {
+    constexpr int kAhead = 4;
+    const int units = M / E, threads = blockDim.x;
+    for (int c0 = threadIdx.x; c0 < units; c0 += kAhead * threads) {
+        float v[kAhead][E];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[k][e] = none;
+            if (q && c0 + k * threads < units) load_params<E>(q, type, int64_t(c0 + k * threads) * E, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int c = c0 + k * threads;
+            if (c >= units) break;
+            if constexpr (E == 1) {
+                to[c] = v[k][0];
+            } else {
+                const int i = c / width, lane = c - i * width;
+#pragma unroll
+                for (int h = 0; h < E / 4; ++h)
+                    *reinterpret_cast<float4 *>(to + ((i * (E / 4) + h) * width + lane) * 4) =
+                        make_float4(v[k][4 * h], v[k][4 * h + 1], v[k][4 * h + 2], v[k][4 * h + 3]);
+            }
+        }
+    }
 }
 
 // A row held in registers by `width` threads, n pieces of E columns each (of at
@@ -276,29 +300,29 @@ __device__ __forceinline__ int w_slot(int m, int width) {
 template <int XT, int E, int NV, bool FULL>
 struct HeldRow {
     Packed<XT, E> raw[NV];
+    bool last;                       // the lane has the last of the n pieces too
 
-    static __device__ __forceinline__ bool has(int i, const Place &p) {
-        return FULL ? true : p.column<E>(i) < p.M;
-    }
+    __device__ __forceinline__ HeldRow(int n, const Place &p) : last(p.column<E>(n - 1) < p.M) {}
+    __device__ __forceinline__ bool has(int i, int n) const { return FULL || i + 1 < n || last; }
     // f(i, values) for each of the thread's pieces.
     template <class F>
-    __device__ __forceinline__ void each(int n, const Place &p, F f) const {
+    __device__ __forceinline__ void each(int n, F f) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (i >= n) break;
             float v[E];
             raw[i].get(v);
-            if (has(i, p)) f(i, v);
+            if (has(i, n)) f(i, v);
         }
     }
-    __device__ __forceinline__ float sum(int n, const Place &p) const {
+    __device__ __forceinline__ float sum(int n) const {
         if constexpr (E == 1) {
             float s = 0.f;
-            each(n, p, [&](int, const float (&v)[E]) { s += v[0]; });
+            each(n, [&](int, const float (&v)[E]) { s += v[0]; });
             return warp_sum(s);
         } else {
             uint64_t acc[2] = {0, 0};
-            each(n, p, [&](int, const float (&v)[E]) {
+            each(n, [&](int, const float (&v)[E]) {
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     acc[(e / 2) & 1] = ptx::add2(acc[(e / 2) & 1], ptx::pack2(v[e], v[e + 1]));
@@ -306,15 +330,15 @@ struct HeldRow {
             return warp_sum(add_halves(ptx::add2(acc[0], acc[1])));
         }
     }
-    __device__ __forceinline__ float squares(int n, const Place &p, float mean) const {
+    __device__ __forceinline__ float squares(int n, float mean) const {
         if constexpr (E == 1) {
             float s = 0.f;
-            each(n, p, [&](int, const float (&v)[E]) { s = fmaf(v[0] - mean, v[0] - mean, s); });
+            each(n, [&](int, const float (&v)[E]) { s = fmaf(v[0] - mean, v[0] - mean, s); });
             return warp_sum(s);
         } else {
             uint64_t acc[2] = {0, 0};
             const uint64_t m2 = both(mean);
-            each(n, p, [&](int, const float (&v)[E]) {
+            each(n, [&](int, const float (&v)[E]) {
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
                     const uint64_t d = ptx::sub2(ptx::pack2(v[e], v[e + 1]), m2);
@@ -342,9 +366,9 @@ __device__ __forceinline__ float warp_columns(int k, int n, const Place &p) {
 template <int XT, int E, int NV, bool FULL, class Meet>
 __device__ __forceinline__ float2 moments(const HeldRow<XT, E, NV, FULL> &row, int n, const Place &p, float eps,
                                           float own, float theirs, float2 *red, Meet meet) {
-    const float s = row.sum(n, p);
+    const float s = row.sum(n);
     float mean = own > 0.f ? s / own : 0.f;
-    float sq = row.squares(n, p, mean);
+    float sq = row.squares(n, mean);
     if (p.warps > 1) {
         const int lane = threadIdx.x & 31;
         if (lane == 0) red[threadIdx.x >> 5] = make_float2(s, sq);
@@ -368,11 +392,11 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) norm_kernel(const NormAr
     if (!in && p.warps == 1) return;
     const auto *x = row_of<XT>(a.x, a.nb_x, in ? t : 0) + p.lane * E;
     const int step = p.width * E, n = a.pieces, lane = threadIdx.x & 31;
-    HeldRow<XT, E, NV, FULL> row;
+    HeldRow<XT, E, NV, FULL> row(n, p);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (i >= n) break;
-        if (row.has(i, p)) row.raw[i] = load_stream<XT, E>(x + i * step);
+        if (row.has(i, n)) row.raw[i] = load_stream<XT, E>(x + i * step);
     }
     const float own = warp_columns<E, FULL>(p.lane >> 5, n, p);
     const float theirs = lane < p.warps ? warp_columns<E, FULL>(lane, n, p) : 0.f;
@@ -393,14 +417,14 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) norm_kernel(const NormAr
                 w[j][e] = 1.f;
                 b[j][e] = 0.f;
             }
-            if (i >= n || !row.has(i, p)) continue;
+            if (i >= n || !row.has(i, n)) continue;
             if (a.w) load_params<E>(a.w, a.w_type, p.column<E>(i), w[j]);
             if (a.b) load_params<E>(a.b, a.w_type, p.column<E>(i), b[j]);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j;
-            if (i >= n || !row.has(i, p)) continue;
+            if (i >= n || !row.has(i, n)) continue;
             float v[E];
             row.raw[i].get(v);
 #pragma unroll
@@ -434,12 +458,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_many_kernel(const NormArg
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.groups + p.group;
     const char *x = static_cast<const char *>(a.x) + r0 * a.nb_x + p.lane * kBytes;
     char *y = static_cast<char *>(a.y) + r0 * a.nb_y + p.lane * (E * plain_size(YT));
+    HeldRow<XT, E, NV, FULL> row(n, p);
     auto issue = [&](int64_t t) {
         if (t < a.T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (i >= n) break;
-                if (HeldRow<XT, E, NV, FULL>::has(i, p))
+                if (row.has(i, n))
                     copy_async<kBytes>(mine + i * piece, x + i * (p.width * kBytes));
             }
         }
@@ -447,17 +472,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_many_kernel(const NormArg
         x += step * a.nb_x;
     };
     issue(r0);
-    for (int m = threadIdx.x; m < p.M; m += p.threads) {
-        ws[w_slot<E>(m, p.width)] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
-        bs[w_slot<E>(m, p.width)] = a.b ? load_any(a.b, a.w_type, m) : 0.f;
-    }
+    stage_params<E>(ws, a.w, a.w_type, 1.f, p.M, p.width);
+    stage_params<E>(bs, a.b, a.w_type, 0.f, p.M, p.width);
     __syncthreads();
     const float own = warp_columns<E, FULL>(p.lane >> 5, n, p);
     const float theirs = lane < p.warps ? warp_columns<E, FULL>(lane, n, p) : 0.f;
     int odd = 0;
     for (int64_t t = r0; t < a.T; t += step) {
         wait_copies(0);
-        HeldRow<XT, E, NV, FULL> row;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (i >= n) break;
@@ -469,7 +491,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_many_kernel(const NormArg
         });
         odd ^= 16;                                   // the other half may still be read
         const uint64_t mean = both(mr.x), rstd = both(mr.y);
-        row.each(n, p, [&](int i, float (&v)[E]) {
+        row.each(n, [&](int i, float (&v)[E]) {
 #pragma unroll
             for (int h = 0; h < E / 4; ++h) {
                 const int at = ((i * (E / 4) + h) * p.width + p.lane) * 4;
@@ -516,10 +538,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_odd_kernel(const NormArgs
     };
     if (r0 < T) copy_row<XT>(rows, x, row_bytes, all, p.lane, p.width);
     commit_copies();
-    for (int m = threadIdx.x; m < p.M; m += p.threads) {
-        ws[m] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
-        bs[m] = a.b ? load_any(a.b, a.w_type, m) : 0.f;
-    }
+    stage_params<1>(ws, a.w, a.w_type, 1.f, p.M, p.width);
+    stage_params<1>(bs, a.b, a.w_type, 0.f, p.M, p.width);
     __syncthreads();
     // columns of this warp, and of warp `lane` of the row: every width-th 32
     auto columns = [&](int k) {
@@ -669,8 +689,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         dy_next += up_dy;
     };
     for (int s = 0; s + 1 < a.stages; ++s) issue(s);
-    for (int m = threadIdx.x; m < p.M; m += p.threads)
-        ws[w_slot<E>(m, p.width)] = a.w ? load_any(a.w, a.w_type, m) : 1.f;
+    stage_params<E>(ws, a.w, a.w_type, 1.f, p.M, p.width);
     __syncthreads();
 
     uint64_t dw[kCount][U::kPairs], db[kCount][U::kPairs];
@@ -943,13 +962,25 @@ cudaError_t launch_norm(NormArgs a, bool wide, cudaStream_t st) {
     };
     if (wide) {
         if (a.T < kFewRows && fits(4, 1024)) return launch_norm_few<XT, YT, E, 4>(a, st);
-        if (fits(20, kMaxThreads)) {
-            const int row = a.pieces * a.width * E, fixed = 256 + 2 * row * 4;
+        // pieces per thread: 20, and fewer where shared memory holds so few rows that
+        // half of the threads would be left over (2048 rows of 13312 bf16: 60 us
+        // against 76 with 20 alone, before w and b were loaded four at a time, 35 us
+        // since; rows of 5120 take 20 either way)
+        NormArgs found = a;
+        int fixed = 0;
+        found.groups = 0;
+        for (int pieces : {20, 10, 5}) {
+            if (!fits(pieces, kMaxThreads)) break;
+            const int row = a.pieces * a.width * E, besides = 256 + 2 * row * 4;
             a.groups = std::min({kMaxThreads / a.width, a.width == 32 ? 16 : 15,
-                                 (kSmem - fixed) / (row * plain_size(XT))});
-            if (a.groups > 0 && a.pieces <= 10) return launch_norm_many<XT, YT, E, 10>(a, fixed, st);
-            if (a.groups > 0) return launch_norm_many<XT, YT, E, 20>(a, fixed, st);
+                                 (kSmem - besides) / (row * plain_size(XT))});
+            if (a.groups < 1) break;
+            found = a;
+            fixed = besides;
+            if (2 * a.groups * a.width > kMaxThreads) break;
         }
+        if (found.groups > 0 && found.pieces <= 10) return launch_norm_many<XT, YT, E, 10>(found, fixed, st);
+        if (found.groups > 0) return launch_norm_many<XT, YT, E, 20>(found, fixed, st);
     } else {
         if (a.T < kFewRows && fits(16, 1024)) return launch_norm_few<XT, YT, 1, 16>(a, st);
         // as many rows as fit twice, and as many threads for each as that leaves
@@ -1066,8 +1097,8 @@ int oop_layer_norm(const void *x, int x_type, int64_t nb_x, const void *w, const
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     const NormArgs a = {x, w, b, y, mean, rstd, nb_x, nb_y, M, T, w_type, 0, 0, 0, eps};
-    const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && is_aligned(w, 32) &&
-                      is_aligned(b, 32) && nb_x % 16 == 0 && nb_y % 16 == 0;
+    const bool wide = M % 8 == 0 && is_aligned(x, 16) && is_aligned(y, 16) && (!w || is_aligned(w, 8 * sw)) &&
+                      (!b || is_aligned(b, 8 * sw)) && nb_x % 16 == 0 && nb_y % 16 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = x_type == OOP_TYPE_F32   ? launch_norm<OOP_TYPE_F32>(a, y_type, wide, st)
                           : x_type == OOP_TYPE_F16 ? launch_norm<OOP_TYPE_F16>(a, y_type, wide, st)
@@ -1133,7 +1164,7 @@ int oop_layer_norm_back(const void *dy, int dy_type, int64_t nb_dy, const void *
     a.T = T;
     a.w_type = w_type;
     const bool wide = M % 8 == 0 && is_aligned(dy, 16) && is_aligned(x, 16) && is_aligned(dx, 16) &&
-                      nb_dy % 16 == 0 && nb_x % 16 == 0 && nb_dx % 16 == 0;
+                      (!w || is_aligned(w, 8 * sw)) && nb_dy % 16 == 0 && nb_x % 16 == 0 && nb_dx % 16 == 0;
     const bool f32 = dy_type == OOP_TYPE_F32;
     cudaError_t e = cudaSuccess;
     switch (x_type) {

@@ -334,6 +334,44 @@ def test_layer_norm_strides_and_in_place(op, how, kind):
     _close(y, np.repeat(want[:1], 9, 0), tol[:1], "broadcast row")
 
 
+@pytest.mark.parametrize("wk", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [1, 4, 8])
+@pytest.mark.parametrize("T", [3, 1300])
+def test_layer_norm_weights_inside_a_larger_vector(op, T, at, kind, wk):
+    """Rows on 16 bytes, w and b where a packed vector of parameters puts them:
+    one, four and eight elements in."""
+    M = 520
+    x, xv = _rand(7, (T, M), kind, 1.5, 0.4)
+    dy, dv = _rand(8, (T, M), kind, 2.0)
+    flat, fv = _rand(9, (2 * M + at,), wk, 0.3, 1.0)
+    w, b, wv, bv = flat[at:at + M], flat[at + M:], fv[at:at + M], fv[at + M:]
+    y, mean, rstd = op.layer_norm(x, w, b, eps=1e-2)
+    want, m, r = tr.layer_norm(xv, wv, bv, 1e-2)
+    tol = _norm_tolerance(xv, wv, bv, 1e-2, m, r, want, kind)
+    for got, w_, t_, what in zip((y, mean, rstd), (want, m, r), tol, ("y", "mean", "rstd")):
+        _close(got, w_, t_, f"layer_norm {what} at={at}")
+    mv, rv = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    want = tr.layer_norm_back(dv, xv, mv, rv, wv)
+    tol = _back_tolerance(dv, xv, mv, rv, wv, want[0], kind)
+    for got, w_, t_, what in zip(op.layer_norm_back(dy, x, mean, rstd, w), want, tol, ("dx", "dw", "db")):
+        _close(got, w_, t_, f"layer_norm_back {what} at={at}")
+
+
+@pytest.mark.parametrize("T,M,kind", [(1300, 16384, "f16"), (1217, 13312, "bf16"), (1300, 9728, "f32"),
+                                      (1300, 5128, "bf16")])
+def test_layer_norm_of_many_wide_rows(op, T, M, kind):
+    """Rows of which shared memory holds only a few at a time."""
+    x, xv = _rand(M, (T, M), kind, 1.5, 0.4)
+    w, wv = _rand(1, (M,), "f32", 0.3, 1.0)
+    b, bv = _rand(2, (M,), "bf16", 0.2)
+    y, mean, rstd = op.layer_norm(x, w, b.float(), eps=1e-5)
+    want, m, r = tr.layer_norm(xv, wv, bv, 1e-5)
+    tol = _norm_tolerance(xv, wv, bv, 1e-5, m, r, want, kind)
+    for got, w_, t_, what in zip((y, mean, rstd), (want, m, r), tol, ("y", "mean", "rstd")):
+        _close(got, w_, t_, f"layer_norm {what} M={M} T={T}")
+
+
 def test_layer_norm_rows_far_from_zero(op):
     """A mean a thousand times the spread: the difference of squares would lose
     every digit."""
