@@ -438,9 +438,9 @@ __global__ void __launch_bounds__(NV > 16 ? 512 : 1024) norm_kernel(const NormAr
     }
 }
 
-// The forward pass of many rows (bf16, 16384 x 5120: 61 us, 5.5 TB/s, 81% of the
-// measured copy rate; a CTA per four rows with w and b from L1: 76 us).  One CTA per SM keeps w and b in shared memory
-// and takes row after row; a warp has as much of a row as its registers hold (20
+// The forward pass of many rows (bf16, 16384 x 5120: 60 us, 5.6 TB/s, 83% of the
+// measured copy rate; a CTA per four rows with w and b from L1: 76 us).  One CTA per
+// SM keeps w and b in shared memory and takes row after row; a warp has as much of a row as its registers hold (20
 // vectors a lane), so that a reduction is paid for by up to 160 columns a lane
 // and most rows need no barrier.  A lane copies its pieces of its next row to
 // shared memory from when it has taken the current one into registers: there is
@@ -648,8 +648,8 @@ struct NormBackArgs {
 // one is reduced: the loads never wait for a row's sums.  Two columns at a time
 // in packed fp32 arithmetic: half the instructions, the same roundings.
 //
-// bf16, 16384 x 5120: 90 us, 5.6 TB/s (82% of the measured copy rate); a main pass of
-// 84 us in which the 15 warps that the registers allow issue in 50% of the
+// bf16, 16384 x 5120: 88 us, 5.7 TB/s (84% of the measured copy rate); a main pass of
+// about 83 us in which the 15 warps that the registers allow issue in 50% of the
 // cycles, waiting for shared memory and for the row's two sums, and 4 us for the
 // sum of the CTAs' parts.  16 columns per thread (20 warps, w and the row in
 // registers): 138 us, the reductions then are most of the work.  (A variant without the
