@@ -829,8 +829,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
     }
 }
 
-// Rows of more columns than 512 threads hold: dx from one CTA per row, then the columns'
-// sums.
+// Rows of more columns than 512 threads hold: the columns' sums, then dx from one
+// CTA per row.
 template <int XT, int DT>
 __global__ void __launch_bounds__(kThreads) norm_back_row_kernel(const NormBackArgs a) {
     __shared__ float part[32];
@@ -1050,14 +1050,17 @@ cudaError_t launch_back(const NormBackArgs &a, bool wide, cudaStream_t st) {
                                      : launch_back_kernel<XT, DT, 1, kSingles>(a, st);
         if (e != cudaErrorNotSupported) return e;
     }
-    norm_back_row_kernel<XT, DT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
     g_kernel_launches = a.part ? 3 : 1;
-    if (!a.part) return cudaGetLastError();
-    const int64_t tiles = (a.M + kThreads - 1) / kThreads, slices = slices_of(a.T);
-    norm_back_cols_kernel<XT, DT>
-        <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(slices)), kThreads, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : join_slices<XT, DT>(a, static_cast<int>(slices), st);
+    if (a.part) {                        // first: dx may be written over dy
+        const int64_t tiles = (a.M + kThreads - 1) / kThreads, slices = slices_of(a.T);
+        norm_back_cols_kernel<XT, DT>
+            <<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(slices)), kThreads, 0, st>>>(a);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = join_slices<XT, DT>(a, static_cast<int>(slices), st);
+        if (e != cudaSuccess) return e;
+    }
+    norm_back_row_kernel<XT, DT><<<static_cast<unsigned>(a.T), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 int check_norm(const int64_t ne[2]) {

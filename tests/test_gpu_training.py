@@ -470,6 +470,43 @@ def test_layer_norm_back_rows_in_turn(op, T, M, kind, grad):
     assert all(torch.equal(p, q) for p, q in zip(got, over))
 
 
+@pytest.mark.parametrize("M,kind,grad", [(11501, "f32", "f32"), (12001, "f32", "f32"), (12289, "bf16", "bf16"),
+                                          (20001, "bf16", "bf16"), (12305, "f16", "f32"), (16392, "f32", "f32"),
+                                          (16392, "bf16", "bf16"), (20480, "f32", "bf16"), (16384, "bf16", "bf16")])
+def test_layer_norm_back_of_wide_rows_over_dy(op, M, kind, grad):
+    """dx written over dy changes neither dw nor db, on both sides of the widths
+    that one pass holds."""
+    import torch
+    x, xv = _rand(M, (37, M), kind, 1.5, 0.4)
+    dy, dv = _rand(M + 1, (37, M), grad, 2.0)
+    w, wv = _rand(1, (M,), "f32", 0.3, 1.0)
+    _, mean, rstd = op.layer_norm(x, eps=1e-2)
+    mv, rv = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    apart = op.layer_norm_back(dy, x, mean, rstd, w)
+    over = op.layer_norm_back(dy, x, mean, rstd, w, out=dy)
+    assert over[0].data_ptr() == dy.data_ptr()
+    want = tr.layer_norm_back(dv, xv, mv, rv, wv)
+    tol = _back_tolerance(dv, xv, mv, rv, wv, want[0], grad)
+    for a, o, w_, t_, what in zip(apart, over, want, tol, ("dx", "dw", "db")):
+        _close(o, w_, t_, f"layer_norm_back over dy: {what} M={M}")
+        assert torch.equal(a, o), what
+
+
+@pytest.mark.parametrize("M", [264, 12377])
+@pytest.mark.parametrize("how", ["dense", "pad", "offset", "wide"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layer_norm_back_over_strided_dy(op, kind, how, M):
+    import torch
+    x, _ = _rand(33, (41, M), kind)
+    dy, _ = _rand(34, (41, M), kind)
+    _, mean, rstd = op.layer_norm(x)
+    ds = _strided(dy, how)
+    apart = op.layer_norm_back(ds, x, mean, rstd)
+    over = op.layer_norm_back(ds, x, mean, rstd, out=ds)
+    assert over[0].data_ptr() == ds.data_ptr()
+    assert all(torch.equal(a, o) for a, o in zip(apart, over))
+
+
 def test_layer_norm_back_many_rows(op):
     """More rows than any launch has CTAs, few columns; and no rows at all."""
     import torch
