@@ -765,8 +765,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
         }
         float r, unused;
         ptx::unpack2(rstd, r, unused);
-        // dx = g * rstd + (x - mean) * slope + level
-        const uint64_t slope = both(-r * r * (sum.y * each)), level = both(-r * (sum.x * each));
+        // dx = rstd * (g + (x - mean) * slope + level).  rstd stays outside, as its square
+        // may be no float: it overflows for rows whose spread is below 5e-20, and
+        // loses digits above 1e18.
+        const uint64_t slope = both(-r * (sum.y * each)), level = both(-(sum.x * each));
 #pragma unroll
         for (int u = 0; u < kCount; ++u) {
             if (!has_unit<E>(u, p)) continue;
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_back_kernel(const NormBac
 #pragma unroll
             for (int j = 0; j < U::kPairs; ++j) {
                 const uint64_t rest = ptx::fma2(ptx::sub2(xh[j], mean), slope, level);
-                g[j] = ptx::fma2(ptx::mul2(g[j], w[j]), rstd, rest);
+                g[j] = ptx::mul2(ptx::fma2(g[j], w[j], rest), rstd);
             }
             put_unit<DT, E>(dx, u, p, g);
         }

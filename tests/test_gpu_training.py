@@ -527,6 +527,25 @@ def test_layer_norm_back_many_rows(op):
     assert op.layer_norm(e)[0].shape == (0, 48)
 
 
+@pytest.mark.parametrize("spread", [1e-20, 1e-25, 1e19])
+@pytest.mark.parametrize("M", [264, 333, 5120, 12377])
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_layer_norm_back_of_tiny_and_huge_spread(op, spread, M, grad):
+    """Rows whose rstd is a float but whose rstd squared is none, or has lost its
+    digits: every product of the formula's own order stays in range."""
+    import torch
+    x, xv = _rand(M, (5, M), "f32", spread, 0.3 * spread)
+    dy, dv = _rand(M + 1, (5, M), grad, 1e-3)
+    _, m, r = tr.layer_norm(xv, None, None, 0.0)
+    mean, rstd = (torch.from_numpy(v.astype(np.float32)).cuda() for v in (m, r))
+    mv, rv = mean.double().cpu().numpy(), rstd.double().cpu().numpy()
+    got = op.layer_norm_back(dy, x, mean, rstd)
+    want = tr.layer_norm_back(dv, xv, mv, rv, None)
+    tol = _back_tolerance(dv, xv, mv, rv, None, want[0], grad)
+    for g, w_, t_, what in zip(got, want, tol, ("dx", "dw", "db")):
+        _close(g, w_, t_, f"layer_norm_back {what} M={M} spread={spread}")
+
+
 def test_layer_norm_gradient_by_differences(op):
     """The GPU's own forward pass, differenced: along a direction v,
     (L(x + h v) - L(x - h v)) / 2h for L = <y, dy> is <dx, v> to O(h^2) and the
