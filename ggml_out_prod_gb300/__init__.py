@@ -789,8 +789,8 @@ def _scratch(nbytes, device, workspace):
         return None, None, 0
     if workspace is None:
         workspace = _rt().empty(nbytes, dtype=_rt().u8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

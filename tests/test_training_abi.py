@@ -207,3 +207,35 @@ def test_refusals_under_sanitizers():
                         os.path.abspath(__file__)], capture_output=True, text=True, timeout=600, env=env, cwd=ROOT)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
     assert "Sanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-3000:]
+
+
+def test_callers_scratch_lies_on_the_device_of_the_call():
+    """A caller's workspace on another GPU, or with gaps, is refused before its
+    pointer is taken."""
+    import torch
+    import ggml_out_prod_gb300 as g
+
+    class Workspace:
+        is_cuda, device = True, torch.device("cuda", 1)
+        contiguous = True
+
+        def is_contiguous(self):
+            return self.contiguous
+
+        def data_ptr(self):
+            return 0x10000
+
+        def numel(self):
+            return 1 << 20
+
+        def element_size(self):
+            return 1
+
+    w = Workspace()
+    assert g._scratch(64, torch.device("cuda", 1), w) == (w, 0x10000, 1 << 20)
+    with pytest.raises(ValueError):
+        g._scratch(64, torch.device("cuda", 0), w)
+    w.contiguous = False
+    with pytest.raises(ValueError):
+        g._scratch(64, torch.device("cuda", 1), w)
+    assert g._scratch(0, torch.device("cuda", 0), w) == (None, None, 0)
