@@ -81,9 +81,10 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// One term; a NaN stays in s, where no maximum can lose it.
+// One term; a NaN stays in s, where no maximum can lose it, and +Inf is one (Inf - Inf)
+// as it is among the vectors.
 __device__ __forceinline__ LogSum term(float x) {
-    return isnan(x) ? LogSum{-INFINITY, x} : LogSum{x, 1.f};
+    return x < INFINITY ? LogSum{x, 1.f} : LogSum{-INFINITY, x - x};
 }
 // The join over a warp, scaled once: every factor's error would add up.
 __device__ __forceinline__ LogSum warp_join(LogSum r) {

@@ -509,7 +509,8 @@ int oop_dropout_back(const void *dy, int type, int64_t nb_dy, void *dx, int64_t 
  * [0, 1] (OOP_ERR_VALUE).  A label >= V is not scored and records
  * OOP_ERR_BAD_ID, as do offsets that are out of order or beyond T (they are
  * clamped).  A -Inf logit has probability 0; a NaN or +Inf logit in a scored
- * row makes its results non-finite.  workspace:
+ * row makes its lse and logps NaN, and with them its sequence's ratio and its
+ * pair's loss.  workspace:
  * oop_preference_loss_workspace_size(...) bytes, 256-byte aligned.
  */
 size_t oop_preference_loss_workspace_size(const int64_t ne[2], int64_t n_pairs);

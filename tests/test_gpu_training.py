@@ -782,6 +782,29 @@ def test_preference_nan_in_a_scored_row(op):
     assert torch.isfinite(r.ratios[1])
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("how", ["dense", "pad", "offset"])
+@pytest.mark.parametrize("V", [5, 37, 300])
+def test_preference_infinite_logit_anywhere(op, V, how, kind):
+    """A logit of +Inf in a scored row makes the row NaN wherever in the row it
+    lies, and with it the pair's loss, chosen or rejected."""
+    import torch
+    x, _ = _rand(V, (V + 1, V), kind)
+    x[torch.arange(V), torch.arange(V)] = float("inf")       # row v has it at v; the last row has none
+    x = _strided(x, how)
+    labels = torch.full((V + 1,), V // 2, dtype=torch.int32, device="cuda")
+    logps, lse = op.token_logps(x, labels)
+    assert torch.isnan(lse[:V]).all() and torch.isnan(logps[:V]).all()
+    assert torch.isfinite(lse[V]) and torch.isfinite(logps[V])
+    for row in (0, V - 1):
+        two = x[[row, V]]
+        for seq in ([0, 1, 2], [0, 2, 2]):
+            ts = torch.tensor(seq, dtype=torch.int32, device="cuda")
+            for pair in (two, two.flip(0)):
+                r = op.preference_loss(pair, labels[:2], ts)
+                assert torch.isnan(r.losses[0]) and torch.isnan(r.loss), (row, seq)
+
+
 def test_preference_bad_labels_and_offsets(op):
     """A label beyond the vocabulary is not scored; offsets out of order or
     beyond the rows are clamped; both set the device status."""
