@@ -65,9 +65,11 @@ __global__ void __launch_bounds__(kThreads) get_rows_kernel(const void *table, i
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (t0 + r >= T) break;
-        if (m == 0 && (id[r] < 0 || id[r] >= V)) record_status(status, OOP_ERR_BAD_ID);
+        const bool in = id[r] >= 0 && id[r] < V;
+        if (m == 0 && !in) record_status(status, OOP_ERR_BAD_ID);
+        const float by = in ? scale : 0.f;             // (0 times an infinite scale is none)
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[r][e] *= scale;
+        for (int e = 0; e < E; ++e) v[r][e] *= by;
         store_stream<OUT, E>(row_of<OUT>(dst, nb_dst, t0 + r) + m, v[r]);
     }
 }

@@ -132,6 +132,26 @@ def test_get_rows_quantised(op, kind, blocks):
         assert (y[5:9] == 0).all()
 
 
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -2.0])
+@pytest.mark.parametrize("T", [5, 2051])
+@pytest.mark.parametrize("kind,out", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"),
+                                      (synth.TYPE_Q8_0, "f32"), (synth.TYPE_Q4_K, "bf16")])
+def test_get_rows_ids_outside_are_zero_at_any_scale(op, kind, out, T, scale):
+    import torch
+    V, M = 9, 256
+    type_id = None
+    if kind in QUANTS:
+        table = torch.zeros((V, M // synth.BLOCK[kind][0] * synth.BLOCK[kind][1]), dtype=torch.uint8, device="cuda")
+        type_id = kind
+    else:
+        table, _ = _rand(3, (V, M), kind)
+    ids = (torch.arange(T, dtype=torch.int32, device="cuda") % (V + 2)) - 1          # -1 .. V
+    y = op.get_rows(table, ids, scale=scale, table_type=type_id, out_dtype=_dt(out))
+    assert op.device_status(clear=True) == op.ERR_BAD_ID
+    outside = y[(ids < 0) | (ids >= V)]
+    assert (outside == 0).all() and not torch.signbit(outside).any()
+
+
 @pytest.mark.parametrize("how", ["pad", "offset", "wide"])
 @pytest.mark.parametrize("kind", TABLES)
 def test_get_rows_strides(op, how, kind):
