@@ -880,6 +880,48 @@ def test_preference_many_pairs(op):
     _check_backward(op, d, xv, labels, seq, r.lse, r.ratios, 0.1, 0.05, "f32", dloss=2.5)
 
 
+def test_preference_ratio_is_summed_in_more_than_32_bits(op):
+    """Differences of 1e4 that cancel: with one logit a row's log probability is
+    0, so the ratio is minus the sum of ref_logps.  A sum in 32 bits loses about
+    0.03 here.  What the kernel may lose: the logarithm of a half to one ulp, 2^-24,
+    for each row; of the low parts (2^-24 of at most 2^17 each, 16 in all), 22
+    roundings; and the rounding of the result."""
+    import torch
+    n = 4096
+    rng = np.random.default_rng(70)
+    half = (rng.standard_normal(n // 2) * 1e4).astype(np.float32)
+    ref = np.concatenate([half, -half + rng.standard_normal(n // 2).astype(np.float32), [0.0]]).astype(np.float32)
+    x, _ = _rand(71, (n + 1, 1), "f32")
+    labels = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    seq = torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda")
+    r = op.preference_loss(x, labels, seq, torch.from_numpy(ref).cuda())
+    want = -ref[:n].astype(np.float64).sum()
+    tol = n * 2.0 ** -24 + 22 * U * 16 + U * abs(want)
+    assert abs(float(r.ratios[0]) - want) <= tol, (float(r.ratios[0]), want, tol)
+
+
+def test_preference_logps_are_not_biased(op):
+    """Over many rows the errors of the log probabilities average out: the
+    fast exponential's mean error (5e-8 of each term) is taken back, and so is what
+    log2 e in one term would cost (1.3e-8 times the distance to the top, 6
+    here).  The bound is half of the smaller of the two.  ref_logps are the exact
+    values rounded, so the ratio is the sum of the errors."""
+    import torch
+    n, V = 1536, 8191
+    rng = np.random.default_rng(72)
+    xv = rng.standard_normal((n + 1, V)).astype(np.float32)
+    labels = rng.integers(0, V - 1, n + 1).astype(np.int32)
+    xv[:, V - 1] = rng.uniform(6.5, 7.5, n + 1)
+    x64 = xv.astype(np.float64)
+    top = x64.max(1, keepdims=True)
+    logps = x64[np.arange(n + 1), labels] - top[:, 0] - np.log(np.exp(x64 - top).sum(1))
+    ref = logps.astype(np.float32)
+    seq = torch.tensor([0, n, n + 1], dtype=torch.int32, device="cuda")
+    r = op.preference_loss(torch.from_numpy(xv).cuda(), torch.from_numpy(labels).cuda(), seq, torch.from_numpy(ref).cuda())
+    mean = (float(r.ratios[0]) - (logps[:n] - ref[:n]).sum()) / n
+    assert abs(mean) <= 2.5e-8, mean
+
+
 def test_preference_without_pairs_or_rows(op):
     import torch
     x, xv, labels, seq, ref, (tl, ts, tr_) = _pairs(58, [300, 301], 130, "bf16")
