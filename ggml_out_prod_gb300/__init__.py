@@ -947,8 +947,10 @@ def dropout(x, p, seed, offset=0, out=None, stream=None):
     1 / (1 - p), p rounded to 1/65536.
 
     The mask is a function of (seed, offset, column, row) and is not stored:
-    dropout_back with the same seed and offset drops the same elements.  x:
-    (..., M) float32 / float16 / bfloat16; ``out=x`` works in place."""
+    dropout_back with the same seed and offset drops the same elements.  Rows
+    and columns count from x's first ones, so a batch that is dropped in parts
+    takes an offset for each part, forward and backward.  x: (..., M) float32 /
+    float16 / bfloat16; ``out=x`` works in place."""
     if stream is not None:
         return _on_stream(stream, lambda: dropout(x, p, seed, offset, out), x, out)
     return _drop(_rt().lib.oop_dropout, "oop_dropout", x, p, seed, offset, out)

@@ -27,7 +27,10 @@ constexpr int kThreads = 256;
 // store, so a CTA waits for memory twice (the ids, then all of its rows).  bf16,
 // 16384 tokens x 4096: 33 us, 8.1 TB/s of rows, of which the frequent ones come
 // from L2 (one token per CTA and scalar loads: 92 us); q8_0, 8192 x 4096 to f32:
-// 34.5 us, 73% of the measured copy rate, decoding four elements per thread.
+// 34.6 us, 72% of the measured copy rate, decoding four elements per thread, one token
+// per CTA.  The other block types to bf16, same sizes: 31 (q4_0) to 41 us (q5_1), and 49
+// (q2_K) to 74 us (q3_K), 41% to 16%: the codes are read by single bytes and a
+// block's scale is found again for every element.
 template <int TYPE, int OUT, int E, int R>
 __global__ void __launch_bounds__(kThreads) get_rows_kernel(const void *table, int64_t nb_table,
                                                             const int32_t *ids, void *dst,

@@ -209,8 +209,8 @@ __device__ __forceinline__ void add_step(LogSum &r, const Packed<XT, E> (&raw)[k
 
 // Bound by memory: the scored rows are read once.  A CTA reads one piece of a row,
 // the loads of the next step in flight while this one's elements are added.
-// bf16, 10018 scored rows (8 pairs) of 128000: 370 us, 7.0 TB/s, above the measured copy
-// rate, which writes as well (all of a CTA's loads first and 71 registers: 520
+// bf16, 10018 scored rows (8 pairs) of 128000: 373 us, 6.9 TB/s, 101% of the measured
+// copy rate, which writes as well (all of a CTA's loads first and 71 registers: 520
 // us; a join per element: 1680).
 template <int XT>
 __global__ void __launch_bounds__(kThreads, 4) loss_part_kernel(const LossArgs a) {

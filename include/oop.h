@@ -398,9 +398,10 @@ int oop_mul_mat_id_weight_grad(const float *x, const int32_t *ids, const float *
  * OOP_ERR_TYPE.  Every sum, mean and softmax statistic is held in 32 bits or
  * more and a result is rounded once, to nearest.  Every sum has one order, so
  * equal calls give equal bits.  Up to 15 bytes beside a row of an input, between
- * its first row and the end of its last, may be read and are not used.  16-byte aligned pointers and strides enable
- * the wide loads.  An output may be its input (equal pointers, types and
- * strides) where this is said; otherwise outputs must not overlap inputs.
+ * its first row and the end of its last, may be read and are not used.  16-byte
+ * aligned pointers and strides enable the wide loads.  An output may be its
+ * input (equal pointers, types and strides) where this is said; otherwise
+ * outputs must not overlap inputs.
  */
 
 /*
@@ -476,7 +477,10 @@ int oop_layer_norm_back(const void *dy, int dy_type, int64_t nb_dy, const void *
  * al., SC 2011) with key = seed and counter = (m / 8, t, offset low, offset
  * high): half (m % 8) of its four words, the low half of a word first.  So the
  * mask depends on seed, offset, m and t alone, not on sizes, strides or
- * types; use another offset for every call that needs a mask of its own.
+ * types.  m and t count from the call's first column and row: the backward pass
+ * has to be called on the same rows and columns as the forward one, and a part
+ * of a matrix that starts elsewhere is masked as if it started at 0.  Use
+ * another offset for every call that needs a mask of its own.
  * p in [0, 1] (OOP_ERR_VALUE), rounded to 1/65536 with the scale to match; p
  * = 1 zeroes all.  A dropped element is 0 whatever x holds.  y may be x.
  * oop_dropout_back is the same map on a gradient (F32 or BF16).

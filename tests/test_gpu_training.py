@@ -622,6 +622,20 @@ def test_dropout_layouts_share_one_mask(op, how, kind):
     assert not torch.equal(other, y)
 
 
+def test_dropout_counts_from_the_first_row_and_column_of_the_call(op):
+    """A part that starts elsewhere is masked as if it started at 0, forward and
+    backward; with an offset of its own it has a mask of its own."""
+    import torch
+    x = torch.ones((11, 520), device="cuda")
+    keep = torch.from_numpy(tr.dropout_keep(11, 520, 0.3, 77, 5)).cuda()
+    for part in (x[5:], x[:, 16:], x[2:9, 3:]):
+        rows, cols = part.shape
+        y = op.dropout(part, 0.3, 77, 5)
+        assert ((y != 0) == keep[:rows, :cols]).all()
+        assert torch.equal(op.dropout_back(part, 0.3, 77, 5), y)
+        assert not torch.equal(op.dropout(part, 0.3, 77, 6), y)
+
+
 def test_dropout_of_infinities(op):
     """A dropped element is zero whatever it held; a kept one stays."""
     import torch
