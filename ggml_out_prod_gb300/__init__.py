@@ -90,6 +90,10 @@ EXPORTS = (
     "oop_layer_norm", "oop_layer_norm_back", "oop_layer_norm_back_workspace_size",
     "oop_dropout", "oop_dropout_back",
     "oop_preference_loss", "oop_preference_loss_back", "oop_preference_loss_workspace_size",
+    "oop_qk_norm_rope", "oop_qk_norm_rope_back", "oop_qk_norm_rope_back_workspace_size",
+    "oop_gated_ffn", "oop_gated_ffn_workspace_size",
+    "oop_gated_ffn_back", "oop_gated_ffn_back_workspace_size",
+    "oop_orthogonalise", "oop_orthogonalise_workspace_size",
 )
 
 
@@ -97,6 +101,19 @@ class OopProblem(ctypes.Structure):
     """oop_out_prod_problem: one narrow single-slice OUT_PROD of a batch."""
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("dst", ctypes.c_void_p),
                 ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("dst_transposed", ctypes.c_int)]
+
+
+class OopHeads(ctypes.Structure):
+    """oop_heads: the heads of the queries or keys, in and out."""
+    _fields_ = [("x", ctypes.c_void_p), ("nb_x", ctypes.c_int64 * 2), ("y", ctypes.c_void_p),
+                ("nb_y", ctypes.c_int64 * 2), ("w", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
+
+
+class OopHeadsGrad(ctypes.Structure):
+    """oop_heads_grad: the same for the backward pass."""
+    _fields_ = [("dy", ctypes.c_void_p), ("nb_dy", ctypes.c_int64 * 2), ("x", ctypes.c_void_p),
+                ("nb_x", ctypes.c_int64 * 2), ("w", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("nb_dx", ctypes.c_int64 * 2), ("dw", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
 
 
 class OopError(RuntimeError):
@@ -217,7 +234,22 @@ def lib():
                     ("oop_preference_loss", i, [_vp, i, i64] + [_vp] * 8 + [_i64p, i64, d, d, _vp,
                                                                             sz, _vp]),
                     ("oop_preference_loss_back", i, [_vp, i, i64] + [_vp] * 6 +
-                     [i, i64, _i64p, i64, d, d, _vp])):
+                     [i, i64, _i64p, i64, d, d, _vp]),
+                    ("oop_qk_norm_rope", i, [_vp, _vp, i, i, _vp, _vp, i64, i64, i64, i, f, _vp]),
+                    ("oop_qk_norm_rope_back_workspace_size", sz, [i64] * 4),
+                    ("oop_qk_norm_rope_back", i, [_vp, _vp, i, i, i, _vp, _vp, i64, i64, i64, i, f,
+                                                  _vp, sz, _vp]),
+                    ("oop_gated_ffn_workspace_size", sz, [i, i, _i64p, i]),
+                    ("oop_gated_ffn", i, [_vp, i, i64, _vp, _vp, i, i64, _vp, i64, _vp, _vp, i64,
+                                          _i64p, i, _vp, sz, _vp]),
+                    ("oop_gated_ffn_back_workspace_size", sz, [i, i, i, _i64p, i]),
+                    ("oop_gated_ffn_back", i, [_vp, i, i64, _vp, i, i64, _vp, _vp, i, i64, _vp, _vp,
+                                               i64, _vp, i64, _vp, _vp, i64, _i64p, i, _vp, sz,
+                                               _vp]),
+                    ("oop_orthogonalise_workspace_size", sz, [_i64p]),
+                    ("oop_orthogonalise", i, [_vp, i, _i64p, _vp, i, _i64p, _i64p, i,
+                                              ctypes.POINTER(ctypes.c_float), f, f, _vp, sz,
+                                              _vp])):
                 fn = getattr(L, name)
                 fn.restype, fn.argtypes = res, args
             _lib = L
@@ -1072,3 +1104,333 @@ def preference_loss_back(logits, labels, seq, lse, ratios, beta=0.1, label_smoot
     if rc != OK:
         raise OopError(rc, "oop_preference_loss_back")
     return d
+
+
+# ---------------------------------------------------------------------------
+# the operators of a decoder layer's training step
+# ---------------------------------------------------------------------------
+
+ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF, ACT_RELU = 0, 1, 2, 3
+_ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF, "relu": ACT_RELU}
+
+_Three = ctypes.c_int64 * 3
+
+
+def _heads(t, name):
+    """(D, heads, T, (byte strides of a head and of a token)) of a CUDA tensor (..., H, D)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have the shape (..., heads, head size)")
+    shape, st, size = t.shape, t.stride(), t.element_size()
+    D, H = shape[-1], shape[-2]
+    if D > 1 and st[-1] != 1:
+        raise ValueError(f"the heads of {name} must be contiguous")
+    T, step = 1, None
+    for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = d
+        elif d != step * T:
+            raise ValueError(f"the tokens of {name} must lie at one stride")
+        T *= n
+    return D, H, T, (st[-2] * size if H > 1 else D * size, (H * D if step is None else step) * size)
+
+
+def _like_heads(out, t, dtype, name):
+    """A new contiguous tensor of t's shape, or the caller's if it fits: (tensor, strides)."""
+    if out is None:
+        out = _rt().empty(t.shape, dtype=dtype, device=t.device)
+    elif out.shape != t.shape or out.dtype != dtype or out.device != t.device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(t.shape)} on {t.device}")
+    return out, _heads(out, name)[3]
+
+
+def _rotation(pos, freqs, T):
+    rt = _rt()
+    n_rot = 0 if freqs is None else 2 * freqs.numel()
+    if n_rot and pos is None:
+        raise ValueError("freqs without pos")
+    return (_vector(pos, "pos", T, rt.i32) if n_rot else None,
+            _vector(freqs, "freqs", n_rot // 2, rt.f32) if n_rot else None, n_rot)
+
+
+def _same_tokens(q, k, what):
+    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype:
+        raise ValueError(f"{what} must have the same tokens, head size and type")
+
+
+def qk_norm_rope(q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 out_q=None, out_k=None, stream=None):
+    """(q, k) with every head RMS-normalised, weighted and rotated by its token's position.
+
+    q: (..., Hq, D), k: (..., Hk, D) or None, of one plain type, for instance
+    slices of one projection's output; pos: int32, one for each token; freqs:
+    float32 (n_rot / 2,), radians per position; the first n_rot elements of a head turn as
+    pairs (i, i + n_rot / 2), or neighbours with ``interleaved``.  freqs None: the norm
+    alone.  Weights: (D,) of one plain type, or None.  ``out_q=q`` works in place."""
+    rt = _rt()
+    if stream is not None:
+        return _on_stream(stream, lambda: qk_norm_rope(q, k, pos, freqs, q_weight, k_weight, eps,
+                                                       interleaved, out_q, out_k),
+                          q, k, pos, freqs, q_weight, k_weight, out_q, out_k)
+    D, H, T, nb = _heads(q, "q")
+    kind = _plain_type(q.dtype, "q")
+    w_kind = _param_type(q_weight, k_weight)
+    pp, pf, n_rot = _rotation(pos, freqs, T)
+    yq, nb_y = _like_heads(out_q, q, q.dtype, "out_q")
+    wq = _vector(q_weight, "q_weight", D, q_weight.dtype) if q_weight is not None else None
+    a = OopHeads(q.data_ptr(), nb, yq.data_ptr(), nb_y, wq, H)
+    b = yk = None
+    if k is not None:
+        _same_tokens(q, k, "q and k")
+        _, Hk, _, nb_k = _heads(k, "k")
+        yk, nb_yk = _like_heads(out_k, k, k.dtype, "out_k")
+        wk = _vector(k_weight, "k_weight", D, k_weight.dtype) if k_weight is not None else None
+        b = OopHeads(k.data_ptr(), nb_k, yk.data_ptr(), nb_yk, wk, Hk)
+    rc = rt.lib.oop_qk_norm_rope(ctypes.byref(a), ctypes.byref(b) if b is not None else None, kind,
+                                 w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
+                                 _current_stream(q, k, pos, freqs, q_weight, k_weight))
+    if rc != OK:
+        raise OopError(rc, "oop_qk_norm_rope")
+    return yq, yk
+
+
+def qk_norm_rope_back(dq, dk, q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6,
+                      interleaved=False, want_dw=True, out_q=None, out_k=None, workspace=None,
+                      stream=None):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope from the gradients of its results.
+
+    dq, dk: float32 or bfloat16, like q and k (the forward's inputs) in shape;
+    the results have their type and may be written over them (``out_q=dq``).
+    The weights' gradients are float32 (D,), or None without ``want_dw`` (and for
+    a k of None)."""
+    rt = _rt()
+    if stream is not None:
+        return _on_stream(stream, lambda: qk_norm_rope_back(
+            dq, dk, q, k, pos, freqs, q_weight, k_weight, eps, interleaved, want_dw, out_q, out_k,
+            workspace), dq, dk, q, k, pos, freqs, q_weight, k_weight, out_q, out_k, workspace)
+    if (k is None) != (dk is None):
+        raise ValueError("k and dk go together")
+    D, H, T, nb_x = _heads(q, "q")
+    Hk = 0
+    if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
+        raise ValueError("a gradient and its input must have one shape")
+    kind, d_kind = _plain_type(q.dtype, "q"), _plain_type(dq.dtype, "dq")
+    w_kind = _param_type(q_weight, k_weight)
+    pp, pf, n_rot = _rotation(pos, freqs, T)
+    dev = q.device
+
+    def grads(x, d, w, out, name):
+        y, nb_y = _like_heads(out, d, d.dtype, "out_" + name)
+        dw = rt.empty(D, dtype=rt.f32, device=dev) if want_dw else None
+        pw = _vector(w, name + "_weight", D, w.dtype) if w is not None else None
+        _, n, _, nb = _heads(x, name)
+        return OopHeadsGrad(d.data_ptr(), _heads(d, "d" + name)[3], x.data_ptr(), nb, pw, y.data_ptr(),
+                            nb_y, dw.data_ptr() if want_dw else None, n), y, dw
+
+    a, yq, dwq = grads(q, dq, q_weight, out_q, "q")
+    b = yk = dwk = None
+    if k is not None:
+        _same_tokens(q, k, "q and k")
+        _same_tokens(dq, dk, "dq and dk")
+        b, yk, dwk = grads(k, dk, k_weight, out_k, "k")
+        Hk = k.shape[-2]
+    st = _current_stream(q, k, dq, dk, pos, freqs, q_weight, k_weight)
+    L = rt.lib
+    ws, pws, nws = _scratch(L.oop_qk_norm_rope_back_workspace_size(D, T, H, Hk) if want_dw else 0,
+                            dev, workspace)
+    rc = L.oop_qk_norm_rope_back(ctypes.byref(a), ctypes.byref(b) if b is not None else None, d_kind,
+                                 kind, w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
+                                 pws, nws, st)
+    if rc != OK:
+        raise OopError(rc, "oop_qk_norm_rope_back")
+    return yq, yk, dwq, dwk
+
+
+class GatedFfn(NamedTuple):
+    """What gated_ffn returns."""
+    h: object           # act(gate) * up
+    gate: object        # x w_gate', or None where it is not kept
+    up: object          # x w_up', or None
+
+
+def _ffn_weights(w_gate, w_up, w_type, K):
+    """(type, F, byte stride of a row) of the two projections."""
+    if w_type is None:
+        w_type = _plain_type(w_gate.dtype, "w_gate")
+    for w, name in ((w_gate, "w_gate"), (w_up, "w_up")):
+        if w.dim() != 2:
+            raise ValueError(f"{name} must have two dimensions")
+        _check_src0(w, w_type, name)
+    if w_gate.shape != w_up.shape or w_gate.dtype != w_up.dtype:
+        raise ValueError("w_gate and w_up must have one shape and type")
+    M, F, nb = _matrix(w_gate, "w_gate")
+    nb_up = _matrix(w_up, "w_up")[2]
+    if F > 1 and nb != nb_up:
+        raise ValueError("the rows of w_gate and w_up must lie at one stride")
+    if w_type in _BLOCKS:
+        qk, nbytes = _BLOCKS[w_type]
+        if M % nbytes:
+            raise ValueError("the weights' rows must be whole blocks")
+        M = M // nbytes * qk
+    if M != K:
+        raise ValueError("x and the weights must have one row length")
+    return w_type, F, nb
+
+
+def _all_aligned(*pairs):
+    """Whether every (tensor, byte stride) starts and steps by multiples of 16 bytes."""
+    return all(t.data_ptr() % 16 == 0 and nb % 16 == 0 for t, nb in pairs)
+
+
+def _act_of(act):
+    kind = _ACTS.get(act)
+    if kind is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}")
+    return kind
+
+
+def gated_ffn(x, w_gate, w_up, act="silu", keep=False, w_type=None, out=None, workspace=None,
+              stream=None):
+    """act(x w_gate') * (x w_up'), a GatedFfn.
+
+    x: (..., K) float32 / float16 / bfloat16; w_gate, w_up: (F, K) of a plain
+    type, or uint8 rows of quantised blocks (give ``w_type``); act: "silu",
+    "gelu_tanh", "gelu_erf" or "relu".  With ``keep`` the two projections are
+    returned as well, as gated_ffn_back takes them.  All results are
+    (..., F) of x's type."""
+    rt = _rt()
+    if stream is not None:
+        return _on_stream(stream, lambda: gated_ffn(x, w_gate, w_up, act, keep, w_type, out,
+                                                    workspace), x, w_gate, w_up, out, workspace)
+    K, T, nb_x = _matrix(x, "x")
+    kind = _plain_type(x.dtype, "x")
+    a_kind = _act_of(act)
+    w_kind, F, nb_w = _ffn_weights(w_gate, w_up, w_type, K)
+    shape = tuple(x.shape[:-1]) + (F,)
+    h, nb_h = _output(out, shape, x.dtype, x.device)
+    gate = rt.empty(shape, dtype=x.dtype, device=x.device) if keep else None
+    up = rt.empty(shape, dtype=x.dtype, device=x.device) if keep else None
+    st = _current_stream(x, w_gate, w_up)
+    ne = _Three(K, F, T)
+    L = rt.lib
+    aligned = _all_aligned((x, nb_x), (w_gate, nb_w), (w_up, nb_w))
+    ws, pws, nws = _scratch(L.oop_gated_ffn_workspace_size(kind, w_kind, ne, aligned), x.device,
+                            workspace)
+    rc = L.oop_gated_ffn(x.data_ptr(), kind, nb_x, w_gate.data_ptr(), w_up.data_ptr(), w_kind, nb_w,
+                         h.data_ptr(), nb_h, gate.data_ptr() if keep else None,
+                         up.data_ptr() if keep else None, F * x.element_size(), ne, a_kind, pws,
+                         nws, st)
+    if rc != OK:
+        raise OopError(rc, "oop_gated_ffn")
+    return GatedFfn(h, gate, up)
+
+
+def gated_ffn_back(dh, x, w_gate, w_up, gate, up, act="silu", want_dx=True, want_dw=True,
+                   w_type=None, out=None, workspace=None, stream=None):
+    """(dx, dw_gate, dw_up) of gated_ffn from dh and the projections that it kept.
+
+    dh: (..., F) float32 or bfloat16, the type of all results; gate, up: (..., F) of
+    x's type.  ``out``: dx's place.  A gradient that is not wanted is None."""
+    rt = _rt()
+    if stream is not None:
+        return _on_stream(stream, lambda: gated_ffn_back(dh, x, w_gate, w_up, gate, up, act,
+                                                         want_dx, want_dw, w_type, out, workspace),
+                          dh, x, w_gate, w_up, gate, up, out, workspace)
+    K, T, nb_x = _matrix(x, "x")
+    kind, d_kind = _plain_type(x.dtype, "x"), _plain_type(dh.dtype, "dh")
+    a_kind = _act_of(act)
+    w_kind, F, nb_w = _ffn_weights(w_gate, w_up, w_type, K)
+    shape = tuple(x.shape[:-1]) + (F,)
+    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have the shape {shape}")
+    if gate.dtype != x.dtype or up.dtype != x.dtype:
+        raise ValueError("gate and up must have x's type")
+    nb_dh, nb_gu = _matrix(dh, "dh")[2], _matrix(gate, "gate")[2]
+    if T > 1 and _matrix(up, "up")[2] != nb_gu:
+        raise ValueError("the rows of gate and up must lie at one stride")
+    dx, nb_dx = _output(out, tuple(x.shape), dh.dtype, x.device) if want_dx else (None, 0)
+    dwg = rt.empty((F, K), dtype=dh.dtype, device=x.device) if want_dw else None
+    dwu = rt.empty((F, K), dtype=dh.dtype, device=x.device) if want_dw else None
+    st = _current_stream(dh, x, w_gate, w_up, gate, up)
+    ne = _Three(K, F, T)
+    L = rt.lib
+    aligned = _all_aligned((x, nb_x), (w_gate, nb_w), (w_up, nb_w))
+    ws, pws, nws = _scratch(L.oop_gated_ffn_back_workspace_size(d_kind, kind, w_kind, ne, aligned),
+                            x.device, workspace)
+    rc = L.oop_gated_ffn_back(dh.data_ptr(), d_kind, nb_dh, x.data_ptr(), kind, nb_x,
+                              w_gate.data_ptr(), w_up.data_ptr(), w_kind, nb_w, gate.data_ptr(),
+                              up.data_ptr(), nb_gu, dx.data_ptr() if want_dx else None, nb_dx,
+                              dwg.data_ptr() if want_dw else None,
+                              dwu.data_ptr() if want_dw else None, K * dh.element_size(), ne,
+                              a_kind, pws, nws, st)
+    if rc != OK:
+        raise OopError(rc, "oop_gated_ffn_back")
+    return dx, dwg, dwu
+
+
+def _matrices(t, name):
+    """({N, M, B}, (byte strides of a row and of a matrix)) of a CUDA tensor (..., M, N)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    shape, st, size = t.shape, t.stride(), t.element_size()
+    M, N = shape[-2], shape[-1]
+    if N > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    B, step = 1, None
+    for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = d
+        elif d != step * B:
+            raise ValueError(f"the matrices of {name} must lie at one stride")
+        B *= n
+    row = st[-2] if M > 1 else N
+    return (N, M, B), (row * size, (M * row if step is None else step) * size)
+
+
+def orthogonalise(x, steps=5, coefs=None, eps=1e-7, scale=1.0, out_dtype=None, out=None,
+                  workspace=None, stream=None):
+    """The update x made nearly orthogonal by Newton-Schulz steps, matrix by matrix.
+
+    x: (..., M, N) float32 or bfloat16, for instance a momentum of weight
+    gradients or of all experts' at once; coefs: (a, b, c), or one triple for
+    each step (default: (3.4445, -4.7750, 2.0315)).  Returns scale * X_steps in
+    ``out_dtype`` (float32 or bfloat16; default: x's); ``out=x`` works in place."""
+    rt = _rt()
+    if stream is not None:
+        return _on_stream(stream, lambda: orthogonalise(x, steps, coefs, eps, scale, out_dtype, out,
+                                                        workspace), x, out, workspace)
+    ne, nb = _matrices(x, "x")
+    kind = _plain_type(x.dtype, "x")
+    table = None
+    if coefs is not None:
+        flat = [float(v) for c in coefs for v in (c if hasattr(c, "__len__") else (c,))]
+        if len(flat) == 3:
+            flat = flat * steps
+        if len(flat) != 3 * steps:
+            raise ValueError("coefs must be one triple, or one for each step")
+        table = (ctypes.c_float * max(1, len(flat)))(*flat)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else x.dtype
+    if out is None:
+        out = rt.empty(x.shape, dtype=out_dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != out_dtype or out.device != x.device:
+        raise ValueError(f"out must be a {out_dtype} tensor of shape {tuple(x.shape)} on {x.device}")
+    nb_y = _matrices(out, "out")[1]
+    st = _current_stream(x)
+    ne = _Three(*ne)
+    L = rt.lib
+    ws, pws, nws = _scratch(L.oop_orthogonalise_workspace_size(ne), x.device, workspace)
+    rc = L.oop_orthogonalise(x.data_ptr(), kind, _Two(*nb), out.data_ptr(),
+                             _plain_type(out_dtype, "out"), _Two(*nb_y), ne, steps, table, eps, scale,
+                             pws, nws, st)
+    if rc != OK:
+        raise OopError(rc, "oop_orthogonalise")
+    return out

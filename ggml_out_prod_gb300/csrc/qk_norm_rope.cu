@@ -1,0 +1,585 @@
+// qk_norm_rope.cu -- RMS norm of every query and key head and the rotation by
+// the token's position, in one pass, and its backward pass.
+//
+//   r = (sum_d x^2 / D + eps)^(-1/2),  n = x r w,  y = R(pos) n
+//   dn = R(-pos) dy,  g = dn w,  dx = r (g - x r^2 sum_d (g x) / D),
+//   dw = sum over tokens and heads of dn x r
+//
+// Bound by memory: x is read once and y written once, nothing else is of their
+// size.  A head is held by a group of 2, 4 .. 32 lanes.  A lane's unit is two
+// chunks of E elements that hold whole pairs: chunk j of the first half of the
+// rotated elements and its partner in the second half, or two neighbouring
+// chunks.  So a rotation needs no other lane, and a lane's frequencies and
+// weights are the same for every head: they stay in registers.
+//
+// The angle pos * freq is held in turns as a 64-bit fraction: freq / 2 pi is
+// rounded once to 2^-64 turns, and the product with the integer position wraps
+// around as the angle does, so no position loses precision.
+#include <algorithm>
+#include <cmath>
+
+#include "oop_internal.cuh"
+#include "rows.cuh"
+
+namespace oop {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxHead = 1024;
+
+// The heads of the queries or of the keys, for either direction.
+struct Side {
+    const void *x, *dy, *w;
+    void *out;                       // y, or dx
+    int64_t x_head, x_tok, dy_head, dy_tok, out_head, out_tok;   // byte strides
+    float *partial;                  // one row of D sums for each CTA of this side, or NULL
+    int heads, ctas;
+    int splits;                      // warps that share a token's heads
+};
+
+struct Args {
+    Side side[2];
+    const int32_t *pos;
+    const float *freqs;
+    int64_t T;
+    int D, half, interleaved, group_shift, units, w_type;
+    float eps, inv_d;
+};
+
+// freq / (2 pi) modulo 1 as a 64-bit fraction: the 24-bit significand times 128
+// bits of 1 / (2 pi), shifted by the exponent, in integers (64-bit floating point has
+// a sixtieth of the rate here).  Exact to 2^-64 for |freq| < 2^40.
+__device__ __forceinline__ uint64_t turns_of(float freq) {
+    constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;   // 2^128 / (2 pi)
+    const uint32_t bits = __float_as_uint(freq);
+    const int exponent = static_cast<int>(bits >> 23 & 0xffu);
+    const uint64_t m = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);
+    const int shift = 64 + 150 - (exponent ? exponent : 1);        // freq = m 2^(64 - shift)
+    const uint64_t low = m * kLo, carry = __umul64hi(m, kLo);
+    const uint64_t mid = m * kHi + carry, top = __umul64hi(m, kHi) + (mid < carry);
+    uint64_t v = 0;
+    if (shift >= 128) v = shift < 192 ? top >> (shift - 128) : 0;
+    else if (shift > 64) v = mid >> (shift - 64) | top << (128 - shift);
+    else if (shift == 64) v = mid;
+    else if (shift > 0) v = low >> shift | mid << (64 - shift);
+    return bits >> 31 ? ~v + 1 : v;
+}
+
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
+    const float x = a * c - b * s;
+    b = a * s + b * c;
+    a = x;
+}
+
+// What a lane holds of one head: U units of two chunks.
+template <int E, int U>
+struct Lane {
+    int c0[U], c1[U];                // first elements of the chunks; -1: none
+    uint64_t step[U][E];             // turns per position of the pairs
+    float bad[U][E];                 // 0, or NaN for a frequency that is not finite
+
+    __device__ __forceinline__ void place(const Args &a, int lane) {
+        const int g = 1 << a.group_shift, rot_units = a.half / E;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = lane + u * g;
+            c0[u] = c1[u] = -1;
+#pragma unroll
+            for (int p = 0; p < E; ++p) {
+                step[u][p] = 0;
+                bad[u][p] = 0.f;
+            }
+            if (j >= a.units) continue;
+            if (j < rot_units) {
+                c0[u] = a.interleaved ? 2 * E * j : E * j;
+                c1[u] = a.interleaved ? c0[u] + E : a.half + E * j;
+#pragma unroll
+                for (int p = 0; p < E; ++p) {
+                    const float f = a.freqs[E * j + p];
+                    bad[u][p] = f * 0.f;
+                    step[u][p] = bad[u][p] == 0.f ? turns_of(f) : 0;
+                }
+            } else {
+                c0[u] = 2 * a.half + 2 * E * (j - rot_units);
+                c1[u] = c0[u] + E < a.D ? c0[u] + E : -1;        // E = 1 and an odd rest
+            }
+        }
+    }
+};
+
+template <int E, int U>
+struct Values {
+    float a[U][E], b[U][E];
+};
+
+template <int TYPE, int E, int U>
+__device__ __forceinline__ void load_head(Values<E, U> &v, const char *row, const Lane<E, U> &l) {
+    using S = typename Plain<TYPE>::S;
+    const S *p = reinterpret_cast<const S *>(row);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v.a[u][i] = v.b[u][i] = 0.f;
+        if (l.c0[u] >= 0) load_stream<TYPE, E>(p + l.c0[u]).get(v.a[u]);
+        if (l.c1[u] >= 0) load_stream<TYPE, E>(p + l.c1[u]).get(v.b[u]);
+    }
+}
+
+template <int TYPE, int E, int U>
+__device__ __forceinline__ void store_head(char *row, const Values<E, U> &v, const Lane<E, U> &l) {
+    using S = typename Plain<TYPE>::S;
+    S *p = reinterpret_cast<S *>(row);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (l.c0[u] >= 0) store_stream<TYPE, E>(p + l.c0[u], v.a[u]);
+        if (l.c1[u] >= 0) store_stream<TYPE, E>(p + l.c1[u], v.b[u]);
+    }
+}
+
+template <int E, int U>
+__device__ __forceinline__ void load_weights(Values<E, U> &w, const Side &s, int type,
+                                             const Lane<E, U> &l) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            w.a[u][i] = l.c0[u] < 0 ? 0.f : s.w ? load_any(s.w, type, l.c0[u] + i) : 1.f;
+            w.b[u][i] = l.c1[u] < 0 ? 0.f : s.w ? load_any(s.w, type, l.c1[u] + i) : 1.f;
+        }
+}
+
+// cos and sin of the token's angles; 0 turns for what is not rotated.
+template <int E, int U>
+__device__ __forceinline__ void angles(float (&c)[U][E], float (&s)[U][E], int64_t pos,
+                                       const Lane<E, U> &l) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int p = 0; p < E; ++p) {
+            const uint64_t t = static_cast<uint64_t>(pos) * l.step[u][p];
+            const int32_t half_turns = static_cast<int32_t>(t >> 32);
+            sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s[u][p], &c[u][p]);
+            s[u][p] += l.bad[u][p];
+            c[u][p] += l.bad[u][p];
+        }
+}
+
+// The lane's pairs turned; DIR = -1: back.
+template <int DIR, int E, int U>
+__device__ __forceinline__ void rotate(Values<E, U> &v, const float (&c)[U][E], const float (&s)[U][E],
+                                       bool interleaved) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (E == 1 || !interleaved) {
+#pragma unroll
+            for (int p = 0; p < E; ++p) turn(v.a[u][p], v.b[u][p], c[u][p], DIR * s[u][p]);
+        } else {
+#pragma unroll
+            for (int p = 0; p < E / 2; ++p) {
+                turn(v.a[u][2 * p], v.a[u][2 * p + 1], c[u][p], DIR * s[u][p]);
+                turn(v.b[u][2 * p], v.b[u][2 * p + 1], c[u][E / 2 + p], DIR * s[u][E / 2 + p]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float group_sum(float v, int group) {
+    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <int E, int U>
+__device__ __forceinline__ float dot(const Values<E, U> &v, const Values<E, U> &w) {
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) s += v.a[u][i] * w.a[u][i] + v.b[u][i] * w.b[u][i];
+    return s;
+}
+
+// A warp takes whole tokens, or with few tokens a share of a token's heads, and
+// its groups the heads in turn.  The first side[0].ctas CTAs work on the queries.
+template <int TYPE, int E, int U>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Args a) {
+    const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
+    const Side &s = a.side[which];
+    const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
+    const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    Lane<E, U> l;
+    l.place(a, lane & (group - 1));
+    Values<E, U> w;
+    load_weights(w, s, a.w_type, l);
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) - (which ? a.side[0].ctas : 0)) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
+    for (int64_t item = first; item < a.T * s.splits; item += warps) {
+        const int64_t t = item / s.splits;
+        const int share = static_cast<int>(item - t * s.splits);
+        float c[U][E], sn[U][E];
+        angles(c, sn, a.half ? a.pos[t] : 0, l);
+        for (int h0 = share * groups; h0 < s.heads; h0 += groups * s.splits) {
+            const int h = h0 + mine;
+            Values<E, U> v = {};
+            if (h < s.heads)
+                load_head<TYPE>(v, static_cast<const char *>(s.x) + t * s.x_tok + h * s.x_head, l);
+            const float r = 1.f / sqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    v.a[u][i] *= r * w.a[u][i];
+                    v.b[u][i] *= r * w.b[u][i];
+                }
+            rotate<1>(v, c, sn, a.interleaved);
+            if (h < s.heads)
+                store_head<TYPE>(static_cast<char *>(s.out) + t * s.out_tok + h * s.out_head, v, l);
+        }
+    }
+}
+
+template <int DTYPE, int TYPE, int E, int U>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Args a) {
+    const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
+    const Side &s = a.side[which];
+    const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
+    const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    Lane<E, U> l;
+    l.place(a, lane & (group - 1));
+    Values<E, U> w, dw = {};
+    load_weights(w, s, a.w_type, l);
+    const int64_t cta = static_cast<int64_t>(blockIdx.x) - (which ? a.side[0].ctas : 0);
+    const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
+    for (int64_t item = cta * (kThreads / 32) + (threadIdx.x >> 5); item < a.T * s.splits; item += warps) {
+        const int64_t t = item / s.splits;
+        const int share = static_cast<int>(item - t * s.splits);
+        float c[U][E], sn[U][E];
+        angles(c, sn, a.half ? a.pos[t] : 0, l);
+        for (int h0 = share * groups; h0 < s.heads; h0 += groups * s.splits) {
+            const int h = h0 + mine;
+            Values<E, U> x = {}, d = {};
+            if (h < s.heads) {
+                load_head<TYPE>(x, static_cast<const char *>(s.x) + t * s.x_tok + h * s.x_head, l);
+                load_head<DTYPE>(d, static_cast<const char *>(s.dy) + t * s.dy_tok + h * s.dy_head, l);
+            }
+            const float r = 1.f / sqrtf(group_sum(dot(x, x), group) * a.inv_d + a.eps);
+            rotate<-1>(d, c, sn, a.interleaved);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < E; ++i) {                      // x becomes x r, d becomes g
+                    x.a[u][i] *= r;
+                    x.b[u][i] *= r;
+                    if (h < s.heads) {
+                        dw.a[u][i] += d.a[u][i] * x.a[u][i];
+                        dw.b[u][i] += d.b[u][i] * x.b[u][i];
+                    }
+                    d.a[u][i] *= w.a[u][i];
+                    d.b[u][i] *= w.b[u][i];
+                }
+            const float m = group_sum(dot(d, x), group) * a.inv_d;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    d.a[u][i] = r * (d.a[u][i] - x.a[u][i] * m);
+                    d.b[u][i] = r * (d.b[u][i] - x.b[u][i] * m);
+                }
+            if (h < s.heads)
+                store_head<DTYPE>(static_cast<char *>(s.out) + t * s.out_tok + h * s.out_head, d, l);
+        }
+    }
+    if (!s.partial) return;
+    // the CTA's sums: every group's, in the order of the groups
+    __shared__ float part[kMaxHead];
+    for (int i = threadIdx.x; i < a.D; i += kThreads) part[i] = 0.f;
+    for (int turn_of = 0; turn_of < kThreads >> a.group_shift; ++turn_of) {
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) >> a.group_shift != turn_of) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                if (l.c0[u] >= 0) part[l.c0[u] + i] += dw.a[u][i];
+                if (l.c1[u] >= 0) part[l.c1[u] + i] += dw.b[u][i];
+            }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.D; i += kThreads) s.partial[cta * a.D + i] = part[i];
+}
+
+// dw of one side (blockIdx.y): the CTAs' rows in order, a warp per element.
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args a, float *dw_q, float *dw_k) {
+    const Side &s = a.side[blockIdx.y];
+    float *dw = blockIdx.y ? dw_k : dw_q;
+    const int d = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (!dw || d >= a.D) return;
+    float v = 0.f;
+    for (int i = threadIdx.x & 31; i < s.ctas; i += 32) v += s.partial[static_cast<int64_t>(i) * a.D + d];
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) dw[d] = v;
+}
+
+// ---- host -----------------------------------------------------------------
+
+// Heads of D elements at byte strides {head, token}: as rows of one matrix, and no two
+// heads of an output may overlap.
+int check_heads(const int64_t nb[2], int64_t D, int64_t H, int64_t T, int size, bool output) {
+    const int64_t row = D * size;
+    for (int i = 0; i < 2; ++i) {
+        const int rc = check_row_stride(row, i ? T : H, nb[i], size, output);
+        if (rc != OOP_OK) return rc;
+    }
+    if (output && H > 1 && T > 1) {
+        const bool head_first = nb[0] <= nb[1];
+        const int64_t lo = head_first ? nb[0] : nb[1], hi = head_first ? nb[1] : nb[0];
+        if (hi < lo * ((head_first ? H : T) - 1) + row) return OOP_ERR_SHAPE;
+    }
+    return OOP_OK;
+}
+
+int check_common(int64_t D, int64_t n_rot, int64_t T, const int32_t *pos, const float *freqs, float eps) {
+    if (D < 1 || D > kMaxHead || T < 0 || T > 0x7fffffffLL || n_rot < 0 || n_rot > D || n_rot % 2)
+        return OOP_ERR_SHAPE;
+    if (!(eps >= 0.f && std::isfinite(eps))) return OOP_ERR_VALUE;
+    if (T > 0 && n_rot > 0) {
+        int rc = check_pointer(pos, 4);
+        if (rc == OOP_OK) rc = check_pointer(freqs, 4);
+        if (rc != OOP_OK) return rc;
+    }
+    return OOP_OK;
+}
+
+constexpr int64_t kMaxHeads = 1 << 20;
+
+// Fills in what follows from the sizes; e is the chunk.
+void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms) {
+    a.T = T;
+    a.D = static_cast<int>(D);
+    a.half = static_cast<int>(n_rot / 2);
+    a.inv_d = 1.f / static_cast<float>(D);
+    a.units = a.half / e + static_cast<int>((D - n_rot + 2 * e - 1) / (2 * e));
+    a.group_shift = 0;
+    while ((1 << a.group_shift) < a.units && a.group_shift < 5) ++a.group_shift;
+    const int64_t groups = 32 >> a.group_shift;
+    const int64_t heads = a.side[0].heads + a.side[1].heads;
+    for (Side &s : a.side) {
+        if (s.heads == 0) continue;                        // no CTAs
+        // a token's heads are split until there are sixteen warps for each SM
+        const int64_t most = (s.heads + groups - 1) / groups;
+        int64_t splits = 1;
+        while (splits < most && T * splits < 16LL * sms) ++splits;
+        s.splits = static_cast<int>(splits);
+        const int64_t items = (T * splits + kThreads / 32 - 1) / (kThreads / 32);
+        const int64_t share = std::max<int64_t>(1, 8LL * sms * s.heads / heads);
+        s.ctas = static_cast<int>(std::min(items, share));
+    }
+}
+
+// The CTAs that have a row of sums: as many as plan() can give one side.
+int64_t partial_rows(int64_t T, int64_t H, int sms) {
+    return H ? std::max<int64_t>(1, std::min<int64_t>(8LL * sms, T * std::max<int64_t>(H, 1))) : 0;
+}
+
+template <int TYPE, int E, int U>
+void start_forward(const Args &a, cudaStream_t st) {
+    forward_kernel<TYPE, E, U><<<a.side[0].ctas + a.side[1].ctas, kThreads, 0, st>>>(a);
+}
+template <int TYPE>
+void launch_forward(const Args &a, int e, cudaStream_t st) {
+    const int per_lane = (a.units + 31) / 32;
+    if constexpr (TYPE != OOP_TYPE_F32) {
+        if (e == 8) return per_lane == 1 ? start_forward<TYPE, 8, 1>(a, st) : start_forward<TYPE, 8, 2>(a, st);
+    }
+    if (e == 4) return per_lane == 1 ? start_forward<TYPE, 4, 1>(a, st) : start_forward<TYPE, 4, 4>(a, st);
+    if (per_lane == 1) return start_forward<TYPE, 1, 1>(a, st);
+    return per_lane <= 4 ? start_forward<TYPE, 1, 4>(a, st) : start_forward<TYPE, 1, 16>(a, st);
+}
+
+template <int DTYPE, int TYPE, int E, int U>
+void start_backward(const Args &a, cudaStream_t st) {
+    backward_kernel<DTYPE, TYPE, E, U><<<a.side[0].ctas + a.side[1].ctas, kThreads, 0, st>>>(a);
+}
+template <int DTYPE, int TYPE>
+void launch_backward(const Args &a, int e, cudaStream_t st) {
+    const int per_lane = (a.units + 31) / 32;
+    if constexpr (TYPE != OOP_TYPE_F32 && DTYPE != OOP_TYPE_F32) {
+        if (e == 8)
+            return per_lane == 1 ? start_backward<DTYPE, TYPE, 8, 1>(a, st) : start_backward<DTYPE, TYPE, 8, 2>(a, st);
+    }
+    if (e == 4)
+        return per_lane == 1 ? start_backward<DTYPE, TYPE, 4, 1>(a, st) : start_backward<DTYPE, TYPE, 4, 4>(a, st);
+    if (per_lane == 1) return start_backward<DTYPE, TYPE, 1, 1>(a, st);
+    return per_lane <= 4 ? start_backward<DTYPE, TYPE, 1, 4>(a, st) : start_backward<DTYPE, TYPE, 1, 16>(a, st);
+}
+template <int DTYPE>
+void launch_backward_of(const Args &a, int x_type, int e, cudaStream_t st) {
+    if (x_type == OOP_TYPE_F32) launch_backward<DTYPE, OOP_TYPE_F32>(a, e, st);
+    else if (x_type == OOP_TYPE_F16) launch_backward<DTYPE, OOP_TYPE_F16>(a, e, st);
+    else launch_backward<DTYPE, OOP_TYPE_BF16>(a, e, st);
+}
+
+// Whether chunks of e elements of this size fit a tensor of heads.
+bool chunks_fit(int e, int size, const void *p, int64_t head, int64_t tok, int64_t H, int64_t T) {
+    const int bytes = std::min(16, e * size);
+    return is_aligned(p, bytes) && (H <= 1 || head % bytes == 0) && (T <= 1 || tok % bytes == 0);
+}
+
+}  // namespace
+}  // namespace oop
+
+using namespace oop;
+
+extern "C" {
+
+int oop_qk_norm_rope(const oop_heads *q, const oop_heads *k, int type, int w_type, const int32_t *pos,
+                     const float *freqs, int64_t D, int64_t n_rot, int64_t T, int interleaved, float eps,
+                     void *stream) {
+    g_kernel_launches = 0;
+    if (!q) return OOP_ERR_NULL;
+    const int size = plain_size(type), w_size = plain_size(w_type);
+    if (!size || !w_size) return OOP_ERR_TYPE;
+    int rc = check_common(D, n_rot, T, pos, freqs, eps);
+    if (rc != OOP_OK) return rc;
+    Args a = {};
+    const oop_heads *in[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        const oop_heads *p = in[i];
+        if (!p) continue;
+        if (p->n_head < 0 || p->n_head > kMaxHeads) return OOP_ERR_SHAPE;
+        if ((rc = check_heads(p->nb_x, D, p->n_head, T, size, false)) != OOP_OK) return rc;
+        if ((rc = check_heads(p->nb_y, D, p->n_head, T, size, true)) != OOP_OK) return rc;
+        if (p->n_head == 0 || T == 0) continue;
+        if ((rc = check_pointer(p->x, size)) != OOP_OK) return rc;
+        if ((rc = check_pointer(p->y, size)) != OOP_OK) return rc;
+        if (p->w && !is_aligned(p->w, w_size)) return OOP_ERR_ALIGN;
+        Side &s = a.side[i];
+        s.x = p->x;
+        s.out = p->y;
+        s.w = p->w;
+        s.x_head = p->nb_x[0], s.x_tok = p->nb_x[1], s.out_head = p->nb_y[0], s.out_tok = p->nb_y[1];
+        s.heads = static_cast<int>(p->n_head);
+    }
+    if (a.side[0].heads + a.side[1].heads == 0) return OOP_OK;
+    int *status = nullptr;
+    if ((rc = device_status_word(&status)) != OOP_OK) return rc;
+    a.pos = pos;
+    a.freqs = freqs;
+    a.w_type = w_type;
+    a.interleaved = interleaved != 0;
+    a.eps = eps;
+    auto fits = [&](int e) {
+        if ((n_rot / 2) % e || (D - n_rot) % (2 * e)) return false;
+        for (const Side &s : a.side)
+            if (s.heads && (!chunks_fit(e, size, s.x, s.x_head, s.x_tok, s.heads, T) ||
+                            !chunks_fit(e, size, s.out, s.out_head, s.out_tok, s.heads, T)))
+                return false;
+        return true;
+    };
+    const int e = size == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
+    plan(a, e, D, n_rot, T, device_sm_count());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (type == OOP_TYPE_F32) launch_forward<OOP_TYPE_F32>(a, e, st);
+    else if (type == OOP_TYPE_F16) launch_forward<OOP_TYPE_F16>(a, e, st);
+    else launch_forward<OOP_TYPE_BF16>(a, e, st);
+    g_kernel_launches = 1;
+    return cuda_status(cudaGetLastError());
+}
+
+// Room for the rows of sums of both sides on a GPU of up to 160 SMs.
+constexpr int kMostSms = 160;
+
+size_t oop_qk_norm_rope_back_workspace_size(int64_t D, int64_t T, int64_t n_head_q, int64_t n_head_k) {
+    if (D < 1 || D > kMaxHead || T < 0 || n_head_q < 0 || n_head_k < 0 || n_head_q > kMaxHeads ||
+        n_head_k > kMaxHeads || T > 0x7fffffffLL)
+        return 0;
+    return static_cast<size_t>(partial_rows(T, n_head_q, kMostSms) + partial_rows(T, n_head_k, kMostSms)) *
+           static_cast<size_t>(D) * sizeof(float);
+}
+
+int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int dy_type, int x_type,
+                          int w_type, const int32_t *pos, const float *freqs, int64_t D, int64_t n_rot,
+                          int64_t T, int interleaved, float eps, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    g_kernel_launches = 0;
+    if (!q) return OOP_ERR_NULL;
+    const int size = plain_size(x_type), d_size = plain_size(dy_type), w_size = plain_size(w_type);
+    if (!size || !w_size || !gradient_type(dy_type)) return OOP_ERR_TYPE;
+    int rc = check_common(D, n_rot, T, pos, freqs, eps);
+    if (rc != OOP_OK) return rc;
+    Args a = {};
+    float *dw[2] = {nullptr, nullptr};
+    int64_t heads[2] = {0, 0};
+    const oop_heads_grad *in[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        const oop_heads_grad *p = in[i];
+        if (!p) continue;
+        if (p->n_head < 0 || p->n_head > kMaxHeads) return OOP_ERR_SHAPE;
+        if ((rc = check_heads(p->nb_x, D, p->n_head, T, size, false)) != OOP_OK) return rc;
+        if ((rc = check_heads(p->nb_dy, D, p->n_head, T, d_size, false)) != OOP_OK) return rc;
+        if ((rc = check_heads(p->nb_dx, D, p->n_head, T, d_size, true)) != OOP_OK) return rc;
+        if (p->dw && !is_aligned(p->dw, 4)) return OOP_ERR_ALIGN;
+        if (p->w && !is_aligned(p->w, w_size)) return OOP_ERR_ALIGN;
+        dw[i] = p->dw;
+        heads[i] = p->n_head;
+        if (p->n_head == 0 || T == 0) continue;
+        if ((rc = check_pointer(p->x, size)) != OOP_OK) return rc;
+        if ((rc = check_pointer(p->dy, d_size)) != OOP_OK) return rc;
+        if ((rc = check_pointer(p->dx, d_size)) != OOP_OK) return rc;
+        Side &s = a.side[i];
+        s.x = p->x;
+        s.dy = p->dy;
+        s.out = p->dx;
+        s.w = p->w;
+        s.x_head = p->nb_x[0], s.x_tok = p->nb_x[1], s.out_head = p->nb_dx[0], s.out_tok = p->nb_dx[1];
+        s.dy_head = p->nb_dy[0], s.dy_tok = p->nb_dy[1];
+        s.heads = static_cast<int>(p->n_head);
+    }
+    const bool any = a.side[0].heads + a.side[1].heads > 0, want = dw[0] || dw[1];
+    if (!any && !want) return OOP_OK;
+    if (any && want) {
+        const size_t need = oop_qk_norm_rope_back_workspace_size(D, T, heads[0], heads[1]);
+        if (!workspace || workspace_bytes < need || !is_aligned(workspace, 256)) return OOP_ERR_WORKSPACE;
+    }
+    int *status = nullptr;
+    if ((rc = device_status_word(&status)) != OOP_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!any) {                                            // sums of nothing
+        for (float *p : dw)
+            if (p && (rc = cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(D) * 4, st))) != OOP_OK) return rc;
+        return OOP_OK;
+    }
+    a.pos = pos;
+    a.freqs = freqs;
+    a.w_type = w_type;
+    a.interleaved = interleaved != 0;
+    a.eps = eps;
+    auto fits = [&](int e) {
+        if ((n_rot / 2) % e || (D - n_rot) % (2 * e)) return false;
+        for (const Side &s : a.side)
+            if (s.heads && (!chunks_fit(e, size, s.x, s.x_head, s.x_tok, s.heads, T) ||
+                            !chunks_fit(e, d_size, s.dy, s.dy_head, s.dy_tok, s.heads, T) ||
+                            !chunks_fit(e, d_size, s.out, s.out_head, s.out_tok, s.heads, T)))
+                return false;
+        return true;
+    };
+    const int e = size == 2 && d_size == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
+    plan(a, e, D, n_rot, T, std::min(device_sm_count(), kMostSms));
+    float *rows = static_cast<float *>(workspace);
+    for (int i = 0; i < 2; ++i) {
+        a.side[i].partial = dw[i] ? rows : nullptr;
+        if (want) rows += static_cast<int64_t>(a.side[i].ctas) * D;
+    }
+    if (dy_type == OOP_TYPE_F32) launch_backward_of<OOP_TYPE_F32>(a, x_type, e, st);
+    else launch_backward_of<OOP_TYPE_BF16>(a, x_type, e, st);
+    if ((rc = cuda_status(cudaGetLastError())) != OOP_OK) return rc;
+    g_kernel_launches = 1;
+    if (want) {
+        const unsigned blocks = static_cast<unsigned>((D + kThreads / 32 - 1) / (kThreads / 32));
+        join_kernel<<<dim3(blocks, 2), kThreads, 0, st>>>(a, dw[0], dw[1]);
+        g_kernel_launches = 2;
+        rc = cuda_status(cudaGetLastError());
+    }
+    return rc;
+}
+
+}  // extern "C"

@@ -542,6 +542,159 @@ int oop_preference_loss_back(const void *logits, int type, int64_t nb, const int
                              const int64_t ne[2], int64_t n_pairs, double beta,
                              double label_smoothing, void *stream);
 
+/*
+ * The operators of a decoder layer's training step (no counterpart on the
+ * pages): what happens to queries and keys before attention, the gated
+ * feed-forward block, and the orthogonalised update of a weight.  The rules on
+ * types, strides, sums and overlap are those of the operators above; where a
+ * matrix product is part of the operator its sums are held in 32 bits.
+ */
+
+/*
+ * RMS norm of every query and key head and the rotation by the token's
+ * position, in one pass.  For each token t and head of D elements x:
+ *
+ *   r = (sum_d x[d]^2 / D + eps)^(-1/2),  n[d] = x[d] * r * w[d]
+ *   y = n with its first n_rot elements turned as pairs (a, b) by the angle
+ *       pos[t] * freqs[i]:  a cos - b sin, a sin + b cos,  i = 0 .. n_rot/2 - 1
+ *
+ * Pair i is (n[i], n[i + n_rot/2]), or with interleaved != 0 (n[2i], n[2i+1]).
+ * The angle is the exact product modulo a whole turn (to 2^-32 turns), so far
+ * positions lose nothing.  freqs: device f32 {n_rot/2}, radians per position.
+ * q and k may be slices of one buffer; k may be NULL (queries only).  D is 1 ..
+ * 1024, n_rot even, 0 .. D (0: norm only, pos and freqs not used).  y may be x.
+ * eps >= 0, finite.  A pair whose frequency is not finite is NaN.
+ */
+typedef struct {
+    const void *x;      /* {D, n_head, T}: device, plain type */
+    int64_t nb_x[2];    /* bytes between heads, between tokens */
+    void *y;            /* {D, n_head, T}: device, x's type, OVERWRITTEN */
+    int64_t nb_y[2];
+    const void *w;      /* {D}: device, plain type; NULL: 1 */
+    int64_t n_head;
+} oop_heads;
+
+int oop_qk_norm_rope(const oop_heads *q, const oop_heads *k, int type, int w_type,
+                     const int32_t *pos, const float *freqs, int64_t D, int64_t n_rot, int64_t T,
+                     int interleaved, float eps, void *stream);
+
+/*
+ * Its backward pass.  With dn = dy turned back by the same angle and g = dn * w:
+ *
+ *   dx = r * (g - x * r^2 * sum_d (g * x) / D),  dw[d] = sum over t, head of dn * x * r
+ *
+ * dy and dx: F32 or BF16, one type; dx may be dy.  x: the forward's input, plain
+ * type; r is computed again.  dw: f32 {D}, OVERWRITTEN; NULL: not computed.
+ * workspace: oop_qk_norm_rope_back_workspace_size(...) bytes, 256-byte
+ * aligned (none needed where both dw are NULL).
+ */
+typedef struct {
+    const void *dy;     /* {D, n_head, T}: device, F32 or BF16 */
+    int64_t nb_dy[2];
+    const void *x;      /* {D, n_head, T}: device, plain type */
+    int64_t nb_x[2];
+    const void *w;      /* {D} or NULL */
+    void *dx;           /* {D, n_head, T}: device, dy's type, OVERWRITTEN */
+    int64_t nb_dx[2];
+    float *dw;          /* {D}: device, f32, OVERWRITTEN; NULL: not computed */
+    int64_t n_head;
+} oop_heads_grad;
+
+size_t oop_qk_norm_rope_back_workspace_size(int64_t D, int64_t T, int64_t n_head_q,
+                                            int64_t n_head_k);
+
+int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int dy_type,
+                          int x_type, int w_type, const int32_t *pos, const float *freqs,
+                          int64_t D, int64_t n_rot, int64_t T, int interleaved, float eps,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gated feed-forward block up to its last projection, ne = {K, F, T}:
+ *
+ *   gate[f, t] = sum_k w_gate[k, f] * x[k, t],   up[f, t] = sum_k w_up[k, f] * x[k, t]
+ *   h[f, t] = act(gate[f, t]) * up[f, t]
+ *
+ *   x {K, T}: plain type     w_gate, w_up {K, F}: one oop_type, quantised
+ *                            blocks along k (K % 32, or % 256), rows nb_w apart
+ *   h, gate, up {F, T}: x's type, OVERWRITTEN; gate and up (rows nb_gu apart)
+ *                       may both be NULL (not kept)
+ *
+ * h is computed from the 32-bit sums and rounded once.  x and the weights of
+ * one 16-bit type go to the tensor cores as they are; other operands as a sum
+ * of bfloat16 terms that keeps fp32's range: three (24 bits) where x is F32,
+ * else two (16 bits or more).  No operand passes through binary16 but those
+ * that are binary16.  Magnitudes below 2^-110 may lose bits.  A non-finite operand
+ * gives non-finite sums.  K == 0: sums of nothing, 0.
+ *
+ * workspace: oop_gated_ffn_workspace_size(...) bytes, 256-byte aligned; with
+ * aligned != 0 for calls whose x and weights have 16-byte aligned pointers and
+ * strides, else for any.
+ */
+typedef enum {
+    OOP_ACT_SILU = 0,      /* v / (1 + exp(-v)) */
+    OOP_ACT_GELU_TANH = 1, /* v/2 * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) */
+    OOP_ACT_GELU_ERF = 2,  /* v/2 * (1 + erf(v / sqrt(2))) */
+    OOP_ACT_RELU = 3       /* max(v, 0); its derivative at 0 is 0 */
+} oop_act;
+
+size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3], int aligned);
+
+int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, const void *w_up,
+                  int w_type, int64_t nb_w, void *h, int64_t nb_h, void *gate, void *up,
+                  int64_t nb_gu, const int64_t ne[3], int act, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * Its backward pass, from the forward's gate and up:
+ *
+ *   dgate = dh * up * act'(gate),   dup = dh * act(gate)
+ *   dx[k, t] = sum_f w_gate[k, f] * dgate[f, t] + w_up[k, f] * dup[f, t]
+ *   dw_gate[k, f] = sum_t dgate[f, t] * x[k, t],   dw_up[k, f] = sum_t dup[f, t] * x[k, t]
+ *
+ * dh {F, T} and every result: F32 or BF16, one type.  dgate and dup are held
+ * in that type between the products (rounded once where it is BF16).  dx may be NULL,
+ * and dw_gate and dw_up both (not computed); dw rows are nb_dw apart.  T == 0
+ * writes zeros to dw_gate and dw_up.  No output may overlap an input.
+ */
+size_t oop_gated_ffn_back_workspace_size(int dh_type, int x_type, int w_type,
+                                         const int64_t ne[3], int aligned);
+
+int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x, int x_type,
+                       int64_t nb_x, const void *w_gate, const void *w_up, int w_type,
+                       int64_t nb_w, const void *gate, const void *up, int64_t nb_gu, void *dx,
+                       int64_t nb_dx, void *dw_gate, void *dw_up, int64_t nb_dw,
+                       const int64_t ne[3], int act, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * The update of a weight made nearly orthogonal by Newton-Schulz steps, as the
+ * Muon optimiser does it, for each of B matrices X of M rows of N elements:
+ *
+ *   X_0 = x / (|x|_F + eps)
+ *   X_s = a_s X + b_s (X X') X + c_s (X X')^2 X      s = 1 .. steps, X = X_(s-1)
+ *   y   = scale * X_steps
+ *
+ *   ne = {N, M, B}   x, y: F32 or BF16; nb_x, nb_y: bytes between rows,
+ *                    between matrices; y may be x
+ *   coefs: HOST f32 {3 * steps}, (a, b, c) of each step; NULL: (3.4445, -4.7750,
+ *          2.0315) at every step
+ *
+ * The norm, the matrices between the products and their sums are held in 32
+ * bits: the products take each factor as two binary16 terms of a scaled value
+ * (22 bits or more), and X_s has to stay below 8 in magnitude, X X' below 64
+ * and a + b X X' + c (X X')^2 below 256, as they do for coefficients that
+ * keep the singular values below 1.5; beyond that the matrix is not finite.  A
+ * matrix of zeros gives zeros (eps > 0), one with a value that is not finite
+ * gives NaN.  steps 0 .. 64.  eps >= 0, scale and coefs finite.  workspace:
+ * oop_orthogonalise_workspace_size(...) bytes, 256-byte aligned.
+ */
+size_t oop_orthogonalise_workspace_size(const int64_t ne[3]);
+
+int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y, int y_type,
+                      const int64_t nb_y[2], const int64_t ne[3], int steps, const float *coefs,
+                      float eps, float scale, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /* Synchronises `stream`, then returns the current device's status word
  * (OOP_OK, or the first device-side error recorded since it was last
  * cleared); clears it when `clear` is non-zero.  Returns OOP_ERR_CUDA if the
