@@ -1,0 +1,52 @@
+// activation.cuh -- the activations of the gated feed-forward block.
+#pragma once
+
+#include "oop_internal.cuh"
+
+namespace oop {
+
+// 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation.
+// exp is kept below 2^116, so that the product of the two is never Inf * 0.
+__device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + expf(-v)); }
+__device__ __forceinline__ float logistic(float v, float &rest) {
+    const float e = expf(fminf(-v, 80.f)), s = 1.f / (1.f + e);
+    rest = e * s;
+    return v != v ? v : s;
+}
+
+constexpr float kGeluTwice = 1.5957691216057308f;          // 2 sqrt(2 / pi)
+
+// (1 + tanh z) / 2 is the logistic function of 2 z: no cancellation for negative v.
+__device__ __forceinline__ float gelu_argument(float v) { return kGeluTwice * (v + 0.044715f * v * v * v); }
+
+__device__ __forceinline__ float activation_of(int act, float v) {
+    if (act == OOP_ACT_SILU) return v * logistic(v);
+    if (act == OOP_ACT_GELU_TANH) return v * logistic(gelu_argument(v));
+    if (act == OOP_ACT_GELU_ERF) return v * (0.5f * erfcf(-v * 0.7071067811865476f));
+    return v < 0.f ? 0.f : v;
+}
+
+// The activation and its derivative.
+__device__ __forceinline__ float activation_and_slope(int act, float v, float &slope) {
+    if (act == OOP_ACT_SILU) {
+        float rest;
+        const float s = logistic(v, rest);
+        slope = s + v * s * rest;
+        return v * s;
+    }
+    if (act == OOP_ACT_GELU_TANH) {
+        float rest;
+        const float s = logistic(gelu_argument(v), rest);
+        slope = s + v * (s * rest) * (kGeluTwice * (1.f + 0.134145f * v * v));
+        return v * s;
+    }
+    if (act == OOP_ACT_GELU_ERF) {
+        const float e = 0.5f * erfcf(-v * 0.7071067811865476f);
+        slope = e + v * (expf(-0.5f * v * v) * 0.3989422804014327f);
+        return v * e;
+    }
+    slope = v > 0.f ? 1.f : v == v ? 0.f : v;
+    return v < 0.f ? 0.f : v;
+}
+
+}  // namespace oop

@@ -7,99 +7,237 @@
 #include <algorithm>
 #include <cmath>
 
+#include "activation.cuh"
 #include "oop_internal.cuh"
-#include "products.cuh"
+#include "pair_product.cuh"
+#include "quant.cuh"
 #include "rows.cuh"
 
 namespace oop {
 namespace {
 
-constexpr float kGelu = 0.7978845608028654f;               // sqrt(2 / pi)
-
-// The activation and its derivative.
-template <bool SLOPE>
-__device__ __forceinline__ float activation(float v, int act, float &slope) {
-    if (act == OOP_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-v));
-        if (SLOPE) slope = s * (1.f + v * (1.f - s));
-        return v * s;
-    }
-    if (act == OOP_ACT_GELU_TANH) {
-        const float t = tanhf(kGelu * (v + 0.044715f * v * v * v));
-        if (SLOPE) slope = 0.5f * (1.f + t) + 0.5f * v * (1.f - t * t) * kGelu * (1.f + 0.134145f * v * v);
-        return 0.5f * v * (1.f + t);
-    }
-    if (act == OOP_ACT_GELU_ERF) {
-        const float e = 0.5f * erfcf(-v * 0.7071067811865476f);
-        if (SLOPE) slope = e + v * expf(-0.5f * v * v) * 0.3989422804014327f;
-        return v * e;
-    }
-    if (SLOPE) slope = v > 0.f ? 1.f : v == v ? 0.f : v;
-    return v > 0.f ? v : v == v ? 0.f : v;
+// The nearest bfloat16; a finite value stays finite.
+__device__ __forceinline__ __nv_bfloat16 nearest_bf16(float v) {
+    const float top = __uint_as_float(0x7f7f0000u);        // the largest one
+    return __float2bfloat16_rn(isfinite(v) ? fminf(fmaxf(v, -top), top) : v);
 }
 
-struct Rows {
-    const void *p;
-    int64_t nb;
-};
+// v as the sum of P bfloat16 values, each the nearest to what is left.
+template <int P>
+__device__ __forceinline__ void split(float v, __nv_bfloat16 (&t)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        t[i] = nearest_bf16(v);
+        v -= __bfloat162float(t[i]);
+    }
+}
 
-// h and the kept projections from the sums (gate in g, up in u, dense).
+// Eight elements of a row from column c, those beyond the row 0.
 template <int TYPE>
-__global__ void gate_kernel(const float *g, const float *u, char *h, int64_t nb_h, char *gate, char *up, int64_t nb_gu,
-                            int64_t F, int64_t T, int act) {
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < F * T; i += gridDim.x * 256LL) {
-        const int64_t t = i / F, f = i - t * F;
-        float none;
-        row_of<TYPE>(h, nb_h, t)[f] = from_float<TYPE>(activation<false>(g[i], act, none) * u[i]);
-        if (gate) {
-            row_of<TYPE>(gate, nb_gu, t)[f] = from_float<TYPE>(g[i]);
-            row_of<TYPE>(up, nb_gu, t)[f] = from_float<TYPE>(u[i]);
+__device__ __forceinline__ void load8(const char *row, int64_t c, int64_t cols, int wide, float (&v)[8]) {
+    if constexpr (plain_size(TYPE) != 0) {
+        using S = typename Plain<TYPE>::S;
+        const S *p = reinterpret_cast<const S *>(row) + c;
+        if (wide && c + 8 <= cols) {
+            constexpr int E = 16 / plain_size(TYPE);
+#pragma unroll
+            for (int i = 0; i < 8; i += E) {
+                float part[E];
+                load_stream<TYPE, E>(p + i).get(part);
+#pragma unroll
+                for (int k = 0; k < E; ++k) v[i + k] = part[k];
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float(p[i]) : 0.f;
+    } else {                                               // whole blocks: cols % 32 == 0
+        using F = QFormat<TYPE>;
+        const uint8_t *blk = reinterpret_cast<const uint8_t *>(row) + c / F::QK * F::BYTES;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = decode<TYPE>(blk, static_cast<int>(c % F::QK) + i);
+    }
+}
+
+template <int P>
+__device__ __forceinline__ void store_planes(const float (&v)[8], __nv_bfloat16 *dst, int64_t plane) {
+    __nv_bfloat16 t[P][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        __nv_bfloat16 one[P];
+        split<P>(v[i], one);
+#pragma unroll
+        for (int p = 0; p < P; ++p) t[p][i] = one[p];
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        uint4 w;
+        __builtin_memcpy(&w, t[p], 16);
+        *reinterpret_cast<uint4 *>(dst + p * plane) = w;
+    }
+}
+
+// Rows of any type as P bfloat16 planes [P][rows][pitch]; P = 0: 16-bit elements copied.
+template <int TYPE, int P>
+__global__ void __launch_bounds__(256) planes_kernel(const char *src, int64_t nb, int64_t cols, int64_t rows,
+                                                     __nv_bfloat16 *dst, int64_t pitch, int wide) {
+    const int64_t per_row = pitch / 8;
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < rows * per_row; i += gridDim.x * 256LL) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+        if constexpr (P == 0) {
+            uint16_t w[8];
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(src + r * nb) + c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = c + k < cols ? p[k] : 0;
+            uint4 o;
+            __builtin_memcpy(&o, w, 16);
+            *reinterpret_cast<uint4 *>(dst + r * pitch + c) = o;
+        } else {
+            float v[8];
+            load8<TYPE>(src + r * nb, c, cols, wide, v);
+            store_planes<P>(v, dst + r * pitch + c, rows * pitch);
         }
     }
 }
 
-__global__ void gate_back_kernel(Rows dh, int d_type, Rows gate, Rows up, int x_type, float *dg, float *du, int64_t F,
-                                 int64_t T, int act) {
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < F * T; i += gridDim.x * 256LL) {
-        const int64_t t = i / F, f = i - t * F;
-        const float d = load_any(static_cast<const char *>(dh.p) + t * dh.nb, d_type, f);
-        const float g = load_any(static_cast<const char *>(gate.p) + t * gate.nb, x_type, f);
-        const float u = load_any(static_cast<const char *>(up.p) + t * up.nb, x_type, f);
-        float slope;
-        const float a = activation<true>(g, act, slope);
-        float vg = d * u * slope, vu = d * a;
-        if (d_type == OOP_TYPE_BF16) {
-            vg = __bfloat162float(__float2bfloat16_rn(vg));
-            vu = __bfloat162float(__float2bfloat16_rn(vu));
+unsigned blocks_of(int64_t n) { return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 1 << 16))); }
+
+template <int P>
+cudaError_t launch_planes_of(const void *src, int type, int64_t nb, int64_t cols, int64_t rows, void *dst, int64_t pitch,
+                             cudaStream_t st) {
+    const char *s = static_cast<const char *>(src);
+    auto *d = static_cast<__nv_bfloat16 *>(dst);
+    const int wide = is_aligned(src, 16) && nb % 16 == 0;
+    const unsigned g = blocks_of(rows * pitch / 8);
+#define OOP_CASE(T) \
+    case T: planes_kernel<T, P><<<g, 256, 0, st>>>(s, nb, cols, rows, d, pitch, wide); break;
+    if constexpr (P == 0) {
+        planes_kernel<OOP_TYPE_BF16, 0><<<g, 256, 0, st>>>(s, nb, cols, rows, d, pitch, wide);
+    } else {
+        switch (type) {
+            OOP_CASE(OOP_TYPE_F32) OOP_CASE(OOP_TYPE_F16) OOP_CASE(OOP_TYPE_Q4_0)
+            OOP_CASE(OOP_TYPE_Q4_1) OOP_CASE(OOP_TYPE_Q5_0) OOP_CASE(OOP_TYPE_Q5_1) OOP_CASE(OOP_TYPE_Q8_0)
+            OOP_CASE(OOP_TYPE_Q2_K) OOP_CASE(OOP_TYPE_Q3_K) OOP_CASE(OOP_TYPE_Q4_K) OOP_CASE(OOP_TYPE_Q5_K)
+            OOP_CASE(OOP_TYPE_Q6_K)
         }
-        dg[i] = vg;
-        du[i] = vu;
+    }
+#undef OOP_CASE
+    ++g_kernel_launches;
+    return cudaGetLastError();
+}
+
+// dgate and dup as P planes [P][2][T][pitch]: dgate = dh up act'(gate), dup = dh act(gate).
+template <int DTYPE, int TYPE, int P>
+__global__ void __launch_bounds__(256) gate_back_kernel(const char *dh, int64_t nb_dh, const char *gate, const char *up, int64_t nb_gu,
+                                                        __nv_bfloat16 *dst, int64_t pitch, int64_t F, int64_t T, int act, int wide) {
+    const int64_t per_row = pitch / 8;
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < T * per_row; i += gridDim.x * 256LL) {
+        const int64_t t = i / per_row, c = (i - t * per_row) * 8;
+        float d[8], g[8], u[8];
+        load8<DTYPE>(dh + t * nb_dh, c, F, wide, d);
+        load8<TYPE>(gate + t * nb_gu, c, F, wide, g);
+        load8<TYPE>(up + t * nb_gu, c, F, wide, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float slope;
+            const float a = activation_and_slope(act, g[k], slope);
+            g[k] = d[k] * u[k] * slope;
+            u[k] = d[k] * a;
+        }
+        store_planes<P>(g, dst + t * pitch + c, 2 * T * pitch);
+        store_planes<P>(u, dst + (T + t) * pitch + c, 2 * T * pitch);
     }
 }
 
-template <int TYPE>
-__global__ void store_kernel(const float *src, char *dst, int64_t nb, int64_t cols, int64_t rows) {
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < cols * rows; i += gridDim.x * 256LL) {
-        const int64_t r = i / cols;
-        row_of<TYPE>(dst, nb, r)[i - r * cols] = from_float<TYPE>(src[i]);
-    }
-}
-
-unsigned blocks_of(int64_t n) { return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 1 << 18))); }
-
-void store(const float *src, void *dst, int type, int64_t nb, int64_t cols, int64_t rows, cudaStream_t st) {
-    char *d = static_cast<char *>(dst);
-    if (type == OOP_TYPE_F32) store_kernel<OOP_TYPE_F32><<<blocks_of(cols * rows), 256, 0, st>>>(src, d, nb, cols, rows);
-    else store_kernel<OOP_TYPE_BF16><<<blocks_of(cols * rows), 256, 0, st>>>(src, d, nb, cols, rows);
+template <int DTYPE, int P>
+void launch_gate_back(int x_type, const char *dh, int64_t nb_dh, const char *gate, const char *up, int64_t nb_gu, void *dst,
+                      int64_t pitch, int64_t F, int64_t T, int act, int wide, cudaStream_t st) {
+    auto *d = static_cast<__nv_bfloat16 *>(dst);
+    const unsigned g = blocks_of(T * pitch / 8);
+    if (x_type == OOP_TYPE_F32) gate_back_kernel<DTYPE, OOP_TYPE_F32, P><<<g, 256, 0, st>>>(dh, nb_dh, gate, up, nb_gu, d, pitch, F, T, act, wide);
+    else if (x_type == OOP_TYPE_F16) gate_back_kernel<DTYPE, OOP_TYPE_F16, P><<<g, 256, 0, st>>>(dh, nb_dh, gate, up, nb_gu, d, pitch, F, T, act, wide);
+    else gate_back_kernel<DTYPE, OOP_TYPE_BF16, P><<<g, 256, 0, st>>>(dh, nb_dh, gate, up, nb_gu, d, pitch, F, T, act, wide);
     ++g_kernel_launches;
 }
 
-// Floats of the workspace: x, both weights, and two matrices {F, T}; back: and the larger result.
-size_t floats_forward(const int64_t ne[3]) {
-    return static_cast<size_t>(ne[0] * ne[2] + 2 * ne[0] * ne[1] + 2 * ne[1] * ne[2]);
+// ---- operands -------------------------------------------------------------
+
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// How a matrix of a type goes to the tensor cores: as it is (0: not even copied), or
+// as so many 16-bit planes in the workspace.
+struct Form {
+    int planes;        // terms of a value
+    bool half, copy;   // binary16; in the workspace
+};
+
+// `native`: the other operand has this 16-bit type too.  `precise`: the product is wanted to 24 bits.
+Form form_of(int type, bool native, bool precise, bool aligned) {
+    if (native) return {1, type == OOP_TYPE_F16, !aligned};
+    if (type == OOP_TYPE_BF16) return {1, false, !aligned};
+    if (type == OOP_TYPE_F16) return {2, false, true};     // 11 bits: two planes hold them
+    return {precise ? 3 : 2, false, true};
 }
-size_t floats_back(const int64_t ne[3]) {
-    return floats_forward(ne) + static_cast<size_t>(std::max(ne[0] * ne[2], ne[0] * ne[1]));
+
+size_t form_bytes(const Form &f, int64_t cols, int64_t rows) {
+    return f.copy ? round256(static_cast<size_t>(f.planes) * static_cast<size_t>(rows * round8(cols)) * 2) : 0;
+}
+
+struct ForwardForms {
+    Form x, w;
+};
+ForwardForms forward_forms(int x_type, int w_type, bool aligned) {
+    const bool native = x_type == w_type && x_type != OOP_TYPE_F32 && plain_size(x_type) == 2;
+    return {form_of(x_type, native, x_type == OOP_TYPE_F32, aligned), form_of(w_type, native, x_type == OOP_TYPE_F32, aligned)};
+}
+struct BackForms {
+    Form d, x, w;
+};
+BackForms back_forms(int dh_type, int x_type, int w_type, bool aligned) {
+    const bool precise = dh_type == OOP_TYPE_F32;
+    return {{precise ? 3 : 1, false, true}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
+}
+
+// A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
+// that this call writes at `at`, which moves on.
+cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_t cols, int64_t rows, bool rows_contiguous,
+                    char *&at, pair::Operand &o, cudaStream_t st) {
+    o = {src, cols, rows, nb, 0, 1, rows_contiguous, f.half};
+    if (!f.copy) return cudaSuccess;
+    const int64_t pitch = round8(cols);
+    o.p = at;
+    o.pitch_bytes = pitch * 2;
+    o.matrix_bytes = rows * pitch * 2;
+    o.matrices = f.planes;
+    at += form_bytes(f, cols, rows);
+    if (f.planes == 1) return launch_planes_of<0>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
+    return f.planes == 2 ? launch_planes_of<2>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st)
+                         : launch_planes_of<3>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
+}
+
+// Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the
+// waves (a narrow tile reads A as often as a wide one for half the sums).
+bool narrow_tiles(int64_t M, int64_t N, int64_t batches, int wide_cols) {
+    const int64_t pairs = std::max(1, device_sm_count() / 2);
+    auto waves = [&](int64_t cols) {
+        const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
+        return (tiles + pairs - 1) / pairs;
+    };
+    return waves(wide_cols / 2) * 23 < waves(wide_cols) * 40;
+}
+
+template <int EPI, bool FOLD>
+cudaError_t product(const pair::Spec &s, int *status, cudaStream_t st) {
+    const int wide_cols = EPI == pair::kGate ? 128 : 256;
+    return narrow_tiles(s.M, s.N, s.batches, wide_cols) ? pair::launch<EPI, FOLD, 128>(s, status, st)
+                                                        : pair::launch<EPI, FOLD, 256>(s, status, st);
+}
+
+cudaError_t zero_rows(void *p, int64_t nb, int64_t row_bytes, int64_t rows, cudaStream_t st) {
+    if (rows == 0 || row_bytes == 0) return cudaSuccess;
+    return cudaMemset2DAsync(p, static_cast<size_t>(rows > 1 ? nb : row_bytes), 0, static_cast<size_t>(row_bytes),
+                             static_cast<size_t>(rows), st);
 }
 
 int check_ffn(int x_type, int w_type, const int64_t ne[3], int act) {
@@ -129,6 +267,9 @@ int check_weights(const void *wg, const void *wu, int w_type, int64_t nb_w, int6
     return rc;
 }
 
+// Rows that TMA and 16-byte accesses can take as they are.
+bool rows_aligned(const void *p, int64_t nb, int64_t rows) { return is_aligned(p, 16) && (rows <= 1 || nb % 16 == 0); }
+
 int check_workspace(const void *ws, size_t have, size_t need) {
     return need == 0 || (ws && have >= need && is_aligned(ws, 256)) ? OOP_OK : OOP_ERR_WORKSPACE;
 }
@@ -141,15 +282,15 @@ using namespace oop;
 extern "C" {
 
 size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3], int aligned) {
-    (void)aligned;
     if (check_ffn(x_type, w_type, ne, 0) != OOP_OK) return 0;
-    return floats_forward(ne) * 4;
+    const ForwardForms f = forward_forms(x_type, w_type, aligned != 0);
+    return form_bytes(f.x, ne[0], ne[2]) + 2 * form_bytes(f.w, ne[0], ne[1]);
 }
 
 size_t oop_gated_ffn_back_workspace_size(int dh_type, int x_type, int w_type, const int64_t ne[3], int aligned) {
-    (void)aligned;
     if (!gradient_type(dh_type) || check_ffn(x_type, w_type, ne, 0) != OOP_OK) return 0;
-    return floats_back(ne) * 4;
+    const BackForms f = back_forms(dh_type, x_type, w_type, aligned != 0);
+    return form_bytes(f.d, ne[1], 2 * ne[2]) + form_bytes(f.x, ne[0], ne[2]) + 2 * form_bytes(f.w, ne[0], ne[1]);
 }
 
 int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, const void *w_up, int w_type,
@@ -169,27 +310,36 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     if (K > 0 && (rc = check_pointer(x, size)) != OOP_OK) return rc;
     if ((rc = check_pointer(h, size)) != OOP_OK) return rc;
     if (gate && ((rc = check_pointer(gate, size)) != OOP_OK || (rc = check_pointer(up, size)) != OOP_OK)) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_workspace_size(x_type, w_type, ne, 0))) != OOP_OK)
+    const bool aligned = rows_aligned(x, nb_x, T) && rows_aligned(w_gate, nb_w, F) && rows_aligned(w_up, nb_w, F);
+    if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_workspace_size(x_type, w_type, ne, aligned))) != OOP_OK)
         return rc;
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    float *xf = static_cast<float *>(workspace), *wf[2] = {xf + K * T, xf + K * T + K * F}, *s[2];
-    s[0] = wf[1] + K * F;
-    s[1] = s[0] + F * T;
-    const void *w[2] = {w_gate, w_up};
-    cudaError_t e = launch_to_f32(x, x_type, nb_x, K, T, xf, K, st);
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-        e = launch_to_f32(w[i], w_type, nb_w, K, F, wf[i], K, st);
-        if (e == cudaSuccess) e = launch_product({xf, wf[i], s[i], T, F, K, 1, K, 1, 0, K, 1, 0, F, 0, 1.f, 0.f}, st);
+    if (K == 0) {                                          // sums of nothing: act(0) * 0
+        cudaError_t e = zero_rows(h, nb_h, F * size, T, st);
+        if (gate && e == cudaSuccess) e = zero_rows(gate, nb_gu, F * size, T, st);
+        if (gate && e == cudaSuccess) e = zero_rows(up, nb_gu, F * size, T, st);
+        return cuda_status(e);
     }
+    const ForwardForms f = forward_forms(x_type, w_type, aligned);
+    char *at = static_cast<char *>(workspace);
+    pair::Spec s = {};
+    cudaError_t e = operand(f.x, x, x_type, nb_x, K, T, false, at, s.a, st);
+    if (e == cudaSuccess) e = operand(f.w, w_gate, w_type, nb_w, K, F, false, at, s.b[0], st);
+    if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, false, at, s.b[1], st);
     if (e != cudaSuccess) return cuda_status(e);
-    char *hp = static_cast<char *>(h), *gp = static_cast<char *>(gate), *up_ = static_cast<char *>(up);
-    if (x_type == OOP_TYPE_F32) gate_kernel<OOP_TYPE_F32><<<blocks_of(F * T), 256, 0, st>>>(s[0], s[1], hp, nb_h, gp, up_, nb_gu, F, T, act);
-    else if (x_type == OOP_TYPE_F16) gate_kernel<OOP_TYPE_F16><<<blocks_of(F * T), 256, 0, st>>>(s[0], s[1], hp, nb_h, gp, up_, nb_gu, F, T, act);
-    else gate_kernel<OOP_TYPE_BF16><<<blocks_of(F * T), 256, 0, st>>>(s[0], s[1], hp, nb_h, gp, up_, nb_gu, F, T, act);
-    ++g_kernel_launches;
-    return cuda_status(cudaGetLastError());
+    s.M = T, s.N = F, s.K = K;
+    s.batches = s.segments = 1;
+    s.planes_a = f.x.planes, s.planes_b = f.w.planes;
+    s.a_plane = s.b_plane = 1;
+    s.out.p0 = h, s.out.p1 = gate, s.out.p2 = up;
+    s.out.nb0 = nb_h, s.out.nb1 = nb_gu;
+    s.out.type = x_type, s.out.act = act;
+    s.out.wide = F * size % 16 == 0 && rows_aligned(h, nb_h, T) &&
+                 (!gate || (rows_aligned(gate, nb_gu, T) && rows_aligned(up, nb_gu, T)));
+    e = x_type == OOP_TYPE_F32 ? product<pair::kGate, true>(s, status, st) : product<pair::kGate, false>(s, status, st);
+    return cuda_status(e);
 }
 
 int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x, int x_type, int64_t nb_x,
@@ -220,40 +370,61 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
     }
     if (want_dx && (rc = check_pointer(dx, d_size)) != OOP_OK) return rc;
     if (want_dw && ((rc = check_pointer(dw_gate, d_size)) != OOP_OK || (rc = check_pointer(dw_up, d_size)) != OOP_OK)) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_back_workspace_size(dh_type, x_type, w_type, ne, 0))) != OOP_OK)
+    const bool aligned = rows_aligned(x, nb_x, T) && rows_aligned(w_gate, nb_w, F) && rows_aligned(w_up, nb_w, F);
+    if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_back_workspace_size(dh_type, x_type, w_type, ne, aligned))) != OOP_OK)
         return rc;
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    float *xf = static_cast<float *>(workspace), *wf[2] = {xf + K * T, xf + K * T + K * F}, *d[2], *out;
-    d[0] = wf[1] + K * F;
-    d[1] = d[0] + F * T;
-    out = d[1] + F * T;
-    if (F * T > 0) {
-        gate_back_kernel<<<blocks_of(F * T), 256, 0, st>>>({dh, nb_dh}, dh_type, {gate, nb_gu}, {up, nb_gu}, x_type, d[0],
-                                                           d[1], F, T, act);
-        ++g_kernel_launches;
+    cudaError_t e = cudaSuccess;
+    if (T == 0 || F == 0) {                                // sums of nothing
+        if (want_dx) e = zero_rows(dx, nb_dx, K * d_size, T, st);
+        if (want_dw && e == cudaSuccess) e = zero_rows(dw_gate, nb_dw, K * d_size, F, st);
+        if (want_dw && e == cudaSuccess) e = zero_rows(dw_up, nb_dw, K * d_size, F, st);
+        return cuda_status(e);
     }
-    cudaError_t e = cudaGetLastError();
-    const void *w[2] = {w_gate, w_up};
-    if (want_dx) {
-        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-            e = launch_to_f32(w[i], w_type, nb_w, K, F, wf[i], K, st);
-            if (e == cudaSuccess)
-                e = launch_product({d[i], wf[i], out, T, K, F, 1, F, 1, 0, 1, K, 0, K, 0, 1.f, i ? 1.f : 0.f}, st);
-        }
-        if (e != cudaSuccess) return cuda_status(e);
-        store(out, dx, dh_type, nb_dx, K, T, st);
+    const BackForms f = back_forms(dh_type, x_type, w_type, aligned);
+    char *at = static_cast<char *>(workspace);
+    const int64_t pitch = round8(F);
+    // [plane][gate, up][T][pitch]
+    pair::Operand d = {at, F, T, pitch * 2, T * pitch * 2, 2 * f.d.planes, false, false};
+    const int wide = rows_aligned(dh, nb_dh, T) && rows_aligned(gate, nb_gu, T) && rows_aligned(up, nb_gu, T);
+    const char *dp = static_cast<const char *>(dh), *gp = static_cast<const char *>(gate), *up_ = static_cast<const char *>(up);
+    if (dh_type == OOP_TYPE_F32) launch_gate_back<OOP_TYPE_F32, 3>(x_type, dp, nb_dh, gp, up_, nb_gu, at, pitch, F, T, act, wide, st);
+    else launch_gate_back<OOP_TYPE_BF16, 1>(x_type, dp, nb_dh, gp, up_, nb_gu, at, pitch, F, T, act, wide, st);
+    e = cudaGetLastError();
+    at += form_bytes(f.d, F, 2 * T);
+    auto run = [&](const pair::Spec &s) {
+        return dh_type == OOP_TYPE_F32 ? product<pair::kPlain, true>(s, status, st) : product<pair::kPlain, false>(s, status, st);
+    };
+    if (want_dx && e == cudaSuccess) {                     // [dgate dup] [Wg; Wu]: two segments of F
+        pair::Spec s = {};
+        s.a = d;
+        e = operand(f.w, w_gate, w_type, nb_w, K, F, true, at, s.b[0], st);
+        if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, true, at, s.b[1], st);
+        s.M = T, s.N = K, s.K = F;
+        s.batches = 1, s.segments = 2;
+        s.planes_a = f.d.planes, s.planes_b = f.w.planes;
+        s.a_plane = 2, s.a_seg = 1, s.b_plane = 1;
+        s.out.p0 = dx, s.out.nb0 = nb_dx, s.out.type = dh_type, s.out.alpha = 1.f;
+        s.out.wide = K * d_size % 16 == 0 && rows_aligned(dx, nb_dx, T);
+        if (e == cudaSuccess) e = run(s);
     }
-    if (want_dw) {
-        e = launch_to_f32(x, x_type, nb_x, K, T, xf, K, st);
-        void *dw[2] = {dw_gate, dw_up};
-        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-            e = launch_product({d[i], xf, out, F, K, T, 1, 1, F, 0, 1, K, 0, K, 0, 1.f, 0.f}, st);
-            if (e == cudaSuccess) store(out, dw[i], dh_type, nb_dw, K, F, st);
-        }
+    if (want_dw && e == cudaSuccess) {                     // dgate' x and dup' x: two batches
+        pair::Spec s = {};
+        s.a = d;
+        s.a.rows_contiguous = true;
+        e = operand(f.x, x, x_type, nb_x, K, T, true, at, s.b[0], st);
+        s.b[1] = s.b[0];
+        s.M = F, s.N = K, s.K = T;
+        s.batches = 2, s.segments = 1;
+        s.planes_a = f.d.planes, s.planes_b = f.x.planes;
+        s.a_plane = 2, s.a_batch = 1, s.b_plane = 1;
+        s.out.p0 = dw_gate, s.out.p1 = dw_up, s.out.nb0 = nb_dw, s.out.type = dh_type, s.out.alpha = 1.f;
+        s.out.wide = K * d_size % 16 == 0 && rows_aligned(dw_gate, nb_dw, F) && rows_aligned(dw_up, nb_dw, F);
+        if (e == cudaSuccess) e = run(s);
     }
-    return cuda_status(e == cudaSuccess ? cudaGetLastError() : e);
+    return cuda_status(e);
 }
 
 }  // extern "C"

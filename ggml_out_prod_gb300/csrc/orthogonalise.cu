@@ -9,7 +9,7 @@
 #include <cmath>
 
 #include "oop_internal.cuh"
-#include "products.cuh"
+#include "pair_product.cuh"
 #include "rows.cuh"
 
 namespace oop {
@@ -17,6 +17,13 @@ namespace {
 
 constexpr int kMaxSteps = 64;
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// The matrices between the products are held as two binary16 planes, hi + lo, of a
+// scaled value: 22 bits or more, as many as a product of three terms keeps.  The
+// scales leave room for magnitudes of 8, 64 and 256 below binary16's largest, and keep
+// the planes of a 4096 x 4096 matrix (X's elements are about 2^-12) out of its
+// subnormals.  bfloat16 planes would need no scale, but three of them and six terms.
+constexpr float kScaleX = 0x1p13f, kScaleA = 0x1p10f, kScaleQ = 0x1p8f;
 
 // Sums of squares of one thread: those of large, ordinary and small magnitudes
 // apart, scaled so that none over- or underflows.
@@ -37,53 +44,65 @@ struct Squares {
     }
 };
 
-// 1 / (|x|_F + eps) of each matrix as two factors of moderate size, by one CTA.
-__global__ void __launch_bounds__(1024) norm_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N,
-                                                    int64_t M, float eps, float2 *inv) {
+// The parts that a matrix's sum of squares is taken in: of its size alone, so that a
+// matrix gives the same bits in any batch.
+int64_t parts_of(int64_t elements) { return std::min<int64_t>(256, (elements + 16383) / 16384); }
+
+// Sum of squares of one part of each matrix (blockIdx.y).
+__global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N,
+                                                      int64_t M, double *sums) {
     __shared__ double part[32];
-    const char *p = x + blockIdx.x * nb_mat;
+    const char *p = x + blockIdx.y * nb_mat;
     Squares s;
-    for (int64_t i = threadIdx.x; i < M * N; i += 1024) {
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
         const int64_t r = i / N;
         s.add(load_any(p + r * nb_row, type, i - r * N));
     }
     const double sum = block_sum(static_cast<double>(s.big) * 0x1p140 + static_cast<double>(s.mid) +
                                      static_cast<double>(s.small) * 0x1p-140, part);
-    if (threadIdx.x == 0) {
-        int e;
-        const double v = 1.0 / (sqrt(sum) + static_cast<double>(eps));
-        const double m = frexp(v, &e);
-        const bool fine = v <= 0x1p200;                    // not Inf (zeros and eps = 0) or NaN
-        inv[blockIdx.x] = fine ? make_float2(static_cast<float>(ldexp(m, e / 2)), static_cast<float>(ldexp(1.0, e - e / 2)))
-                               : make_float2(static_cast<float>(v), 1.f);
-    }
+    if (threadIdx.x == 0) sums[blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
-__global__ void start_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N, int64_t M,
-                             const float2 *inv, float *dst) {
-    const float2 f = inv[blockIdx.y];
+// 1 / (|x|_F + eps) as two factors of moderate size, by the first warp; NaN where a value is not finite.
+__device__ __forceinline__ float2 inverse_norm(const double *sums, int parts, float eps) {
+    double sum = 0.0;
+    for (int i = threadIdx.x & 31; i < parts; i += 32) sum += sums[i];
+    sum = warp_sum(sum);
+    const double v = 1.0 / (sqrt(sum) + static_cast<double>(eps));
+    if (!(sum <= 0x1p1000)) return make_float2(__int_as_float(0x7fc00000), 1.f);
+    if (!(v <= 0x1p300)) return make_float2(static_cast<float>(v), 1.f);       // zeros and eps = 0
+    int e;
+    const double m = frexp(v, &e);
+    return make_float2(static_cast<float>(ldexp(m, e / 2)), static_cast<float>(ldexp(1.0, e - e / 2)));
+}
+
+// X_0, scaled, as planes [2][B][M][pitch]; with DIRECT (no steps) scale * X_0 to y.
+template <bool DIRECT>
+__global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N, int64_t M,
+                                                    const double *sums, int parts, float eps, __half *dst, int64_t pitch, char *y,
+                                                    int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
+    __shared__ float2 factors;
+    if (threadIdx.x < 32) {
+        const float2 f = inverse_norm(sums + static_cast<int64_t>(blockIdx.y) * parts, parts, eps);
+        if (threadIdx.x == 0) factors = f;
+    }
+    __syncthreads();
+    const float2 f = factors;
     const char *p = x + blockIdx.y * nb_mat;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
-        const int64_t r = i / N;
-        dst[blockIdx.y * M * N + i] = load_any(p + r * nb_row, type, i - r * N) * f.x * f.y;
-    }
-}
-
-// q = a I + b A + c AA over B matrices {n, n}; A in p, AA in q.
-__global__ void polynomial_kernel(const float *p, float *q, int64_t n, float a, float b, float c) {
-    const int64_t base = blockIdx.y * n * n;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n * n; i += gridDim.x * 256LL)
-        q[base + i] = (i / n == i % n ? a : 0.f) + b * p[base + i] + c * q[base + i];
-}
-
-__global__ void finish_kernel(const float *src, char *y, int type, int64_t nb_row, int64_t nb_mat, int64_t N, int64_t M,
-                              float scale) {
-    char *p = y + blockIdx.y * nb_mat;
+    const int64_t plane = gridDim.y * M * pitch;
     for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
         const int64_t r = i / N, c = i - r * N;
-        const float v = scale * src[blockIdx.y * M * N + i];
-        if (type == OOP_TYPE_F32) row_of<OOP_TYPE_F32>(p, nb_row, r)[c] = v;
-        else row_of<OOP_TYPE_BF16>(p, nb_row, r)[c] = __float2bfloat16_rn(v);
+        const float v = load_any(p + r * nb_row, type, c) * f.x * f.y;
+        if constexpr (DIRECT) {
+            char *row = y + blockIdx.y * nb_y_mat + r * nb_y;
+            if (y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[c] = scale * v;
+            else reinterpret_cast<__nv_bfloat16 *>(row)[c] = __float2bfloat16_rn(scale * v);
+        } else {
+            __half *d = dst + (blockIdx.y * M + r) * pitch + c;
+            const __half hi = __float2half_rn(v * kScaleX);
+            d[0] = hi;
+            d[plane] = __float2half_rn(v * kScaleX - __half2float(hi));
+        }
     }
 }
 
@@ -101,6 +120,48 @@ int check_matrices(const int64_t nb[2], const int64_t ne[3], int size, bool outp
     return check_row_stride(bytes, ne[2], nb[1], size, output);
 }
 
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+size_t plane_pair_bytes(int64_t cols, int64_t rows, int64_t B) {
+    return round256(static_cast<size_t>(2 * B * rows * round8(cols)) * 2);
+}
+
+// B matrices of two planes: [2][B][rows][pitch].
+struct Planes {
+    char *p;
+    int64_t cols, rows, B;
+    int64_t pitch() const { return round8(cols); }
+    int64_t matrix_bytes() const { return rows * pitch() * 2; }
+    __half *hi() const { return reinterpret_cast<__half *>(p); }
+    __half *lo() const { return reinterpret_cast<__half *>(p + B * matrix_bytes()); }
+    pair::Operand operand(bool rows_contiguous) const {
+        return {p, cols, rows, pitch() * 2, matrix_bytes(), 2 * B, rows_contiguous, true};
+    }
+};
+
+// A product of two such operands over all matrices.
+pair::Spec product_of(const Planes &a, bool a_rows, const Planes &b, bool b_rows, int64_t M, int64_t N, int64_t K) {
+    pair::Spec s = {};
+    s.a = a.operand(a_rows);
+    s.b[0] = s.b[1] = b.operand(b_rows);
+    s.M = M, s.N = N, s.K = K;
+    s.batches = static_cast<int>(a.B);
+    s.segments = 1;
+    s.planes_a = s.planes_b = 2;
+    s.a_plane = s.b_plane = static_cast<int>(a.B);
+    s.a_batch = s.b_batch = 1;
+    return s;
+}
+
+void to_planes(pair::Spec &s, const Planes &d, float alpha) {
+    s.out.p0 = d.hi();
+    s.out.p1 = d.lo();
+    s.out.nb0 = d.pitch() * 2;
+    s.out.batch = d.matrix_bytes();
+    s.out.alpha = alpha;
+}
+
 }  // namespace
 }  // namespace oop
 
@@ -111,8 +172,8 @@ extern "C" {
 size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     if (check_sizes(ne) != OOP_OK || ne[0] == 0 || ne[1] == 0 || ne[2] == 0) return 0;
     const int64_t n = std::min(ne[0], ne[1]);
-    return static_cast<size_t>(ne[2] * 8 + 255) / 256 * 256 +
-           static_cast<size_t>(ne[2]) * static_cast<size_t>(2 * ne[0] * ne[1] + 2 * n * n) * 4;
+    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(double)) +
+           2 * plane_pair_bytes(ne[0], ne[1], ne[2]) + 2 * plane_pair_bytes(n, n, ne[2]);
 }
 
 int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y, int y_type, const int64_t nb_y[2],
@@ -138,34 +199,58 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t n = std::min(M, N);
-    float2 *inv = static_cast<float2 *>(workspace);
-    float *cur = reinterpret_cast<float *>(static_cast<char *>(workspace) + (B * 8 + 255) / 256 * 256);
-    float *next = cur + B * M * N, *A = next + B * M * N, *Q = A + B * n * n;
+    const int64_t n = std::min(M, N), deep = std::max(M, N);
+    const bool tall = M > N;
+    const int parts = static_cast<int>(parts_of(M * N));
+    double *sums = static_cast<double *>(workspace);
+    char *at = static_cast<char *>(workspace) + round256(static_cast<size_t>(B * parts) * sizeof(double));
+    Planes X = {at, N, M, B}, next = {at + plane_pair_bytes(N, M, B), N, M, B};
+    const Planes A = {next.p + plane_pair_bytes(N, M, B), n, n, B}, Q = {A.p + plane_pair_bytes(n, n, B), n, n, B};
     const char *xp = static_cast<const char *>(x);
-    auto grid = [&](int64_t c) { return dim3(static_cast<unsigned>(std::min<int64_t>((c + 255) / 256, 4096)), static_cast<unsigned>(B)); };
-    norm_kernel<<<static_cast<unsigned>(B), 1024, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, eps, inv);
-    start_kernel<<<grid(M * N), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, inv, cur);
+    char *yp = static_cast<char *>(y);
+    const unsigned nb = static_cast<unsigned>(B);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((M * N + 1023) / 1024, 2048));
+    squares_kernel<<<dim3(static_cast<unsigned>(parts), nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums);
+    if (steps == 0)
+        start_kernel<true><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums, parts, eps, nullptr, 0, yp,
+                                                             y_type, nb_y[0], nb_y[1], scale);
+    else
+        start_kernel<false><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums, parts, eps, X.hi(), X.pitch(),
+                                                              nullptr, 0, 0, 0, 0.f);
     g_kernel_launches = 2;
     cudaError_t e = cudaGetLastError();
-    for (int s = 0; s < steps && e == cudaSuccess; ++s) {
-        const float *c = coefs ? coefs + 3 * s : kDefault;
-        // A[i, j] = sum over the larger side
-        const int64_t row = M <= N ? N : 1, col = M <= N ? 1 : N, deep = std::max(M, N);
-        e = launch_product({cur, cur, A, n, n, deep, B, row, col, M * N, row, col, M * N, n, n * n, 1.f, 0.f}, st);
-        if (e == cudaSuccess)
-            e = launch_product({A, A, Q, n, n, n, B, n, 1, n * n, n, 1, n * n, n, n * n, 1.f, 0.f}, st);
+    for (int i = 0; i < steps && e == cudaSuccess; ++i) {
+        const float *c = coefs ? coefs + 3 * i : kDefault;
+        pair::Spec s = product_of(X, tall, X, tall, n, n, deep);               // A = X X', or X' X
+        s.symmetric = true;
+        to_planes(s, A, kScaleA / (kScaleX * kScaleX));
+        e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         if (e != cudaSuccess) break;
-        polynomial_kernel<<<grid(n * n), 256, 0, st>>>(A, Q, n, c[0], c[1], c[2]);
-        ++g_kernel_launches;
-        if (M <= N) e = launch_product({Q, cur, next, M, N, M, B, n, 1, n * n, 1, N, M * N, N, M * N, 1.f, 0.f}, st);
-        else e = launch_product({cur, Q, next, M, N, N, B, N, 1, M * N, n, 1, n * n, N, M * N, 1.f, 0.f}, st);
-        std::swap(cur, next);
+        s = product_of(A, false, A, false, n, n, n);                           // Q = a + b A + c A A
+        s.symmetric = true;
+        to_planes(s, Q, c[2] * (kScaleQ / (kScaleA * kScaleA)));
+        s.out.c_hi = A.hi();
+        s.out.c_lo = A.lo();
+        s.out.beta = c[1] * (kScaleQ / kScaleA);
+        s.out.diag = c[0] * kScaleQ;
+        e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+        if (e != cudaSuccess) break;
+        s = tall ? product_of(X, false, Q, false, M, N, N) : product_of(Q, false, X, true, M, N, M);   // X Q, or Q X
+        if (i + 1 < steps) {
+            to_planes(s, next, 1.f / kScaleQ);
+            e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+        } else {
+            s.out.p0 = yp;
+            s.out.nb0 = nb_y[0];
+            s.out.batch = nb_y[1];
+            s.out.type = y_type;
+            s.out.alpha = scale / (kScaleQ * kScaleX);
+            s.out.wide = N * ys % 16 == 0 && is_aligned(y, 16) && (M <= 1 || nb_y[0] % 16 == 0) && (B <= 1 || nb_y[1] % 16 == 0);
+            e = pair::launch<pair::kPlain, true, 256>(s, status, st);
+        }
+        std::swap(X, next);
     }
-    if (e != cudaSuccess) return cuda_status(e);
-    finish_kernel<<<grid(M * N), 256, 0, st>>>(cur, static_cast<char *>(y), y_type, nb_y[0], nb_y[1], N, M, scale);
-    ++g_kernel_launches;
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 }  // extern "C"

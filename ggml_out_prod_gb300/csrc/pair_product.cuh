@@ -1,0 +1,618 @@
+// pair_product.cuh -- the tensor-core matrix product inside the operators of a
+// layer's training step: D[m, n] = sum_k A[m, k] B[n, k], two SMs to a tile.
+//
+// Operands are 16-bit planes (bfloat16, or binary16): a matrix of more precise
+// values is the sum of its planes, and the product the sum of the plane
+// products that matter (the terms), all in one accumulator.  Either operand may
+// lie with k or with its rows contiguous (the tensor core reads both from
+// shared memory), so no transpose is ever written.
+//
+// A cluster of two CTAs owns a tile of 256 rows of A and BN rows of B
+// (tcgen05.mma.cta_group::2: each SM holds 128 rows of A, half of B's, and 128 x BN
+// sums in its tensor memory), so a byte of B that one SM loads is used by two.  The
+// grid is persistent.  In each CTA warp 0 loads (TMA, a ring of stages of 64 k, each
+// with every plane), warp 1 of the first CTA issues the products of both, and eight
+// warps take finished sums to the epilogue while the next tile's products run
+// (two buffers of BN columns of tensor memory).
+//
+// With FOLD the sums of a few stages at a time are added up in registers: the
+// tensor core's additions cut off instead of rounding, which over a whole row of
+// f32 terms would cost more than the terms themselves keep.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "activation.cuh"
+#include "oop_internal.cuh"
+#include "rows.cuh"
+#include "tc_ptx.cuh"
+
+namespace oop {
+namespace pair {
+
+constexpr int kThreads = 384, kEpilogueWarps = 8;
+constexpr int kTileM = 256, kDepth = 64, kMaxTerms = 6, kMaxStages = 8;
+constexpr int kPlaneBytes = 128 * kDepth * 2;              // A's plane of a stage, in one CTA
+constexpr int kHeader = 1024;                              // barriers, before the stages
+constexpr int kSmem = 227 * 1024;
+
+// Where finished sums go.
+enum Epilogue {
+    kPlain,      // alpha * sum, rounded once, to a matrix
+    kGate,       // act(gate) * up, and the two themselves if they are kept
+    kSplit       // alpha * sum + beta * C + diag on the diagonal, as two binary16 planes
+};
+
+struct Out {
+    void *p0, *p1, *p2;            // matrix (p1: that of batch 1, or NULL); h, gate, up; the planes hi and lo
+    int64_t nb0, nb1, batch;       // bytes between rows of p0, of p1 and p2; between batches of p0 (and p1 for planes)
+    const __half *c_hi, *c_lo;     // kSplit: C's planes, laid out as the result's
+    float alpha, beta, diag;
+    int type, act;
+    int wide;                      // 16-byte stores are allowed
+};
+
+struct Job {
+    CUtensorMap a, b[2];
+    Out out;
+    int *status;
+    int64_t M, N;                  // kGate: N features, BN / 2 of them to a tile
+    int m_tiles, n_tiles, tiles, batches;   // tiles of a batch
+    int k_blocks, segments;        // stages of a segment; with two, b[s] and a's plane + s * a_seg
+    int planes_a, planes_b, terms;
+    int a_plane, a_batch, a_seg, b_plane, b_batch;   // third coordinates
+    int term_a[kMaxTerms], term_b[kMaxTerms];
+    int stages, stage_bytes;
+    int chunk;                     // stages of one partial sum
+    int a_rows, b_rows;            // the operand lies with its rows contiguous
+    int symmetric;                 // only tiles on and above the diagonal, mirrored
+    uint32_t idesc;
+};
+
+// ---- device ---------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The shared address of the first CTA's copy of a variable.
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(ptx::smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once every product issued so far is done.
+__device__ __forceinline__ void commit_both(const void *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+
+// Shared-memory descriptor of a plane, 128-byte swizzle.  k contiguous: rows of 64 k,
+// groups of 8 rows 1024 bytes apart.  Rows contiguous: blocks of 64 rows by 64 k, 8 KB each (the leading offset),
+// in them one k every 128 bytes (groups of 8 k 1024 bytes apart).
+__device__ __forceinline__ uint64_t plane_desc(uint32_t addr, int rows_contiguous) {
+    uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(rows_contiguous ? 8192 >> 4 : 1) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 consecutive elements of a row from column c, those below N.
+template <int TYPE>
+__device__ __forceinline__ void store_row(char *row, const float (&v)[32], int64_t c, int64_t N, int wide) {
+    constexpr int E = 16 / plain_size(TYPE);
+    auto *p = reinterpret_cast<typename Plain<TYPE>::S *>(row) + c;
+    if (wide) {                                            // N is a multiple of E then
+#pragma unroll
+        for (int i = 0; i < 32; i += E) {
+            float part[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) part[j] = v[i + j];
+            Packed<TYPE, E> w;
+            w.set(part);
+            if (c + i < N) *reinterpret_cast<typename Words<16>::T *>(p + i) = w.raw;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c + i < N) p[i] = from_float<TYPE>(v[i]);
+    }
+}
+__device__ __forceinline__ void store_row(int type, char *row, const float (&v)[32], int64_t c, int64_t N, int wide) {
+    if (type == OOP_TYPE_F32) store_row<OOP_TYPE_F32>(row, v, c, N, wide);
+    else if (type == OOP_TYPE_F16) store_row<OOP_TYPE_F16>(row, v, c, N, wide);
+    else store_row<OOP_TYPE_BF16>(row, v, c, N, wide);
+}
+
+struct Tile {
+    int m, n, z;
+};
+
+// Tile i: batches outermost, then bands of eight row tiles, so that the tiles of a
+// wave share their operands in L2.
+__device__ __forceinline__ Tile tile_of(const Job &j, int i) {
+    Tile t;
+    t.z = i / j.tiles;
+    i -= t.z * j.tiles;
+    if (j.symmetric) {                                     // row tile m has n_tiles - m tiles
+        t.m = 0;
+        for (int left = j.n_tiles; i >= left; --left) {
+            i -= left;
+            ++t.m;
+        }
+        t.n = t.m + i;
+        return t;
+    }
+    const int band = i / (8 * j.n_tiles), rest = i - band * 8 * j.n_tiles;
+    const int rows = min(8, j.m_tiles - 8 * band);
+    t.n = rest / rows;
+    t.m = 8 * band + rest - t.n * rows;
+    return t;
+}
+
+// One row's 32 sums (from column c of the tile's row r) as two binary16 planes.
+__device__ __forceinline__ void store_split(const Out &o, float (&v)[32], int64_t z, int64_t r, int64_t c, int64_t M, int64_t N,
+                                            bool mirror) {
+    const int64_t at = z * o.batch / 2, pitch = o.nb0 / 2;
+    __half hi[32], lo[32];
+    const bool in = r < M;
+    if (o.c_hi) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (in && c + i < N) {                         // whole pitches are readable
+                a = *reinterpret_cast<const uint4 *>(o.c_hi + at + r * pitch + c + i);
+                b = *reinterpret_cast<const uint4 *>(o.c_lo + at + r * pitch + c + i);
+            }
+            __half ha[8], hb[8];
+            __builtin_memcpy(ha, &a, 16);
+            __builtin_memcpy(hb, &b, 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i + j] = fmaf(o.alpha, v[i + j], o.beta * (__half2float(ha[j]) + __half2float(hb[j])));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= o.alpha;
+    }
+    if (o.diag != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c + i == r) v[i] += o.diag;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        hi[i] = __float2half_rn(v[i]);
+        lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
+    }
+    __half *ph = static_cast<__half *>(o.p0) + at, *pl = static_cast<__half *>(o.p1) + at;
+    if (in) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            if (c + i < N) {
+                uint4 w;
+                __builtin_memcpy(&w, hi + i, 16);
+                *reinterpret_cast<uint4 *>(ph + r * pitch + c + i) = w;
+                __builtin_memcpy(&w, lo + i, 16);
+                *reinterpret_cast<uint4 *>(pl + r * pitch + c + i) = w;
+            }
+        if (mirror) {                                      // lanes hold consecutive rows
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < N) {
+                    ph[(c + i) * pitch + r] = hi[i];
+                    pl[(c + i) * pitch + r] = lo[i];
+                }
+        }
+    }
+}
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2];
+    uint32_t tmem;
+    int abort;
+};
+
+template <int EPI, bool FOLD, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Job j) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    constexpr int kPlaneB = BN / 2 * kDepth * 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            ptx::mbar_init(&sh.full[i], 1);
+            ptx::mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.sums_full[i], 1);
+            ptx::mbar_init(&sh.sums_empty[i], 2 * kEpilogueWarps);
+        }
+        sh.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(&sh.tmem)),
+                     "r"(static_cast<uint32_t>(2 * BN))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
+    const uint32_t stage0 = ptx::smem_u32(smem) + kHeader;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches;
+    const int blocks = j.k_blocks * j.segments;
+    // one second, and two microseconds for every product that a wait may be for
+    const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(min(j.chunk, blocks)) * j.terms * 4;
+    bool timed_out = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (try_wait(bar, parity)) return true;
+        const uint64_t t0 = ptx::globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if (try_wait(bar, parity)) return true;
+            if ((it & 3) == 0) {
+                if (*const_cast<volatile int *>(&sh.abort)) return false;
+                if (ptx::globaltimer() - t0 > limit) {
+                    *const_cast<volatile int *>(&sh.abort) = 1;
+                    timed_out = true;
+                    return false;
+                }
+            }
+        }
+    };
+
+    if (warp == 0) {
+        if (ptx::elect_one()) {
+            ptx::prefetch_tmap(&j.a);
+            ptx::prefetch_tmap(&j.b[0]);
+            ptx::prefetch_tmap(&j.b[1]);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = first; i < total; i += step) {
+                const Tile t = tile_of(j, i);
+                const int am = t.m * kTileM + static_cast<int>(rank) * 128;
+                const int bn = EPI == kGate ? t.n * (BN / 2) : t.n * BN + static_cast<int>(rank) * (BN / 2);
+                bool ok = true;
+                for (int kb = 0; kb < blocks && ok; ++kb) {
+                    ok = wait(&sh.empty[stage], phase ^ 1);
+                    if (!ok) break;
+                    const uint32_t bar = leader_addr(&sh.full[stage]);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * j.stage_bytes);
+                    const int seg = kb >= j.k_blocks ? 1 : 0;
+                    const int k = (kb - seg * j.k_blocks) * kDepth;
+                    uint32_t dst = stage0 + stage * j.stage_bytes;
+                    for (int p = 0; p < j.planes_a; ++p, dst += kPlaneBytes) {
+                        const int z = p * j.a_plane + t.z * j.a_batch + seg * j.a_seg;
+                        if (j.a_rows) {
+                            load_3d(dst, &j.a, bar, am, k, z);
+                            load_3d(dst + 8192, &j.a, bar, am + 64, k, z);
+                        } else {
+                            load_3d(dst, &j.a, bar, k, am, z);
+                        }
+                    }
+                    const CUtensorMap *bm = &j.b[EPI == kGate ? rank : seg];
+                    for (int p = 0; p < j.planes_b; ++p, dst += kPlaneB) {
+                        const int z = p * j.b_plane + t.z * j.b_batch;
+                        if (j.b_rows) {
+#pragma unroll
+                            for (int c = 0; c < BN / 128; ++c) load_3d(dst + 8192 * c, bm, bar, bn + 64 * c, k, z);
+                        } else {
+                            load_3d(dst, bm, bar, k, bn, z);
+                        }
+                    }
+                    if (++stage == j.stages) stage = 0, phase ^= 1;
+                }
+                if (!ok) break;
+            }
+            // the last stages are read before this CTA may end
+            for (int i = 0; i < j.stages; ++i) {
+                if (!wait(&sh.empty[stage], phase ^ 1)) break;
+                if (++stage == j.stages) stage = 0, phase ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        if (ptx::elect_one()) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            const uint64_t ka = j.a_rows ? 128 : 2, kb_step = j.b_rows ? 128 : 2;      // 16 k, in 16-byte units
+            bool ok = true;
+            for (int i = first; i < total && ok; i += step) {
+                for (int kb = 0; kb < blocks && ok;) {
+                    ok = wait(&sh.sums_empty[buf], buf_phase ^ 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const int end = min(blocks, kb + j.chunk);
+                    uint32_t add = 0;
+                    for (; kb < end; ++kb) {
+                        ok = wait(&sh.full[stage], phase);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t sa = stage0 + stage * j.stage_bytes, sb = sa + j.planes_a * kPlaneBytes;
+                        for (int q = 0; q < j.terms; ++q) {
+                            const uint64_t da = plane_desc(sa + j.term_a[q] * kPlaneBytes, j.a_rows);
+                            const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB, j.b_rows);
+#pragma unroll
+                            for (int k = 0; k < kDepth / 16; ++k) {
+                                mma(tmem + buf * BN, da + k * ka, db + k * kb_step, j.idesc, add);
+                                add = 1;
+                            }
+                        }
+                        commit_both(&sh.empty[stage]);
+                        if (++stage == j.stages) stage = 0, phase ^= 1;
+                    }
+                    if (!ok) break;
+                    commit_both(&sh.sums_full[buf]);
+                    buf ^= 1;
+                    if (buf == 0) buf_phase ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t empty_bar[2] = {leader_addr(&sh.sums_empty[0]), leader_addr(&sh.sums_empty[1])};
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        constexpr int kCols = BN / 2;                      // of this warp
+        // column of piece p (32 columns): a gate's pieces come in pairs, gate and up of the same features
+        auto column = [&](int p) {
+            return EPI == kGate ? (p & 1) * (BN / 2) + half * (BN / 4) + (p >> 1) * 32 : half * kCols + p * 32;
+        };
+        bool ok = true;
+        for (int i = first; i < total && ok; i += step) {
+            const Tile t = tile_of(j, i);
+            const int64_t r = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32 + lane;
+            float sums[FOLD ? kCols / 32 : 1][32];
+            for (int kb = 0; kb < blocks; kb += j.chunk) {
+                ok = __all_sync(0xffffffffu, wait(&sh.sums_full[buf], buf_phase));
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t from = tmem + lanes + buf * BN;
+                if constexpr (FOLD) {
+#pragma unroll
+                    for (int p = 0; p < kCols / 32; ++p) {
+                        float v[32];
+                        load_sums(from + column(p), v);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) sums[p][c] = kb == 0 ? v[c] : sums[p][c] + v[c];
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(empty_bar[buf]);
+                }
+                if (!FOLD || kb + j.chunk >= blocks) {
+                    if constexpr (EPI == kGate) {
+                        const int64_t f0 = static_cast<int64_t>(t.n) * (BN / 2) + half * (BN / 4);
+#pragma unroll
+                        for (int p = 0; p < kCols / 32; p += 2) {
+                            float g[32], u[32];
+                            if constexpr (FOLD) {
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) g[c] = sums[p][c], u[c] = sums[p + 1][c];
+                            } else {
+                                load_sums(from + column(p), g);
+                                load_sums(from + column(p + 1), u);
+                                if (p + 2 == kCols / 32) {
+                                    ptx::tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) arrive_cluster(empty_bar[buf]);
+                                }
+                            }
+                            if (r < j.M) {
+                                const int64_t c = f0 + (p >> 1) * 32;
+                                if (j.out.p1) {
+                                    store_row(j.out.type, static_cast<char *>(j.out.p1) + r * j.out.nb1, g, c, j.N, j.out.wide);
+                                    store_row(j.out.type, static_cast<char *>(j.out.p2) + r * j.out.nb1, u, c, j.N, j.out.wide);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) g[k] = activation_of(j.out.act, g[k]) * u[k];
+                                store_row(j.out.type, static_cast<char *>(j.out.p0) + r * j.out.nb0, g, c, j.N, j.out.wide);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < kCols / 32; ++p) {
+                            float v[32];
+                            if constexpr (FOLD) {
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) v[c] = sums[p][c];
+                            } else {
+                                load_sums(from + column(p), v);
+                                if (p + 1 == kCols / 32) {
+                                    ptx::tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) arrive_cluster(empty_bar[buf]);
+                                }
+                            }
+                            const int64_t c = static_cast<int64_t>(t.n) * BN + column(p);
+                            if constexpr (EPI == kSplit) {
+                                store_split(j.out, v, t.z, r, c, j.M, j.N, j.symmetric && t.m != t.n);
+                            } else if (r < j.M) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
+                                char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
+                                                             : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
+                                store_row(j.out.type, base + r * j.out.nb0, v, c, j.N, j.out.wide);
+                            }
+                        }
+                    }
+                }
+                buf ^= 1;
+                if (buf == 0) buf_phase ^= 1;
+            }
+        }
+        __syncwarp();
+    }
+    if (timed_out) record_status(j.status, OOP_ERR_DEVICE_TIMEOUT);
+    __syncthreads();
+    if (sh.abort) {                                        // copies and products in flight end before the CTA does
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 50000000ull) __nanosleep(1000);
+    }
+    ptx::tc_fence_before();
+    cluster_sync();
+    ptx::tc_fence_after();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(2 * BN))
+                     : "memory");
+}
+
+// ---- host -----------------------------------------------------------------
+
+// One operand: `planes` planes of `batches` matrices of `rows` x `k`, their rows or their k contiguous.
+struct Operand {
+    const void *p;
+    int64_t inner, outer, pitch_bytes;         // contiguous extent, the other one, bytes between its lines
+    int64_t matrix_bytes, matrices;            // all planes and batches, one after the other
+    bool rows_contiguous;
+    bool half;                                 // binary16, else bfloat16
+};
+
+inline bool make_map(CUtensorMap *map, const Operand &o, int tile_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.outer),
+                                static_cast<cuuint64_t>(o.matrices)};
+    // a stride over a single line is not used, but has to be a multiple of 16
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.outer > 1 ? o.pitch_bytes : 16),
+                                   static_cast<cuuint64_t>(o.matrices > 1 ? o.matrix_bytes : 16)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(o.rows_contiguous ? 64 : tile_rows), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return fn(map, o.half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(o.p), dims,
+              strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What the caller says of a product; the rest of the Job follows.
+struct Spec {
+    Operand a, b[2];
+    int64_t M, N, K;               // K of one segment
+    int batches, segments, planes_a, planes_b;
+    int a_plane, a_batch, a_seg, b_plane, b_batch;
+    bool symmetric;
+    Out out;
+};
+
+// The terms that matter: planes i and j with i + j below the larger number of
+// planes (each plane is 2^-8, or 2^-11, of the one before).
+inline int list_terms(int pa, int pb, int (&ta)[kMaxTerms], int (&tb)[kMaxTerms]) {
+    const int top = pa > pb ? pa : pb;
+    int n = 0;
+    for (int s = top - 1; s >= 0; --s)                     // small ones first
+        for (int i = 0; i <= s; ++i)
+            if (i < pa && s - i < pb) {
+                ta[n] = i;
+                tb[n++] = s - i;
+            }
+    return n;
+}
+
+template <int EPI, bool FOLD, int BN>
+cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
+    Job j = {};
+    if (!make_map(&j.a, s.a, 128) || !make_map(&j.b[0], s.b[0], BN / 2) || !make_map(&j.b[1], s.b[1], BN / 2))
+        return cudaErrorInvalidValue;
+    j.out = s.out;
+    j.status = status;
+    j.M = s.M;
+    j.N = s.N;
+    constexpr int kTileN = EPI == kGate ? BN / 2 : BN;
+    const int64_t mt = (s.M + kTileM - 1) / kTileM, nt = (s.N + kTileN - 1) / kTileN;
+    const int64_t tiles = s.symmetric ? nt * (nt + 1) / 2 : mt * nt;
+    const int64_t blocks = (s.K + kDepth - 1) / kDepth;
+    if (tiles * s.batches > 0x7fffffffLL || blocks * s.segments > 0x7fffffffLL) return cudaErrorInvalidValue;
+    j.m_tiles = static_cast<int>(mt);
+    j.n_tiles = static_cast<int>(nt);
+    j.tiles = static_cast<int>(tiles);
+    j.batches = s.batches;
+    j.k_blocks = static_cast<int>(blocks);
+    j.segments = s.segments;
+    j.planes_a = s.planes_a;
+    j.planes_b = s.planes_b;
+    j.terms = list_terms(s.planes_a, s.planes_b, j.term_a, j.term_b);
+    j.a_plane = s.a_plane, j.a_batch = s.a_batch, j.a_seg = s.a_seg, j.b_plane = s.b_plane, j.b_batch = s.b_batch;
+    j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
+    j.stages = (kSmem - kHeader) / j.stage_bytes;
+    if (j.stages > kMaxStages) j.stages = kMaxStages;
+    // partial sums of 128 k: 48 additions of the tensor core at six terms
+    j.chunk = FOLD ? 2 : static_cast<int>(blocks * s.segments);
+    j.a_rows = s.a.rows_contiguous;
+    j.b_rows = s.b[0].rows_contiguous;
+    j.symmetric = s.symmetric;
+    const uint32_t kind = s.a.half ? 0u : 1u;
+    j.idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(j.a_rows) << 15) |
+              (static_cast<uint32_t>(j.b_rows) << 16) | (static_cast<uint32_t>(BN >> 3) << 17) |
+              (static_cast<uint32_t>(kTileM >> 4) << 24);
+    const int sms = device_sm_count();
+    int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
+    if (pairs > tiles * s.batches) pairs = tiles * s.batches;
+    const cudaError_t e = allow_smem<product_kernel<EPI, FOLD, BN>>();
+    if (e != cudaSuccess) return e;
+    product_kernel<EPI, FOLD, BN><<<static_cast<unsigned>(2 * pairs), kThreads, kHeader + j.stages * j.stage_bytes, st>>>(j);
+    ++g_kernel_launches;
+    return cudaGetLastError();
+}
+
+}  // namespace pair
+}  // namespace oop
