@@ -46,17 +46,45 @@ struct Squares {
 
 // The parts that a matrix's sum of squares is taken in: of its size alone, so that a
 // matrix gives the same bits in any batch.
-int64_t parts_of(int64_t elements) { return std::min<int64_t>(256, (elements + 16383) / 16384); }
+int64_t parts_of(int64_t elements) { return std::min<int64_t>(592, (elements + 16383) / 16384); }
+
+// A warp's unit of work: up to kSpan columns of a row.
+constexpr int kSpan = 2048;
+
+// Eight elements from column c, those from column N on 0.
+__device__ __forceinline__ void load8(const char *row, int type, int64_t c, int64_t N, bool wide, float (&v)[8]) {
+    if (wide && c + 8 <= N) {
+        if (type == OOP_TYPE_F32) {
+            float a[4], b[4];
+            load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c).get(a);
+            load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c + 4).get(b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+        } else {
+            load_stream<OOP_TYPE_BF16, 8>(reinterpret_cast<const __nv_bfloat16 *>(row) + c).get(v);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < N ? load_any(row, type, c + i) : 0.f;
+}
 
 // Sum of squares of one part of each matrix (blockIdx.y).
 __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N,
-                                                      int64_t M, double *sums) {
+                                                      int64_t M, bool wide, double *sums) {
     __shared__ double part[32];
     const char *p = x + blockIdx.y * nb_mat;
+    const int64_t spans = (N + kSpan - 1) / kSpan;
     Squares s;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
-        const int64_t r = i / N;
-        s.add(load_any(p + r * nb_row, type, i - r * N));
+    for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M * spans; i += gridDim.x * 8LL) {
+        const int64_t r = i / spans, c0 = (i - r * spans) * kSpan, end = min(N, c0 + kSpan);
+#pragma unroll 4
+        for (int64_t c = c0 + (threadIdx.x & 31) * 8; c < end; c += 256) {
+            float v[8];
+            load8(p + r * nb_row, type, c, N, wide, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s.add(v[k]);
+        }
     }
     const double sum = block_sum(static_cast<double>(s.big) * 0x1p140 + static_cast<double>(s.mid) +
                                      static_cast<double>(s.small) * 0x1p-140, part);
@@ -79,8 +107,8 @@ __device__ __forceinline__ float2 inverse_norm(const double *sums, int parts, fl
 // X_0, scaled, as planes [2][B][M][pitch]; with DIRECT (no steps) scale * X_0 to y.
 template <bool DIRECT>
 __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N, int64_t M,
-                                                    const double *sums, int parts, float eps, __half *dst, int64_t pitch, char *y,
-                                                    int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
+                                                    bool wide, const double *sums, int parts, float eps, __half *dst, int64_t pitch,
+                                                    char *y, int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
     __shared__ float2 factors;
     if (threadIdx.x < 32) {
         const float2 f = inverse_norm(sums + static_cast<int64_t>(blockIdx.y) * parts, parts, eps);
@@ -89,19 +117,37 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
     __syncthreads();
     const float2 f = factors;
     const char *p = x + blockIdx.y * nb_mat;
-    const int64_t plane = gridDim.y * M * pitch;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
-        const int64_t r = i / N, c = i - r * N;
-        const float v = load_any(p + r * nb_row, type, c) * f.x * f.y;
-        if constexpr (DIRECT) {
-            char *row = y + blockIdx.y * nb_y_mat + r * nb_y;
-            if (y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[c] = scale * v;
-            else reinterpret_cast<__nv_bfloat16 *>(row)[c] = __float2bfloat16_rn(scale * v);
-        } else {
-            __half *d = dst + (blockIdx.y * M + r) * pitch + c;
-            const __half hi = __float2half_rn(v * kScaleX);
-            d[0] = hi;
-            d[plane] = __float2half_rn(v * kScaleX - __half2float(hi));
+    const int64_t plane = gridDim.y * M * pitch, spans = (N + kSpan - 1) / kSpan;
+    for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M * spans; i += gridDim.x * 8LL) {
+        const int64_t r = i / spans, c0 = (i - r * spans) * kSpan, end = min(N, c0 + kSpan);
+#pragma unroll 4
+        for (int64_t c = c0 + (threadIdx.x & 31) * 8; c < end; c += 256) {
+            float v[8];
+            load8(p + r * nb_row, type, c, N, wide, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = v[k] * f.x * f.y;
+            if constexpr (DIRECT) {
+                char *row = y + blockIdx.y * nb_y_mat + r * nb_y;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (c + k >= N) continue;
+                    if (y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[c + k] = scale * v[k];
+                    else reinterpret_cast<__nv_bfloat16 *>(row)[c + k] = __float2bfloat16_rn(scale * v[k]);
+                }
+            } else {                                       // whole pitches
+                __half hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    hi[k] = __float2half_rn(v[k] * kScaleX);
+                    lo[k] = __float2half_rn(v[k] * kScaleX - __half2float(hi[k]));
+                }
+                __half *d = dst + (blockIdx.y * M + r) * pitch + c;
+                uint4 w;
+                __builtin_memcpy(&w, hi, 16);
+                *reinterpret_cast<uint4 *>(d) = w;
+                __builtin_memcpy(&w, lo, 16);
+                *reinterpret_cast<uint4 *>(d + plane) = w;
+            }
         }
     }
 }
@@ -209,13 +255,15 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     const char *xp = static_cast<const char *>(x);
     char *yp = static_cast<char *>(y);
     const unsigned nb = static_cast<unsigned>(B);
-    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((M * N + 1023) / 1024, 2048));
-    squares_kernel<<<dim3(static_cast<unsigned>(parts), nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums);
+    const bool wide = is_aligned(x, 16) && (M <= 1 || nb_x[0] % 16 == 0) && (B <= 1 || nb_x[1] % 16 == 0);
+    const int64_t units = M * ((N + kSpan - 1) / kSpan);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 1216));
+    squares_kernel<<<dim3(static_cast<unsigned>(parts), nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums);
     if (steps == 0)
-        start_kernel<true><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums, parts, eps, nullptr, 0, yp,
+        start_kernel<true><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums, parts, eps, nullptr, 0, yp,
                                                              y_type, nb_y[0], nb_y[1], scale);
     else
-        start_kernel<false><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, sums, parts, eps, X.hi(), X.pitch(),
+        start_kernel<false><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums, parts, eps, X.hi(), X.pitch(),
                                                               nullptr, 0, 0, 0, 0.f);
     g_kernel_launches = 2;
     cudaError_t e = cudaGetLastError();

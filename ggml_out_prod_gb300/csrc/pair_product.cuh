@@ -152,6 +152,43 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 64 columns of this warp's 32 lanes added to sums held as pairs.
+__device__ __forceinline__ void add_sums(uint32_t taddr, uint64_t *sums) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        sums[i] = ptx::add2(sums[i], ptx::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+}
+
+__device__ __forceinline__ void add_sums_32(uint32_t taddr, uint64_t *sums) {
+    float v[32];
+    load_sums(taddr, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sums[i] = ptx::add2(sums[i], ptx::pack2(v[2 * i], v[2 * i + 1]));
+}
+// 32 sums from pair i on.
+__device__ __forceinline__ void take_sums(const uint64_t *sums, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ptx::unpack2(sums[i], v[2 * i], v[2 * i + 1]);
+}
+
 // 32 consecutive elements of a row from column c, those below N.
 template <int TYPE>
 __device__ __forceinline__ void store_row(char *row, const float (&v)[32], int64_t c, int64_t N, int wide) {
@@ -320,8 +357,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         }
     };
 
-    if (warp == 0) {
-        if (ptx::elect_one()) {
+    // With FOLD the epilogue's warps need more registers than an even share: the first
+    // warpgroup gives up its own (128 * 48 + 256 * 224 of the 384 * 168 at launch).
+    if (warp < 4) {
+        if constexpr (FOLD) ptx::setmaxnreg_dec<48>();
+        if (warp == 0 && ptx::elect_one()) {
             ptx::prefetch_tmap(&j.a);
             ptx::prefetch_tmap(&j.b[0]);
             ptx::prefetch_tmap(&j.b[1]);
@@ -369,9 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 if (++stage == j.stages) stage = 0, phase ^= 1;
             }
         }
-        __syncwarp();
-    } else if (warp == 1 && rank == 0) {
-        if (ptx::elect_one()) {
+        if (warp == 1 && rank == 0 && ptx::elect_one()) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             const uint64_t ka = j.a_rows ? 128 : 2, kb_step = j.b_rows ? 128 : 2;      // 16 k, in 16-byte units
@@ -408,7 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (FOLD) ptx::setmaxnreg_inc<224>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t empty_bar[2] = {leader_addr(&sh.sums_empty[0]), leader_addr(&sh.sums_empty[1])};
@@ -423,19 +462,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile_of(j, i);
             const int64_t r = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32 + lane;
-            float sums[FOLD ? kCols / 32 : 1][32];
+            uint64_t sums[FOLD ? kCols / 2 : 1];
+            if constexpr (FOLD) {
+#pragma unroll
+                for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
+            }
             for (int kb = 0; kb < blocks; kb += j.chunk) {
                 ok = __all_sync(0xffffffffu, wait(&sh.sums_full[buf], buf_phase));
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t from = tmem + lanes + buf * BN;
                 if constexpr (FOLD) {
+                    // pieces of 64 columns; a gate's: its kCols / 2 gates, then the ups of the same features
 #pragma unroll
-                    for (int p = 0; p < kCols / 32; ++p) {
-                        float v[32];
-                        load_sums(from + column(p), v);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) sums[p][c] = kb == 0 ? v[c] : sums[p][c] + v[c];
+                    for (int p = 0; p < kCols / 64; ++p) {
+                        const int at = EPI == kGate ? p * (BN / 2) + half * (BN / 4) : half * kCols + p * 64;
+                        if constexpr (EPI == kGate && BN == 128) {
+                            add_sums_32(from + half * 32, sums);
+                            add_sums_32(from + 64 + half * 32, sums + 16);
+                        } else {
+                            add_sums(from + at, sums + 32 * p);
+                        }
                     }
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -448,8 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                         for (int p = 0; p < kCols / 32; p += 2) {
                             float g[32], u[32];
                             if constexpr (FOLD) {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) g[c] = sums[p][c], u[c] = sums[p + 1][c];
+                                take_sums(sums + p / 2 * 16, g);
+                                take_sums(sums + kCols / 4 + p / 2 * 16, u);
                             } else {
                                 load_sums(from + column(p), g);
                                 load_sums(from + column(p + 1), u);
@@ -475,8 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                         for (int p = 0; p < kCols / 32; ++p) {
                             float v[32];
                             if constexpr (FOLD) {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) v[c] = sums[p][c];
+                                take_sums(sums + 16 * p, v);
                             } else {
                                 load_sums(from + column(p), v);
                                 if (p + 1 == kCols / 32) {
@@ -595,8 +641,8 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
     j.stages = (kSmem - kHeader) / j.stage_bytes;
     if (j.stages > kMaxStages) j.stages = kMaxStages;
-    // partial sums of 128 k: 48 additions of the tensor core at six terms
-    j.chunk = FOLD ? 2 : static_cast<int>(blocks * s.segments);
+    // partial sums of 64 k, the small terms first: four additions at the sum's full size
+    j.chunk = FOLD ? 1 : static_cast<int>(blocks * s.segments);
     j.a_rows = s.a.rows_contiguous;
     j.b_rows = s.b[0].rows_contiguous;
     j.symmetric = s.symmetric;
@@ -607,8 +653,15 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     const int sms = device_sm_count();
     int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
     if (pairs > tiles * s.batches) pairs = tiles * s.batches;
-    const cudaError_t e = allow_smem<product_kernel<EPI, FOLD, BN>>();
+    cudaError_t e = allow_smem<product_kernel<EPI, FOLD, BN>>();
     if (e != cudaSuccess) return e;
+    if (FOLD) {                                            // another split would wait forever for its registers
+        static const int registers = [] {
+            cudaFuncAttributes attr = {};
+            return cudaFuncGetAttributes(&attr, product_kernel<EPI, FOLD, BN>) == cudaSuccess ? attr.numRegs : 0;
+        }();
+        if (registers != 168) return cudaErrorLaunchOutOfResources;
+    }
     product_kernel<EPI, FOLD, BN><<<static_cast<unsigned>(2 * pairs), kThreads, kHeader + j.stages * j.stage_bytes, st>>>(j);
     ++g_kernel_launches;
     return cudaGetLastError();
