@@ -15,9 +15,9 @@
 // warps take finished sums to the epilogue while the next tile's products run
 // (two buffers of BN columns of tensor memory).
 //
-// With FOLD the sums of a few stages at a time are added up in registers: the
-// tensor core's additions cut off instead of rounding, which over a whole row of
-// f32 terms would cost more than the terms themselves keep.
+// With FOLD the sums of one stage (64 k, the small terms first) at a time are
+// added up in registers: the tensor core's additions cut off instead of rounding, which over a
+// whole row of f32 terms would cost more than the terms themselves keep.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -63,7 +63,7 @@ struct Job {
     int a_plane, a_batch, a_seg, b_plane, b_batch;   // third coordinates
     int term_a[kMaxTerms], term_b[kMaxTerms];
     int stages, stage_bytes;
-    int chunk;                     // stages of one partial sum
+    int sum_blocks;                // stages of one sum in tensor memory
     int a_rows, b_rows;            // the operand lies with its rows contiguous
     int symmetric;                 // only tiles on and above the diagonal, mirrored
     uint32_t idesc;
@@ -177,11 +177,30 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, uint64_t *sums) {
         sums[i] = ptx::add2(sums[i], ptx::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
 }
 
-__device__ __forceinline__ void add_sums_32(uint32_t taddr, uint64_t *sums) {
-    float v[32];
-    load_sums(taddr, v);
+// The same of 32 gates, and of the ups of their features 64 columns further on.
+__device__ __forceinline__ void add_gates(uint32_t taddr, uint64_t *sums) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr), "r"(taddr + 64)
+        : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sums[i] = ptx::add2(sums[i], ptx::pack2(v[2 * i], v[2 * i + 1]));
+    for (int i = 0; i < 32; ++i)
+        sums[i] = ptx::add2(sums[i], ptx::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
 }
 // 32 sums from pair i on.
 __device__ __forceinline__ void take_sums(const uint64_t *sums, float (&v)[32]) {
@@ -300,7 +319,7 @@ __device__ __forceinline__ void store_split(const Out &o, float (&v)[32], int64_
 }
 
 struct Shared {
-    uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], sums_full[4], sums_empty[4];
     uint32_t tmem;
     int abort;
 };
@@ -312,12 +331,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     constexpr int kPlaneB = BN / 2 * kDepth * 2;
+    // Buffers of sums in tensor memory.  With FOLD a buffer is taken every 64 k, so four small
+    // ones hide the way from the tensor core to the registers and back better than two; a
+    // tile of 256 columns then fills two of them, from the halves of each CTA's rows of B.
+    constexpr int kBufCols = FOLD ? 128 : BN, kBuffers = FOLD ? 4 : 2, kHalves = BN / kBufCols;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             ptx::mbar_init(&sh.full[i], 1);
             ptx::mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBuffers; ++i) {
             ptx::mbar_init(&sh.sums_full[i], 1);
             ptx::mbar_init(&sh.sums_empty[i], 2 * kEpilogueWarps);
         }
@@ -326,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(&sh.tmem)),
-                     "r"(static_cast<uint32_t>(2 * BN))
+                     "r"(static_cast<uint32_t>(kBuffers * kBufCols))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -339,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches;
     const int blocks = j.k_blocks * j.segments;
     // one second, and two microseconds for every product that a wait may be for
-    const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(min(j.chunk, blocks)) * j.terms * 4;
+    const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(j.sum_blocks) * j.terms * 4;
     bool timed_out = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         if (try_wait(bar, parity)) return true;
@@ -415,13 +438,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             const uint64_t ka = j.a_rows ? 128 : 2, kb_step = j.b_rows ? 128 : 2;      // 16 k, in 16-byte units
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
-                for (int kb = 0; kb < blocks && ok;) {
+                if constexpr (FOLD) {
+                    for (int kb = 0; kb < blocks && ok; ++kb) {
+                        ok = wait(&sh.full[stage], phase);
+                        const uint32_t sa = stage0 + stage * j.stage_bytes, sb = sa + j.planes_a * kPlaneBytes;
+                        for (int h = 0; h < kHalves && ok; ++h) {
+                            ok = wait(&sh.sums_empty[buf], buf_phase ^ 1);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            uint32_t add = 0;
+                            for (int q = 0; q < j.terms; ++q) {
+                                const uint64_t da = plane_desc(sa + j.term_a[q] * kPlaneBytes, j.a_rows);
+                                const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB + h * 8192, j.b_rows);
+#pragma unroll
+                                for (int k = 0; k < kDepth / 16; ++k) {
+                                    mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, j.idesc, add);
+                                    add = 1;
+                                }
+                            }
+                            commit_both(&sh.sums_full[buf]);
+                            if (++buf == kBuffers) buf = 0, buf_phase ^= 1;
+                        }
+                        if (!ok) break;
+                        commit_both(&sh.empty[stage]);
+                        if (++stage == j.stages) stage = 0, phase ^= 1;
+                    }
+                } else {
                     ok = wait(&sh.sums_empty[buf], buf_phase ^ 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const int end = min(blocks, kb + j.chunk);
                     uint32_t add = 0;
-                    for (; kb < end; ++kb) {
+                    for (int kb = 0; kb < blocks; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         if (!ok) break;
                         ptx::tc_fence_after();
@@ -431,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                             const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB, j.b_rows);
 #pragma unroll
                             for (int k = 0; k < kDepth / 16; ++k) {
-                                mma(tmem + buf * BN, da + k * ka, db + k * kb_step, j.idesc, add);
+                                mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, j.idesc, add);
                                 add = 1;
                             }
                         }
@@ -440,8 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     }
                     if (!ok) break;
                     commit_both(&sh.sums_full[buf]);
-                    buf ^= 1;
-                    if (buf == 0) buf_phase ^= 1;
+                    if (++buf == kBuffers) buf = 0, buf_phase ^= 1;
                 }
             }
         }
@@ -450,102 +496,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         if constexpr (FOLD) ptx::setmaxnreg_inc<224>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t empty_bar[2] = {leader_addr(&sh.sums_empty[0]), leader_addr(&sh.sums_empty[1])};
+        const uint32_t empty_bar = leader_addr(&sh.sums_empty[0]);
         int buf = 0;
         uint32_t buf_phase = 0;
         constexpr int kCols = BN / 2;                      // of this warp
-        // column of piece p (32 columns): a gate's pieces come in pairs, gate and up of the same features
-        auto column = [&](int p) {
-            return EPI == kGate ? (p & 1) * (BN / 2) + half * (BN / 4) + (p >> 1) * 32 : half * kCols + p * 32;
-        };
         bool ok = true;
+        auto sums_ready = [&] {
+            ok = __all_sync(0xffffffffu, wait(&sh.sums_full[buf], buf_phase));
+            if (ok) ptx::tc_fence_after();
+            return ok;
+        };
+        auto sums_taken = [&] {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(empty_bar + 8 * buf);
+            if (++buf == kBuffers) buf = 0, buf_phase ^= 1;
+        };
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile_of(j, i);
             const int64_t r = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32 + lane;
-            uint64_t sums[FOLD ? kCols / 2 : 1];
+            // a gate's pieces: the gates and ups of 32 features
+            auto gate = [&](float (&g)[32], float (&u)[32], int64_t f) {
+                if (r >= j.M) return;
+                if (j.out.p1) {
+                    store_row(j.out.type, static_cast<char *>(j.out.p1) + r * j.out.nb1, g, f, j.N, j.out.wide);
+                    store_row(j.out.type, static_cast<char *>(j.out.p2) + r * j.out.nb1, u, f, j.N, j.out.wide);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) g[k] = activation_of(j.out.act, g[k]) * u[k];
+                store_row(j.out.type, static_cast<char *>(j.out.p0) + r * j.out.nb0, g, f, j.N, j.out.wide);
+            };
+            auto plain = [&](float (&v)[32], int64_t c) {
+                if constexpr (EPI == kSplit) {
+                    store_split(j.out, v, t.z, r, c, j.M, j.N, j.symmetric && t.m != t.n);
+                } else if (r < j.M) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
+                    char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
+                                                 : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
+                    store_row(j.out.type, base + r * j.out.nb0, v, c, j.N, j.out.wide);
+                }
+            };
             if constexpr (FOLD) {
+                uint64_t sums[kCols / 2];                  // of each half: 64 columns, or 32 gates and 32 ups
 #pragma unroll
                 for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
-            }
-            for (int kb = 0; kb < blocks; kb += j.chunk) {
-                ok = __all_sync(0xffffffffu, wait(&sh.sums_full[buf], buf_phase));
+                for (int kb = 0; kb < blocks && ok; ++kb) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        if (!sums_ready()) break;
+                        const uint32_t from = tmem + lanes + buf * kBufCols;
+                        if constexpr (EPI == kGate) add_gates(from + half * 32, sums + 32 * h);
+                        else add_sums(from + half * 64, sums + 32 * h);
+                        sums_taken();
+                    }
+                }
                 if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t from = tmem + lanes + buf * BN;
-                if constexpr (FOLD) {
-                    // pieces of 64 columns; a gate's: its kCols / 2 gates, then the ups of the same features
 #pragma unroll
-                    for (int p = 0; p < kCols / 64; ++p) {
-                        const int at = EPI == kGate ? p * (BN / 2) + half * (BN / 4) : half * kCols + p * 64;
-                        if constexpr (EPI == kGate && BN == 128) {
-                            add_sums_32(from + half * 32, sums);
-                            add_sums_32(from + 64 + half * 32, sums + 16);
-                        } else {
-                            add_sums(from + at, sums + 32 * p);
-                        }
-                    }
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(empty_bar[buf]);
-                }
-                if (!FOLD || kb + j.chunk >= blocks) {
+                for (int p = 0; p < kCols / 32; ++p) {
+                    float v[32], u[32];
+                    take_sums(sums + 16 * p, v);
                     if constexpr (EPI == kGate) {
-                        const int64_t f0 = static_cast<int64_t>(t.n) * (BN / 2) + half * (BN / 4);
-#pragma unroll
-                        for (int p = 0; p < kCols / 32; p += 2) {
-                            float g[32], u[32];
-                            if constexpr (FOLD) {
-                                take_sums(sums + p / 2 * 16, g);
-                                take_sums(sums + kCols / 4 + p / 2 * 16, u);
-                            } else {
-                                load_sums(from + column(p), g);
-                                load_sums(from + column(p + 1), u);
-                                if (p + 2 == kCols / 32) {
-                                    ptx::tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) arrive_cluster(empty_bar[buf]);
-                                }
-                            }
-                            if (r < j.M) {
-                                const int64_t c = f0 + (p >> 1) * 32;
-                                if (j.out.p1) {
-                                    store_row(j.out.type, static_cast<char *>(j.out.p1) + r * j.out.nb1, g, c, j.N, j.out.wide);
-                                    store_row(j.out.type, static_cast<char *>(j.out.p2) + r * j.out.nb1, u, c, j.N, j.out.wide);
-                                }
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) g[k] = activation_of(j.out.act, g[k]) * u[k];
-                                store_row(j.out.type, static_cast<char *>(j.out.p0) + r * j.out.nb0, g, c, j.N, j.out.wide);
-                            }
-                        }
+                        if (p & 1) continue;
+                        take_sums(sums + 16 * p + 16, u);
+                        gate(v, u, static_cast<int64_t>(t.n) * (BN / 2) + p * 32 + half * 32);
                     } else {
-#pragma unroll
-                        for (int p = 0; p < kCols / 32; ++p) {
-                            float v[32];
-                            if constexpr (FOLD) {
-                                take_sums(sums + 16 * p, v);
-                            } else {
-                                load_sums(from + column(p), v);
-                                if (p + 1 == kCols / 32) {
-                                    ptx::tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) arrive_cluster(empty_bar[buf]);
-                                }
-                            }
-                            const int64_t c = static_cast<int64_t>(t.n) * BN + column(p);
-                            if constexpr (EPI == kSplit) {
-                                store_split(j.out, v, t.z, r, c, j.M, j.N, j.symmetric && t.m != t.n);
-                            } else if (r < j.M) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
-                                char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
-                                                             : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
-                                store_row(j.out.type, base + r * j.out.nb0, v, c, j.N, j.out.wide);
-                            }
-                        }
+                        plain(v, static_cast<int64_t>(t.n) * BN + half * kCols + p * 32);
                     }
                 }
-                buf ^= 1;
-                if (buf == 0) buf_phase ^= 1;
+            } else {
+                if (!sums_ready()) break;
+                const uint32_t from = tmem + lanes + buf * kBufCols;
+                if constexpr (EPI == kGate) {
+                    const int at = half * (BN / 4);
+#pragma unroll
+                    for (int p = 0; p < BN / 4; p += 32) {
+                        float g[32], u[32];
+                        load_sums(from + at + p, g);
+                        load_sums(from + BN / 2 + at + p, u);
+                        if (p + 32 == BN / 4) sums_taken();
+                        gate(g, u, static_cast<int64_t>(t.n) * (BN / 2) + at + p);
+                    }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < kCols; p += 32) {
+                        float v[32];
+                        load_sums(from + half * kCols + p, v);
+                        if (p + 32 == kCols) sums_taken();
+                        plain(v, static_cast<int64_t>(t.n) * BN + half * kCols + p);
+                    }
+                }
             }
         }
         __syncwarp();
@@ -560,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     cluster_sync();
     ptx::tc_fence_after();
     if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(2 * BN))
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kBuffers * kBufCols))
                      : "memory");
 }
 
@@ -641,14 +681,13 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
     j.stages = (kSmem - kHeader) / j.stage_bytes;
     if (j.stages > kMaxStages) j.stages = kMaxStages;
-    // partial sums of 64 k, the small terms first: four additions at the sum's full size
-    j.chunk = FOLD ? 1 : static_cast<int>(blocks * s.segments);
+    j.sum_blocks = FOLD ? 1 : static_cast<int>(blocks * s.segments);
     j.a_rows = s.a.rows_contiguous;
     j.b_rows = s.b[0].rows_contiguous;
     j.symmetric = s.symmetric;
     const uint32_t kind = s.a.half ? 0u : 1u;
     j.idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(j.a_rows) << 15) |
-              (static_cast<uint32_t>(j.b_rows) << 16) | (static_cast<uint32_t>(BN >> 3) << 17) |
+              (static_cast<uint32_t>(j.b_rows) << 16) | (static_cast<uint32_t>((FOLD ? 128 : BN) >> 3) << 17) |
               (static_cast<uint32_t>(kTileM >> 4) << 24);
     const int sms = device_sm_count();
     int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
