@@ -85,8 +85,10 @@ __device__ __forceinline__ uint32_t leader_addr(const void *p) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(ptx::smem_u32(p)));
     return r;
 }
+// No memory is handed over with it (the tcgen05 fences order tensor memory), so the
+// plain form does: releasing to the cluster costs about a thousand cycles.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z) {
     asm volatile(
@@ -110,18 +112,6 @@ __device__ __forceinline__ void commit_both(const void *bar) {
         "h"(static_cast<uint16_t>(3))
         : "memory");
 }
-__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    return ok != 0;
-}
-
 // Shared-memory descriptor of a plane, 128-byte swizzle.  k contiguous: rows of 64 k,
 // groups of 8 rows 1024 bytes apart.  Rows contiguous: blocks of 64 rows by 64 k, 8 KB each (the leading offset),
 // in them one k every 128 bytes (groups of 8 k 1024 bytes apart).
@@ -365,10 +355,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(j.sum_blocks) * j.terms * 4;
     bool timed_out = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (try_wait(bar, parity)) return true;
+        if (ptx::mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = ptx::globaltimer();
         for (uint32_t it = 1;; ++it) {
-            if (try_wait(bar, parity)) return true;
+            if (ptx::mbar_try_wait(bar, parity)) return true;
             if ((it & 3) == 0) {
                 if (*const_cast<volatile int *>(&sh.abort)) return false;
                 if (ptx::globaltimer() - t0 > limit) {
