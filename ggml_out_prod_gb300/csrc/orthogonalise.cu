@@ -275,7 +275,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         if (e != cudaSuccess) break;
         s = product_of(A, false, A, false, n, n, n);                           // Q = a + b A + c A A
-        s.symmetric = true;
+        s.symmetric = s.a_half = s.b_half = true;
         to_planes(s, Q, c[2] * (kScaleQ / (kScaleA * kScaleA)));
         s.out.c_hi = A.hi();
         s.out.c_lo = A.lo();
@@ -284,6 +284,8 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         if (e != cudaSuccess) break;
         s = tall ? product_of(X, false, Q, false, M, N, N) : product_of(Q, false, X, true, M, N, M);   // X Q, or Q X
+        s.a_half = !tall;
+        s.b_half = tall;
         if (i + 1 < steps) {
             to_planes(s, next, 1.f / kScaleQ);
             e = pair::launch<pair::kSplit, true, 256>(s, status, st);

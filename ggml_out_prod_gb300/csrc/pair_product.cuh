@@ -34,6 +34,7 @@ constexpr int kThreads = 384, kEpilogueWarps = 8;
 constexpr int kTileM = 256, kDepth = 64, kMaxTerms = 6, kMaxStages = 8;
 constexpr int kPlaneBytes = 128 * kDepth * 2;              // A's plane of a stage, in one CTA
 constexpr int kHeader = 1024;                              // barriers, before the stages
+constexpr int kOutBytes = 4096;                            // of each epilogue warp, behind the stages
 constexpr int kSmem = 227 * 1024;
 
 // Where finished sums go.
@@ -54,6 +55,7 @@ struct Out {
 
 struct Job {
     CUtensorMap a, b[2];
+    CUtensorMap a_turned, b_turned;   // a_half, b_half: the same matrix with its rows as k
     Out out;
     int *status;
     int64_t M, N;                  // kGate: N features, BN / 2 of them to a tile
@@ -65,7 +67,8 @@ struct Job {
     int stages, stage_bytes;
     int sum_blocks;                // stages of one sum in tensor memory
     int a_rows, b_rows;            // the operand lies with its rows contiguous
-    int symmetric;                 // only tiles on and above the diagonal, mirrored
+    int symmetric;                 // only tiles on and above the diagonal
+    int a_half, b_half;            // the operand is a result of that kind
     uint32_t idesc;
 };
 
@@ -198,31 +201,54 @@ __device__ __forceinline__ void take_sums(const uint64_t *sums, float (&v)[32]) 
     for (int i = 0; i < 16; ++i) ptx::unpack2(sums[i], v[2 * i], v[2 * i + 1]);
 }
 
-// 32 consecutive elements of a row from column c, those below N.
+// 32 columns of the warp's 32 rows (a lane's row each) to memory: `row` is the first one's, from
+// column c on; `rows` and `cols` of them exist.  A lane's row goes through the
+// warp's part of shared memory, so that a store covers whole 64- or 128-byte pieces of few
+// rows instead of 16 bytes of 32 (the XOR keeps both sides free of bank conflicts).
 template <int TYPE>
-__device__ __forceinline__ void store_row(char *row, const float (&v)[32], int64_t c, int64_t N, int wide) {
-    constexpr int E = 16 / plain_size(TYPE);
-    auto *p = reinterpret_cast<typename Plain<TYPE>::S *>(row) + c;
-    if (wide) {                                            // N is a multiple of E then
-#pragma unroll
-        for (int i = 0; i < 32; i += E) {
-            float part[E];
-#pragma unroll
-            for (int j = 0; j < E; ++j) part[j] = v[i + j];
-            Packed<TYPE, E> w;
-            w.set(part);
-            if (c + i < N) *reinterpret_cast<typename Words<16>::T *>(p + i) = w.raw;
-        }
-    } else {
+__device__ __forceinline__ void store_block(uint8_t *stage, const float (&v)[32], char *row, int64_t nb, int64_t rows,
+                                            int64_t cols, int wide) {
+    constexpr int kSize = plain_size(TYPE), E = 16 / kSize, kPieces = 32 / E;
+    const int lane = threadIdx.x & 31;
+    if (!wide) {
+        if (lane >= rows) return;
+        auto *p = reinterpret_cast<typename Plain<TYPE>::S *>(row + lane * nb);
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (c + i < N) p[i] = from_float<TYPE>(v[i]);
+            if (i < cols) p[i] = from_float<TYPE>(v[i]);
+        return;
+    }
+    auto place = [&](int r, int piece) {
+        return stage + r * (32 * kSize) + ((piece ^ (kPieces == 8 ? r & 7 : r >> 1 & 3)) * 16);
+    };
+    __syncwarp();                                          // the last block is out of the stage
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        float part[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) part[i] = v[k * E + i];
+        Packed<TYPE, E> w;
+        w.set(part);
+        *reinterpret_cast<typename Words<16>::T *>(place(lane, k)) = w.raw;
+    }
+    __syncwarp();
+    const int piece = lane % kPieces, first = lane / kPieces;
+    uint4 w[kPieces];                                      // all of them before the first store, which the compiler could not pass
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) w[i] = *reinterpret_cast<const uint4 *>(place(i * (32 / kPieces) + first, piece));
+    if (piece * E < cols) {                                // cols is a multiple of E
+        char *p = row + first * nb + piece * 16;
+        const int64_t step = nb * (32 / kPieces);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i, p += step)
+            if (i * (32 / kPieces) + first < rows) *reinterpret_cast<uint4 *>(p) = w[i];
     }
 }
-__device__ __forceinline__ void store_row(int type, char *row, const float (&v)[32], int64_t c, int64_t N, int wide) {
-    if (type == OOP_TYPE_F32) store_row<OOP_TYPE_F32>(row, v, c, N, wide);
-    else if (type == OOP_TYPE_F16) store_row<OOP_TYPE_F16>(row, v, c, N, wide);
-    else store_row<OOP_TYPE_BF16>(row, v, c, N, wide);
+__device__ __forceinline__ void store_block(int type, uint8_t *stage, const float (&v)[32], char *row, int64_t nb, int64_t rows,
+                                            int64_t cols, int wide) {
+    if (type == OOP_TYPE_F32) store_block<OOP_TYPE_F32>(stage, v, row, nb, rows, cols, wide);
+    else if (type == OOP_TYPE_F16) store_block<OOP_TYPE_F16>(stage, v, row, nb, rows, cols, wide);
+    else store_block<OOP_TYPE_BF16>(stage, v, row, nb, rows, cols, wide);
 }
 
 struct Tile {
@@ -251,11 +277,16 @@ __device__ __forceinline__ Tile tile_of(const Job &j, int i) {
     return t;
 }
 
-// One row's 32 sums (from column c of the tile's row r) as two binary16 planes.
-__device__ __forceinline__ void store_split(const Out &o, float (&v)[32], int64_t z, int64_t r, int64_t c, int64_t M, int64_t N,
-                                            bool mirror) {
-    const int64_t at = z * o.batch / 2, pitch = o.nb0 / 2;
-    __half hi[32], lo[32];
+// Whether a symmetric matrix of which only the tiles on and above the diagonal exist has to be
+// read as its transpose at k of row tile `tile`: then the tensor core takes the mirrored
+// tile with its rows contiguous, and nothing is ever mirrored in memory.
+__device__ __forceinline__ int below(int half, int k, int tile) { return half && k / kTileM < tile; }
+
+// 32 columns (from c) of the warp's rows (from r0) as two binary16 planes.
+__device__ __forceinline__ void store_split(uint8_t *stage, const Out &o, float (&v)[32], int64_t z, int64_t r0, int64_t c, int64_t M,
+                                            int64_t N) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = z * o.batch / 2, pitch = o.nb0 / 2, r = r0 + lane;
     const bool in = r < M;
     if (o.c_hi) {
 #pragma unroll
@@ -281,30 +312,13 @@ __device__ __forceinline__ void store_split(const Out &o, float (&v)[32], int64_
         for (int i = 0; i < 32; ++i)
             if (c + i == r) v[i] += o.diag;
     }
+    __half *planes[2] = {static_cast<__half *>(o.p0) + at, static_cast<__half *>(o.p1) + at};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        hi[i] = __float2half_rn(v[i]);
-        lo[i] = __float2half_rn(v[i] - __half2float(hi[i]));
-    }
-    __half *ph = static_cast<__half *>(o.p0) + at, *pl = static_cast<__half *>(o.p1) + at;
-    if (in) {
+    for (int p = 0; p < 2; ++p) {
+        // whole pitches are writable
+        store_block<OOP_TYPE_F16>(stage, v, reinterpret_cast<char *>(planes[p] + r0 * pitch + c), o.nb0, M - r0, (N - c + 7) / 8 * 8, 1);
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            if (c + i < N) {
-                uint4 w;
-                __builtin_memcpy(&w, hi + i, 16);
-                *reinterpret_cast<uint4 *>(ph + r * pitch + c + i) = w;
-                __builtin_memcpy(&w, lo + i, 16);
-                *reinterpret_cast<uint4 *>(pl + r * pitch + c + i) = w;
-            }
-        if (mirror) {                                      // lanes hold consecutive rows
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (c + i < N) {
-                    ph[(c + i) * pitch + r] = hi[i];
-                    pl[(c + i) * pitch + r] = lo[i];
-                }
-        }
+        for (int i = 0; i < 32; ++i) v[i] -= __half2float(__float2half_rn(v[i]));
     }
 }
 
@@ -392,20 +406,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * j.stage_bytes);
                     const int seg = kb >= j.k_blocks ? 1 : 0;
                     const int k = (kb - seg * j.k_blocks) * kDepth;
+                    const bool a_turned = below(j.a_half, k, t.m), b_turned = below(j.b_half, k, t.n);
                     uint32_t dst = stage0 + stage * j.stage_bytes;
                     for (int p = 0; p < j.planes_a; ++p, dst += kPlaneBytes) {
                         const int z = p * j.a_plane + t.z * j.a_batch + seg * j.a_seg;
-                        if (j.a_rows) {
-                            load_3d(dst, &j.a, bar, am, k, z);
-                            load_3d(dst + 8192, &j.a, bar, am + 64, k, z);
+                        if (j.a_rows || a_turned) {
+                            const CUtensorMap *am_map = a_turned ? &j.a_turned : &j.a;
+                            load_3d(dst, am_map, bar, am, k, z);
+                            load_3d(dst + 8192, am_map, bar, am + 64, k, z);
                         } else {
                             load_3d(dst, &j.a, bar, k, am, z);
                         }
                     }
-                    const CUtensorMap *bm = &j.b[EPI == kGate ? rank : seg];
+                    const CUtensorMap *bm = b_turned ? &j.b_turned : &j.b[EPI == kGate ? rank : seg];
                     for (int p = 0; p < j.planes_b; ++p, dst += kPlaneB) {
                         const int z = p * j.b_plane + t.z * j.b_batch;
-                        if (j.b_rows) {
+                        if (j.b_rows || b_turned) {
 #pragma unroll
                             for (int c = 0; c < BN / 128; ++c) load_3d(dst + 8192 * c, bm, bar, bn + 64 * c, k, z);
                         } else {
@@ -425,24 +441,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         if (warp == 1 && rank == 0 && ptx::elect_one()) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
-            const uint64_t ka = j.a_rows ? 128 : 2, kb_step = j.b_rows ? 128 : 2;      // 16 k, in 16-byte units
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
                 if constexpr (FOLD) {
+                    const Tile t = tile_of(j, i);
                     for (int kb = 0; kb < blocks && ok; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         const uint32_t sa = stage0 + stage * j.stage_bytes, sb = sa + j.planes_a * kPlaneBytes;
+                        const int a_rows = j.a_rows | below(j.a_half, kb * kDepth, t.m);
+                        const int b_rows = j.b_rows | below(j.b_half, kb * kDepth, t.n);
+                        const uint64_t ka = a_rows ? 128 : 2, kb_step = b_rows ? 128 : 2;      // 16 k, in 16-byte units
+                        const uint32_t idesc = j.idesc | static_cast<uint32_t>(a_rows) << 15 | static_cast<uint32_t>(b_rows) << 16;
                         for (int h = 0; h < kHalves && ok; ++h) {
                             ok = wait(&sh.sums_empty[buf], buf_phase ^ 1);
                             if (!ok) break;
                             ptx::tc_fence_after();
                             uint32_t add = 0;
                             for (int q = 0; q < j.terms; ++q) {
-                                const uint64_t da = plane_desc(sa + j.term_a[q] * kPlaneBytes, j.a_rows);
-                                const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB + h * 8192, j.b_rows);
+                                const uint64_t da = plane_desc(sa + j.term_a[q] * kPlaneBytes, a_rows);
+                                const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB + h * 8192, b_rows);
 #pragma unroll
                                 for (int k = 0; k < kDepth / 16; ++k) {
-                                    mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, j.idesc, add);
+                                    mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, idesc, add);
                                     add = 1;
                                 }
                             }
@@ -453,7 +473,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                         commit_both(&sh.empty[stage]);
                         if (++stage == j.stages) stage = 0, phase ^= 1;
                     }
-                } else {
+                } else {                                   // a_half, b_half: not in this form
+                    const uint64_t ka = j.a_rows ? 128 : 2, kb_step = j.b_rows ? 128 : 2;
+                    const uint32_t idesc = j.idesc | static_cast<uint32_t>(j.a_rows) << 15 | static_cast<uint32_t>(j.b_rows) << 16;
                     ok = wait(&sh.sums_empty[buf], buf_phase ^ 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -468,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                             const uint64_t db = plane_desc(sb + j.term_b[q] * kPlaneB, j.b_rows);
 #pragma unroll
                             for (int k = 0; k < kDepth / 16; ++k) {
-                                mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, j.idesc, add);
+                                mma(tmem + buf * kBufCols, da + k * ka, db + k * kb_step, idesc, add);
                                 add = 1;
                             }
                         }
@@ -487,6 +509,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t empty_bar = leader_addr(&sh.sums_empty[0]);
+        uint8_t *stage_out = smem + kHeader + j.stages * j.stage_bytes + (warp - 4) * kOutBytes;
+        const int element = plain_size(j.out.type);
         int buf = 0;
         uint32_t buf_phase = 0;
         constexpr int kCols = BN / 2;                      // of this warp
@@ -504,27 +528,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         };
         for (int i = first; i < total && ok; i += step) {
             const Tile t = tile_of(j, i);
-            const int64_t r = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32 + lane;
+            const int64_t r0 = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32, rows = j.M - r0;
             // a gate's pieces: the gates and ups of 32 features
             auto gate = [&](float (&g)[32], float (&u)[32], int64_t f) {
-                if (r >= j.M) return;
+                if (rows <= 0 || f >= j.N) return;
+                auto put = [&](const float (&v)[32], void *p, int64_t nb) {
+                    store_block(j.out.type, stage_out, v, static_cast<char *>(p) + r0 * nb + f * element, nb, rows, j.N - f, j.out.wide);
+                };
                 if (j.out.p1) {
-                    store_row(j.out.type, static_cast<char *>(j.out.p1) + r * j.out.nb1, g, f, j.N, j.out.wide);
-                    store_row(j.out.type, static_cast<char *>(j.out.p2) + r * j.out.nb1, u, f, j.N, j.out.wide);
+                    put(g, j.out.p1, j.out.nb1);
+                    put(u, j.out.p2, j.out.nb1);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) g[k] = activation_of(j.out.act, g[k]) * u[k];
-                store_row(j.out.type, static_cast<char *>(j.out.p0) + r * j.out.nb0, g, f, j.N, j.out.wide);
+                put(g, j.out.p0, j.out.nb0);
             };
             auto plain = [&](float (&v)[32], int64_t c) {
+                if (rows <= 0 || c >= j.N) return;
                 if constexpr (EPI == kSplit) {
-                    store_split(j.out, v, t.z, r, c, j.M, j.N, j.symmetric && t.m != t.n);
-                } else if (r < j.M) {
+                    store_split(stage_out, j.out, v, t.z, r0, c, j.M, j.N);
+                } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
                     char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
                                                  : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
-                    store_row(j.out.type, base + r * j.out.nb0, v, c, j.N, j.out.wide);
+                    store_block(j.out.type, stage_out, v, base + r0 * j.out.nb0 + c * element, j.out.nb0, rows, j.N - c, j.out.wide);
                 }
             };
             if constexpr (FOLD) {
@@ -627,6 +655,7 @@ struct Spec {
     int batches, segments, planes_a, planes_b;
     int a_plane, a_batch, a_seg, b_plane, b_batch;
     bool symmetric;
+    bool a_half, b_half;           // FOLD and 256 columns only
     Out out;
 };
 
@@ -649,6 +678,14 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     Job j = {};
     if (!make_map(&j.a, s.a, 128) || !make_map(&j.b[0], s.b[0], BN / 2) || !make_map(&j.b[1], s.b[1], BN / 2))
         return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i) {
+        Operand o = i ? s.b[0] : s.a;
+        o.rows_contiguous = true;
+        if ((i ? s.b_half : s.a_half) && !make_map(i ? &j.b_turned : &j.a_turned, o, 0)) return cudaErrorInvalidValue;
+    }
+    static_assert(BN == 256 || EPI != kSplit, "symmetric results have square tiles");
+    j.a_half = s.a_half;
+    j.b_half = s.b_half;
     j.out = s.out;
     j.status = status;
     j.M = s.M;
@@ -669,15 +706,14 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.terms = list_terms(s.planes_a, s.planes_b, j.term_a, j.term_b);
     j.a_plane = s.a_plane, j.a_batch = s.a_batch, j.a_seg = s.a_seg, j.b_plane = s.b_plane, j.b_batch = s.b_batch;
     j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
-    j.stages = (kSmem - kHeader) / j.stage_bytes;
+    j.stages = (kSmem - kHeader - kEpilogueWarps * kOutBytes) / j.stage_bytes;
     if (j.stages > kMaxStages) j.stages = kMaxStages;
     j.sum_blocks = FOLD ? 1 : static_cast<int>(blocks * s.segments);
     j.a_rows = s.a.rows_contiguous;
     j.b_rows = s.b[0].rows_contiguous;
     j.symmetric = s.symmetric;
     const uint32_t kind = s.a.half ? 0u : 1u;
-    j.idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(j.a_rows) << 15) |
-              (static_cast<uint32_t>(j.b_rows) << 16) | (static_cast<uint32_t>((FOLD ? 128 : BN) >> 3) << 17) |
+    j.idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>((FOLD ? 128 : BN) >> 3) << 17) |
               (static_cast<uint32_t>(kTileM >> 4) << 24);
     const int sms = device_sm_count();
     int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
@@ -691,7 +727,7 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
         }();
         if (registers != 168) return cudaErrorLaunchOutOfResources;
     }
-    product_kernel<EPI, FOLD, BN><<<static_cast<unsigned>(2 * pairs), kThreads, kHeader + j.stages * j.stage_bytes, st>>>(j);
+    product_kernel<EPI, FOLD, BN><<<static_cast<unsigned>(2 * pairs), kThreads, kHeader + j.stages * j.stage_bytes + kEpilogueWarps * kOutBytes, st>>>(j);
     ++g_kernel_launches;
     return cudaGetLastError();
 }
