@@ -91,11 +91,9 @@ __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, i
     if (threadIdx.x == 0) sums[blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
-// 1 / (|x|_F + eps) as two factors of moderate size, by the first warp; NaN where a value is not finite.
-__device__ __forceinline__ float2 inverse_norm(const double *sums, int parts, float eps) {
-    double sum = 0.0;
-    for (int i = threadIdx.x & 31; i < parts; i += 32) sum += sums[i];
-    sum = warp_sum(sum);
+// 1 / (|x|_F + eps) as two factors of moderate size, from the sum of squares; NaN where a
+// value is not finite.
+__device__ __forceinline__ float2 inverse_norm(double sum, float eps) {
     const double v = 1.0 / (sqrt(sum) + static_cast<double>(eps));
     if (!(sum <= 0x1p1000)) return make_float2(__int_as_float(0x7fc00000), 1.f);
     if (!(v <= 0x1p300)) return make_float2(static_cast<float>(v), 1.f);       // zeros and eps = 0
@@ -111,8 +109,10 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
                                                     char *y, int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
     __shared__ float2 factors;
     if (threadIdx.x < 32) {
-        const float2 f = inverse_norm(sums + static_cast<int64_t>(blockIdx.y) * parts, parts, eps);
-        if (threadIdx.x == 0) factors = f;
+        double sum = 0.0;
+        for (int i = threadIdx.x; i < parts; i += 32) sum += sums[static_cast<int64_t>(blockIdx.y) * parts + i];
+        sum = warp_sum(sum);
+        if (threadIdx.x == 0) factors = inverse_norm(sum, eps);
     }
     __syncthreads();
     const float2 f = factors;
@@ -150,6 +150,241 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
             }
         }
     }
+}
+
+// ---- few rows -------------------------------------------------------------
+//
+// A matrix whose smaller side n is at most 64 (an adapter's): all steps in one
+// launch.  A cluster of up to eight CTAs holds X in shared memory as floats, each CTA
+// a slice of the longer side; only the n x n partial products pass between them.
+// Bound by latency: per step one exchange over the cluster, three barriers, and
+// n^2 products per column, which the CUDA cores do faster than a tile of 256 rows
+// could be loaded.  8 x 2560 in one launch instead of seventeen.
+
+constexpr int kSmallThreads = 256, kSmallCtas = 8;
+
+struct SmallArgs {
+    const char *x;
+    char *y;
+    int64_t x_row, x_mat, y_row, y_mat;          // bytes
+    int n, deep, slice, x_type, y_type, tall, steps;
+    float eps, scale;
+    float coefs[3 * kMaxSteps];
+};
+
+// Floats between columns of the slice: 16-byte units in odd number, so that
+// neighbouring threads' columns lie in different banks.
+__host__ __device__ constexpr int small_pitch(int nmax) { return nmax / 4 % 2 ? nmax : nmax + 4; }
+__host__ __device__ constexpr int small_parts(int nmax) { return nmax > 32 ? 2 : 8; }
+constexpr size_t small_fixed_bytes(int nmax) {
+    // partial products (two steps'), the warps' parts, A and Q
+    return static_cast<size_t>(2 * nmax * nmax + small_parts(nmax) * nmax * nmax + 2 * nmax * (nmax + 4)) * 4;
+}
+constexpr int small_columns(int nmax) {          // of a CTA, at most
+    return static_cast<int>((kMostSmem - 2048 - small_fixed_bytes(nmax)) / (small_pitch(nmax) * 4));
+}
+
+__device__ __forceinline__ uint32_t cta_of_cluster() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t ctas_of_cluster() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void sync_cluster() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t address_in(const void *p, uint32_t cta) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(cta));
+    return r;
+}
+__device__ __forceinline__ float load_float(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ double load_double(uint32_t addr) {
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int NMAX>
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ SmallArgs a) {
+    constexpr int kPitch = small_pitch(NMAX), kParts = small_parts(NMAX), kSquare = NMAX * NMAX, kLd = NMAX + 4;
+    constexpr int kRows = NMAX > 32 ? NMAX / 32 : 1;       // of a lane, in the products
+    constexpr int kGroups = NMAX >= 32 ? 1 : 32 / NMAX;    // columns of a warp at once
+    extern __shared__ __align__(16) float small_smem[];
+    __shared__ double reduce[32], my_sum;
+    __shared__ float2 factors;
+    float *partial = small_smem, *parts = partial + 2 * kSquare, *A = parts + kParts * kSquare, *Q = A + NMAX * kLd;
+    float *xs = Q + NMAX * kLd;
+    const uint32_t cta = cta_of_cluster(), ctas = ctas_of_cluster();
+    const int64_t matrix = blockIdx.x / ctas;
+    const int s0 = static_cast<int>(cta) * a.slice, cols = max(0, min(a.slice, a.deep - s0));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const char *x = a.x + matrix * a.x_mat;
+    char *y = a.y + matrix * a.y_mat;
+
+    Squares sq;
+    for (int i = tid; i < cols * (NMAX - a.n); i += kSmallThreads)               // rows that do not exist
+        xs[i / (NMAX - a.n) * kPitch + a.n + i % (NMAX - a.n)] = 0.f;
+    // thread i takes element i of the slice in the order of memory
+    for (int i = tid; i < cols * a.n; i += kSmallThreads) {
+        const int r = a.tall ? i % a.n : i / cols, s = a.tall ? i / a.n : i % cols;
+        const float v = a.tall ? load_any(x + static_cast<int64_t>(s0 + s) * a.x_row, a.x_type, r)
+                               : load_any(x + r * a.x_row, a.x_type, s0 + s);
+        sq.add(v);
+        xs[s * kPitch + r] = v;
+    }
+    const double sum = block_sum(static_cast<double>(sq.big) * 0x1p140 + static_cast<double>(sq.mid) +
+                                     static_cast<double>(sq.small) * 0x1p-140, reduce);
+    if (tid == 0) my_sum = sum;
+    sync_cluster();
+    if (warp == 0) {
+        double v = 0.0;
+        for (uint32_t c = 0; c < ctas; ++c) v += load_double(address_in(&my_sum, c));
+        if (lane == 0) factors = inverse_norm(v, a.eps);
+    }
+    __syncthreads();
+    const float2 f = factors;
+    for (int i = tid; i < cols * NMAX; i += kSmallThreads) {
+        float &v = xs[i / NMAX * kPitch + i % NMAX];
+        v = v * f.x * f.y;
+    }
+    for (int step = 0; step < a.steps; ++step) {
+        __syncthreads();
+        // products of rows over this CTA's columns: a lane's row(s) with every row
+        float acc[kRows][NMAX];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int j = 0; j < NMAX; ++j) acc[r][j] = 0.f;
+        const int row = lane % (NMAX < 32 ? NMAX : 32), group = lane / (NMAX < 32 ? NMAX : 32);
+        for (int s = warp * kGroups + group; s < cols; s += 8 * kGroups) {
+            const float *c = xs + s * kPitch;
+            float mine[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) mine[r] = c[row + 32 * r];
+#pragma unroll
+            for (int j = 0; j < NMAX; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(c + j);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    acc[r][j] = fmaf(mine[r], v.x, acc[r][j]);
+                    acc[r][j + 1] = fmaf(mine[r], v.y, acc[r][j + 1]);
+                    acc[r][j + 2] = fmaf(mine[r], v.z, acc[r][j + 2]);
+                    acc[r][j + 3] = fmaf(mine[r], v.w, acc[r][j + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = NMAX; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < NMAX; ++j) acc[0][j] += __shfl_xor_sync(0xffffffffu, acc[0][j], o);
+        for (int turn = 0; turn < 8 / kParts; ++turn) {    // warps turn * kParts .. share the parts
+            if (warp / kParts == turn && group == 0) {
+                float *p = parts + (warp % kParts) * kSquare;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                    for (int j = 0; j < NMAX; ++j) {
+                        float &v = p[j * NMAX + row + 32 * r];
+                        v = turn ? v + acc[r][j] : acc[r][j];
+                    }
+            }
+            __syncthreads();
+        }
+        float *mine = partial + (step & 1) * kSquare;      // two steps' apart: a slow CTA may still read the last one's
+        for (int e = tid; e < kSquare; e += kSmallThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) v += parts[p * kSquare + e];
+            mine[e] = v;
+        }
+        sync_cluster();
+        for (int e = tid; e < kSquare; e += kSmallThreads) {
+            float v = 0.f;
+#pragma unroll 8
+            for (uint32_t c = 0; c < ctas; ++c) v += load_float(address_in(mine + e, c));
+            A[e / NMAX * kLd + e % NMAX] = v;
+        }
+        __syncthreads();
+        const float *co = a.coefs + 3 * step;
+        for (int e = tid; e < kSquare; e += kSmallThreads) {
+            const int i = e / NMAX, j = e % NMAX;
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < NMAX; k += 4) {
+                const float4 p = *reinterpret_cast<const float4 *>(A + i * kLd + k), q = *reinterpret_cast<const float4 *>(A + j * kLd + k);
+                v = fmaf(p.x, q.x, fmaf(p.y, q.y, fmaf(p.z, q.z, fmaf(p.w, q.w, v))));
+            }
+            Q[i * kLd + j] = fmaf(co[2], v, fmaf(co[1], A[i * kLd + j], i == j ? co[0] : 0.f));
+        }
+        __syncthreads();
+        for (int s = tid; s < cols; s += kSmallThreads) {
+            float *c = xs + s * kPitch, v[NMAX];
+#pragma unroll
+            for (int j = 0; j < NMAX; j += 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(c + j);
+                v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
+            }
+#pragma unroll 4
+            for (int i = 0; i < NMAX; ++i) {
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < NMAX; j += 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(Q + i * kLd + j);
+                    sum0 = fmaf(q.x, v[j], fmaf(q.y, v[j + 1], sum0));
+                    sum1 = fmaf(q.z, v[j + 2], fmaf(q.w, v[j + 3], sum1));
+                }
+                c[i] = sum0 + sum1;
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < cols * a.n; i += kSmallThreads) {
+        const int r = a.tall ? i % a.n : i / cols, s = a.tall ? i / a.n : i % cols;
+        const float v = a.scale * xs[s * kPitch + r];
+        char *row = a.tall ? y + static_cast<int64_t>(s0 + s) * a.y_row : y + r * a.y_row;
+        const int64_t at = a.tall ? r : s0 + s;
+        if (a.y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[at] = v;
+        else reinterpret_cast<__nv_bfloat16 *>(row)[at] = __float2bfloat16_rn(v);
+    }
+    sync_cluster();                                        // no CTA ends while another reads its sums
+}
+
+// CTAs of a matrix's cluster, 0 where it has to go the other way: by its size alone.
+int small_ctas(int64_t n, int64_t deep) {
+    if (n > 64) return 0;
+    const int nmax = n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+    int ctas = 1;
+    // 64 columns to a CTA: fewer would not shorten the step's exchange
+    while (ctas < kSmallCtas && deep > 64LL * ctas) ctas *= 2;
+    return deep <= static_cast<int64_t>(small_columns(nmax)) * ctas ? ctas : 0;
+}
+
+template <int NMAX>
+cudaError_t launch_small(const SmallArgs &a, int ctas, int64_t matrices, cudaStream_t st) {
+    cudaError_t e = allow_smem<small_kernel<NMAX>>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas * matrices));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = small_fixed_bytes(NMAX) + static_cast<size_t>(a.slice) * small_pitch(NMAX) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    ++g_kernel_launches;
+    return cudaLaunchKernelEx(&cfg, small_kernel<NMAX>, a);
 }
 
 int check_sizes(const int64_t ne[3]) {
@@ -218,6 +453,7 @@ extern "C" {
 size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     if (check_sizes(ne) != OOP_OK || ne[0] == 0 || ne[1] == 0 || ne[2] == 0) return 0;
     const int64_t n = std::min(ne[0], ne[1]);
+    if (small_ctas(n, std::max(ne[0], ne[1]))) return 0;
     return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(double)) +
            2 * plane_pair_bytes(ne[0], ne[1], ne[2]) + 2 * plane_pair_bytes(n, n, ne[2]);
 }
@@ -240,13 +476,31 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     if (N == 0 || M == 0 || B == 0) return OOP_OK;
     if ((rc = check_pointer(x, xs)) != OOP_OK) return rc;
     if ((rc = check_pointer(y, ys)) != OOP_OK) return rc;
-    if (!workspace || workspace_bytes < oop_orthogonalise_workspace_size(ne) || !is_aligned(workspace, 256))
+    const int64_t n = std::min(M, N), deep = std::max(M, N);
+    const bool tall = M > N;
+    const int ctas = small_ctas(n, deep);
+    if (!ctas && (!workspace || workspace_bytes < oop_orthogonalise_workspace_size(ne) || !is_aligned(workspace, 256)))
         return OOP_ERR_WORKSPACE;
     int *status = nullptr;
     if ((rc = device_status_word(&status)) != OOP_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t n = std::min(M, N), deep = std::max(M, N);
-    const bool tall = M > N;
+    if (ctas) {
+        SmallArgs a = {};
+        a.x = static_cast<const char *>(x);
+        a.y = static_cast<char *>(y);
+        a.x_row = nb_x[0], a.x_mat = nb_x[1], a.y_row = nb_y[0], a.y_mat = nb_y[1];
+        a.n = static_cast<int>(n);
+        a.deep = static_cast<int>(deep);
+        a.slice = static_cast<int>((deep + ctas - 1) / ctas);
+        a.x_type = x_type, a.y_type = y_type, a.tall = tall, a.steps = steps;
+        a.eps = eps, a.scale = scale;
+        for (int i = 0; i < 3 * steps; ++i) a.coefs[i] = coefs ? coefs[i] : kDefault[i % 3];
+        const cudaError_t e = n <= 8    ? launch_small<8>(a, ctas, B, st)
+                              : n <= 16 ? launch_small<16>(a, ctas, B, st)
+                              : n <= 32 ? launch_small<32>(a, ctas, B, st)
+                                        : launch_small<64>(a, ctas, B, st);
+        return cuda_status(e);
+    }
     const int parts = static_cast<int>(parts_of(M * N));
     double *sums = static_cast<double *>(workspace);
     char *at = static_cast<char *>(workspace) + round256(static_cast<size_t>(B * parts) * sizeof(double));

@@ -154,9 +154,9 @@ def orth(L, x=P, xt=F32, nbx=(256, 4096), y=P, yt=F32, nby=(256, 4096), ne=(64, 
     (dict(nby=(256, 256)), SHAPE), (dict(nbx=(-256, 4096)), SHAPE), (dict(steps=-1), VALUE), (dict(steps=65), VALUE),
     (dict(eps=-1.0), VALUE), (dict(eps=float("nan")), VALUE), (dict(scale=float("inf")), VALUE),
     (dict(steps=1, coefs=[1.0, float("nan"), 0.0]), VALUE), (dict(x=ODD), ALIGN), (dict(y=ODD), ALIGN),
-    (dict(ws=None, ne=(64, 64, 2), nbx=(256, 16384), nby=(256, 16384)), WORKSPACE),
-    (dict(nws=64, ne=(64, 64, 2), nbx=(256, 16384), nby=(256, 16384)), WORKSPACE),
-    (dict(ws=0x10010, ne=(64, 64, 2), nbx=(256, 16384), nby=(256, 16384)), WORKSPACE), (dict(ne=(64, 16, 0)), 0),
+    (dict(ws=None, ne=(96, 80, 2), nbx=(384, 30720), nby=(384, 30720)), WORKSPACE),
+    (dict(nws=64, ne=(96, 80, 2), nbx=(384, 30720), nby=(384, 30720)), WORKSPACE),
+    (dict(ws=0x10010, ne=(96, 80, 2), nbx=(384, 30720), nby=(384, 30720)), WORKSPACE), (dict(ne=(64, 16, 0)), 0),
     (dict(ne=(64, 0, 2)), 0), (dict(ne=(0, 16, 2)), 0),
 ])
 def test_orthogonalise_refusals(L, kw, want):
@@ -165,7 +165,7 @@ def test_orthogonalise_refusals(L, kw, want):
 
 def test_orthogonalise_workspace(L):
     assert L.oop_orthogonalise_workspace_size(_i64(-1, 4, 4)) == 0 and L.oop_orthogonalise_workspace_size(None) == 0
-    assert L.oop_orthogonalise_workspace_size(_i64(64, 64, 2)) > 0
+    assert L.oop_orthogonalise_workspace_size(_i64(96, 80, 2)) > 0
 
 
 def test_python_refusals():
