@@ -71,34 +71,42 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
     a = x;
 }
 
+// The turns per position of every pair, one copy for the CTA.
+struct Steps {
+    uint64_t of[kMaxHead / 2];
+    float bad[kMaxHead / 2];         // NaN for a frequency that is not finite, else 0
+    int any_bad;
+};
+
+__device__ __forceinline__ void fill_steps(Steps &s, const Args &a) {
+    if (threadIdx.x == 0) s.any_bad = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.half; i += kThreads) {
+        const float f = a.freqs[i], bad = f * 0.f;
+        s.of[i] = bad == 0.f ? turns_of(f) : 0;
+        s.bad[i] = bad;
+        if (bad != 0.f) s.any_bad = 1;
+    }
+    __syncthreads();
+}
+
 // What a lane holds of one head: U units of two chunks.
 template <int E, int U>
 struct Lane {
     int c0[U], c1[U];                // first elements of the chunks; -1: none
-    uint64_t step[U][E];             // turns per position of the pairs
-    float bad[U][E];                 // 0, or NaN for a frequency that is not finite
+    int freq[U];                     // first frequency; -1: not rotated
 
     __device__ __forceinline__ void place(const Args &a, int lane) {
         const int g = 1 << a.group_shift, rot_units = a.half / E;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = lane + u * g;
-            c0[u] = c1[u] = -1;
-#pragma unroll
-            for (int p = 0; p < E; ++p) {
-                step[u][p] = 0;
-                bad[u][p] = 0.f;
-            }
+            c0[u] = c1[u] = freq[u] = -1;
             if (j >= a.units) continue;
             if (j < rot_units) {
                 c0[u] = a.interleaved ? 2 * E * j : E * j;
                 c1[u] = a.interleaved ? c0[u] + E : a.half + E * j;
-#pragma unroll
-                for (int p = 0; p < E; ++p) {
-                    const float f = a.freqs[E * j + p];
-                    bad[u][p] = f * 0.f;
-                    step[u][p] = bad[u][p] == 0.f ? turns_of(f) : 0;
-                }
+                freq[u] = E * j;
             } else {
                 c0[u] = 2 * a.half + 2 * E * (j - rot_units);
                 c1[u] = c0[u] + E < a.D ? c0[u] + E : -1;        // E = 1 and an odd rest
@@ -112,18 +120,29 @@ struct Values {
     float a[U][E], b[U][E];
 };
 
+// A head as it lies in memory.
 template <int TYPE, int E, int U>
-__device__ __forceinline__ void load_head(Values<E, U> &v, const char *row, const Lane<E, U> &l) {
-    using S = typename Plain<TYPE>::S;
-    const S *p = reinterpret_cast<const S *>(row);
+struct Raw {
+    Packed<TYPE, E> a[U], b[U];
+
+    __device__ __forceinline__ void load(const char *row, bool exists, const Lane<E, U> &l) {
+        using S = typename Plain<TYPE>::S;
+        const S *p = reinterpret_cast<const S *>(row);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) v.a[u][i] = v.b[u][i] = 0.f;
-        if (l.c0[u] >= 0) load_stream<TYPE, E>(p + l.c0[u]).get(v.a[u]);
-        if (l.c1[u] >= 0) load_stream<TYPE, E>(p + l.c1[u]).get(v.b[u]);
+        for (int u = 0; u < U; ++u) {
+            a[u].raw = b[u].raw = {};
+            if (exists && l.c0[u] >= 0) a[u] = load_stream<TYPE, E>(p + l.c0[u]);
+            if (exists && l.c1[u] >= 0) b[u] = load_stream<TYPE, E>(p + l.c1[u]);
+        }
     }
-}
+    __device__ __forceinline__ void get(Values<E, U> &v) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u].get(v.a[u]);
+            b[u].get(v.b[u]);
+        }
+    }
+};
 
 template <int TYPE, int E, int U>
 __device__ __forceinline__ void store_head(char *row, const Values<E, U> &v, const Lane<E, U> &l) {
@@ -148,19 +167,30 @@ __device__ __forceinline__ void load_weights(Values<E, U> &w, const Side &s, int
         }
 }
 
-// cos and sin of the token's angles; 0 turns for what is not rotated.
-template <int E, int U>
+// cos and sin of the token's angles; 0 turns for what is not rotated.  FAST: for
+// results of 16 bits, the hardware's functions, off by 2^-21 on (-pi, pi).
+template <bool FAST, int E, int U>
 __device__ __forceinline__ void angles(float (&c)[U][E], float (&s)[U][E], int64_t pos,
-                                       const Lane<E, U> &l) {
+                                       const Steps &steps, const Lane<E, U> &l) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int p = 0; p < E; ++p) {
-            const uint64_t t = static_cast<uint64_t>(pos) * l.step[u][p];
-            const int32_t half_turns = static_cast<int32_t>(t >> 32);
-            sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s[u][p], &c[u][p]);
-            s[u][p] += l.bad[u][p];
-            c[u][p] += l.bad[u][p];
+            c[u][p] = 1.f;
+            s[u][p] = 0.f;
+            if (l.freq[u] < 0) continue;
+            const uint64_t t = static_cast<uint64_t>(pos) * steps.of[l.freq[u] + p];
+            const float half_turns = static_cast<float>(static_cast<int32_t>(t >> 32));
+            if constexpr (FAST) {
+                c[u][p] = __cosf(half_turns * (3.14159265f * 0x1p-31f));
+                s[u][p] = __sinf(half_turns * (3.14159265f * 0x1p-31f));
+            } else {
+                sincospif(half_turns * 0x1p-31f, &s[u][p], &c[u][p]);
+            }
+            if (steps.any_bad) {
+                s[u][p] += steps.bad[l.freq[u] + p];
+                c[u][p] += steps.bad[l.freq[u] + p];
+            }
         }
 }
 
@@ -190,22 +220,29 @@ __device__ __forceinline__ float group_sum(float v, int group) {
 
 template <int E, int U>
 __device__ __forceinline__ float dot(const Values<E, U> &v, const Values<E, U> &w) {
-    float s = 0.f;
+    float s = 0.f, z = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < E; ++i) s += v.a[u][i] * w.a[u][i] + v.b[u][i] * w.b[u][i];
-    return s;
+        for (int i = 0; i < E; ++i) {
+            s = fmaf(v.a[u][i], w.a[u][i], s);
+            z = fmaf(v.b[u][i], w.b[u][i], z);
+        }
+    return s + z;
 }
 
 // A warp takes whole tokens, or with few tokens a share of a token's heads, and
-// its groups the heads in turn.  The first side[0].ctas CTAs work on the queries.
+// its groups the heads in turn, kAhead turns' loads before the first is used.  The first side[0].ctas CTAs
+// work on the queries.
 template <int TYPE, int E, int U>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) forward_kernel(const __grid_constant__ Args a) {
+    constexpr int kAhead = E * U <= 8 ? 4 : 1;
+    __shared__ Steps steps;
     const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
     const Side &s = a.side[which];
     const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
     const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    fill_steps(steps, a);
     Lane<E, U> l;
     l.place(a, lane & (group - 1));
     Values<E, U> w;
@@ -214,35 +251,48 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const __grid_constant
     const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
     for (int64_t item = first; item < a.T * s.splits; item += warps) {
         const int64_t t = item / s.splits;
-        const int share = static_cast<int>(item - t * s.splits);
+        const int share = static_cast<int>(item - t * s.splits), step = groups * s.splits;
+        const char *x = static_cast<const char *>(s.x) + t * s.x_tok;
+        char *y = static_cast<char *>(s.out) + t * s.out_tok;
         float c[U][E], sn[U][E];
-        angles(c, sn, a.half ? a.pos[t] : 0, l);
-        for (int h0 = share * groups; h0 < s.heads; h0 += groups * s.splits) {
-            const int h = h0 + mine;
-            Values<E, U> v = {};
-            if (h < s.heads)
-                load_head<TYPE>(v, static_cast<const char *>(s.x) + t * s.x_tok + h * s.x_head, l);
-            const float r = 1.f / sqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+        for (int h0 = share * groups; h0 < s.heads; h0 += step * kAhead) {
+            Raw<TYPE, E, U> raw[kAhead];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int k = 0; k < kAhead; ++k) {
+                const int h = h0 + k * step + mine;
+                raw[k].load(x + h * s.x_head, h < s.heads, l);
+            }
+            if (h0 == share * groups) angles<TYPE != OOP_TYPE_F32>(c, sn, a.half ? a.pos[t] : 0, steps, l);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    v.a[u][i] *= r * w.a[u][i];
-                    v.b[u][i] *= r * w.b[u][i];
-                }
-            rotate<1>(v, c, sn, a.interleaved);
-            if (h < s.heads)
-                store_head<TYPE>(static_cast<char *>(s.out) + t * s.out_tok + h * s.out_head, v, l);
+            for (int k = 0; k < kAhead; ++k) {
+                if (h0 + k * step >= s.heads) break;       // the same for the warp
+                const int h = h0 + k * step + mine;
+                Values<E, U> v;
+                raw[k].get(v);
+                const float r = rsqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        v.a[u][i] *= r * w.a[u][i];
+                        v.b[u][i] *= r * w.b[u][i];
+                    }
+                rotate<1>(v, c, sn, a.interleaved);
+                if (h < s.heads) store_head<TYPE>(y + h * s.out_head, v, l);
+            }
         }
     }
 }
 
 template <int DTYPE, int TYPE, int E, int U>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(const __grid_constant__ Args a) {
+    constexpr int kAhead = E * U <= 4 ? 4 : E * U <= 8 ? 2 : 1;
+    __shared__ Steps steps;
     const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
     const Side &s = a.side[which];
     const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
     const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    fill_steps(steps, a);
     Lane<E, U> l;
     l.place(a, lane & (group - 1));
     Values<E, U> w, dw = {};
@@ -251,41 +301,51 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const __grid_constan
     const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
     for (int64_t item = cta * (kThreads / 32) + (threadIdx.x >> 5); item < a.T * s.splits; item += warps) {
         const int64_t t = item / s.splits;
-        const int share = static_cast<int>(item - t * s.splits);
+        const int share = static_cast<int>(item - t * s.splits), step = groups * s.splits;
+        const char *xt = static_cast<const char *>(s.x) + t * s.x_tok, *dt = static_cast<const char *>(s.dy) + t * s.dy_tok;
+        char *yt = static_cast<char *>(s.out) + t * s.out_tok;
         float c[U][E], sn[U][E];
-        angles(c, sn, a.half ? a.pos[t] : 0, l);
-        for (int h0 = share * groups; h0 < s.heads; h0 += groups * s.splits) {
-            const int h = h0 + mine;
-            Values<E, U> x = {}, d = {};
-            if (h < s.heads) {
-                load_head<TYPE>(x, static_cast<const char *>(s.x) + t * s.x_tok + h * s.x_head, l);
-                load_head<DTYPE>(d, static_cast<const char *>(s.dy) + t * s.dy_tok + h * s.dy_head, l);
+        for (int h0 = share * groups; h0 < s.heads; h0 += step * kAhead) {
+            Raw<TYPE, E, U> raw_x[kAhead];
+            Raw<DTYPE, E, U> raw_d[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {             // what does not exist is 0, and adds nothing
+                const int h = h0 + k * step + mine;
+                raw_x[k].load(xt + h * s.x_head, h < s.heads, l);
+                raw_d[k].load(dt + h * s.dy_head, h < s.heads, l);
             }
-            const float r = 1.f / sqrtf(group_sum(dot(x, x), group) * a.inv_d + a.eps);
-            rotate<-1>(d, c, sn, a.interleaved);
+            if (h0 == share * groups) angles<DTYPE != OOP_TYPE_F32>(c, sn, a.half ? a.pos[t] : 0, steps, l);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int k = 0; k < kAhead; ++k) {
+                if (h0 + k * step >= s.heads) break;
+                const int h = h0 + k * step + mine;
+                Values<E, U> x, d;
+                raw_x[k].get(x);
+                raw_d[k].get(d);
+                float r = rsqrtf(group_sum(dot(x, x), group) * a.inv_d + a.eps);
+                if (h >= s.heads) r = 0.f;                 // eps = 0: not 0 * Inf
+                rotate<-1>(d, c, sn, a.interleaved);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {                      // x becomes x r, d becomes g
-                    x.a[u][i] *= r;
-                    x.b[u][i] *= r;
-                    if (h < s.heads) {
-                        dw.a[u][i] += d.a[u][i] * x.a[u][i];
-                        dw.b[u][i] += d.b[u][i] * x.b[u][i];
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {          // x becomes x r, d becomes g
+                        x.a[u][i] *= r;
+                        x.b[u][i] *= r;
+                        dw.a[u][i] = fmaf(d.a[u][i], x.a[u][i], dw.a[u][i]);
+                        dw.b[u][i] = fmaf(d.b[u][i], x.b[u][i], dw.b[u][i]);
+                        d.a[u][i] *= w.a[u][i];
+                        d.b[u][i] *= w.b[u][i];
                     }
-                    d.a[u][i] *= w.a[u][i];
-                    d.b[u][i] *= w.b[u][i];
-                }
-            const float m = group_sum(dot(d, x), group) * a.inv_d;
+                const float m = group_sum(dot(d, x), group) * a.inv_d;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    d.a[u][i] = r * (d.a[u][i] - x.a[u][i] * m);
-                    d.b[u][i] = r * (d.b[u][i] - x.b[u][i] * m);
-                }
-            if (h < s.heads)
-                store_head<DTYPE>(static_cast<char *>(s.out) + t * s.out_tok + h * s.out_head, d, l);
+                    for (int i = 0; i < E; ++i) {
+                        d.a[u][i] = r * (d.a[u][i] - x.a[u][i] * m);
+                        d.b[u][i] = r * (d.b[u][i] - x.b[u][i] * m);
+                    }
+                if (h < s.heads) store_head<DTYPE>(yt + h * s.out_head, d, l);
+            }
         }
     }
     if (!s.partial) return;
@@ -370,7 +430,7 @@ void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms) {
         while (splits < most && T * splits < 16LL * sms) ++splits;
         s.splits = static_cast<int>(splits);
         const int64_t items = (T * splits + kThreads / 32 - 1) / (kThreads / 32);
-        const int64_t share = std::max<int64_t>(1, 8LL * sms * s.heads / heads);
+        const int64_t share = std::max<int64_t>(1, 2LL * sms * s.heads / heads);     // as many as are resident
         s.ctas = static_cast<int>(std::min(items, share));
     }
 }
