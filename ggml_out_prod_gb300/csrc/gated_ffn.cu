@@ -32,6 +32,29 @@ __device__ __forceinline__ void split(float v, __nv_bfloat16 (&t)[P]) {
     }
 }
 
+// Eight aligned elements of a plain type as they lie in memory: the load alone, so
+// that several can be in flight.
+template <int TYPE>
+struct Eight {
+    static constexpr int E = 16 / plain_size(TYPE);
+    Packed<TYPE, E> part[8 / E];
+
+    __device__ __forceinline__ void load(const char *row, int64_t c) {
+        const auto *p = reinterpret_cast<const typename Plain<TYPE>::S *>(row) + c;
+#pragma unroll
+        for (int i = 0; i < 8 / E; ++i) part[i] = load_stream<TYPE, E>(p + i * E);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8 / E; ++i) {
+            float f[E];
+            part[i].get(f);
+#pragma unroll
+            for (int k = 0; k < E; ++k) v[i * E + k] = f[k];
+        }
+    }
+};
+
 // Eight elements of a row from column c, those beyond the row 0.
 template <int TYPE>
 __device__ __forceinline__ void load8(const char *row, int64_t c, int64_t cols, int wide, float (&v)[8]) {
@@ -39,14 +62,9 @@ __device__ __forceinline__ void load8(const char *row, int64_t c, int64_t cols, 
         using S = typename Plain<TYPE>::S;
         const S *p = reinterpret_cast<const S *>(row) + c;
         if (wide && c + 8 <= cols) {
-            constexpr int E = 16 / plain_size(TYPE);
-#pragma unroll
-            for (int i = 0; i < 8; i += E) {
-                float part[E];
-                load_stream<TYPE, E>(p + i).get(part);
-#pragma unroll
-                for (int k = 0; k < E; ++k) v[i + k] = part[k];
-            }
+            Eight<TYPE> e;
+            e.load(row, c);
+            e.get(v);
             return;
         }
 #pragma unroll
@@ -126,6 +144,138 @@ cudaError_t launch_planes_of(const void *src, int type, int64_t nb, int64_t cols
     return cudaGetLastError();
 }
 
+// ---- few tokens -----------------------------------------------------------
+//
+// Up to eight tokens: the weights' bytes are all there is to do, and the tensor
+// cores' tiles of 256 tokens would only be waited for.  A warp takes a feature: its
+// gate and its up row, each read once in long runs (five or six 16-byte loads of each row in flight per lane),
+// against the tokens in shared memory as floats.  Sums in fp32 on the CUDA cores, which any
+// type of weight allows without a copy.  bf16, 1 x 2560 x 9728: @FEW@.
+constexpr int kFewThreads = 512, kFewTokens = 8;
+constexpr int64_t kFewBytes = 180 * 1024;
+
+struct FewArgs {
+    const char *x, *w[2];
+    char *h, *gate, *up;
+    int64_t nb_x, nb_w, nb_h, nb_gu, K, F;
+    int T, x_type, act, wide;
+};
+
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs a) {
+    // x by eights: the first four of each eight of all tokens, then the last four, so that
+    // neighbouring lanes read neighbouring 16 bytes
+    extern __shared__ __align__(16) float few_x[];
+    const int64_t eights = (a.K + 7) / 8, half = eights * 4;
+    for (int64_t i = threadIdx.x; i < NT * eights * 8; i += kFewThreads) {
+        const int64_t t = i / (eights * 8), k = i - t * eights * 8;
+        const float v = t < a.T && k < a.K ? load_any(a.x + t * a.nb_x, a.x_type, k) : 0.f;
+        few_x[(t * 2 + (k >> 2 & 1)) * half + (k >> 3) * 4 + (k & 3)] = v;
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t f = blockIdx.x * (kFewThreads / 32) + warp; f < a.F; f += gridDim.x * (kFewThreads / 32)) {
+        uint64_t acc[2][NT] = {};                          // pairs: even and odd columns
+        const char *row[2] = {a.w[0] + f * a.nb_w, a.w[1] + f * a.nb_w};
+        auto add = [&](const float (&w)[2][8], int64_t e) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float4 v = *reinterpret_cast<const float4 *>(few_x + (t * 2 + q) * half + e * 4);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        acc[r][t] = ptx::fma2(ptx::pack2(w[r][4 * q], w[r][4 * q + 1]), ptx::pack2(v.x, v.y), acc[r][t]);
+                        acc[r][t] = ptx::fma2(ptx::pack2(w[r][4 * q + 2], w[r][4 * q + 3]), ptx::pack2(v.z, v.w), acc[r][t]);
+                    }
+                }
+            }
+        };
+        int64_t e = lane;
+        if constexpr (plain_size(TYPE) != 0) {
+            constexpr int kAhead = TYPE == OOP_TYPE_F32 ? 3 : 5;
+            for (; a.wide && e - lane + 32 * kAhead <= a.K / 8; e += 32 * kAhead) {
+                Eight<TYPE> raw[kAhead][2];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) raw[k][r].load(row[r], (e + 32 * k) * 8);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    float w[2][8];
+                    raw[k][0].get(w[0]);
+                    raw[k][1].get(w[1]);
+                    add(w, e + 32 * k);
+                }
+            }
+        }
+        for (; e < eights; e += 32) {
+            float w[2][8];
+            load8<TYPE>(row[0], e * 8, a.K, a.wide, w[0]);
+            load8<TYPE>(row[1], e * 8, a.K, a.wide, w[1]);
+            add(w, e);
+        }
+        float g = 0.f, u = 0.f;                            // lane t: token t's
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float lo, hi;
+            ptx::unpack2(acc[0][t], lo, hi);
+            const float gt = warp_sum(lo + hi);
+            ptx::unpack2(acc[1][t], lo, hi);
+            const float ut = warp_sum(lo + hi);
+            if (lane == t) g = gt, u = ut;
+        }
+        if (lane >= a.T) continue;
+        auto put = [&](char *p, int64_t nb, float v) {
+            char *row = p + lane * nb;
+            if (a.x_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[f] = v;
+            else if (a.x_type == OOP_TYPE_F16) reinterpret_cast<__half *>(row)[f] = __float2half_rn(v);
+            else reinterpret_cast<__nv_bfloat16 *>(row)[f] = __float2bfloat16_rn(v);
+        };
+        put(a.h, a.nb_h, activation_of(a.act, g) * u);
+        if (a.gate) {
+            put(a.gate, a.nb_gu, g);
+            put(a.up, a.nb_gu, u);
+        }
+    }
+}
+
+bool few_tokens(int64_t T, int64_t K, int w_type) {
+    const int64_t nt = !plain_size(w_type) ? 8 : T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
+    return T <= kFewTokens && nt * ((K + 7) / 8) * 32 <= kFewBytes;
+}
+
+template <int TYPE, int NT>
+cudaError_t launch_few(const FewArgs &a, cudaStream_t st) {
+    const cudaError_t e = allow_smem<few_kernel<TYPE, NT>>();
+    if (e != cudaSuccess) return e;
+    const int64_t per = kFewThreads / 32, ctas = std::min<int64_t>((a.F + per - 1) / per, device_sm_count());
+    few_kernel<TYPE, NT><<<static_cast<unsigned>(ctas), kFewThreads, static_cast<size_t>(NT * ((a.K + 7) / 8) * 32), st>>>(a);
+    ++g_kernel_launches;
+    return cudaGetLastError();
+}
+template <int TYPE>
+cudaError_t launch_few(const FewArgs &a, cudaStream_t st) {
+    if constexpr (plain_size(TYPE) != 0) {
+        if (a.T <= 1) return launch_few<TYPE, 1>(a, st);
+        if (a.T <= 2) return launch_few<TYPE, 2>(a, st);
+        if (a.T <= 4) return launch_few<TYPE, 4>(a, st);
+    }
+    return launch_few<TYPE, 8>(a, st);
+}
+cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
+#define OOP_CASE(T) \
+    case T: return launch_few<T>(a, st);
+    switch (w_type) {
+        OOP_CASE(OOP_TYPE_F32) OOP_CASE(OOP_TYPE_F16) OOP_CASE(OOP_TYPE_BF16) OOP_CASE(OOP_TYPE_Q4_0)
+        OOP_CASE(OOP_TYPE_Q4_1) OOP_CASE(OOP_TYPE_Q5_0) OOP_CASE(OOP_TYPE_Q5_1) OOP_CASE(OOP_TYPE_Q8_0)
+        OOP_CASE(OOP_TYPE_Q2_K) OOP_CASE(OOP_TYPE_Q3_K) OOP_CASE(OOP_TYPE_Q4_K) OOP_CASE(OOP_TYPE_Q5_K)
+        OOP_CASE(OOP_TYPE_Q6_K)
+    }
+#undef OOP_CASE
+    return cudaErrorInvalidValue;
+}
+
 // dgate and dup as P planes [P][2][T][pitch]: dgate = dh up act'(gate), dup = dh act(gate).
 template <int DTYPE, int TYPE, int P>
 __global__ void __launch_bounds__(256) gate_back_kernel(const char *dh, int64_t nb_dh, const char *gate, const char *up, int64_t nb_gu,
@@ -134,9 +284,20 @@ __global__ void __launch_bounds__(256) gate_back_kernel(const char *dh, int64_t 
     for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < T * per_row; i += gridDim.x * 256LL) {
         const int64_t t = i / per_row, c = (i - t * per_row) * 8;
         float d[8], g[8], u[8];
-        load8<DTYPE>(dh + t * nb_dh, c, F, wide, d);
-        load8<TYPE>(gate + t * nb_gu, c, F, wide, g);
-        load8<TYPE>(up + t * nb_gu, c, F, wide, u);
+        if (wide && c + 8 <= F) {
+            Eight<DTYPE> ed;
+            Eight<TYPE> eg, eu;
+            ed.load(dh + t * nb_dh, c);
+            eg.load(gate + t * nb_gu, c);
+            eu.load(up + t * nb_gu, c);
+            ed.get(d);
+            eg.get(g);
+            eu.get(u);
+        } else {
+            load8<DTYPE>(dh + t * nb_dh, c, F, 0, d);
+            load8<TYPE>(gate + t * nb_gu, c, F, 0, g);
+            load8<TYPE>(up + t * nb_gu, c, F, 0, u);
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float slope;
@@ -282,7 +443,7 @@ using namespace oop;
 extern "C" {
 
 size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3], int aligned) {
-    if (check_ffn(x_type, w_type, ne, 0) != OOP_OK) return 0;
+    if (check_ffn(x_type, w_type, ne, 0) != OOP_OK || few_tokens(ne[2], ne[0], w_type)) return 0;
     const ForwardForms f = forward_forms(x_type, w_type, aligned != 0);
     return form_bytes(f.x, ne[0], ne[2]) + 2 * form_bytes(f.w, ne[0], ne[1]);
 }
@@ -321,6 +482,13 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
         if (gate && e == cudaSuccess) e = zero_rows(gate, nb_gu, F * size, T, st);
         if (gate && e == cudaSuccess) e = zero_rows(up, nb_gu, F * size, T, st);
         return cuda_status(e);
+    }
+    if (few_tokens(T, K, w_type)) {
+        FewArgs a = {static_cast<const char *>(x), {static_cast<const char *>(w_gate), static_cast<const char *>(w_up)},
+                     static_cast<char *>(h), static_cast<char *>(gate), static_cast<char *>(up), nb_x, nb_w, nb_h, nb_gu, K, F,
+                     static_cast<int>(T), x_type, act, 0};
+        a.wide = rows_aligned(w_gate, nb_w, F) && rows_aligned(w_up, nb_w, F);
+        return cuda_status(launch_few(a, w_type, st));
     }
     const ForwardForms f = forward_forms(x_type, w_type, aligned);
     char *at = static_cast<char *>(workspace);
