@@ -240,9 +240,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
 }
 
-bool few_tokens(int64_t T, int64_t K, int w_type) {
+// Operands that the tensor cores take as they are go there from five tokens on (5120 x
+// 17408: 77 us for 4 tokens here, 131 for 8, 85 there), others have to be copied first (f32: 164, 597).
+bool few_tokens(int64_t T, int64_t K, int x_type, int w_type) {
     const int64_t nt = !plain_size(w_type) ? 8 : T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
-    return T <= kFewTokens && nt * ((K + 7) / 8) * 32 <= kFewBytes;
+    const bool native = x_type == w_type && plain_size(w_type) == 2;
+    return T <= (native ? 4 : kFewTokens) && nt * ((K + 7) / 8) * 32 <= kFewBytes;
 }
 
 template <int TYPE, int NT>
@@ -443,7 +446,7 @@ using namespace oop;
 extern "C" {
 
 size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3], int aligned) {
-    if (check_ffn(x_type, w_type, ne, 0) != OOP_OK || few_tokens(ne[2], ne[0], w_type)) return 0;
+    if (check_ffn(x_type, w_type, ne, 0) != OOP_OK || few_tokens(ne[2], ne[0], x_type, w_type)) return 0;
     const ForwardForms f = forward_forms(x_type, w_type, aligned != 0);
     return form_bytes(f.x, ne[0], ne[2]) + 2 * form_bytes(f.w, ne[0], ne[1]);
 }
@@ -483,7 +486,7 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
         if (gate && e == cudaSuccess) e = zero_rows(up, nb_gu, F * size, T, st);
         return cuda_status(e);
     }
-    if (few_tokens(T, K, w_type)) {
+    if (few_tokens(T, K, x_type, w_type)) {
         FewArgs a = {static_cast<const char *>(x), {static_cast<const char *>(w_gate), static_cast<const char *>(w_up)},
                      static_cast<char *>(h), static_cast<char *>(gate), static_cast<char *>(up), nb_x, nb_w, nb_h, nb_gu, K, F,
                      static_cast<int>(T), x_type, act, 0};
