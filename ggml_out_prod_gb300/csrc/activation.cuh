@@ -6,10 +6,11 @@
 namespace oop {
 
 // 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation.
-// exp is kept below 2^116, so that the product of the two is never Inf * 0.
-__device__ __forceinline__ float logistic(float v) { return 1.f / (1.f + expf(-v)); }
+// exp is kept below 2^116: within the fast division's range (2 ulp), and the product of the
+// two is never Inf * 0.
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + expf(fminf(-v, 80.f))); }
 __device__ __forceinline__ float logistic(float v, float &rest) {
-    const float e = expf(fminf(-v, 80.f)), s = 1.f / (1.f + e);
+    const float e = expf(fminf(-v, 80.f)), s = __fdividef(1.f, 1.f + e);
     rest = e * s;
     return v != v ? v : s;
 }
@@ -25,6 +26,9 @@ __device__ __forceinline__ float activation_of(int act, float v) {
     if (act == OOP_ACT_GELU_ERF) return v * (0.5f * erfcf(-v * 0.7071067811865476f));
     return v < 0.f ? 0.f : v;
 }
+
+// The same as a call, where its code would be repeated for every register of a row.
+static __device__ __noinline__ float activation_call(int act, float v) { return activation_of(act, v); }
 
 // The activation and its derivative.
 __device__ __forceinline__ float activation_and_slope(int act, float v, float &slope) {
