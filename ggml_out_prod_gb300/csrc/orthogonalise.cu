@@ -436,10 +436,10 @@ pair::Spec product_of(const Planes &a, bool a_rows, const Planes &b, bool b_rows
 }
 
 void to_planes(pair::Spec &s, const Planes &d, float alpha) {
-    s.out.p0 = d.hi();
-    s.out.p1 = d.lo();
+    s.result = d.operand(false);
     s.out.nb0 = d.pitch() * 2;
     s.out.batch = d.matrix_bytes();
+    s.out.planes = static_cast<int>(d.B);
     s.out.alpha = alpha;
 }
 
@@ -526,15 +526,22 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         pair::Spec s = product_of(X, tall, X, tall, n, n, deep);               // A = X X', or X' X
         s.symmetric = true;
         to_planes(s, A, kScaleA / (kScaleX * kScaleX));
+        // a + b A + c A A = c (A + b / 2c)^2 + a - b^2 / 4c: with the shift in A's diagonal Q is
+        // one product, and A need not be read again.  The shift has to be of A's size.
+        const bool square = c[2] != 0.f && std::fabs(c[1]) <= 8.f * std::fabs(c[2]);
+        const double shift = square ? 0.5 * c[1] / c[2] : 0.0;
+        s.out.diag = static_cast<float>(shift * kScaleA);
         e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         if (e != cudaSuccess) break;
         s = product_of(A, false, A, false, n, n, n);                           // Q = a + b A + c A A
         s.symmetric = s.a_half = s.b_half = true;
         to_planes(s, Q, c[2] * (kScaleQ / (kScaleA * kScaleA)));
-        s.out.c_hi = A.hi();
-        s.out.c_lo = A.lo();
-        s.out.beta = c[1] * (kScaleQ / kScaleA);
-        s.out.diag = c[0] * kScaleQ;
+        s.out.diag = static_cast<float>((c[0] - c[2] * shift * shift) * kScaleQ);
+        if (!square) {
+            s.out.c_hi = A.hi();
+            s.out.c_lo = A.lo();
+            s.out.beta = c[1] * (kScaleQ / kScaleA);
+        }
         e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         if (e != cudaSuccess) break;
         s = tall ? product_of(X, false, Q, false, M, N, N) : product_of(Q, false, X, true, M, N, M);   // X Q, or Q X

@@ -49,6 +49,7 @@ struct Out {
     int64_t nb0, nb1, batch;       // bytes between rows of p0, of p1 and p2; between batches of p0 (and p1 for planes)
     const __half *c_hi, *c_lo;     // kSplit: C's planes, laid out as the result's
     float alpha, beta, diag;
+    int planes;                    // kSplit: matrices of a plane
     int type, act;
     int wide;                      // 16-byte stores are allowed
 };
@@ -56,6 +57,7 @@ struct Out {
 struct Job {
     CUtensorMap a, b[2];
     CUtensorMap a_turned, b_turned;   // a_half, b_half: the same matrix with its rows as k
+    CUtensorMap result;               // kSplit: the planes, by blocks of 32 x 32
     Out out;
     int *status;
     int64_t M, N;                  // kGate: N features, BN / 2 of them to a tile
@@ -282,19 +284,21 @@ __device__ __forceinline__ Tile tile_of(const Job &j, int i) {
 // tile with its rows contiguous, and nothing is ever mirrored in memory.
 __device__ __forceinline__ int below(int half, int k, int tile) { return half && k / kTileM < tile; }
 
-// 32 columns (from c) of the warp's rows (from r0) as two binary16 planes.
-__device__ __forceinline__ void store_split(uint8_t *stage, const Out &o, float (&v)[32], int64_t z, int64_t r0, int64_t c, int64_t M,
-                                            int64_t N) {
+// 32 columns (from c) of the warp's rows (from r0) as two binary16 planes, each staged in its
+// half of the warp's shared memory (swizzled as TMA reads it: 64-byte rows) and copied from there while
+// the warp goes on: every tile of a wave ends at once, and plain stores held the products up for as long
+// as L2 took to swallow them all (32 x 768 x 2048: 290 of 1840 us).
+__device__ __forceinline__ void store_split(uint8_t *stage, const CUtensorMap *map, const Out &o, float (&v)[32], int z, int64_t r0,
+                                            int64_t c, int64_t M) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = z * o.batch / 2, pitch = o.nb0 / 2, r = r0 + lane;
-    const bool in = r < M;
     if (o.c_hi) {
+        const int64_t at = z * o.batch / 2 + (r0 + lane) * (o.nb0 / 2) + c;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
             uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (in && c + i < N) {                         // whole pitches are readable
-                a = *reinterpret_cast<const uint4 *>(o.c_hi + at + r * pitch + c + i);
-                b = *reinterpret_cast<const uint4 *>(o.c_lo + at + r * pitch + c + i);
+            if (r0 + lane < M && c + i < o.nb0 / 2) {      // whole pitches are readable
+                a = *reinterpret_cast<const uint4 *>(o.c_hi + at + i);
+                b = *reinterpret_cast<const uint4 *>(o.c_lo + at + i);
             }
             __half ha[8], hb[8];
             __builtin_memcpy(ha, &a, 16);
@@ -307,18 +311,38 @@ __device__ __forceinline__ void store_split(uint8_t *stage, const Out &o, float 
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= o.alpha;
     }
-    if (o.diag != 0.f) {
+    if (c == r0) {                                         // the diagonal crosses this block
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (c + i == r) v[i] += o.diag;
+        for (int i = 0; i < 32; ++i) v[i] += i == lane ? o.diag : 0.f;
     }
-    __half *planes[2] = {static_cast<__half *>(o.p0) + at, static_cast<__half *>(o.p1) + at};
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-        // whole pitches are writable
-        store_block<OOP_TYPE_F16>(stage, v, reinterpret_cast<char *>(planes[p] + r0 * pitch + c), o.nb0, M - r0, (N - c + 7) / 8 * 8, 1);
+        uint8_t *part = stage + p * 2048;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");    // the copy before the last has left this half
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] -= __half2float(__float2half_rn(v[i]));
+        for (int k = 0; k < 4; ++k) {
+            __half2 h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[i] = __floats2half2_rn(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+                const float2 f = __half22float2(h[i]);
+                v[8 * k + 2 * i] -= f.x;
+                v[8 * k + 2 * i + 1] -= f.y;
+            }
+            uint4 w;
+            __builtin_memcpy(&w, h, 16);
+            *reinterpret_cast<uint4 *>(part + lane * 64 + ((k ^ (lane >> 1 & 3)) * 16)) = w;
+        }
+        ptx::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"(ptx::smem_u32(part)), "r"(static_cast<int>(c)), "r"(static_cast<int>(r0)), "r"(z + p * o.planes)
+                         : "memory");
+            ptx::bulk_commit();
+        }
     }
 }
 
@@ -548,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             auto plain = [&](float (&v)[32], int64_t c) {
                 if (rows <= 0 || c >= j.N) return;
                 if constexpr (EPI == kSplit) {
-                    store_split(stage_out, j.out, v, t.z, r0, c, j.M, j.N);
+                    store_split(stage_out, &j.result, j.out, v, t.z, r0, c, j.M);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
@@ -609,6 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             }
         }
         __syncwarp();
+        if (EPI == kSplit && lane == 0) ptx::bulk_wait();
     }
     if (timed_out) record_status(j.status, OOP_ERR_DEVICE_TIMEOUT);
     __syncthreads();
@@ -635,7 +660,7 @@ struct Operand {
     bool half;                                 // binary16, else bfloat16
 };
 
-inline bool make_map(CUtensorMap *map, const Operand &o, int tile_rows) {
+inline bool make_map(CUtensorMap *map, const Operand &o, int tile_rows, bool block = false) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.outer),
@@ -643,10 +668,10 @@ inline bool make_map(CUtensorMap *map, const Operand &o, int tile_rows) {
     // a stride over a single line is not used, but has to be a multiple of 16
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.outer > 1 ? o.pitch_bytes : 16),
                                    static_cast<cuuint64_t>(o.matrices > 1 ? o.matrix_bytes : 16)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(o.rows_contiguous ? 64 : tile_rows), 1};
+    const cuuint32_t box[3] = {block ? 32u : 64u, static_cast<cuuint32_t>(block ? 32 : o.rows_contiguous ? 64 : tile_rows), 1};
     const cuuint32_t ones[3] = {1, 1, 1};
     return fn(map, o.half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(o.p), dims,
-              strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, block ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -658,6 +683,7 @@ struct Spec {
     int a_plane, a_batch, a_seg, b_plane, b_batch;
     bool symmetric;
     bool a_half, b_half;           // FOLD and 256 columns only
+    Operand result;                // kSplit
     Out out;
 };
 
@@ -685,6 +711,7 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
         o.rows_contiguous = true;
         if ((i ? s.b_half : s.a_half) && !make_map(i ? &j.b_turned : &j.a_turned, o, 0)) return cudaErrorInvalidValue;
     }
+    if (EPI == kSplit && !make_map(&j.result, s.result, 0, true)) return cudaErrorInvalidValue;
     static_assert(BN == 256 || EPI != kSplit, "symmetric results have square tiles");
     j.a_half = s.a_half;
     j.b_half = s.b_half;
