@@ -51,22 +51,60 @@ int64_t parts_of(int64_t elements) { return std::min<int64_t>(592, (elements + 1
 // A warp's unit of work: up to kSpan columns of a row.
 constexpr int kSpan = 2048;
 
-// Eight elements from column c, those from column N on 0.
-__device__ __forceinline__ void load8(const char *row, int type, int64_t c, int64_t N, bool wide, float (&v)[8]) {
-    if (wide && c + 8 <= N) {
+// Eight aligned elements as they lie in memory.
+struct Eight {
+    uint4 a, b;
+
+    __device__ __forceinline__ void load(const char *row, int type, int64_t c) {
         if (type == OOP_TYPE_F32) {
-            float a[4], b[4];
-            load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c).get(a);
-            load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c + 4).get(b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+            a = load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c).raw;
+            b = load_stream<OOP_TYPE_F32, 4>(reinterpret_cast<const float *>(row) + c + 4).raw;
         } else {
-            load_stream<OOP_TYPE_BF16, 8>(reinterpret_cast<const __nv_bfloat16 *>(row) + c).get(v);
+            a = load_stream<OOP_TYPE_BF16, 8>(reinterpret_cast<const __nv_bfloat16 *>(row) + c).raw;
         }
-        return;
     }
+    __device__ __forceinline__ void get(int type, float (&v)[8]) const {
+        if (type == OOP_TYPE_F32) {
+            __builtin_memcpy(v, &a, 16);
+            __builtin_memcpy(v + 4, &b, 16);
+        } else {
+            Packed<OOP_TYPE_BF16, 8> p;
+            p.raw = a;
+            p.get(v);
+        }
+    }
+};
+
+// use(values, column) for every eight columns of a warp's span, four loads ahead where the
+// rows are aligned; columns from N on are 0.
+template <class F>
+__device__ __forceinline__ void each_eight(const char *row, int type, int64_t c0, int64_t end, int64_t N, bool wide, F &&use) {
+    int64_t c = c0 + (threadIdx.x & 31) * 8;
+    if (wide) {
+        for (; c + 768 + 8 <= end; c += 1024) {
+            Eight e[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < N ? load_any(row, type, c + i) : 0.f;
+            for (int k = 0; k < 4; ++k) e[k].load(row, type, c + 256 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v[8];
+                e[k].get(type, v);
+                use(v, c + 256 * k);
+            }
+        }
+    }
+    for (; c < end; c += 256) {
+        float v[8];
+        if (wide && c + 8 <= N) {
+            Eight e;
+            e.load(row, type, c);
+            e.get(type, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < N ? load_any(row, type, c + i) : 0.f;
+        }
+        use(v, c);
+    }
 }
 
 // Sum of squares of one part of each matrix (blockIdx.y).
@@ -78,13 +116,10 @@ __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, i
     Squares s;
     for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M * spans; i += gridDim.x * 8LL) {
         const int64_t r = i / spans, c0 = (i - r * spans) * kSpan, end = min(N, c0 + kSpan);
-#pragma unroll 4
-        for (int64_t c = c0 + (threadIdx.x & 31) * 8; c < end; c += 256) {
-            float v[8];
-            load8(p + r * nb_row, type, c, N, wide, v);
+        each_eight(p + r * nb_row, type, c0, end, N, wide, [&](const float (&v)[8], int64_t) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) s.add(v[k]);
-        }
+        });
     }
     const double sum = block_sum(static_cast<double>(s.big) * 0x1p140 + static_cast<double>(s.mid) +
                                      static_cast<double>(s.small) * 0x1p-140, part);
@@ -120,10 +155,7 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
     const int64_t plane = gridDim.y * M * pitch, spans = (N + kSpan - 1) / kSpan;
     for (int64_t i = blockIdx.x * 8LL + (threadIdx.x >> 5); i < M * spans; i += gridDim.x * 8LL) {
         const int64_t r = i / spans, c0 = (i - r * spans) * kSpan, end = min(N, c0 + kSpan);
-#pragma unroll 4
-        for (int64_t c = c0 + (threadIdx.x & 31) * 8; c < end; c += 256) {
-            float v[8];
-            load8(p + r * nb_row, type, c, N, wide, v);
+        each_eight(p + r * nb_row, type, c0, end, N, wide, [&](float (&v)[8], int64_t c) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = v[k] * f.x * f.y;
             if constexpr (DIRECT) {
@@ -148,7 +180,7 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
                 __builtin_memcpy(&w, lo, 16);
                 *reinterpret_cast<uint4 *>(d + plane) = w;
             }
-        }
+        });
     }
 }
 
@@ -421,6 +453,30 @@ struct Planes {
     }
 };
 
+// The largest |a + b l + c l^2| for eigenvalues l of A from 0 to 1.5.
+double largest_q(const float *c) {
+    double most = 0.0;
+    for (int i = 0; i <= 48; ++i) {
+        const double l = i / 32.0;
+        most = std::max(most, std::fabs(c[0] + l * (c[1] + l * c[2])));
+    }
+    return most;
+}
+
+// Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all products but the
+// first and the last are of the smaller side alone, 3 r + 4 s - 3 of them (in n^3, symmetric
+// results counted half) against s (3 r + 1) for a matrix r times as long as wide: fewer from r = 1.25 on.  What
+// it costs is precision: a rounding of A grows by Q^2 at every step, where one of X grows by
+// Q, and reaches the last Q as this share of it.  So only results of 16 bits are
+// computed this way, and only where the share stays below their rounding (five
+// steps of the usual coefficients).
+double rounding_of_a(int steps, const float *coefs) {
+    double grown = 0x1p-24;
+    for (int i = 0; i + 1 < steps; ++i) grown *= std::pow(largest_q(coefs ? coefs + 3 * i : kDefault), 2);
+    const float *last = coefs ? coefs + 3 * (steps - 1) : kDefault;
+    return grown * std::fabs(last[1]) / std::max(1e-3, std::fabs(static_cast<double>(last[0])));
+}
+
 // A product of two such operands over all matrices.
 pair::Spec product_of(const Planes &a, bool a_rows, const Planes &b, bool b_rows, int64_t M, int64_t N, int64_t K) {
     pair::Spec s = {};
@@ -454,8 +510,8 @@ size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     if (check_sizes(ne) != OOP_OK || ne[0] == 0 || ne[1] == 0 || ne[2] == 0) return 0;
     const int64_t n = std::min(ne[0], ne[1]);
     if (small_ctas(n, std::max(ne[0], ne[1]))) return 0;
-    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(double)) +
-           2 * plane_pair_bytes(ne[0], ne[1], ne[2]) + 2 * plane_pair_bytes(n, n, ne[2]);
+    const size_t x = plane_pair_bytes(ne[0], ne[1], ne[2]), a = plane_pair_bytes(n, n, ne[2]);
+    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(double)) + std::max(2 * x + 2 * a, x + 5 * a);
 }
 
 int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y, int y_type, const int64_t nb_y[2],
@@ -521,6 +577,72 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
                                                               nullptr, 0, 0, 0, 0.f);
     g_kernel_launches = 2;
     cudaError_t e = cudaGetLastError();
+    auto last_product = [&](pair::Spec p, float alpha) {
+        p.out.p0 = yp;
+        p.out.nb0 = nb_y[0];
+        p.out.batch = nb_y[1];
+        p.out.type = y_type;
+        p.out.alpha = scale * alpha;
+        p.out.wide = N * ys % 16 == 0 && is_aligned(y, 16) && (M <= 1 || nb_y[0] % 16 == 0) && (B <= 1 || nb_y[1] % 16 == 0);
+        return pair::launch<pair::kPlain, true, 256>(p, status, st);
+    };
+    if (e == cudaSuccess && steps >= 2 && y_type == OOP_TYPE_BF16 && 4 * deep >= 5 * n && rounding_of_a(steps, coefs) <= 0x1p-9) {
+        Planes pool[4], Z = {}, P = Q;                     // beside A: P, Q, Z and the next Z
+        for (int i = 0; i < 4; ++i) pool[i] = {next.p + (1 + i) * plane_pair_bytes(n, n, B), n, n, B};
+        const Planes G = {next.p, n, n, B};                // A
+        int free_ones[3] = {1, 2, 3};                      // pool[0] is P's
+        P = pool[0];
+        double z_scale = 1.0, z_bound = 1.0;
+        pair::Spec s = product_of(X, tall, X, tall, n, n, deep);
+        s.symmetric = true;
+        to_planes(s, G, kScaleA / (kScaleX * kScaleX));
+        e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+        auto symmetric = [&](const Planes &a, const Planes &b, const Planes &d, double alpha) {
+            s = product_of(a, false, b, false, n, n, n);
+            s.symmetric = s.a_half = s.b_half = true;
+            to_planes(s, d, static_cast<float>(alpha));
+        };
+        int z_at = -1;
+        for (int i = 0; i < steps && e == cudaSuccess; ++i) {
+            const float *c = coefs ? coefs + 3 * i : kDefault;
+            int q_at = -1;
+            for (int k : free_ones)
+                if (k != z_at && q_at < 0) q_at = k;
+            const Planes q = pool[q_at];
+            symmetric(G, G, q, c[2] * (kScaleQ / (kScaleA * kScaleA)));        // Q = a + b A + c A A
+            s.out.c_hi = G.hi();
+            s.out.c_lo = G.lo();
+            s.out.beta = c[1] * (kScaleQ / kScaleA);
+            s.out.diag = c[0] * kScaleQ;
+            e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+            z_bound *= largest_q(c);
+            if (i == 0) {
+                z_at = q_at;
+                z_scale = kScaleQ;
+            } else if (e == cudaSuccess) {                 // Z <- Q Z
+                int to = -1;
+                for (int k : free_ones)
+                    if (k != z_at && k != q_at) to = k;
+                const double next_scale = std::exp2(std::floor(std::log2(32768.0 / std::max(z_bound, 1.0))));
+                symmetric(q, pool[z_at], pool[to], next_scale / (kScaleQ * z_scale));
+                e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+                z_scale = next_scale;
+                z_at = to;
+            }
+            if (i + 1 < steps && e == cudaSuccess) {       // A <- Q A Q
+                symmetric(G, q, P, 1.0 / kScaleQ);
+                e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+                symmetric(P, q, G, 1.0 / kScaleQ);
+                if (e == cudaSuccess) e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+            }
+        }
+        if (e != cudaSuccess) return cuda_status(e);
+        Z = pool[z_at];
+        s = tall ? product_of(X, false, Z, false, M, N, N) : product_of(Z, false, X, true, M, N, M);
+        s.a_half = !tall;
+        s.b_half = tall;
+        return cuda_status(last_product(s, static_cast<float>(1.0 / (z_scale * kScaleX))));
+    }
     for (int i = 0; i < steps && e == cudaSuccess; ++i) {
         const float *c = coefs ? coefs + 3 * i : kDefault;
         pair::Spec s = product_of(X, tall, X, tall, n, n, deep);               // A = X X', or X' X
@@ -551,13 +673,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
             to_planes(s, next, 1.f / kScaleQ);
             e = pair::launch<pair::kSplit, true, 256>(s, status, st);
         } else {
-            s.out.p0 = yp;
-            s.out.nb0 = nb_y[0];
-            s.out.batch = nb_y[1];
-            s.out.type = y_type;
-            s.out.alpha = scale / (kScaleQ * kScaleX);
-            s.out.wide = N * ys % 16 == 0 && is_aligned(y, 16) && (M <= 1 || nb_y[0] % 16 == 0) && (B <= 1 || nb_y[1] % 16 == 0);
-            e = pair::launch<pair::kPlain, true, 256>(s, status, st);
+            e = last_product(s, 1.f / (kScaleQ * kScaleX));
         }
         std::swap(X, next);
     }
