@@ -100,6 +100,7 @@ template <int TYPE, int P>
 __global__ void __launch_bounds__(256) planes_kernel(const char *src, int64_t nb, int64_t cols, int64_t rows,
                                                      __nv_bfloat16 *dst, int64_t pitch, int wide) {
     const int64_t per_row = pitch / 8;
+    let_next_start();
     for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < rows * per_row; i += gridDim.x * 256LL) {
         const int64_t r = i / per_row, c = (i - r * per_row) * 8;
         if constexpr (P == 0) {
@@ -284,6 +285,7 @@ template <int DTYPE, int TYPE, int P>
 __global__ void __launch_bounds__(256) gate_back_kernel(const char *dh, int64_t nb_dh, const char *gate, const char *up, int64_t nb_gu,
                                                         __nv_bfloat16 *dst, int64_t pitch, int64_t F, int64_t T, int act, int wide) {
     const int64_t per_row = pitch / 8;
+    let_next_start();
     for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < T * per_row; i += gridDim.x * 256LL) {
         const int64_t t = i / per_row, c = (i - t * per_row) * 8;
         float d[8], g[8], u[8];

@@ -111,6 +111,7 @@ __device__ __forceinline__ void each_eight(const char *row, int type, int64_t c0
 __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N,
                                                       int64_t M, bool wide, double *sums) {
     __shared__ double part[32];
+    let_next_start();
     const char *p = x + blockIdx.y * nb_mat;
     const int64_t spans = (N + kSpan - 1) / kSpan;
     Squares s;
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
                                                     bool wide, const double *sums, int parts, float eps, __half *dst, int64_t pitch,
                                                     char *y, int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
     __shared__ float2 factors;
+    let_next_start();
+    wait_previous();
     if (threadIdx.x < 32) {
         double sum = 0.0;
         for (int i = threadIdx.x; i < parts; i += 32) sum += sums[static_cast<int64_t>(blockIdx.y) * parts + i];
@@ -569,14 +572,13 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     const int64_t units = M * ((N + kSpan - 1) / kSpan);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((units + 7) / 8, 1216));
     squares_kernel<<<dim3(static_cast<unsigned>(parts), nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums);
-    if (steps == 0)
-        start_kernel<true><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums, parts, eps, nullptr, 0, yp,
-                                                             y_type, nb_y[0], nb_y[1], scale);
-    else
-        start_kernel<false><<<dim3(blocks, nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums, parts, eps, X.hi(), X.pitch(),
-                                                              nullptr, 0, 0, 0, 0.f);
-    g_kernel_launches = 2;
+    auto start = [&](auto kernel, __half *planes, int64_t pitch) {
+        return launch_dependent(kernel, dim3(blocks, nb), 256, 0, st, xp, x_type, nb_x[0], nb_x[1], N, M, wide,
+                                static_cast<const double *>(sums), parts, eps, planes, pitch, yp, y_type, nb_y[0], nb_y[1], scale);
+    };
     cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = steps == 0 ? start(start_kernel<true>, nullptr, 0) : start(start_kernel<false>, X.hi(), X.pitch());
+    g_kernel_launches = 2;
     auto last_product = [&](pair::Spec p, float alpha) {
         p.out.p0 = yp;
         p.out.nb0 = nb_y[0];

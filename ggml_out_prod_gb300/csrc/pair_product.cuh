@@ -386,6 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
+    // all of the above may run while the kernel before this one ends
+    let_next_start();
+    wait_previous();
     const uint32_t stage0 = ptx::smem_u32(smem) + kHeader;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches;
     const int blocks = j.k_blocks * j.segments;
@@ -756,9 +759,9 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
         }();
         if (registers != 168) return cudaErrorLaunchOutOfResources;
     }
-    product_kernel<EPI, FOLD, BN><<<static_cast<unsigned>(2 * pairs), kThreads, kHeader + j.stages * j.stage_bytes + kEpilogueWarps * kOutBytes, st>>>(j);
     ++g_kernel_launches;
-    return cudaGetLastError();
+    return launch_dependent(product_kernel<EPI, FOLD, BN>, dim3(static_cast<unsigned>(2 * pairs)), kThreads,
+                            static_cast<size_t>(kHeader + j.stages * j.stage_bytes + kEpilogueWarps * kOutBytes), st, j);
 }
 
 }  // namespace pair
