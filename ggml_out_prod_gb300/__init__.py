@@ -104,16 +104,18 @@ class OopProblem(ctypes.Structure):
 
 
 class OopHeads(ctypes.Structure):
-    """oop_heads: the heads of the queries or keys, in and out."""
-    _fields_ = [("x", ctypes.c_void_p), ("nb_x", ctypes.c_int64 * 2), ("y", ctypes.c_void_p),
-                ("nb_y", ctypes.c_int64 * 2), ("w", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
+    """oop_heads: the heads of the queries or keys, in and out (nb_x and nb_y field by field)."""
+    _fields_ = [("x", ctypes.c_void_p), ("nb_x0", ctypes.c_int64), ("nb_x1", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("nb_y0", ctypes.c_int64), ("nb_y1", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
 
 
 class OopHeadsGrad(ctypes.Structure):
     """oop_heads_grad: the same for the backward pass."""
-    _fields_ = [("dy", ctypes.c_void_p), ("nb_dy", ctypes.c_int64 * 2), ("x", ctypes.c_void_p),
-                ("nb_x", ctypes.c_int64 * 2), ("w", ctypes.c_void_p), ("dx", ctypes.c_void_p),
-                ("nb_dx", ctypes.c_int64 * 2), ("dw", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
+    _fields_ = [("dy", ctypes.c_void_p), ("nb_dy0", ctypes.c_int64), ("nb_dy1", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("nb_x0", ctypes.c_int64), ("nb_x1", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("nb_dx0", ctypes.c_int64),
+                ("nb_dx1", ctypes.c_int64), ("dw", ctypes.c_void_p), ("n_head", ctypes.c_int64)]
 
 
 class OopError(RuntimeError):
@@ -1117,48 +1119,59 @@ _Three = ctypes.c_int64 * 3
 
 
 def _heads(t, name):
-    """(D, heads, T, (byte strides of a head and of a token)) of a CUDA tensor (..., H, D)."""
+    """(D, heads, T, byte strides of a head and of a token) of a CUDA tensor (..., H, D)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() < 2:
-        raise ValueError(f"{name} must have the shape (..., heads, head size)")
     shape, st, size = t.shape, t.stride(), t.element_size()
+    if len(shape) < 2:
+        raise ValueError(f"{name} must have the shape (..., heads, head size)")
     D, H = shape[-1], shape[-2]
     if D > 1 and st[-1] != 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    T, step = 1, None
-    for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
-        if n == 1:
-            continue
+    if len(shape) == 3:
+        T = shape[0]
+        step = st[0] if T > 1 else H * D
+    else:
+        T, step = 1, None
+        for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
+            if n == 1:
+                continue
+            if step is None:
+                step = d
+            elif d != step * T:
+                raise ValueError(f"the tokens of {name} must lie at one stride")
+            T *= n
         if step is None:
-            step = d
-        elif d != step * T:
-            raise ValueError(f"the tokens of {name} must lie at one stride")
-        T *= n
-    return D, H, T, (st[-2] * size if H > 1 else D * size, (H * D if step is None else step) * size)
+            step = H * D
+    return D, H, T, (st[-2] if H > 1 else D) * size, step * size
 
 
 def _like_heads(out, t, dtype, name):
     """A new contiguous tensor of t's shape, or the caller's if it fits: (tensor, strides)."""
     if out is None:
-        out = _rt().empty(t.shape, dtype=dtype, device=t.device)
-    elif out.shape != t.shape or out.dtype != dtype or out.device != t.device:
+        shape = t.shape
+        out = _rt().empty(shape, dtype=dtype, device=t.device)
+        row = shape[-1] * out.element_size()
+        return out, row, shape[-2] * row
+    if out.shape != t.shape or out.dtype != dtype or out.device != t.device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(t.shape)} on {t.device}")
-    return out, _heads(out, name)[3]
+    return (out,) + _heads(out, name)[3:]
 
 
 def _rotation(pos, freqs, T):
     rt = _rt()
-    n_rot = 0 if freqs is None else 2 * freqs.numel()
-    if n_rot and pos is None:
+    if freqs is None:
+        return None, None, 0
+    n = freqs.numel()
+    if n and pos is None:
         raise ValueError("freqs without pos")
-    return (_vector(pos, "pos", T, rt.i32) if n_rot else None,
-            _vector(freqs, "freqs", n_rot // 2, rt.f32) if n_rot else None, n_rot)
+    if not n:
+        return None, None, 0
+    return _vector(pos, "pos", T, rt.i32), _vector(freqs, "freqs", n, rt.f32), 2 * n
 
 
-def _same_tokens(q, k, what):
-    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype:
-        raise ValueError(f"{what} must have the same tokens, head size and type")
+def _head_weight(w, name, D):
+    return _vector(w, name, D, w.dtype) if w is not None else None
 
 
 def qk_norm_rope(q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -1175,20 +1188,22 @@ def qk_norm_rope(q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6, inter
         return _on_stream(stream, lambda: qk_norm_rope(q, k, pos, freqs, q_weight, k_weight, eps,
                                                        interleaved, out_q, out_k),
                           q, k, pos, freqs, q_weight, k_weight, out_q, out_k)
-    D, H, T, nb = _heads(q, "q")
-    kind = _plain_type(q.dtype, "q")
+    D, H, T, head, token = _heads(q, "q")
+    dtype = q.dtype
+    kind = _plain_type(dtype, "q")
     w_kind = _param_type(q_weight, k_weight)
     pp, pf, n_rot = _rotation(pos, freqs, T)
-    yq, nb_y = _like_heads(out_q, q, q.dtype, "out_q")
-    wq = _vector(q_weight, "q_weight", D, q_weight.dtype) if q_weight is not None else None
-    a = OopHeads(q.data_ptr(), nb, yq.data_ptr(), nb_y, wq, H)
+    yq, y_head, y_token = _like_heads(out_q, q, dtype, "out_q")
+    a = OopHeads(q.data_ptr(), head, token, yq.data_ptr(), y_head, y_token,
+                 _head_weight(q_weight, "q_weight", D), H)
     b = yk = None
     if k is not None:
-        _same_tokens(q, k, "q and k")
-        _, Hk, _, nb_k = _heads(k, "k")
-        yk, nb_yk = _like_heads(out_k, k, k.dtype, "out_k")
-        wk = _vector(k_weight, "k_weight", D, k_weight.dtype) if k_weight is not None else None
-        b = OopHeads(k.data_ptr(), nb_k, yk.data_ptr(), nb_yk, wk, Hk)
+        Dk, Hk, Tk, head, token = _heads(k, "k")
+        if Dk != D or Tk != T or k.dtype != dtype:
+            raise ValueError("q and k must have the same tokens, head size and type")
+        yk, y_head, y_token = _like_heads(out_k, k, dtype, "out_k")
+        b = OopHeads(k.data_ptr(), head, token, yk.data_ptr(), y_head, y_token,
+                     _head_weight(k_weight, "k_weight", D), Hk)
     rc = rt.lib.oop_qk_norm_rope(ctypes.byref(a), ctypes.byref(b) if b is not None else None, kind,
                                  w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
                                  _current_stream(q, k, pos, freqs, q_weight, k_weight))
@@ -1213,30 +1228,35 @@ def qk_norm_rope_back(dq, dk, q, k, pos, freqs, q_weight=None, k_weight=None, ep
             workspace), dq, dk, q, k, pos, freqs, q_weight, k_weight, out_q, out_k, workspace)
     if (k is None) != (dk is None):
         raise ValueError("k and dk go together")
-    D, H, T, nb_x = _heads(q, "q")
-    Hk = 0
-    if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
-        raise ValueError("a gradient and its input must have one shape")
-    kind, d_kind = _plain_type(q.dtype, "q"), _plain_type(dq.dtype, "dq")
+    D, H, T, head, token = _heads(q, "q")
+    dtype, d_type, dev = q.dtype, dq.dtype, q.device
+    kind, d_kind = _plain_type(dtype, "q"), _plain_type(d_type, "dq")
     w_kind = _param_type(q_weight, k_weight)
     pp, pf, n_rot = _rotation(pos, freqs, T)
-    dev = q.device
+    empty, f32 = rt.empty, rt.f32
 
-    def grads(x, d, w, out, name):
-        y, nb_y = _like_heads(out, d, d.dtype, "out_" + name)
-        dw = rt.empty(D, dtype=rt.f32, device=dev) if want_dw else None
-        pw = _vector(w, name + "_weight", D, w.dtype) if w is not None else None
-        _, n, _, nb = _heads(x, name)
-        return OopHeadsGrad(d.data_ptr(), _heads(d, "d" + name)[3], x.data_ptr(), nb, pw, y.data_ptr(),
-                            nb_y, dw.data_ptr() if want_dw else None, n), y, dw
-
-    a, yq, dwq = grads(q, dq, q_weight, out_q, "q")
+    if dq.shape != q.shape:
+        raise ValueError("a gradient and its input must have one shape")
+    _, _, _, d_head, d_token = _heads(dq, "dq")
+    yq, y_head, y_token = _like_heads(out_q, dq, d_type, "out_q")
+    dwq = empty(D, dtype=f32, device=dev) if want_dw else None
+    a = OopHeadsGrad(dq.data_ptr(), d_head, d_token, q.data_ptr(), head, token,
+                     _head_weight(q_weight, "q_weight", D), yq.data_ptr(), y_head, y_token,
+                     dwq.data_ptr() if want_dw else None, H)
     b = yk = dwk = None
+    Hk = 0
     if k is not None:
-        _same_tokens(q, k, "q and k")
-        _same_tokens(dq, dk, "dq and dk")
-        b, yk, dwk = grads(k, dk, k_weight, out_k, "k")
-        Hk = k.shape[-2]
+        Dk, Hk, Tk, head, token = _heads(k, "k")
+        if Dk != D or Tk != T or k.dtype != dtype or dk.dtype != d_type:
+            raise ValueError("q and k must have the same tokens, head size and type")
+        if dk.shape != k.shape:
+            raise ValueError("a gradient and its input must have one shape")
+        _, _, _, d_head, d_token = _heads(dk, "dk")
+        yk, y_head, y_token = _like_heads(out_k, dk, d_type, "out_k")
+        dwk = empty(D, dtype=f32, device=dev) if want_dw else None
+        b = OopHeadsGrad(dk.data_ptr(), d_head, d_token, k.data_ptr(), head, token,
+                         _head_weight(k_weight, "k_weight", D), yk.data_ptr(), y_head, y_token,
+                         dwk.data_ptr() if want_dw else None, Hk)
     st = _current_stream(q, k, dq, dk, pos, freqs, q_weight, k_weight)
     L = rt.lib
     ws, pws, nws = _scratch(L.oop_qk_norm_rope_back_workspace_size(D, T, H, Hk) if want_dw else 0,

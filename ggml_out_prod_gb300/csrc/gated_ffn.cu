@@ -360,9 +360,11 @@ ForwardForms forward_forms(int x_type, int w_type, bool aligned) {
 struct BackForms {
     Form d, x, w;
 };
-BackForms back_forms(int dh_type, int x_type, int w_type, bool aligned) {
+// dgate and dup of few tokens keep 16 bits where dh has 8: reading the weights takes longer than
+// twice the products, and a gradient of few terms would show their rounding.
+BackForms back_forms(int dh_type, int x_type, int w_type, int64_t T, bool aligned) {
     const bool precise = dh_type == OOP_TYPE_F32;
-    return {{precise ? 3 : 1, false, true}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
+    return {{precise ? 3 : T <= pair::kTileM ? 2 : 1, false, true}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
 }
 
 // A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
@@ -383,14 +385,43 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
 }
 
 // Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the
-// waves (a narrow tile reads A as often as a wide one for half the sums).
+// waves (a narrow tile reads A as often as a wide one for half the sums).  The SMs are
+// a GB300's, so that sizes can be asked for without one.
+constexpr int64_t kPairs = 76;
+
 bool narrow_tiles(int64_t M, int64_t N, int64_t batches, int wide_cols) {
-    const int64_t pairs = std::max(1, device_sm_count() / 2);
     auto waves = [&](int64_t cols) {
         const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
-        return (tiles + pairs - 1) / pairs;
+        return (tiles + kPairs - 1) / kPairs;
     };
     return waves(wide_cols / 2) * 23 < waves(wide_cols) * 40;
+}
+
+// Parts of k of a product whose tiles fill less than half of the SMs, each of eight
+// stages or more: 333 x 1001 x 3074 in f32 has 16 tiles, whose 50 stages would take 40 us.
+int parts_of_k(int64_t M, int64_t N, int64_t K, int64_t batches, int64_t segments) {
+    const int64_t cols = narrow_tiles(M, N, batches, 256) ? 128 : 256;
+    const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
+    const int64_t blocks = (K + pair::kDepth - 1) / pair::kDepth * segments;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / std::max<int64_t>(tiles, 1), blocks / 8, 16})));
+}
+size_t parts_bytes(int parts, int64_t M, int64_t N, int64_t batches) {
+    return parts > 1 ? round256(static_cast<size_t>(parts) * static_cast<size_t>(M * N * batches) * 4) : 0;
+}
+
+// Sums of the parts {N, M} of each batch, in their order, to p0 (and p1: the second batch's).
+template <int TYPE>
+__global__ void __launch_bounds__(256) join_kernel(const float *parts, int count, int64_t M, int64_t N, char *p0, char *p1, int64_t nb) {
+    let_next_start();
+    wait_previous();
+    const float *src = parts + blockIdx.y * count * M * N;
+    char *dst = blockIdx.y ? p1 : p0;
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
+        float v = src[i];
+        for (int k = 1; k < count; ++k) v += src[k * M * N + i];
+        const int64_t r = i / N;
+        row_of<TYPE>(dst, nb, r)[i - r * N] = from_float<TYPE>(v);
+    }
 }
 
 template <int EPI, bool FOLD>
@@ -398,6 +429,27 @@ cudaError_t product(const pair::Spec &s, int *status, cudaStream_t st) {
     const int wide_cols = EPI == pair::kGate ? 128 : 256;
     return narrow_tiles(s.M, s.N, s.batches, wide_cols) ? pair::launch<EPI, FOLD, 128>(s, status, st)
                                                         : pair::launch<EPI, FOLD, 256>(s, status, st);
+}
+
+// A gradient's product, in parts of k where that fills the SMs.
+template <bool FOLD>
+cudaError_t gradient(pair::Spec s, void *workspace, int *status, cudaStream_t st) {
+    const int parts = parts_of_k(s.M, s.N, s.K, s.batches, s.segments);
+    if (parts == 1) return product<pair::kPlain, FOLD>(s, status, st);
+    const pair::Out out = s.out;
+    s.splits = parts;
+    s.out.p0 = workspace, s.out.p1 = nullptr;
+    s.out.nb0 = s.N * 4, s.out.batch = s.M * s.N * 4;
+    s.out.type = OOP_TYPE_F32;
+    s.out.wide = s.N % 4 == 0;
+    const cudaError_t e = product<pair::kPlain, FOLD>(s, status, st);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(blocks_of(s.M * s.N), static_cast<unsigned>(s.batches));
+    const float *p = static_cast<const float *>(workspace);
+    char *p0 = static_cast<char *>(out.p0), *p1 = static_cast<char *>(out.p1);
+    ++g_kernel_launches;
+    return out.type == OOP_TYPE_F32 ? launch_dependent(join_kernel<OOP_TYPE_F32>, grid, 256, 0, st, p, parts, s.M, s.N, p0, p1, out.nb0)
+                                    : launch_dependent(join_kernel<OOP_TYPE_BF16>, grid, 256, 0, st, p, parts, s.M, s.N, p0, p1, out.nb0);
 }
 
 cudaError_t zero_rows(void *p, int64_t nb, int64_t row_bytes, int64_t rows, cudaStream_t st) {
@@ -455,8 +507,11 @@ size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3],
 
 size_t oop_gated_ffn_back_workspace_size(int dh_type, int x_type, int w_type, const int64_t ne[3], int aligned) {
     if (!gradient_type(dh_type) || check_ffn(x_type, w_type, ne, 0) != OOP_OK) return 0;
-    const BackForms f = back_forms(dh_type, x_type, w_type, aligned != 0);
-    return form_bytes(f.d, ne[1], 2 * ne[2]) + form_bytes(f.x, ne[0], ne[2]) + 2 * form_bytes(f.w, ne[0], ne[1]);
+    const BackForms f = back_forms(dh_type, x_type, w_type, ne[2], aligned != 0);
+    const int64_t K = ne[0], F = ne[1], T = ne[2];
+    // the parts of the two products follow each other in one place
+    const size_t parts = std::max(parts_bytes(parts_of_k(T, K, F, 1, 2), T, K, 1), parts_bytes(parts_of_k(F, K, T, 2, 1), F, K, 2));
+    return form_bytes(f.d, F, 2 * T) + form_bytes(f.x, K, T) + 2 * form_bytes(f.w, K, F) + parts;
 }
 
 int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, const void *w_up, int w_type,
@@ -556,7 +611,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
         if (want_dw && e == cudaSuccess) e = zero_rows(dw_up, nb_dw, K * d_size, F, st);
         return cuda_status(e);
     }
-    const BackForms f = back_forms(dh_type, x_type, w_type, aligned);
+    const BackForms f = back_forms(dh_type, x_type, w_type, T, aligned);
     char *at = static_cast<char *>(workspace);
     const int64_t pitch = round8(F);
     // [plane][gate, up][T][pitch]
@@ -564,11 +619,13 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
     const int wide = rows_aligned(dh, nb_dh, T) && rows_aligned(gate, nb_gu, T) && rows_aligned(up, nb_gu, T);
     const char *dp = static_cast<const char *>(dh), *gp = static_cast<const char *>(gate), *up_ = static_cast<const char *>(up);
     if (dh_type == OOP_TYPE_F32) launch_gate_back<OOP_TYPE_F32, 3>(x_type, dp, nb_dh, gp, up_, nb_gu, at, pitch, F, T, act, wide, st);
+    else if (f.d.planes == 2) launch_gate_back<OOP_TYPE_BF16, 2>(x_type, dp, nb_dh, gp, up_, nb_gu, at, pitch, F, T, act, wide, st);
     else launch_gate_back<OOP_TYPE_BF16, 1>(x_type, dp, nb_dh, gp, up_, nb_gu, at, pitch, F, T, act, wide, st);
     e = cudaGetLastError();
     at += form_bytes(f.d, F, 2 * T);
+    char *parts = at + form_bytes(f.x, K, T) + 2 * form_bytes(f.w, K, F);
     auto run = [&](const pair::Spec &s) {
-        return dh_type == OOP_TYPE_F32 ? product<pair::kPlain, true>(s, status, st) : product<pair::kPlain, false>(s, status, st);
+        return dh_type == OOP_TYPE_F32 ? gradient<true>(s, parts, status, st) : gradient<false>(s, parts, status, st);
     };
     if (want_dx && e == cudaSuccess) {                     // [dgate dup] [Wg; Wu]: two segments of F
         pair::Spec s = {};

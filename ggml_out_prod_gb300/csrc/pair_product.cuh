@@ -63,6 +63,7 @@ struct Job {
     int64_t M, N;                  // kGate: N features, BN / 2 of them to a tile
     int m_tiles, n_tiles, tiles, batches;   // tiles of a batch
     int k_blocks, segments;        // stages of a segment; with two, b[s] and a's plane + s * a_seg
+    int splits;                    // parts of k, each a tile of its own, summed by another kernel
     int planes_a, planes_b, terms;
     int a_plane, a_batch, a_seg, b_plane, b_batch;   // third coordinates
     int term_a[kMaxTerms], term_b[kMaxTerms];
@@ -254,8 +255,14 @@ __device__ __forceinline__ void store_block(int type, uint8_t *stage, const floa
 }
 
 struct Tile {
-    int m, n, z;
+    int m, n, z;                   // z: batch
+    int part;                      // of k
 };
+
+// First stage of a part of k.
+__device__ __forceinline__ int part_start(const Job &j, int part) {
+    return static_cast<int>(static_cast<int64_t>(j.k_blocks) * j.segments * part / j.splits);
+}
 
 // Tile i: batches outermost, then bands of eight row tiles, so that the tiles of a
 // wave share their operands in L2.
@@ -263,6 +270,8 @@ __device__ __forceinline__ Tile tile_of(const Job &j, int i) {
     Tile t;
     t.z = i / j.tiles;
     i -= t.z * j.tiles;
+    t.part = t.z % j.splits;
+    t.z /= j.splits;
     if (j.symmetric) {                                     // row tile m has n_tiles - m tiles
         t.m = 0;
         for (int left = j.n_tiles; i >= left; --left) {
@@ -390,8 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     let_next_start();
     wait_previous();
     const uint32_t stage0 = ptx::smem_u32(smem) + kHeader;
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches;
-    const int blocks = j.k_blocks * j.segments;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches * j.splits;
     // one second, and two microseconds for every product that a wait may be for
     const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(j.sum_blocks) * j.terms * 4;
     bool timed_out = false;
@@ -426,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 const int am = t.m * kTileM + static_cast<int>(rank) * 128;
                 const int bn = EPI == kGate ? t.n * (BN / 2) : t.n * BN + static_cast<int>(rank) * (BN / 2);
                 bool ok = true;
-                for (int kb = 0; kb < blocks && ok; ++kb) {
+                const int end = part_start(j, t.part + 1);
+                for (int kb = part_start(j, t.part); kb < end && ok; ++kb) {
                     ok = wait(&sh.empty[stage], phase ^ 1);
                     if (!ok) break;
                     const uint32_t bar = leader_addr(&sh.full[stage]);
@@ -470,9 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
+                const Tile t = tile_of(j, i);
+                const int end = part_start(j, t.part + 1);
                 if constexpr (FOLD) {
-                    const Tile t = tile_of(j, i);
-                    for (int kb = 0; kb < blocks && ok; ++kb) {
+                    for (int kb = part_start(j, t.part); kb < end && ok; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         const uint32_t sa = stage0 + stage * j.stage_bytes, sb = sa + j.planes_a * kPlaneBytes;
                         const int a_rows = j.a_rows | below(j.a_half, kb * kDepth, t.m);
@@ -507,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     if (!ok) break;
                     ptx::tc_fence_after();
                     uint32_t add = 0;
-                    for (int kb = 0; kb < blocks; ++kb) {
+                    for (int kb = part_start(j, t.part); kb < end; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         if (!ok) break;
                         ptx::tc_fence_after();
@@ -580,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
                     char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
-                                                 : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
+                                                 : static_cast<char *>(j.out.p0) + (t.z * j.splits + t.part) * j.out.batch;
                     store_block(j.out.type, stage_out, v, base + r0 * j.out.nb0 + c * element, j.out.nb0, rows, j.N - c, j.out.wide);
                 }
             };
@@ -588,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 uint64_t sums[kCols / 2];                  // of each half: 64 columns, or 32 gates and 32 ups
 #pragma unroll
                 for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
-                for (int kb = 0; kb < blocks && ok; ++kb) {
+                for (int kb = part_start(j, t.part); kb < part_start(j, t.part + 1) && ok; ++kb) {
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h) {
                         if (!sums_ready()) break;
@@ -683,6 +693,7 @@ struct Spec {
     Operand a, b[2];
     int64_t M, N, K;               // K of one segment
     int batches, segments, planes_a, planes_b;
+    int splits;                    // of k (0: 1); kPlain: each to a batch of its own, batch * splits + part
     int a_plane, a_batch, a_seg, b_plane, b_batch;
     bool symmetric;
     bool a_half, b_half;           // FOLD and 256 columns only
@@ -726,7 +737,8 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     const int64_t mt = (s.M + kTileM - 1) / kTileM, nt = (s.N + kTileN - 1) / kTileN;
     const int64_t tiles = s.symmetric ? nt * (nt + 1) / 2 : mt * nt;
     const int64_t blocks = (s.K + kDepth - 1) / kDepth;
-    if (tiles * s.batches > 0x7fffffffLL || blocks * s.segments > 0x7fffffffLL) return cudaErrorInvalidValue;
+    j.splits = s.splits > 1 ? s.splits : 1;
+    if (tiles * s.batches * j.splits > 0x7fffffffLL || blocks * s.segments > 0x7fffffffLL) return cudaErrorInvalidValue;
     j.m_tiles = static_cast<int>(mt);
     j.n_tiles = static_cast<int>(nt);
     j.tiles = static_cast<int>(tiles);
@@ -749,7 +761,7 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
               (static_cast<uint32_t>(kTileM >> 4) << 24);
     const int sms = device_sm_count();
     int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-    if (pairs > tiles * s.batches) pairs = tiles * s.batches;
+    if (pairs > tiles * s.batches * j.splits) pairs = tiles * s.batches * j.splits;
     cudaError_t e = allow_smem<product_kernel<EPI, FOLD, BN>>();
     if (e != cudaSuccess) return e;
     if (FOLD) {                                            // another split would wait forever for its registers

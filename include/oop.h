@@ -651,8 +651,9 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
  *   dx[k, t] = sum_f w_gate[k, f] * dgate[f, t] + w_up[k, f] * dup[f, t]
  *   dw_gate[k, f] = sum_t dgate[f, t] * x[k, t],   dw_up[k, f] = sum_t dup[f, t] * x[k, t]
  *
- * dh {F, T} and every result: F32 or BF16, one type.  dgate and dup are held
- * in that type between the products (rounded once where it is BF16).  dx may be NULL,
+ * dh {F, T} and every result: F32 or BF16, one type.  Between the
+ * products dgate and dup are held to 24 bits where dh is F32, to 16 where it is BF16 and T is
+ * at most 256, else in BF16.  dx may be NULL,
  * and dw_gate and dw_up both (not computed); dw rows are nb_dw apart.  T == 0
  * writes zeros to dw_gate and dw_up.  No output may overlap an input.
  */

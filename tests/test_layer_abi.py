@@ -34,7 +34,7 @@ def _i64(*v):
 
 def _heads(x=P, nb_x=(256, 1024), y=P, nb_y=(256, 1024), w=P, n=4):
     import ggml_out_prod_gb300 as g
-    return g.OopHeads(x, nb_x, y, nb_y, w, n)
+    return g.OopHeads(x, *nb_x, y, *nb_y, w, n)
 
 
 def norm(L, q={}, k={}, t=F32, wt=F32, pos=P, freqs=P, D=64, rot=64, T=3, eps=1e-6):
@@ -63,7 +63,7 @@ def test_qk_norm_rope_refusals(L, kw, want):
 
 def _grads(dy=P, nb_dy=(256, 1024), x=P, nb_x=(256, 1024), w=P, dx=P, nb_dx=(256, 1024), dw=P, n=4):
     import ggml_out_prod_gb300 as g
-    return g.OopHeadsGrad(dy, nb_dy, x, nb_x, w, dx, nb_dx, dw, n)
+    return g.OopHeadsGrad(dy, *nb_dy, x, *nb_x, w, dx, *nb_dx, dw, n)
 
 
 def norm_back(L, q={}, k={}, dt=F32, t=F32, wt=F32, pos=P, freqs=P, D=64, rot=64, T=3, eps=1e-6, ws=P, nws=1 << 30):
