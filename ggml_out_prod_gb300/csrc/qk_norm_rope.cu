@@ -231,54 +231,73 @@ __device__ __forceinline__ float dot(const Values<E, U> &v, const Values<E, U> &
     return s + z;
 }
 
-// A warp takes whole tokens, or with few tokens a share of a token's heads, and
-// its groups the heads in turn, kAhead turns' loads before the first is used.  The first side[0].ctas CTAs
-// work on the queries.
+// Weights of both sides in shared memory, as floats.
+__device__ __forceinline__ void fill_weights(float *w, const Side &s, int type, int D) {
+    for (int i = threadIdx.x; i < D; i += kThreads) w[i] = s.w && s.heads ? load_any(s.w, type, i) : 1.f;
+}
+
+// A warp takes whole tokens, or with few tokens a share of a token's heads: the queries'
+// and then the keys', its groups the heads in turn, kAhead turns' loads before the first is used.
 template <int TYPE, int E, int U>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) forward_kernel(const __grid_constant__ Args a) {
     constexpr int kAhead = E * U <= 8 ? 4 : 1;
     __shared__ Steps steps;
-    const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
-    const Side &s = a.side[which];
+    __shared__ __align__(16) float weights[2][kMaxHead];
     const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
     const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    fill_weights(weights[0], a.side[0], a.w_type, a.D);
+    fill_weights(weights[1], a.side[1], a.w_type, a.D);
     fill_steps(steps, a);
     Lane<E, U> l;
     l.place(a, lane & (group - 1));
-    Values<E, U> w;
-    load_weights(w, s, a.w_type, l);
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) - (which ? a.side[0].ctas : 0)) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
-    for (int64_t item = first; item < a.T * s.splits; item += warps) {
-        const int64_t t = item / s.splits;
-        const int share = static_cast<int>(item - t * s.splits), step = groups * s.splits;
-        const char *x = static_cast<const char *>(s.x) + t * s.x_tok;
-        char *y = static_cast<char *>(s.out) + t * s.out_tok;
+    const int splits = a.side[0].splits, step = groups * splits;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); item < a.T * splits; item += warps) {
+        const int64_t t = item / splits;
+        const int share = static_cast<int>(item - t * splits);
         float c[U][E], sn[U][E];
-        for (int h0 = share * groups; h0 < s.heads; h0 += step * kAhead) {
-            Raw<TYPE, E, U> raw[kAhead];
+        bool turned = false;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const Side &s = a.side[which];
+            const char *x = static_cast<const char *>(s.x) + t * s.x_tok;
+            char *y = static_cast<char *>(s.out) + t * s.out_tok;
+            const float *w = weights[which];
+#pragma unroll 1
+            for (int h0 = share * groups; h0 < s.heads; h0 += step * kAhead) {
+                Raw<TYPE, E, U> raw[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * step + mine;
-                raw[k].load(x + h * s.x_head, h < s.heads, l);
-            }
-            if (h0 == share * groups) angles<TYPE != OOP_TYPE_F32>(c, sn, a.half ? a.pos[t] : 0, steps, l);
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                if (h0 + k * step >= s.heads) break;       // the same for the warp
-                const int h = h0 + k * step + mine;
-                Values<E, U> v;
-                raw[k].get(v);
-                const float r = rsqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int h = h0 + k * step + mine;
+                    raw[k].load(x + h * s.x_head, h < s.heads, l);
+                }
+                if (!turned) angles<TYPE != OOP_TYPE_F32>(c, sn, a.half ? a.pos[t] : 0, steps, l);
+                turned = true;
+                Values<E, U> wv;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
-                        v.a[u][i] *= r * w.a[u][i];
-                        v.b[u][i] *= r * w.b[u][i];
+                        wv.a[u][i] = l.c0[u] < 0 ? 0.f : w[l.c0[u] + i];
+                        wv.b[u][i] = l.c1[u] < 0 ? 0.f : w[l.c1[u] + i];
                     }
-                rotate<1>(v, c, sn, a.interleaved);
-                if (h < s.heads) store_head<TYPE>(y + h * s.out_head, v, l);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (h0 + k * step >= s.heads) break;   // the same for the warp
+                    const int h = h0 + k * step + mine;
+                    Values<E, U> v;
+                    raw[k].get(v);
+                    const float r = rsqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            v.a[u][i] *= r * wv.a[u][i];
+                            v.b[u][i] *= r * wv.b[u][i];
+                        }
+                    rotate<1>(v, c, sn, a.interleaved);
+                    if (h < s.heads) store_head<TYPE>(y + h * s.out_head, v, l);
+                }
             }
         }
     }
@@ -412,7 +431,7 @@ int check_common(int64_t D, int64_t n_rot, int64_t T, const int32_t *pos, const 
 constexpr int64_t kMaxHeads = 1 << 20;
 
 // Fills in what follows from the sizes; e is the chunk.
-void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms) {
+void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms, bool backward) {
     a.T = T;
     a.D = static_cast<int>(D);
     a.half = static_cast<int>(n_rot / 2);
@@ -421,28 +440,47 @@ void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms) {
     a.group_shift = 0;
     while ((1 << a.group_shift) < a.units && a.group_shift < 5) ++a.group_shift;
     const int64_t groups = 32 >> a.group_shift;
-    const int64_t heads = a.side[0].heads + a.side[1].heads;
-    for (Side &s : a.side) {
-        if (s.heads == 0) continue;                        // no CTAs
-        // a token's heads are split until there are sixteen warps for each SM
-        const int64_t most = (s.heads + groups - 1) / groups;
-        int64_t splits = 1;
-        while (splits < most && T * splits < 16LL * sms) ++splits;
-        s.splits = static_cast<int>(splits);
-        const int64_t items = (T * splits + kThreads / 32 - 1) / (kThreads / 32);
-        const int64_t share = std::max<int64_t>(1, 2LL * sms * s.heads / heads);     // as many as are resident
-        s.ctas = static_cast<int>(std::min(items, share));
+    // a token's heads are split until there are sixteen warps for each SM
+    auto splits_of = [&](int64_t heads) {
+        const int64_t most = (heads + groups - 1) / groups;
+        int64_t n = 1;
+        while (n < most && T * n < 16LL * sms) ++n;
+        return static_cast<int>(n);
+    };
+    const int64_t resident = 2LL * sms, warps = kThreads / 32;
+    if (!backward) {
+        a.side[0].splits = splits_of(std::max(a.side[0].heads, a.side[1].heads));
+        a.side[0].ctas = static_cast<int>(std::min<int64_t>(resident, (T * a.side[0].splits + warps - 1) / warps));
+        return;
     }
+    int64_t items[2] = {0, 0}, cost[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        Side &s = a.side[i];
+        if (s.heads == 0) continue;                        // no CTAs
+        s.splits = splits_of(s.heads);
+        items[i] = (T * s.splits + warps - 1) / warps;
+        // turns of an item, and about one for its angles
+        cost[i] = (s.heads + groups * s.splits - 1) / (groups * s.splits) + 1;
+    }
+    // the share of the resident CTAs that ends both sides together
+    auto rounds = [&](int i, int64_t ctas) { return (items[i] + ctas - 1) / ctas * cost[i]; };
+    int64_t best = 0, split = 0;
+    for (int64_t n = 1; n < resident; ++n) {
+        const int64_t time = std::max(rounds(0, n), rounds(1, resident - n));
+        if (!split || time < best) best = time, split = n;
+    }
+    for (int i = 0; i < 2; ++i)
+        if (items[i]) a.side[i].ctas = static_cast<int>(std::min(items[i], !items[1 - i] ? resident : i ? resident - split : split));
 }
 
 // The CTAs that have a row of sums: as many as plan() can give one side.
 int64_t partial_rows(int64_t T, int64_t H, int sms) {
-    return H ? std::max<int64_t>(1, std::min<int64_t>(8LL * sms, T * std::max<int64_t>(H, 1))) : 0;
+    return H ? std::max<int64_t>(1, std::min<int64_t>(2LL * sms, T * H)) : 0;
 }
 
 template <int TYPE, int E, int U>
 void start_forward(const Args &a, cudaStream_t st) {
-    forward_kernel<TYPE, E, U><<<a.side[0].ctas + a.side[1].ctas, kThreads, 0, st>>>(a);
+    forward_kernel<TYPE, E, U><<<a.side[0].ctas, kThreads, 0, st>>>(a);
 }
 template <int TYPE>
 void launch_forward(const Args &a, int e, cudaStream_t st) {
@@ -536,7 +574,7 @@ int oop_qk_norm_rope(const oop_heads *q, const oop_heads *k, int type, int w_typ
         return true;
     };
     const int e = size == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
-    plan(a, e, D, n_rot, T, device_sm_count());
+    plan(a, e, D, n_rot, T, device_sm_count(), false);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (type == OOP_TYPE_F32) launch_forward<OOP_TYPE_F32>(a, e, st);
     else if (type == OOP_TYPE_F16) launch_forward<OOP_TYPE_F16>(a, e, st);
@@ -623,7 +661,7 @@ int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int 
         return true;
     };
     const int e = size == 2 && d_size == 2 && fits(8) ? 8 : fits(4) ? 4 : 1;
-    plan(a, e, D, n_rot, T, std::min(device_sm_count(), kMostSms));
+    plan(a, e, D, n_rot, T, std::min(device_sm_count(), kMostSms), true);
     float *rows = static_cast<float *>(workspace);
     for (int i = 0; i < 2; ++i) {
         a.side[i].partial = dw[i] ? rows : nullptr;
