@@ -211,9 +211,12 @@ struct SmallArgs {
 // neighbouring threads' columns lie in different banks.
 __host__ __device__ constexpr int small_pitch(int nmax) { return nmax / 4 % 2 ? nmax : nmax + 4; }
 __host__ __device__ constexpr int small_parts(int nmax) { return nmax > 32 ? 2 : 8; }
+// Copies of the partial products: up to 32 rows every CTA's, sent to all of them as they are
+// ready; beyond that a CTA's own, read by the others (the room is X's).
+__host__ __device__ constexpr int small_copies(int nmax) { return nmax > 32 ? 1 : kSmallCtas; }
 constexpr size_t small_fixed_bytes(int nmax) {
     // partial products (two steps'), the warps' parts, A and Q
-    return static_cast<size_t>(2 * nmax * nmax + small_parts(nmax) * nmax * nmax + 2 * nmax * (nmax + 4)) * 4;
+    return static_cast<size_t>(2 * small_copies(nmax) * nmax * nmax + small_parts(nmax) * nmax * nmax + 2 * nmax * (nmax + 4)) * 4;
 }
 constexpr int small_columns(int nmax) {          // of a CTA, at most
     return static_cast<int>((kMostSmem - 2048 - small_fixed_bytes(nmax)) / (small_pitch(nmax) * 4));
@@ -242,6 +245,9 @@ __device__ __forceinline__ float load_float(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ void store_float(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 __device__ __forceinline__ double load_double(uint32_t addr) {
     double v;
     asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
@@ -252,11 +258,12 @@ template <int NMAX>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ SmallArgs a) {
     constexpr int kPitch = small_pitch(NMAX), kParts = small_parts(NMAX), kSquare = NMAX * NMAX, kLd = NMAX + 4;
     constexpr int kRows = NMAX > 32 ? NMAX / 32 : 1;       // of a lane, in the products
+    constexpr int kCopies = small_copies(NMAX);
     constexpr int kGroups = NMAX >= 32 ? 1 : 32 / NMAX;    // columns of a warp at once
     extern __shared__ __align__(16) float small_smem[];
     __shared__ double reduce[32], my_sum;
     __shared__ float2 factors;
-    float *partial = small_smem, *parts = partial + 2 * kSquare, *A = parts + kParts * kSquare, *Q = A + NMAX * kLd;
+    float *partial = small_smem, *parts = partial + 2 * kCopies * kSquare, *A = parts + kParts * kSquare, *Q = A + NMAX * kLd;
     float *xs = Q + NMAX * kLd;
     const uint32_t cta = cta_of_cluster(), ctas = ctas_of_cluster();
     const int64_t matrix = blockIdx.x / ctas;
@@ -268,13 +275,37 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
     Squares sq;
     for (int i = tid; i < cols * (NMAX - a.n); i += kSmallThreads)               // rows that do not exist
         xs[i / (NMAX - a.n) * kPitch + a.n + i % (NMAX - a.n)] = 0.f;
-    // thread i takes element i of the slice in the order of memory
-    for (int i = tid; i < cols * a.n; i += kSmallThreads) {
-        const int r = a.tall ? i % a.n : i / cols, s = a.tall ? i / a.n : i % cols;
-        const float v = a.tall ? load_any(x + static_cast<int64_t>(s0 + s) * a.x_row, a.x_type, r)
-                               : load_any(x + r * a.x_row, a.x_type, s0 + s);
+    auto take = [&](int r, int s, float v) {
         sq.add(v);
         xs[s * kPitch + r] = v;
+    };
+    constexpr int kAhead = 8;                              // loads before the first is used
+    if (a.tall) {                                          // lanes along the rows, which are short
+        const int total = cols * a.n;
+        for (int i0 = tid; i0 < total; i0 += kSmallThreads * kAhead) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kSmallThreads, s = i / a.n;
+                v[k] = i < total ? load_any(x + static_cast<int64_t>(s0 + s) * a.x_row, a.x_type, i - s * a.n) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kSmallThreads, s = i / a.n;
+                if (i < total) take(i - s * a.n, s, v[k]);
+            }
+        }
+    } else {                                               // a warp to a row
+        for (int r = warp; r < a.n; r += kSmallThreads / 32)
+            for (int c0 = lane; c0 < cols; c0 += 32 * kAhead) {
+                float v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    v[k] = c0 + 32 * k < cols ? load_any(x + r * a.x_row, a.x_type, s0 + c0 + 32 * k) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (c0 + 32 * k < cols) take(r, c0 + 32 * k, v[k]);
+            }
     }
     const double sum = block_sum(static_cast<double>(sq.big) * 0x1p140 + static_cast<double>(sq.mid) +
                                      static_cast<double>(sq.small) * 0x1p-140, reduce);
@@ -334,18 +365,30 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
             }
             __syncthreads();
         }
-        float *mine = partial + (step & 1) * kSquare;      // two steps' apart: a slow CTA may still read the last one's
+        // two steps' apart: a slow CTA may still read the last one's
+        float *mine = partial + (step & 1) * kCopies * kSquare + (kCopies > 1 ? cta * kSquare : 0);
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
 #pragma unroll
             for (int p = 0; p < kParts; ++p) v += parts[p * kSquare + e];
-            mine[e] = v;
+            if constexpr (kCopies > 1) {
+                for (uint32_t c = 0; c < ctas; ++c) store_float(address_in(mine + e, c), v);
+            } else {
+                mine[e] = v;
+            }
         }
         sync_cluster();
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
+            if constexpr (kCopies > 1) {
+                const float *all = partial + (step & 1) * kCopies * kSquare + e;
+#pragma unroll
+                for (uint32_t c = 0; c < kSmallCtas; ++c)
+                    if (c < ctas) v += all[c * kSquare];
+            } else {
 #pragma unroll 8
-            for (uint32_t c = 0; c < ctas; ++c) v += load_float(address_in(mine + e, c));
+                for (uint32_t c = 0; c < ctas; ++c) v += load_float(address_in(mine + e, c));
+            }
             A[e / NMAX * kLd + e % NMAX] = v;
         }
         __syncthreads();

@@ -155,18 +155,6 @@ __device__ __forceinline__ void store_head(char *row, const Values<E, U> &v, con
     }
 }
 
-template <int E, int U>
-__device__ __forceinline__ void load_weights(Values<E, U> &w, const Side &s, int type,
-                                             const Lane<E, U> &l) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            w.a[u][i] = l.c0[u] < 0 ? 0.f : s.w ? load_any(s.w, type, l.c0[u] + i) : 1.f;
-            w.b[u][i] = l.c1[u] < 0 ? 0.f : s.w ? load_any(s.w, type, l.c1[u] + i) : 1.f;
-        }
-}
-
 // cos and sin of the token's angles; 0 turns for what is not rotated.  FAST: for
 // results of 16 bits, the hardware's functions, off by 2^-21 on (-pi, pi).
 template <bool FAST, int E, int U>
@@ -307,15 +295,16 @@ template <int DTYPE, int TYPE, int E, int U>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(const __grid_constant__ Args a) {
     constexpr int kAhead = E * U <= 4 ? 4 : E * U <= 8 ? 2 : 1;
     __shared__ Steps steps;
+    __shared__ __align__(16) float weights[kMaxHead];
     const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
     const Side &s = a.side[which];
     const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
     const int groups = 32 >> a.group_shift, mine = lane >> a.group_shift;
+    fill_weights(weights, s, a.w_type, a.D);
     fill_steps(steps, a);
     Lane<E, U> l;
     l.place(a, lane & (group - 1));
-    Values<E, U> w, dw = {};
-    load_weights(w, s, a.w_type, l);
+    Values<E, U> dw = {};
     const int64_t cta = static_cast<int64_t>(blockIdx.x) - (which ? a.side[0].ctas : 0);
     const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
     for (int64_t item = cta * (kThreads / 32) + (threadIdx.x >> 5); item < a.T * s.splits; item += warps) {
@@ -352,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(cons
                         x.b[u][i] *= r;
                         dw.a[u][i] = fmaf(d.a[u][i], x.a[u][i], dw.a[u][i]);
                         dw.b[u][i] = fmaf(d.b[u][i], x.b[u][i], dw.b[u][i]);
-                        d.a[u][i] *= w.a[u][i];
-                        d.b[u][i] *= w.b[u][i];
+                        d.a[u][i] *= l.c0[u] < 0 ? 0.f : weights[l.c0[u] + i];
+                        d.b[u][i] *= l.c1[u] < 0 ? 0.f : weights[l.c1[u] + i];
                     }
                 const float m = group_sum(dot(d, x), group) * a.inv_d;
 #pragma unroll
@@ -368,18 +357,25 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(cons
         }
     }
     if (!s.partial) return;
-    // the CTA's sums: every group's, in the order of the groups
-    __shared__ float part[kMaxHead];
-    for (int i = threadIdx.x; i < a.D; i += kThreads) part[i] = 0.f;
-    for (int turn_of = 0; turn_of < kThreads >> a.group_shift; ++turn_of) {
+    // the CTA's sums: those of a warp's groups, then the warps' in their order
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            for (int o = group; o < 32; o <<= 1) {
+                dw.a[u][i] += __shfl_xor_sync(0xffffffffu, dw.a[u][i], o);
+                dw.b[u][i] += __shfl_xor_sync(0xffffffffu, dw.b[u][i], o);
+            }
+    float *part = weights;                                 // no longer needed
+    for (int turn_of = 0; turn_of < kThreads / 32; ++turn_of) {
         __syncthreads();
-        if (static_cast<int>(threadIdx.x) >> a.group_shift != turn_of) continue;
+        if (static_cast<int>(threadIdx.x >> 5) != turn_of || mine != 0) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                if (l.c0[u] >= 0) part[l.c0[u] + i] += dw.a[u][i];
-                if (l.c1[u] >= 0) part[l.c1[u] + i] += dw.b[u][i];
+                if (l.c0[u] >= 0) part[l.c0[u] + i] = (turn_of ? part[l.c0[u] + i] : 0.f) + dw.a[u][i];
+                if (l.c1[u] >= 0) part[l.c1[u] + i] = (turn_of ? part[l.c1[u] + i] : 0.f) + dw.b[u][i];
             }
     }
     __syncthreads();
