@@ -25,27 +25,49 @@ constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 // subnormals.  bfloat16 planes would need no scale, but three of them and six terms.
 constexpr float kScaleX = 0x1p13f, kScaleA = 0x1p10f, kScaleQ = 0x1p8f;
 
-// Sums of squares of one thread: those of large, ordinary and small magnitudes
-// apart, scaled so that none over- or underflows.
+// Sums of squares: those of large, ordinary and small magnitudes apart, scaled so that
+// none over- or underflows (the idea of Blue, "A portable Fortran program to find the
+// Euclidean norm of a vector", TOMS 1978).
+constexpr float kBigScale = 0x1p-80f, kSmallScale = 0x1p90f;
+
 struct Squares {
     float big = 0.f, mid = 0.f, small = 0.f;
     __device__ __forceinline__ void add(float v) {
         const float m = fabsf(v);
         if (m > 0x1p50f) {
-            const float s = v * 0x1p-70f;
+            const float s = v * kBigScale;
             big = fmaf(s, s, big);
         } else if (m < 0x1p-40f) {
-            const float s = v * 0x1p70f;
+            const float s = v * kSmallScale;
             small = fmaf(s, s, small);
         } else {
-            mid = fmaf(v, v, mid);
+            mid = fmaf(v, v, mid);                         // and NaN
         }
-        if (m != m) mid += m;
     }
 };
 
-// The parts that a matrix's sum of squares is taken in: of its size alone, so that a
-// matrix gives the same bits in any batch.
+// 1 / (|x|_F + eps) as two factors, x * f.y * f.x; NaN where a value is not finite.
+__device__ __forceinline__ float2 inverse_norm(const Squares &s, float eps) {
+    float scale = 1.f, sum = s.mid + s.small * (1.f / kSmallScale) * (1.f / kSmallScale);
+    if (s.big > 0.f) {
+        scale = kBigScale;
+        sum = s.big + s.mid * kBigScale * kBigScale;
+    } else if (s.mid == 0.f && s.small > 0.f) {
+        scale = kSmallScale;
+        sum = s.small;
+    }
+    if (!(sum < __int_as_float(0x7f800000))) return make_float2(__int_as_float(0x7fc00000), 1.f);
+    return make_float2(1.f / (sqrtf(sum) + eps * scale), scale);
+}
+
+__device__ __forceinline__ Squares warp_squares(Squares s) {
+    s.big = warp_sum(s.big);
+    s.mid = warp_sum(s.mid);
+    s.small = warp_sum(s.small);
+    return s;
+}
+
+// The parts that a matrix's sum of squares is taken in.
 int64_t parts_of(int64_t elements) { return std::min<int64_t>(592, (elements + 16383) / 16384); }
 
 // A warp's unit of work: up to kSpan columns of a row.
@@ -109,8 +131,8 @@ __device__ __forceinline__ void each_eight(const char *row, int type, int64_t c0
 
 // Sum of squares of one part of each matrix (blockIdx.y).
 __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N,
-                                                      int64_t M, bool wide, double *sums) {
-    __shared__ double part[32];
+                                                      int64_t M, bool wide, Squares *sums) {
+    __shared__ Squares part[8];
     let_next_start();
     const char *p = x + blockIdx.y * nb_mat;
     const int64_t spans = (N + kSpan - 1) / kSpan;
@@ -122,34 +144,36 @@ __global__ void __launch_bounds__(256) squares_kernel(const char *x, int type, i
             for (int k = 0; k < 8; ++k) s.add(v[k]);
         });
     }
-    const double sum = block_sum(static_cast<double>(s.big) * 0x1p140 + static_cast<double>(s.mid) +
-                                     static_cast<double>(s.small) * 0x1p-140, part);
-    if (threadIdx.x == 0) sums[blockIdx.y * gridDim.x + blockIdx.x] = sum;
-}
-
-// 1 / (|x|_F + eps) as two factors of moderate size, from the sum of squares; NaN where a
-// value is not finite.
-__device__ __forceinline__ float2 inverse_norm(double sum, float eps) {
-    const double v = 1.0 / (sqrt(sum) + static_cast<double>(eps));
-    if (!(sum <= 0x1p1000)) return make_float2(__int_as_float(0x7fc00000), 1.f);
-    if (!(v <= 0x1p300)) return make_float2(static_cast<float>(v), 1.f);       // zeros and eps = 0
-    int e;
-    const double m = frexp(v, &e);
-    return make_float2(static_cast<float>(ldexp(m, e / 2)), static_cast<float>(ldexp(1.0, e - e / 2)));
+    s = warp_squares(s);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i) {
+            s.big += part[i].big;
+            s.mid += part[i].mid;
+            s.small += part[i].small;
+        }
+        sums[blockIdx.y * gridDim.x + blockIdx.x] = s;
+    }
 }
 
 // X_0, scaled, as planes [2][B][M][pitch]; with DIRECT (no steps) scale * X_0 to y.
 template <bool DIRECT>
 __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int64_t nb_row, int64_t nb_mat, int64_t N, int64_t M,
-                                                    bool wide, const double *sums, int parts, float eps, __half *dst, int64_t pitch,
+                                                    bool wide, const Squares *sums, int parts, float eps, __half *dst, int64_t pitch,
                                                     char *y, int y_type, int64_t nb_y, int64_t nb_y_mat, float scale) {
     __shared__ float2 factors;
     let_next_start();
     wait_previous();
     if (threadIdx.x < 32) {
-        double sum = 0.0;
-        for (int i = threadIdx.x; i < parts; i += 32) sum += sums[static_cast<int64_t>(blockIdx.y) * parts + i];
-        sum = warp_sum(sum);
+        Squares sum;
+        for (int i = threadIdx.x; i < parts; i += 32) {
+            const Squares one = sums[static_cast<int64_t>(blockIdx.y) * parts + i];
+            sum.big += one.big;
+            sum.mid += one.mid;
+            sum.small += one.small;
+        }
+        sum = warp_squares(sum);
         if (threadIdx.x == 0) factors = inverse_norm(sum, eps);
     }
     __syncthreads();
@@ -160,7 +184,7 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
         const int64_t r = i / spans, c0 = (i - r * spans) * kSpan, end = min(N, c0 + kSpan);
         each_eight(p + r * nb_row, type, c0, end, N, wide, [&](float (&v)[8], int64_t c) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = v[k] * f.x * f.y;
+            for (int k = 0; k < 8; ++k) v[k] = v[k] * f.y * f.x;
             if constexpr (DIRECT) {
                 char *row = y + blockIdx.y * nb_y_mat + r * nb_y;
 #pragma unroll
@@ -189,14 +213,15 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
 
 // ---- few rows -------------------------------------------------------------
 //
-// A matrix whose smaller side n is at most 64 (an adapter's): all steps in one
+// A matrix whose smaller side n is at most 32 (an adapter's): all steps in one
 // launch.  A cluster of up to eight CTAs holds X in shared memory as floats, each CTA
 // a slice of the longer side; only the n x n partial products pass between them.
 // Bound by latency: per step one exchange over the cluster, three barriers, and
 // n^2 products per column, which the CUDA cores do faster than a tile of 256 rows
 // could be loaded.  8 x 2560 in one launch instead of seventeen.
 
-constexpr int kSmallThreads = 256, kSmallCtas = 8;
+constexpr int kSmallCtas = 8;
+constexpr int kSmallThreads = 256;
 
 struct SmallArgs {
     const char *x;
@@ -210,13 +235,9 @@ struct SmallArgs {
 // Floats between columns of the slice: 16-byte units in odd number, so that
 // neighbouring threads' columns lie in different banks.
 __host__ __device__ constexpr int small_pitch(int nmax) { return nmax / 4 % 2 ? nmax : nmax + 4; }
-__host__ __device__ constexpr int small_parts(int nmax) { return nmax > 32 ? 2 : 8; }
-// Copies of the partial products: up to 32 rows every CTA's, sent to all of them as they are
-// ready; beyond that a CTA's own, read by the others (the room is X's).
-__host__ __device__ constexpr int small_copies(int nmax) { return nmax > 32 ? 1 : kSmallCtas; }
 constexpr size_t small_fixed_bytes(int nmax) {
-    // partial products (two steps'), the warps' parts, A and Q
-    return static_cast<size_t>(2 * small_copies(nmax) * nmax * nmax + small_parts(nmax) * nmax * nmax + 2 * nmax * (nmax + 4)) * 4;
+    // every CTA's partial products (two steps'), the warps' parts, A and Q
+    return static_cast<size_t>((2 * kSmallCtas + kSmallThreads / 32) * nmax * nmax + 2 * nmax * (nmax + 4)) * 4;
 }
 constexpr int small_columns(int nmax) {          // of a CTA, at most
     return static_cast<int>((kMostSmem - 2048 - small_fixed_bytes(nmax)) / (small_pitch(nmax) * 4));
@@ -248,22 +269,15 @@ __device__ __forceinline__ float load_float(uint32_t addr) {
 __device__ __forceinline__ void store_float(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ double load_double(uint32_t addr) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 template <int NMAX>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ SmallArgs a) {
-    constexpr int kPitch = small_pitch(NMAX), kParts = small_parts(NMAX), kSquare = NMAX * NMAX, kLd = NMAX + 4;
-    constexpr int kRows = NMAX > 32 ? NMAX / 32 : 1;       // of a lane, in the products
-    constexpr int kCopies = small_copies(NMAX);
-    constexpr int kGroups = NMAX >= 32 ? 1 : 32 / NMAX;    // columns of a warp at once
+    constexpr int kWarps = kSmallThreads / 32;
+    constexpr int kPitch = small_pitch(NMAX), kSquare = NMAX * NMAX, kLd = NMAX + 4;
+    constexpr int kGroups = 32 / NMAX;                     // columns of a warp at once
     extern __shared__ __align__(16) float small_smem[];
-    __shared__ double reduce[32], my_sum;
+    __shared__ Squares reduce[32], my_sum;
     __shared__ float2 factors;
-    float *partial = small_smem, *parts = partial + 2 * kCopies * kSquare, *A = parts + kParts * kSquare, *Q = A + NMAX * kLd;
+    float *partial = small_smem, *parts = partial + 2 * kSmallCtas * kSquare, *A = parts + kWarps * kSquare, *Q = A + NMAX * kLd;
     float *xs = Q + NMAX * kLd;
     const uint32_t cta = cta_of_cluster(), ctas = ctas_of_cluster();
     const int64_t matrix = blockIdx.x / ctas;
@@ -280,6 +294,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
         xs[s * kPitch + r] = v;
     };
     constexpr int kAhead = 8;                              // loads before the first is used
+    constexpr int kShare = kWarps > 8 ? kWarps / 8 : 1;    // warps of a row
     if (a.tall) {                                          // lanes along the rows, which are short
         const int total = cols * a.n;
         for (int i0 = tid; i0 < total; i0 += kSmallThreads * kAhead) {
@@ -295,9 +310,9 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
                 if (i < total) take(i - s * a.n, s, v[k]);
             }
         }
-    } else {                                               // a warp to a row
-        for (int r = warp; r < a.n; r += kSmallThreads / 32)
-            for (int c0 = lane; c0 < cols; c0 += 32 * kAhead) {
+    } else {                                               // a row to the warps of a share
+        for (int r = warp / kShare; r < a.n; r += kWarps / kShare)
+            for (int c0 = warp % kShare * 32 * kAhead + lane; c0 < cols; c0 += 32 * kAhead * kShare) {
                 float v[kAhead];
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
@@ -307,88 +322,77 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
                     if (c0 + 32 * k < cols) take(r, c0 + 32 * k, v[k]);
             }
     }
-    const double sum = block_sum(static_cast<double>(sq.big) * 0x1p140 + static_cast<double>(sq.mid) +
-                                     static_cast<double>(sq.small) * 0x1p-140, reduce);
-    if (tid == 0) my_sum = sum;
-    sync_cluster();
+    sq = warp_squares(sq);
+    if (lane == 0) reduce[warp] = sq;
+    __syncthreads();
     if (warp == 0) {
-        double v = 0.0;
-        for (uint32_t c = 0; c < ctas; ++c) v += load_double(address_in(&my_sum, c));
-        if (lane == 0) factors = inverse_norm(v, a.eps);
+        sq = warp_squares(lane < kWarps ? reduce[lane] : Squares());
+        if (lane == 0) my_sum = sq;
     }
+    if (ctas > 1) {
+        sync_cluster();
+        if (warp == 0) {                                   // a lane reads a CTA's
+            Squares s;
+            if (lane < ctas) {
+                const uint32_t at = address_in(&my_sum, lane);
+                s.big = load_float(at);
+                s.mid = load_float(at + 4);
+                s.small = load_float(at + 8);
+            }
+            sq = warp_squares(s);
+        }
+    }
+    if (tid == 0) factors = inverse_norm(sq, a.eps);
     __syncthreads();
     const float2 f = factors;
     for (int i = tid; i < cols * NMAX; i += kSmallThreads) {
         float &v = xs[i / NMAX * kPitch + i % NMAX];
-        v = v * f.x * f.y;
+        v = v * f.y * f.x;
     }
     for (int step = 0; step < a.steps; ++step) {
         __syncthreads();
-        // products of rows over this CTA's columns: a lane's row(s) with every row
-        float acc[kRows][NMAX];
+        // products of rows over this CTA's columns: a lane's row with every row
+        float acc[NMAX];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int j = 0; j < NMAX; ++j) acc[r][j] = 0.f;
-        const int row = lane % (NMAX < 32 ? NMAX : 32), group = lane / (NMAX < 32 ? NMAX : 32);
-        for (int s = warp * kGroups + group; s < cols; s += 8 * kGroups) {
+        for (int j = 0; j < NMAX; ++j) acc[j] = 0.f;
+        const int row = lane % NMAX, group = lane / NMAX;
+#pragma unroll 4
+        for (int s = warp * kGroups + group; s < cols; s += kWarps * kGroups) {
             const float *c = xs + s * kPitch;
-            float mine[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) mine[r] = c[row + 32 * r];
+            const float own = c[row];
 #pragma unroll
             for (int j = 0; j < NMAX; j += 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(c + j);
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    acc[r][j] = fmaf(mine[r], v.x, acc[r][j]);
-                    acc[r][j + 1] = fmaf(mine[r], v.y, acc[r][j + 1]);
-                    acc[r][j + 2] = fmaf(mine[r], v.z, acc[r][j + 2]);
-                    acc[r][j + 3] = fmaf(mine[r], v.w, acc[r][j + 3]);
-                }
+                acc[j] = fmaf(own, v.x, acc[j]);
+                acc[j + 1] = fmaf(own, v.y, acc[j + 1]);
+                acc[j + 2] = fmaf(own, v.z, acc[j + 2]);
+                acc[j + 3] = fmaf(own, v.w, acc[j + 3]);
             }
         }
 #pragma unroll
         for (int o = NMAX; o < 32; o <<= 1)
 #pragma unroll
-            for (int j = 0; j < NMAX; ++j) acc[0][j] += __shfl_xor_sync(0xffffffffu, acc[0][j], o);
-        for (int turn = 0; turn < 8 / kParts; ++turn) {    // warps turn * kParts .. share the parts
-            if (warp / kParts == turn && group == 0) {
-                float *p = parts + (warp % kParts) * kSquare;
+            for (int j = 0; j < NMAX; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+        if (group == 0) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
-#pragma unroll
-                    for (int j = 0; j < NMAX; ++j) {
-                        float &v = p[j * NMAX + row + 32 * r];
-                        v = turn ? v + acc[r][j] : acc[r][j];
-                    }
-            }
-            __syncthreads();
+            for (int j = 0; j < NMAX; ++j) parts[warp * kSquare + j * NMAX + row] = acc[j];
         }
-        // two steps' apart: a slow CTA may still read the last one's
-        float *mine = partial + (step & 1) * kCopies * kSquare + (kCopies > 1 ? cta * kSquare : 0);
+        __syncthreads();
+        // sent to every CTA as they are ready; two steps' apart, as a slow CTA may still read the last one's
+        float *all = partial + (step & 1) * kSmallCtas * kSquare;
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) v += parts[p * kSquare + e];
-            if constexpr (kCopies > 1) {
-                for (uint32_t c = 0; c < ctas; ++c) store_float(address_in(mine + e, c), v);
-            } else {
-                mine[e] = v;
-            }
+            for (int p = 0; p < kWarps; ++p) v += parts[p * kSquare + e];
+            for (uint32_t c = 0; c < ctas; ++c) store_float(address_in(all + cta * kSquare + e, c), v);
         }
-        sync_cluster();
+        if (ctas > 1) sync_cluster();
+        else __syncthreads();
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
-            if constexpr (kCopies > 1) {
-                const float *all = partial + (step & 1) * kCopies * kSquare + e;
 #pragma unroll
-                for (uint32_t c = 0; c < kSmallCtas; ++c)
-                    if (c < ctas) v += all[c * kSquare];
-            } else {
-#pragma unroll 8
-                for (uint32_t c = 0; c < ctas; ++c) v += load_float(address_in(mine + e, c));
-            }
+            for (uint32_t c = 0; c < kSmallCtas; ++c)
+                if (c < ctas) v += all[c * kSquare + e];
             A[e / NMAX * kLd + e % NMAX] = v;
         }
         __syncthreads();
@@ -411,38 +415,50 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
                 const float4 w = *reinterpret_cast<const float4 *>(c + j);
                 v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
             }
-#pragma unroll 4
-            for (int i = 0; i < NMAX; ++i) {
-                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll(NMAX > 8 ? 1 : 2)
+            for (int i0 = 0; i0 < NMAX; i0 += 4) {
+                float4 out;
+                float *o = &out.x;
 #pragma unroll
-                for (int j = 0; j < NMAX; j += 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(Q + i * kLd + j);
-                    sum0 = fmaf(q.x, v[j], fmaf(q.y, v[j + 1], sum0));
-                    sum1 = fmaf(q.z, v[j + 2], fmaf(q.w, v[j + 3], sum1));
+                for (int i = 0; i < 4; ++i) {
+                    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NMAX; j += 4) {
+                        const float4 q = *reinterpret_cast<const float4 *>(Q + (i0 + i) * kLd + j);
+                        sum0 = fmaf(q.x, v[j], fmaf(q.y, v[j + 1], sum0));
+                        sum1 = fmaf(q.z, v[j + 2], fmaf(q.w, v[j + 3], sum1));
+                    }
+                    o[i] = sum0 + sum1;
                 }
-                c[i] = sum0 + sum1;
+                *reinterpret_cast<float4 *>(c + i0) = out;
             }
         }
     }
     __syncthreads();
-    for (int i = tid; i < cols * a.n; i += kSmallThreads) {
-        const int r = a.tall ? i % a.n : i / cols, s = a.tall ? i / a.n : i % cols;
-        const float v = a.scale * xs[s * kPitch + r];
-        char *row = a.tall ? y + static_cast<int64_t>(s0 + s) * a.y_row : y + r * a.y_row;
-        const int64_t at = a.tall ? r : s0 + s;
-        if (a.y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[at] = v;
-        else reinterpret_cast<__nv_bfloat16 *>(row)[at] = __float2bfloat16_rn(v);
+    auto put = [&](char *row, int64_t at, float v) {
+        if (a.y_type == OOP_TYPE_F32) reinterpret_cast<float *>(row)[at] = a.scale * v;
+        else reinterpret_cast<__nv_bfloat16 *>(row)[at] = __float2bfloat16_rn(a.scale * v);
+    };
+    if (a.tall) {
+        for (int i = tid; i < cols * a.n; i += kSmallThreads) {
+            const int s = i / a.n, r = i - s * a.n;
+            put(y + static_cast<int64_t>(s0 + s) * a.y_row, r, xs[s * kPitch + r]);
+        }
+    } else {
+        for (int r = warp / kShare; r < a.n; r += kWarps / kShare)
+#pragma unroll 4
+            for (int c = warp % kShare * 32 + lane; c < cols; c += 32 * kShare) put(y + r * a.y_row, s0 + c, xs[c * kPitch + r]);
     }
-    sync_cluster();                                        // no CTA ends while another reads its sums
+    if (ctas > 1) sync_cluster();                          // no CTA ends while another reads its sums
 }
 
 // CTAs of a matrix's cluster, 0 where it has to go the other way: by its size alone.
 int small_ctas(int64_t n, int64_t deep) {
-    if (n > 64) return 0;
-    const int nmax = n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+    if (n > 32) return 0;
+    const int nmax = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+    // 128 columns to a CTA: fewer would not shorten the step, whose exchange takes 1300 cycles
     int ctas = 1;
-    // 64 columns to a CTA: fewer would not shorten the step's exchange
-    while (ctas < kSmallCtas && deep > 64LL * ctas) ctas *= 2;
+    while (ctas < kSmallCtas && deep > 128LL * ctas) ctas *= 2;
     return deep <= static_cast<int64_t>(small_columns(nmax)) * ctas ? ctas : 0;
 }
 
@@ -486,6 +502,21 @@ size_t plane_pair_bytes(int64_t cols, int64_t rows, int64_t B) {
     return round256(static_cast<size_t>(2 * B * rows * round8(cols)) * 2);
 }
 
+constexpr int64_t kPairs = 76;                             // of SMs: sizes can be asked for without a GPU
+
+// Parts of k of A = X X' where its tiles fill less than half of the SMs (76 pairs), each of
+// eight stages or more: 200 x 2560 is one tile of 40 stages, 32 us.
+int parts_of_a(int64_t n, int64_t deep, int64_t B) {
+    const int64_t t = (n + 255) / 256, tiles = t * (t + 1) / 2 * B, blocks = (deep + pair::kDepth - 1) / pair::kDepth;
+    return blocks < 24 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, blocks / 8, 16})));
+}
+// About the time of a product in microseconds: 9 for a launch, 0.8 for each stage of a wave of
+// tiles, 6 for the join of parts.
+double product_time(int64_t tiles, int64_t k, int parts) {
+    const int64_t blocks = (k + pair::kDepth - 1) / pair::kDepth, waves = (tiles * parts + kPairs - 1) / kPairs;
+    return 9.0 + 0.8 * static_cast<double>(waves * ((blocks + parts - 1) / parts)) + (parts > 1 ? 6.0 : 0.0);
+}
+
 // B matrices of two planes: [2][B][rows][pitch].
 struct Planes {
     char *p;
@@ -511,8 +542,8 @@ double largest_q(const float *c) {
 
 // Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all products but the
 // first and the last are of the smaller side alone, 3 r + 4 s - 3 of them (in n^3, symmetric
-// results counted half) against s (3 r + 1) for a matrix r times as long as wide: fewer from r = 1.25 on.  What
-// it costs is precision: a rounding of A grows by Q^2 at every step, where one of X grows by
+// results counted half) against s (3 r + 1) for a matrix r times as long as wide: fewer from r = 1.25 on,
+// but more launches.  What it costs is precision: a rounding of A grows by Q^2 at every step, where one of X grows by
 // Q, and reaches the last Q as this share of it.  So only results of 16 bits are
 // computed this way, and only where the share stays below their rounding (five
 // steps of the usual coefficients).
@@ -521,6 +552,36 @@ double rounding_of_a(int steps, const float *coefs) {
     for (int i = 0; i + 1 < steps; ++i) grown *= std::pow(largest_q(coefs ? coefs + 3 * i : kDefault), 2);
     const float *last = coefs ? coefs + 3 * (steps - 1) : kDefault;
     return grown * std::fabs(last[1]) / std::max(1e-3, std::fabs(static_cast<double>(last[0])));
+}
+bool on_a_alone(int64_t n, int64_t deep, int64_t B, int steps, const float *coefs) {
+    if (steps < 2 || rounding_of_a(steps, coefs) > 0x1p-9) return false;
+    const int64_t t = (n + 255) / 256, half = t * (t + 1) / 2 * B, whole = t * ((deep + 255) / 256) * B;
+    const double first = product_time(half, deep, parts_of_a(n, deep, B)), square = product_time(half, n, 1), with_x = product_time(whole, n, 1);
+    return first + (4 * steps - 3) * square + with_x < steps * (first + square + with_x);
+}
+
+size_t parts_bytes(int64_t n, int64_t deep, int64_t B) {
+    const int parts = parts_of_a(n, deep, B);
+    return parts > 1 ? round256(static_cast<size_t>(parts) * static_cast<size_t>(B * n * n) * 4) : 0;
+}
+
+// The parts {n, n} of each matrix summed in their order, on and above the diagonal's tiles, scaled
+// and with the shift on the diagonal, as planes.
+__global__ void __launch_bounds__(256) join_kernel(const float *parts, int count, int64_t n, int64_t pitch, float alpha, float diag,
+                                                   __half *hi, __half *lo) {
+    let_next_start();
+    wait_previous();
+    const float *src = parts + blockIdx.y * count * n * n;
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n * n; i += gridDim.x * 256LL) {
+        const int64_t r = i / n, c = i - r * n;
+        if (c / pair::kTileM < r / pair::kTileM) continue;
+        float v = src[i];
+        for (int k = 1; k < count; ++k) v += src[k * n * n + i];
+        v = v * alpha + (r == c ? diag : 0.f);
+        const int64_t at = (blockIdx.y * n + r) * pitch + c;
+        hi[at] = __float2half_rn(v);
+        lo[at] = __float2half_rn(v - __half2float(hi[at]));
+    }
 }
 
 // A product of two such operands over all matrices.
@@ -557,7 +618,8 @@ size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     const int64_t n = std::min(ne[0], ne[1]);
     if (small_ctas(n, std::max(ne[0], ne[1]))) return 0;
     const size_t x = plane_pair_bytes(ne[0], ne[1], ne[2]), a = plane_pair_bytes(n, n, ne[2]);
-    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(double)) + std::max(2 * x + 2 * a, x + 5 * a);
+    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(Squares)) + std::max(2 * x + 2 * a, x + 5 * a) +
+           parts_bytes(n, std::max(ne[0], ne[1]), ne[2]);
 }
 
 int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y, int y_type, const int64_t nb_y[2],
@@ -599,13 +661,12 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         for (int i = 0; i < 3 * steps; ++i) a.coefs[i] = coefs ? coefs[i] : kDefault[i % 3];
         const cudaError_t e = n <= 8    ? launch_small<8>(a, ctas, B, st)
                               : n <= 16 ? launch_small<16>(a, ctas, B, st)
-                              : n <= 32 ? launch_small<32>(a, ctas, B, st)
-                                        : launch_small<64>(a, ctas, B, st);
+                                        : launch_small<32>(a, ctas, B, st);
         return cuda_status(e);
     }
     const int parts = static_cast<int>(parts_of(M * N));
-    double *sums = static_cast<double *>(workspace);
-    char *at = static_cast<char *>(workspace) + round256(static_cast<size_t>(B * parts) * sizeof(double));
+    Squares *sums = static_cast<Squares *>(workspace);
+    char *at = static_cast<char *>(workspace) + round256(static_cast<size_t>(B * parts) * sizeof(Squares));
     Planes X = {at, N, M, B}, next = {at + plane_pair_bytes(N, M, B), N, M, B};
     const Planes A = {next.p + plane_pair_bytes(N, M, B), n, n, B}, Q = {A.p + plane_pair_bytes(n, n, B), n, n, B};
     const char *xp = static_cast<const char *>(x);
@@ -617,11 +678,37 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     squares_kernel<<<dim3(static_cast<unsigned>(parts), nb), 256, 0, st>>>(xp, x_type, nb_x[0], nb_x[1], N, M, wide, sums);
     auto start = [&](auto kernel, __half *planes, int64_t pitch) {
         return launch_dependent(kernel, dim3(blocks, nb), 256, 0, st, xp, x_type, nb_x[0], nb_x[1], N, M, wide,
-                                static_cast<const double *>(sums), parts, eps, planes, pitch, yp, y_type, nb_y[0], nb_y[1], scale);
+                                static_cast<const Squares *>(sums), parts, eps, planes, pitch, yp, y_type, nb_y[0], nb_y[1], scale);
     };
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = steps == 0 ? start(start_kernel<true>, nullptr, 0) : start(start_kernel<false>, X.hi(), X.pitch());
     g_kernel_launches = 2;
+    // A = X X', or X' X, with a shift in its diagonal
+    float *parts_at = reinterpret_cast<float *>(
+        X.p + std::max(2 * plane_pair_bytes(N, M, B) + 2 * plane_pair_bytes(n, n, B), plane_pair_bytes(N, M, B) + 5 * plane_pair_bytes(n, n, B)));
+    const int k_parts = parts_of_a(n, deep, B);
+    auto square_of = [&](const Planes &x_now, const Planes &d, double shift) {
+        pair::Spec p = product_of(x_now, tall, x_now, tall, n, n, deep);
+        p.symmetric = true;
+        if (k_parts == 1) {
+            to_planes(p, d, kScaleA / (kScaleX * kScaleX));
+            p.out.diag = static_cast<float>(shift * kScaleA);
+            return pair::launch<pair::kSplit, true, 256>(p, status, st);
+        }
+        p.splits = k_parts;
+        p.out.p0 = parts_at;
+        p.out.nb0 = n * 4;
+        p.out.batch = n * n * 4;
+        p.out.type = OOP_TYPE_F32;
+        p.out.alpha = 1.f;
+        p.out.wide = n % 4 == 0;
+        const cudaError_t err = pair::launch<pair::kPlain, true, 256>(p, status, st);
+        if (err != cudaSuccess) return err;
+        ++g_kernel_launches;
+        return launch_dependent(join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n * n + 255) / 256, 1024)), nb), 256, 0, st,
+                                static_cast<const float *>(parts_at), k_parts, n, d.pitch(), kScaleA / (kScaleX * kScaleX),
+                                static_cast<float>(shift * kScaleA), d.hi(), d.lo());
+    };
     auto last_product = [&](pair::Spec p, float alpha) {
         p.out.p0 = yp;
         p.out.nb0 = nb_y[0];
@@ -631,17 +718,15 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         p.out.wide = N * ys % 16 == 0 && is_aligned(y, 16) && (M <= 1 || nb_y[0] % 16 == 0) && (B <= 1 || nb_y[1] % 16 == 0);
         return pair::launch<pair::kPlain, true, 256>(p, status, st);
     };
-    if (e == cudaSuccess && steps >= 2 && y_type == OOP_TYPE_BF16 && 4 * deep >= 5 * n && rounding_of_a(steps, coefs) <= 0x1p-9) {
+    if (e == cudaSuccess && y_type == OOP_TYPE_BF16 && on_a_alone(n, deep, B, steps, coefs)) {
         Planes pool[4], Z = {}, P = Q;                     // beside A: P, Q, Z and the next Z
         for (int i = 0; i < 4; ++i) pool[i] = {next.p + (1 + i) * plane_pair_bytes(n, n, B), n, n, B};
         const Planes G = {next.p, n, n, B};                // A
         int free_ones[3] = {1, 2, 3};                      // pool[0] is P's
         P = pool[0];
         double z_scale = 1.0, z_bound = 1.0;
-        pair::Spec s = product_of(X, tall, X, tall, n, n, deep);
-        s.symmetric = true;
-        to_planes(s, G, kScaleA / (kScaleX * kScaleX));
-        e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+        pair::Spec s;
+        e = square_of(X, G, 0.0);
         auto symmetric = [&](const Planes &a, const Planes &b, const Planes &d, double alpha) {
             s = product_of(a, false, b, false, n, n, n);
             s.symmetric = s.a_half = s.b_half = true;
@@ -690,17 +775,13 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     }
     for (int i = 0; i < steps && e == cudaSuccess; ++i) {
         const float *c = coefs ? coefs + 3 * i : kDefault;
-        pair::Spec s = product_of(X, tall, X, tall, n, n, deep);               // A = X X', or X' X
-        s.symmetric = true;
-        to_planes(s, A, kScaleA / (kScaleX * kScaleX));
         // a + b A + c A A = c (A + b / 2c)^2 + a - b^2 / 4c: with the shift in A's diagonal Q is
         // one product, and A need not be read again.  The shift has to be of A's size.
         const bool square = c[2] != 0.f && std::fabs(c[1]) <= 8.f * std::fabs(c[2]);
         const double shift = square ? 0.5 * c[1] / c[2] : 0.0;
-        s.out.diag = static_cast<float>(shift * kScaleA);
-        e = pair::launch<pair::kSplit, true, 256>(s, status, st);
+        e = square_of(X, A, shift);
         if (e != cudaSuccess) break;
-        s = product_of(A, false, A, false, n, n, n);                           // Q = a + b A + c A A
+        pair::Spec s = product_of(A, false, A, false, n, n, n);                           // Q = a + b A + c A A
         s.symmetric = s.a_half = s.b_half = true;
         to_planes(s, Q, c[2] * (kScaleQ / (kScaleA * kScaleA)));
         s.out.diag = static_cast<float>((c[0] - c[2] * shift * shift) * kScaleQ);
