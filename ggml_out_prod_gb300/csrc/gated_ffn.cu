@@ -280,6 +280,101 @@ cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
+// Rows of any type as P binary16 planes [P][rows][pitch] of a scaled value, hi + lo: a row is
+// scaled by the power of two that brings its largest magnitude to 2^13 .. 2^14, so nothing
+// overflows, what is above 2^-15 of the largest keeps 22 bits or more, and what is below is
+// off by 2^-39 of the largest, which is in every sum of the row.  factors: the inverse scales.  Two planes and
+// three terms do for the forward products of f32 what three bfloat16 planes and six terms do elsewhere, whose
+// sums run over other rows' scales.  A CTA takes a row, read once up to 8192 columns.
+template <int TYPE, int P>
+__global__ void __launch_bounds__(256) halves_kernel(const char *src, int64_t nb, int64_t cols, int64_t rows, __half *dst, int64_t pitch,
+                                                     float *factors, int wide) {
+    constexpr int kHold = 4;
+    __shared__ float part[8];
+    let_next_start();
+    const char *row = src + blockIdx.x * nb;
+    float held[kHold][8], top = 0.f;
+    auto largest = [&](const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = v[i] == v[i] ? fmaxf(top, fabsf(v[i])) : __int_as_float(0x7f800000);
+    };
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const int64_t c = (threadIdx.x + 256 * h) * 8;
+        if (c < cols) {
+            load8<TYPE>(row, c, cols, wide, held[h]);
+            largest(held[h]);
+        }
+    }
+    for (int64_t c = (threadIdx.x + 256 * kHold) * 8; c < cols; c += 256 * 8) {
+        float v[8];
+        load8<TYPE>(row, c, cols, wide, v);
+        largest(v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, part[i]);
+    // 13 - floor(log2 top), within a float's exponents; 0 for a row of zeros or one that is not finite
+    const int exponent = static_cast<int>(__float_as_uint(top) >> 23);
+    const int e = top > 0.f && exponent < 255 ? max(-126, min(126, 13 + 127 - exponent)) : 0;
+    const float scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (threadIdx.x == 0) factors[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    __half *d = dst + blockIdx.x * pitch;
+    auto put = [&](const float (&v)[8], int64_t c) {
+        float left[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) left[i] = v[i] * scale;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            __half h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] = __float2half_rn(left[i]);
+                left[i] -= __half2float(h[i]);
+            }
+            uint4 w;
+            __builtin_memcpy(&w, h, 16);
+            *reinterpret_cast<uint4 *>(d + p * rows * pitch + c) = w;
+        }
+    };
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+        const int64_t c = (threadIdx.x + 256 * h) * 8;
+        if (c < cols) put(held[h], c);
+    }
+    for (int64_t c = (threadIdx.x + 256 * kHold) * 8; c < cols; c += 256 * 8) {
+        float v[8];
+        load8<TYPE>(row, c, cols, wide, v);
+        put(v, c);
+    }
+}
+
+template <int P>
+cudaError_t launch_halves_of(const void *src, int type, int64_t nb, int64_t cols, int64_t rows, void *dst, int64_t pitch,
+                             float *factors, cudaStream_t st) {
+    const char *s = static_cast<const char *>(src);
+    auto *d = static_cast<__half *>(dst);
+    const int wide = is_aligned(src, 16) && nb % 16 == 0;
+    const unsigned g = static_cast<unsigned>(rows);
+#define OOP_CASE(T) \
+    case T: halves_kernel<T, P><<<g, 256, 0, st>>>(s, nb, cols, rows, d, pitch, factors, wide); break;
+    if constexpr (P == 1) {
+        switch (type) { OOP_CASE(OOP_TYPE_F16) OOP_CASE(OOP_TYPE_BF16) }
+    } else {
+        switch (type) {
+            OOP_CASE(OOP_TYPE_F32) OOP_CASE(OOP_TYPE_Q4_0) OOP_CASE(OOP_TYPE_Q4_1) OOP_CASE(OOP_TYPE_Q5_0) OOP_CASE(OOP_TYPE_Q5_1)
+            OOP_CASE(OOP_TYPE_Q8_0) OOP_CASE(OOP_TYPE_Q2_K) OOP_CASE(OOP_TYPE_Q3_K) OOP_CASE(OOP_TYPE_Q4_K) OOP_CASE(OOP_TYPE_Q5_K)
+            OOP_CASE(OOP_TYPE_Q6_K)
+        }
+    }
+#undef OOP_CASE
+    ++g_kernel_launches;
+    return cudaGetLastError();
+}
+
 // dgate and dup as P planes [P][2][T][pitch]: dgate = dh up act'(gate), dup = dh act(gate).
 template <int DTYPE, int TYPE, int P>
 __global__ void __launch_bounds__(256) gate_back_kernel(const char *dh, int64_t nb_dh, const char *gate, const char *up, int64_t nb_gu,
@@ -336,18 +431,21 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 struct Form {
     int planes;        // terms of a value
     bool half, copy;   // binary16; in the workspace
+    bool scaled;       // by rows
 };
 
 // `native`: the other operand has this 16-bit type too.  `precise`: the product is wanted to 24 bits.
 Form form_of(int type, bool native, bool precise, bool aligned) {
-    if (native) return {1, type == OOP_TYPE_F16, !aligned};
-    if (type == OOP_TYPE_BF16) return {1, false, !aligned};
-    if (type == OOP_TYPE_F16) return {2, false, true};     // 11 bits: two planes hold them
-    return {precise ? 3 : 2, false, true};
+    if (native) return {1, type == OOP_TYPE_F16, !aligned, false};
+    if (type == OOP_TYPE_BF16) return {1, false, !aligned, false};
+    if (type == OOP_TYPE_F16) return {2, false, true, false};              // 11 bits: two planes hold them
+    return {precise ? 3 : 2, false, true, false};
 }
 
 size_t form_bytes(const Form &f, int64_t cols, int64_t rows) {
-    return f.copy ? round256(static_cast<size_t>(f.planes) * static_cast<size_t>(rows * round8(cols)) * 2) : 0;
+    if (!f.copy) return 0;
+    return round256(static_cast<size_t>(f.planes) * static_cast<size_t>(rows * round8(cols)) * 2) +
+           (f.scaled ? round256(static_cast<size_t>(rows) * 4) : 0);
 }
 
 struct ForwardForms {
@@ -355,7 +453,9 @@ struct ForwardForms {
 };
 ForwardForms forward_forms(int x_type, int w_type, bool aligned) {
     const bool native = x_type == w_type && x_type != OOP_TYPE_F32 && plain_size(x_type) == 2;
-    return {form_of(x_type, native, x_type == OOP_TYPE_F32, aligned), form_of(w_type, native, x_type == OOP_TYPE_F32, aligned)};
+    if (x_type == OOP_TYPE_F32)                            // a sum's factors are of its row and its column: both can be scaled
+        return {{2, true, true, true}, {plain_size(w_type) == 2 ? 1 : 2, true, true, true}};
+    return {form_of(x_type, native, false, aligned), form_of(w_type, native, false, aligned)};
 }
 struct BackForms {
     Form d, x, w;
@@ -364,13 +464,13 @@ struct BackForms {
 // twice the products, and a gradient of few terms would show their rounding.
 BackForms back_forms(int dh_type, int x_type, int w_type, int64_t T, bool aligned) {
     const bool precise = dh_type == OOP_TYPE_F32;
-    return {{precise ? 3 : T <= pair::kTileM ? 2 : 1, false, true}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
+    return {{precise ? 3 : T <= pair::kTileM ? 2 : 1, false, true, false}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
 }
 
 // A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
 // that this call writes at `at`, which moves on.
 cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_t cols, int64_t rows, bool rows_contiguous,
-                    char *&at, pair::Operand &o, cudaStream_t st) {
+                    char *&at, pair::Operand &o, cudaStream_t st, const float **factors_at = nullptr) {
     o = {src, cols, rows, nb, 0, 1, rows_contiguous, f.half};
     if (!f.copy) return cudaSuccess;
     const int64_t pitch = round8(cols);
@@ -379,6 +479,12 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
     o.matrix_bytes = rows * pitch * 2;
     o.matrices = f.planes;
     at += form_bytes(f, cols, rows);
+    if (f.scaled) {
+        float *factors = reinterpret_cast<float *>(at - round256(static_cast<size_t>(rows) * 4));
+        if (factors_at) *factors_at = factors;
+        return f.planes == 1 ? launch_halves_of<1>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, factors, st)
+                             : launch_halves_of<2>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, factors, st);
+    }
     if (f.planes == 1) return launch_planes_of<0>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
     return f.planes == 2 ? launch_planes_of<2>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st)
                          : launch_planes_of<3>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
@@ -553,9 +659,9 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     const ForwardForms f = forward_forms(x_type, w_type, aligned);
     char *at = static_cast<char *>(workspace);
     pair::Spec s = {};
-    cudaError_t e = operand(f.x, x, x_type, nb_x, K, T, false, at, s.a, st);
-    if (e == cudaSuccess) e = operand(f.w, w_gate, w_type, nb_w, K, F, false, at, s.b[0], st);
-    if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, false, at, s.b[1], st);
+    cudaError_t e = operand(f.x, x, x_type, nb_x, K, T, false, at, s.a, st, &s.out.row_scale);
+    if (e == cudaSuccess) e = operand(f.w, w_gate, w_type, nb_w, K, F, false, at, s.b[0], st, &s.out.col_scale[0]);
+    if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, false, at, s.b[1], st, &s.out.col_scale[1]);
     if (e != cudaSuccess) return cuda_status(e);
     s.M = T, s.N = F, s.K = K;
     s.batches = s.segments = 1;

@@ -48,6 +48,8 @@ struct Out {
     void *p0, *p1, *p2;            // matrix (p1: that of batch 1, or NULL); h, gate, up; the planes hi and lo
     int64_t nb0, nb1, batch;       // bytes between rows of p0, of p1 and p2; between batches of p0 (and p1 for planes)
     const __half *c_hi, *c_lo;     // kSplit: C's planes, laid out as the result's
+    const float *row_scale;        // kGate with FOLD: factors of the rows, and of the gates' and
+    const float *col_scale[2];     // the ups' columns, powers of two
     float alpha, beta, diag;
     int planes;                    // kSplit: matrices of a plane
     int type, act;
@@ -571,6 +573,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             // a gate's pieces: the gates and ups of 32 features
             auto gate = [&](float (&g)[32], float (&u)[32], int64_t f) {
                 if (rows <= 0 || f >= j.N) return;
+                if constexpr (FOLD) {
+                    const float by = lane < rows ? j.out.row_scale[r0 + lane] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int64_t c = min(f + k, j.N - 1);
+                        g[k] *= by * j.out.col_scale[0][c];
+                        u[k] *= by * j.out.col_scale[1][c];
+                    }
+                }
                 auto put = [&](const float (&v)[32], void *p, int64_t nb) {
                     store_block(j.out.type, stage_out, v, static_cast<char *>(p) + r0 * nb + f * element, nb, rows, j.N - f, j.out.wide);
                 };

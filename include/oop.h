@@ -620,11 +620,12 @@ int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int 
  *                       may both be NULL (not kept)
  *
  * h is computed from the 32-bit sums and rounded once.  x and the weights of
- * one 16-bit type go to the tensor cores as they are; other operands as a sum
- * of bfloat16 terms that keeps fp32's range: three (24 bits) where x is F32,
- * else two (16 bits or more).  No operand passes through binary16 but those
- * that are binary16.  Magnitudes below 2^-110 may lose bits.  A non-finite operand
- * gives non-finite sums.  K == 0: sums of nothing, 0.
+ * one 16-bit type go to the tensor cores as they are.  Where x is F32, its rows and the
+ * weights' go as two binary16 terms (one for 16-bit weights) scaled by a power of two for each
+ * row: an element keeps 22 bits or more, or is off by 2^-39 of its row's largest.  Other
+ * operands go as two bfloat16 terms, 16 bits.  Nothing overflows on the way that fp32 holds.
+ * Magnitudes below 2^-110 may lose bits.  A non-finite operand gives non-finite
+ * sums.  K == 0: sums of nothing, 0.
  *
  * workspace: oop_gated_ffn_workspace_size(...) bytes, 256-byte aligned; with
  * aligned != 0 for calls whose x and weights have 16-byte aligned pointers and
@@ -651,7 +652,9 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
  *   dx[k, t] = sum_f w_gate[k, f] * dgate[f, t] + w_up[k, f] * dup[f, t]
  *   dw_gate[k, f] = sum_t dgate[f, t] * x[k, t],   dw_up[k, f] = sum_t dup[f, t] * x[k, t]
  *
- * dh {F, T} and every result: F32 or BF16, one type.  Between the
+ * dh {F, T} and every result: F32 or BF16, one type.  Operands that are not BF16 go
+ * to the tensor cores as sums of bfloat16 terms: two for F16, else three (24 bits) where
+ * dh is F32 and two (16 bits) where it is BF16.  Between the
  * products dgate and dup are held to 24 bits where dh is F32, to 16 where it is BF16 and T is
  * at most 256, else in BF16.  dx may be NULL,
  * and dw_gate and dw_up both (not computed); dw rows are nb_dw apart.  T == 0
