@@ -27,8 +27,10 @@ __device__ __forceinline__ float activation_of(int act, float v) {
     return v < 0.f ? 0.f : v;
 }
 
-// The same as a call, where its code would be repeated for every register of a row.
-static __device__ __noinline__ float activation_call(int act, float v) { return activation_of(act, v); }
+// Four at a time as a call, where the code would be repeated for every register of a row.
+static __device__ __noinline__ float4 activation_call(int act, float4 v) {
+    return make_float4(activation_of(act, v.x), activation_of(act, v.y), activation_of(act, v.z), activation_of(act, v.w));
+}
 
 // The activation and its derivative.
 __device__ __forceinline__ float activation_and_slope(int act, float v, float &slope) {

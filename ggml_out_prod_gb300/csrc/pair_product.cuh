@@ -215,14 +215,6 @@ __device__ __forceinline__ void store_block(uint8_t *stage, const float (&v)[32]
                                             int64_t cols, int wide) {
     constexpr int kSize = plain_size(TYPE), E = 16 / kSize, kPieces = 32 / E;
     const int lane = threadIdx.x & 31;
-    if (!wide) {
-        if (lane >= rows) return;
-        auto *p = reinterpret_cast<typename Plain<TYPE>::S *>(row + lane * nb);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < cols) p[i] = from_float<TYPE>(v[i]);
-        return;
-    }
     auto place = [&](int r, int piece) {
         return stage + r * (32 * kSize) + ((piece ^ (kPieces == 8 ? r & 7 : r >> 1 & 3)) * 16);
     };
@@ -237,6 +229,15 @@ __device__ __forceinline__ void store_block(uint8_t *stage, const float (&v)[32]
         *reinterpret_cast<typename Words<16>::T *>(place(lane, k)) = w.raw;
     }
     __syncwarp();
+    if (!wide) {                                           // a row at a time, a column to a lane
+        using S = typename Plain<TYPE>::S;
+        if (lane >= cols) return;
+        const int most = static_cast<int>(rows < 32 ? rows : 32);
+#pragma unroll 4
+        for (int r = 0; r < most; ++r)
+            reinterpret_cast<S *>(row + r * nb)[lane] = reinterpret_cast<const S *>(place(r, lane / E))[lane % E];
+        return;
+    }
     const int piece = lane % kPieces, first = lane / kPieces;
     uint4 w[kPieces];                                      // all of them before the first store, which the compiler could not pass
 #pragma unroll
@@ -589,8 +590,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     put(g, j.out.p1, j.out.nb1);
                     put(u, j.out.p2, j.out.nb1);
                 }
+                if constexpr (FOLD) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) g[k] = (FOLD ? activation_call(j.out.act, g[k]) : activation_of(j.out.act, g[k])) * u[k];
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 h = activation_call(j.out.act, make_float4(g[k], g[k + 1], g[k + 2], g[k + 3]));
+                        g[k] = h.x * u[k];
+                        g[k + 1] = h.y * u[k + 1];
+                        g[k + 2] = h.z * u[k + 2];
+                        g[k + 3] = h.w * u[k + 3];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) g[k] = activation_of(j.out.act, g[k]) * u[k];
+                }
                 put(g, j.out.p0, j.out.nb0);
             };
             auto plain = [&](float (&v)[32], int64_t c) {
