@@ -1300,9 +1300,9 @@ def _ffn_weights(w_gate, w_up, w_type, K):
     return w_type, F, nb
 
 
-def _all_aligned(*pairs):
-    """Whether every (tensor, byte stride) starts and steps by multiples of 16 bytes."""
-    return all(t.data_ptr() % 16 == 0 and nb % 16 == 0 for t, nb in pairs)
+def _apart(t, nb):
+    """Whether rows start and step by multiples of 16 bytes and do not overlap."""
+    return t.data_ptr() % 16 == 0 and nb % 16 == 0 and nb >= t.shape[-1] * t.element_size()
 
 
 def _act_of(act):
@@ -1336,7 +1336,7 @@ def gated_ffn(x, w_gate, w_up, act="silu", keep=False, w_type=None, out=None, wo
     st = _current_stream(x, w_gate, w_up)
     ne = _Three(K, F, T)
     L = rt.lib
-    aligned = _all_aligned((x, nb_x), (w_gate, nb_w), (w_up, nb_w))
+    aligned = _apart(x, nb_x) and _apart(w_gate, nb_w) and _apart(w_up, nb_w)
     ws, pws, nws = _scratch(L.oop_gated_ffn_workspace_size(kind, w_kind, ne, aligned), x.device,
                             workspace)
     rc = L.oop_gated_ffn(x.data_ptr(), kind, nb_x, w_gate.data_ptr(), w_up.data_ptr(), w_kind, nb_w,
@@ -1378,7 +1378,7 @@ def gated_ffn_back(dh, x, w_gate, w_up, gate, up, act="silu", want_dx=True, want
     st = _current_stream(dh, x, w_gate, w_up, gate, up)
     ne = _Three(K, F, T)
     L = rt.lib
-    aligned = _all_aligned((x, nb_x), (w_gate, nb_w), (w_up, nb_w))
+    aligned = _apart(x, nb_x) and _apart(w_gate, nb_w) and _apart(w_up, nb_w)
     ws, pws, nws = _scratch(L.oop_gated_ffn_back_workspace_size(d_kind, kind, w_kind, ne, aligned),
                             x.device, workspace)
     rc = L.oop_gated_ffn_back(dh.data_ptr(), d_kind, nb_dh, x.data_ptr(), kind, nb_x,

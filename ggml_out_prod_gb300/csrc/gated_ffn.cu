@@ -591,8 +591,11 @@ int check_weights(const void *wg, const void *wu, int w_type, int64_t nb_w, int6
     return rc;
 }
 
-// Rows that TMA and 16-byte accesses can take as they are.
+// Rows that 16-byte accesses can take as they are, and those that TMA can: apart as well.
 bool rows_aligned(const void *p, int64_t nb, int64_t rows) { return is_aligned(p, 16) && (rows <= 1 || nb % 16 == 0); }
+bool rows_apart(const void *p, int64_t nb, int64_t rows, int64_t row_bytes) {
+    return rows_aligned(p, nb, rows) && (rows <= 1 || nb >= row_bytes);
+}
 
 int check_workspace(const void *ws, size_t have, size_t need) {
     return need == 0 || (ws && have >= need && is_aligned(ws, 256)) ? OOP_OK : OOP_ERR_WORKSPACE;
@@ -637,7 +640,8 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     if (K > 0 && (rc = check_pointer(x, size)) != OOP_OK) return rc;
     if ((rc = check_pointer(h, size)) != OOP_OK) return rc;
     if (gate && ((rc = check_pointer(gate, size)) != OOP_OK || (rc = check_pointer(up, size)) != OOP_OK)) return rc;
-    const bool aligned = rows_aligned(x, nb_x, T) && rows_aligned(w_gate, nb_w, F) && rows_aligned(w_up, nb_w, F);
+    const int64_t w_bytes = weight_row_bytes(w_type, K);
+    const bool aligned = rows_apart(x, nb_x, T, K * size) && rows_apart(w_gate, nb_w, F, w_bytes) && rows_apart(w_up, nb_w, F, w_bytes);
     if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_workspace_size(x_type, w_type, ne, aligned))) != OOP_OK)
         return rc;
     int *status = nullptr;
@@ -704,7 +708,8 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
     }
     if (want_dx && (rc = check_pointer(dx, d_size)) != OOP_OK) return rc;
     if (want_dw && ((rc = check_pointer(dw_gate, d_size)) != OOP_OK || (rc = check_pointer(dw_up, d_size)) != OOP_OK)) return rc;
-    const bool aligned = rows_aligned(x, nb_x, T) && rows_aligned(w_gate, nb_w, F) && rows_aligned(w_up, nb_w, F);
+    const int64_t w_bytes = weight_row_bytes(w_type, K);
+    const bool aligned = rows_apart(x, nb_x, T, K * size) && rows_apart(w_gate, nb_w, F, w_bytes) && rows_apart(w_up, nb_w, F, w_bytes);
     if ((rc = check_workspace(workspace, workspace_bytes, oop_gated_ffn_back_workspace_size(dh_type, x_type, w_type, ne, aligned))) != OOP_OK)
         return rc;
     int *status = nullptr;

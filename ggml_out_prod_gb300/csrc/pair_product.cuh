@@ -579,8 +579,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         const int64_t c = min(f + k, j.N - 1);
-                        g[k] *= by * j.out.col_scale[0][c];
-                        u[k] *= by * j.out.col_scale[1][c];
+                        const float bg = j.out.col_scale[0][c], bu = j.out.col_scale[1][c];
+                        g[k] = g[k] * fminf(by, bg) * fmaxf(by, bg);       // the small one first: no step leaves fp32's
+                        u[k] = u[k] * fminf(by, bu) * fmaxf(by, bu);       // range that the result does not leave
                     }
                 }
                 auto put = [&](const float (&v)[32], void *p, int64_t nb) {

@@ -559,8 +559,9 @@ int oop_preference_loss_back(const void *logits, int type, int64_t nb, const int
  *       pos[t] * freqs[i]:  a cos - b sin, a sin + b cos,  i = 0 .. n_rot/2 - 1
  *
  * Pair i is (n[i], n[i + n_rot/2]), or with interleaved != 0 (n[2i], n[2i+1]).
- * The angle is the exact product modulo a whole turn (to 2^-32 turns), so far
- * positions lose nothing.  freqs: device f32 {n_rot/2}, radians per position.
+ * The angle is the exact product modulo a whole turn (to 2^-32 turns, for |freqs| below
+ * 2^40), so far positions lose nothing; its sine and cosine are off by 2^-21 at most
+ * where the results have 16 bits.  freqs: device f32 {n_rot/2}, radians per position.
  * q and k may be slices of one buffer; k may be NULL (queries only).  D is 1 ..
  * 1024, n_rot even, 0 .. D (0: norm only, pos and freqs not used).  y may be x.
  * eps >= 0, finite.  A pair whose frequency is not finite is NaN.
@@ -629,7 +630,7 @@ int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int 
  *
  * workspace: oop_gated_ffn_workspace_size(...) bytes, 256-byte aligned; with
  * aligned != 0 for calls whose x and weights have 16-byte aligned pointers and
- * strides, else for any.
+ * strides and rows that do not overlap, else for any.
  */
 typedef enum {
     OOP_ACT_SILU = 0,      /* v / (1 + exp(-v)) */

@@ -402,6 +402,74 @@ def test_gated_ffn_strides(op, kind, extra, at):
     assert torch.isnan(dx[:, :at]).all() and torch.isnan(dx[:, at + K:]).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+def test_gated_ffn_repeated_and_overlapping_rows(op, kind):
+    """A stride of 0 (one row for all tokens) and rows that share elements."""
+    import torch
+    T, K, F = 40, 64, 72
+    line, lv = _rand(1, (K + 8 * T,), kind)
+    wg, wgv = _rand(2, (F, K), kind, K ** -0.5)
+    for step in (0, 8):
+        x = torch.as_strided(line, (T, K), (step, 1))
+        xd = x.contiguous()
+        a, b = op.gated_ffn(x, wg, wg, keep=True), op.gated_ffn(xd, wg, wg, keep=True)
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+        w = torch.as_strided(line, (F - 40, K), (step, 1))
+        assert torch.equal(op.gated_ffn(xd, w, w).h, op.gated_ffn(xd, w.contiguous(), w.contiguous()).h)
+        d = torch.ones((T, F), dtype=torch.float32 if kind == "f32" else torch.bfloat16, device="cuda")
+        for u, v in zip(op.gated_ffn_back(d, x, wg, wg, a.gate, a.up), op.gated_ffn_back(d, xd, wg, wg, a.gate, a.up)):
+            assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K,F", [(8, 16), (1000, 37), (6000, 40)])
+def test_gated_ffn_of_few_tokens(op, T, kind, K, F):
+    """Around the number of tokens where the form changes, and where their values no longer fit shared memory."""
+    x, xv = _rand(T, (T, K), kind)
+    wg, wgv = _rand(K, (F, K), kind, K ** -0.5)
+    wu, wuv = _rand(F, (F, K), kind, K ** -0.5)
+    h, gate, up = layer.gated_ffn(xv, wgv, wuv, "silu")
+    tol = _h_tol(xv, wgv, wuv, gate, up, "silu", _prod_kind(kind, kind), kind)
+    for w in ((wg, wu), (_framed(wg), _framed(wu))):
+        for got, want, t in zip(op.gated_ffn(x, *w, keep=True), (h, gate, up), tol):
+            _close(got, want, t, "few tokens")
+
+
+@pytest.mark.parametrize("T,K,F", [(300, 200, 3000), (64, 136, 2048), (256, 96, 520), (257, 96, 520), (2100, 72, 80)])
+@pytest.mark.parametrize("x_kind,d_kind", [("f32", "f32"), ("bf16", "bf16"), ("f16", "bf16")])
+def test_gated_ffn_back_in_parts(op, T, K, F, x_kind, d_kind):
+    """Long sums over few tiles, which are taken in parts, and the number of tokens where dgate's bits change."""
+    x, xv = _rand(T, (T, K), x_kind)
+    wg, wgv = _rand(K, (F, K), x_kind, K ** -0.5)
+    wu, wuv = _rand(F, (F, K), x_kind, K ** -0.5)
+    d, dv = _rand(T + 7, (T, F), d_kind)
+    _check_back(op, x, xv, wg, wgv, wu, wuv, d, dv, "silu", x_kind, x_kind)
+
+
+def test_gated_ffn_rows_of_all_scales(op):
+    """f32 rows from the smallest normal numbers to the largest, of zeros, and with one element far above the rest:
+    what an element loses is 2^-24 of itself and 2^-39 of its row's largest."""
+    import torch
+    T, K, F = 64, 100, 48
+    x, xv = _rand(1, (T, K), "f32")
+    wg, wgv = _rand(2, (F, K), "f32", 0.1)
+    wu, wuv = _rand(3, (F, K), "f32", 0.1)
+    scale = 2.0 ** np.linspace(-120, 120, T).round()
+    scale[5] = 0.0
+    x, xv = x * torch.from_numpy(scale).float().cuda()[:, None], xv * scale[:, None]
+    x[9, 3], xv[9, 3] = 2.0 ** 60, 2.0 ** 60
+    ws = 2.0 ** np.linspace(-20, 3, F).round()
+    wg, wgv = wg * torch.from_numpy(ws).float().cuda()[:, None], wgv * ws[:, None]
+    for rows in (slice(0, T), slice(4, 10)):                       # on the tensor cores, and few of them
+        _, gate, up = layer.gated_ffn(xv[rows], wgv, wuv, "relu")
+        r = op.gated_ffn(x[rows], wg, wu, act="relu", keep=True)
+        for got, want, wv in ((r.gate, gate, wgv), (r.up, up, wuv)):
+            ax, aw = np.abs(xv[rows]), np.abs(wv)
+            tol = PROD(K, "f32") * (ax @ aw.T) + 2.0 ** -39 * (ax.max(1)[:, None] * aw.sum(1) + ax.sum(1)[:, None] * aw.max(1))
+            _close(got, want, tol + 2.0 ** -126, "all scales")
+
+
 def test_gated_ffn_empty(op):
     import torch
     for T, K, F in ((0, 8, 16), (4, 8, 0), (4, 0, 16), (0, 0, 0)):
@@ -539,6 +607,18 @@ def test_orthogonalise_scale_of_the_input(op, M, N):
         bad[1, M // 2, N // 3] = v
         y = op.orthogonalise(bad)
         assert torch.isnan(y[1]).all() and torch.equal(y[0], op.orthogonalise(x))
+
+
+@pytest.mark.parametrize("M,N,out", [(200, 3000, "f32"), (3000, 200, "bf16"), (40, 5000, "f32"), (1600, 4800, "bf16"),
+                                     (4200, 1300, "bf16")])
+def test_orthogonalise_in_parts_and_on_the_smaller_side(op, M, N, out):
+    """Few tiles of a long sum, and 16-bit results whose steps run on A alone."""
+    x, xv = _rand(M, (M, N), "f32", 1e-3)
+    y = op.orthogonalise(x, out_dtype=_dt(out))
+    want = layer.orthogonalise(xv, 5, [USUAL] * 5, 1e-7)
+    # on A alone: the rounding of A that reaches the last step, below 2^-9 of it
+    extra = 2.0 ** -9 * np.linalg.norm(want) if out == "bf16" else 0.0
+    assert np.linalg.norm(_np(y) - want) <= _orth_tol(want, 5, out) + extra
 
 
 def test_orthogonalise_low_rank(op):
