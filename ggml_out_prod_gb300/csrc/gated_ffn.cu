@@ -4,6 +4,17 @@
 //   gate = x Wg',  up = x Wu',  h = act(gate) up
 //   dgate = dh up act'(gate),  dup = dh act(gate)
 //   dx = dgate Wg + dup Wu,  dWg = dgate' x,  dWu = dup' x
+//
+// Bound by the tensor cores from a few hundred tokens on.  Forward: one product whose
+// tiles take half their columns from each weight, so that a tile's epilogue holds the gates
+// and the ups of the same features and nothing goes to memory between.  Backward: one pass over dh, gate
+// and up writes dgate and dup (16 bits each where dh has 16), then dx as one product over
+// both weights' rows, and both weight gradients as one product of two batches; the operands
+// lie as they are, with their rows or their k contiguous.
+//
+// Measured: bf16 8192 x 5120 x 17408, gate and up kept: 1.53 ms, 1.91 PFLOP/s (97% of the
+// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x 2560 x 9728: 1.10 ms, 1.48
+// PFLOP/s, of it 0.13 for dgate and dup and a last wave of dx that fills a fifth of the SMs.
 #include <algorithm>
 #include <cmath>
 
@@ -151,7 +162,8 @@ cudaError_t launch_planes_of(const void *src, int type, int64_t nb, int64_t cols
 // cores' tiles of 256 tokens would only be waited for.  A warp takes a feature: its
 // gate and its up row, each read once in long runs (five or six 16-byte loads of each row in flight per lane),
 // against the tokens in shared memory as floats.  Sums in fp32 on the CUDA cores, which any
-// type of weight allows without a copy.  bf16, 1 x 2560 x 9728: @FEW@.
+// type of weight allows without a copy.  bf16, 1 x 2560 x 9728: 17.7 us,
+// 5.6 TB/s, 84% of the measured copy rate (one load of each row at a time: 48 us; on the tensor cores 44 us).
 constexpr int kFewThreads = 512, kFewTokens = 8;
 constexpr int64_t kFewBytes = 180 * 1024;
 

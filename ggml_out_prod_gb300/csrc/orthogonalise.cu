@@ -5,6 +5,10 @@
 //
 // A is taken on the smaller side: with M > N, X <- X (a + b X'X + c (X'X)^2) is
 // the same polynomial of the singular values.
+//
+// Bound by the tensor cores (three products of binary16 planes for one of 22 bits), whose
+// sums are folded every 64 k, and for few rows by launches.  f32, five steps: 8 x 2560
+// 13 to 15 us, 32 x 768 x 2048 1.63 ms, 9728 x 2560 to bf16 1.09 ms (1.97 with the steps on X itself).
 #include <algorithm>
 #include <cmath>
 

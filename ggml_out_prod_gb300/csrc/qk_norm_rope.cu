@@ -6,7 +6,9 @@
 //   dw = sum over tokens and heads of dn x r
 //
 // Bound by memory: x is read once and y written once, nothing else is of their
-// size.  A head is held by a group of 2, 4 .. 32 lanes.  A lane's unit is two
+// size.  bf16, 16384 tokens of 32 + 8 heads of 128: 63 us, 5.3 TB/s (80% of the measured
+// copy rate), backward 106 us, 4.7 TB/s (71%): half of the issue slots are taken, and 16 warps
+// per SM wait for their loads and shuffles.  A head is held by a group of 2, 4 .. 32 lanes.  A lane's unit is two
 // chunks of E elements that hold whole pairs: chunk j of the first half of the
 // rotated elements and its partner in the second half, or two neighbouring
 // chunks.  So a rotation needs no other lane, and a lane's frequencies and

@@ -5,9 +5,10 @@ Tolerances follow from the arithmetic and are written before any run.  u = 2^-24
 rounding to fp32 and UOUT one to the output's type.  A product's sum of K terms is
 off by at most PROD(K, kind) of the sum of the terms' magnitudes:
 
-  f32     operands as three bfloat16 terms each: what is dropped is below 2^-25 of a
-          product; at most 48 tensor-core additions into one partial sum, each off by at most
-          2^-23 of the magnitudes, then one rounding for each of K / 128 partial sums
+  f32     operands as three bfloat16 terms each, or two scaled binary16 ones: what is dropped is
+          below 2^-22 of a product; at most 24 tensor-core additions into one partial sum, each off by
+          at most 2^-23 of the magnitudes, then one rounding for each of K / 64 partial sums: together
+          below 50 * 2^-23 + K / 128 * 2^-24 + 2^-25
   16 bit  exact products; K / 16 + 1 tensor-core additions
   mixed   operands as two terms each: three quantities below 2^-18 of a product, and
           three times the additions of the 16-bit form
@@ -315,9 +316,10 @@ def test_gated_ffn_mixed_types(op, x_kind, w_kind, T, K, F):
 
 @pytest.mark.parametrize("kind", [synth.TYPE_Q8_0, synth.TYPE_Q4_0, synth.TYPE_Q5_1, synth.TYPE_Q4_K, synth.TYPE_Q6_K])
 @pytest.mark.parametrize("x_kind", ["f32", "bf16"])
-def test_gated_ffn_quantised(op, kind, x_kind):
+@pytest.mark.parametrize("T", [3, 33])
+def test_gated_ffn_quantised(op, kind, x_kind, T):
     import torch
-    T, F = 33, 72
+    F = 72
     K = synth.BLOCK[kind][0] * 3
     x, xv = _rand(T, (T, K), x_kind)
     raw = [synth.quantize(kind, synth.normal(s, F * K, std=K ** -0.5).reshape(F, K)).reshape(F, -1) for s in (1, 2)]
@@ -739,6 +741,40 @@ def test_offsets_beyond_32_bits(op):
     assert torch.equal(op.orthogonalise(m), want)
     op.orthogonalise(dense, out=m)
     assert torch.equal(m, want)
+
+
+def test_more_than_32_bits_of_bytes(op):
+    """Results and inputs of more than 2^32 bytes: their last rows are those of a small call."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    T, H, D = 430000, 40, 128
+    q = torch.empty((T, H, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    pos, freqs = torch.arange(T, dtype=torch.int32, device="cuda"), torch.linspace(1, 0.001, D // 2).cuda()
+    want = op.qk_norm_rope(q[-3:].clone(), None, pos[-3:].clone(), freqs)[0]
+    back = op.qk_norm_rope_back(q[-3:].clone(), None, q[-3:].clone(), None, pos[-3:].clone(), freqs, want_dw=False)[0]
+    dx = op.qk_norm_rope_back(q, None, q, None, pos, freqs, want_dw=False)[0]
+    assert torch.equal(dx[-3:], back)
+    del dx
+    assert torch.equal(op.qk_norm_rope(q, None, pos, freqs, out_q=q)[0][-3:], want)
+    del q
+    T, K, F = 36000, 64, 61000
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.empty((2, F, K), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    r = op.gated_ffn(x, w[0], w[1], keep=True)
+    small = op.gated_ffn(x[-300:].clone(), w[0, -500:].clone(), w[1, -500:].clone(), keep=True)
+    assert all(torch.equal(a[-300:, -500:], b) for a, b in zip(r, small))
+    dx, dwg, dwu = op.gated_ffn_back(r.h, x, w[0], w[1], r.gate, r.up)
+    assert torch.isfinite(dx).all() and torch.isfinite(dwg).all() and torch.isfinite(dwu).all()
+    part = op.gated_ffn_back(r.h[:, -256:].clone(), x, w[0, -256:].clone(), w[1, -256:].clone(), r.gate[:, -256:].clone(),
+                             r.up[:, -256:].clone(), want_dx=False)
+    for a, b in ((dwg, part[1]), (dwu, part[2])):
+        a, b = a[-256:].double(), b.double()
+        assert float((a - b).norm()) <= 2.0 ** -8 * float(b.norm())
+    del r, dx, x, w
+    m = torch.empty((4200, 512, 512), device="cuda").normal_(generator=g)
+    y = op.orthogonalise(m)
+    assert torch.equal(y[-2:], op.orthogonalise(m[-2:].clone())) and torch.equal(y[:2], op.orthogonalise(m[:2].clone()))
 
 
 def test_callers_workspace(op):
