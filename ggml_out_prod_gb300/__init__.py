@@ -14,7 +14,9 @@ quantised src0 is a uint8 tensor whose last axis holds one row's bytes.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -1118,31 +1120,59 @@ _ACTS = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, "gelu_erf": ACT_GELU_ERF,
 _Three = ctypes.c_int64 * 3
 
 
+# oop_heads and oop_heads_grad as bytes, field by field: a tenth of the time of a ctypes structure
+_pack_heads = struct.Struct("@PqqPqqPq").pack
+_pack_heads_grad = struct.Struct("@PqqPqqPPqqPq").pack
+_sizes = {}
+
+
+def _size_of(t):
+    """Bytes of an element, looked up by type."""
+    size = _sizes.get(t.dtype)
+    if size is None:
+        size = _sizes[t.dtype] = t.element_size()
+    return size
+
+
+def _rows(t, name):
+    """_matrix, short for a contiguous tensor of two dimensions."""
+    shape = t.shape
+    if len(shape) == 2 and t.is_cuda and t.is_contiguous():
+        M = shape[1]
+        return M, shape[0], M * _size_of(t)
+    return _matrix(t, name)
+
+
 def _heads(t, name):
     """(D, heads, T, byte strides of a head and of a token) of a CUDA tensor (..., H, D)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape, st, size = t.shape, t.stride(), t.element_size()
+    shape, size = t.shape, _size_of(t)
+    if len(shape) == 3:
+        T, H, D = shape
+        if t.is_contiguous():
+            return D, H, T, D * size, H * D * size
+        token, head, one = t.stride()
+        if D > 1 and one != 1:
+            raise ValueError(f"the heads of {name} must be contiguous")
+        return D, H, T, (head if H > 1 else D) * size, (token if T > 1 else H * D) * size
     if len(shape) < 2:
         raise ValueError(f"{name} must have the shape (..., heads, head size)")
+    st = t.stride()
     D, H = shape[-1], shape[-2]
     if D > 1 and st[-1] != 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    if len(shape) == 3:
-        T = shape[0]
-        step = st[0] if T > 1 else H * D
-    else:
-        T, step = 1, None
-        for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
-            if n == 1:
-                continue
-            if step is None:
-                step = d
-            elif d != step * T:
-                raise ValueError(f"the tokens of {name} must lie at one stride")
-            T *= n
+    T, step = 1, None
+    for n, d in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if n == 1:
+            continue
         if step is None:
-            step = H * D
+            step = d
+        elif d != step * T:
+            raise ValueError(f"the tokens of {name} must lie at one stride")
+        T *= n
+    if step is None:
+        step = H * D
     return D, H, T, (st[-2] if H > 1 else D) * size, step * size
 
 
@@ -1150,8 +1180,10 @@ def _like_heads(out, t, dtype, name):
     """A new contiguous tensor of t's shape, or the caller's if it fits: (tensor, strides)."""
     if out is None:
         shape = t.shape
-        out = _rt().empty(shape, dtype=dtype, device=t.device)
-        row = shape[-1] * out.element_size()
+        rt = _rt()
+        out = rt.empty_like(t) if t.dtype == dtype and t.is_contiguous() else \
+            rt.empty(shape, dtype=dtype, device=t.device)
+        row = shape[-1] * _size_of(out)
         return out, row, shape[-2] * row
     if out.shape != t.shape or out.dtype != dtype or out.device != t.device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(t.shape)} on {t.device}")
@@ -1171,7 +1203,7 @@ def _rotation(pos, freqs, T):
 
 
 def _head_weight(w, name, D):
-    return _vector(w, name, D, w.dtype) if w is not None else None
+    return 0 if w is None else _vector(w, name, D, w.dtype) or 0
 
 
 def qk_norm_rope(q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -1194,18 +1226,17 @@ def qk_norm_rope(q, k, pos, freqs, q_weight=None, k_weight=None, eps=1e-6, inter
     w_kind = _param_type(q_weight, k_weight)
     pp, pf, n_rot = _rotation(pos, freqs, T)
     yq, y_head, y_token = _like_heads(out_q, q, dtype, "out_q")
-    a = OopHeads(q.data_ptr(), head, token, yq.data_ptr(), y_head, y_token,
-                 _head_weight(q_weight, "q_weight", D), H)
+    a = _pack_heads(q.data_ptr(), head, token, yq.data_ptr(), y_head, y_token,
+                    _head_weight(q_weight, "q_weight", D), H)
     b = yk = None
     if k is not None:
         Dk, Hk, Tk, head, token = _heads(k, "k")
         if Dk != D or Tk != T or k.dtype != dtype:
             raise ValueError("q and k must have the same tokens, head size and type")
         yk, y_head, y_token = _like_heads(out_k, k, dtype, "out_k")
-        b = OopHeads(k.data_ptr(), head, token, yk.data_ptr(), y_head, y_token,
-                     _head_weight(k_weight, "k_weight", D), Hk)
-    rc = rt.lib.oop_qk_norm_rope(ctypes.byref(a), ctypes.byref(b) if b is not None else None, kind,
-                                 w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
+        b = _pack_heads(k.data_ptr(), head, token, yk.data_ptr(), y_head, y_token,
+                        _head_weight(k_weight, "k_weight", D), Hk)
+    rc = rt.lib.oop_qk_norm_rope(a, b, kind, w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
                                  _current_stream(q, k, pos, freqs, q_weight, k_weight))
     if rc != OK:
         raise OopError(rc, "oop_qk_norm_rope")
@@ -1240,9 +1271,9 @@ def qk_norm_rope_back(dq, dk, q, k, pos, freqs, q_weight=None, k_weight=None, ep
     _, _, _, d_head, d_token = _heads(dq, "dq")
     yq, y_head, y_token = _like_heads(out_q, dq, d_type, "out_q")
     dwq = empty(D, dtype=f32, device=dev) if want_dw else None
-    a = OopHeadsGrad(dq.data_ptr(), d_head, d_token, q.data_ptr(), head, token,
-                     _head_weight(q_weight, "q_weight", D), yq.data_ptr(), y_head, y_token,
-                     dwq.data_ptr() if want_dw else None, H)
+    a = _pack_heads_grad(dq.data_ptr(), d_head, d_token, q.data_ptr(), head, token,
+                         _head_weight(q_weight, "q_weight", D), yq.data_ptr(), y_head, y_token,
+                         dwq.data_ptr() if want_dw else 0, H)
     b = yk = dwk = None
     Hk = 0
     if k is not None:
@@ -1253,16 +1284,15 @@ def qk_norm_rope_back(dq, dk, q, k, pos, freqs, q_weight=None, k_weight=None, ep
             raise ValueError("a gradient and its input must have one shape")
         _, _, _, d_head, d_token = _heads(dk, "dk")
         yk, y_head, y_token = _like_heads(out_k, dk, d_type, "out_k")
-        dwk = empty(D, dtype=f32, device=dev) if want_dw else None
-        b = OopHeadsGrad(dk.data_ptr(), d_head, d_token, k.data_ptr(), head, token,
-                         _head_weight(k_weight, "k_weight", D), yk.data_ptr(), y_head, y_token,
-                         dwk.data_ptr() if want_dw else None, Hk)
+        dwk = rt.empty_like(dwq) if want_dw else None
+        b = _pack_heads_grad(dk.data_ptr(), d_head, d_token, k.data_ptr(), head, token,
+                             _head_weight(k_weight, "k_weight", D), yk.data_ptr(), y_head, y_token,
+                             dwk.data_ptr() if want_dw else 0, Hk)
     st = _current_stream(q, k, dq, dk, pos, freqs, q_weight, k_weight)
     L = rt.lib
     ws, pws, nws = _scratch(L.oop_qk_norm_rope_back_workspace_size(D, T, H, Hk) if want_dw else 0,
                             dev, workspace)
-    rc = L.oop_qk_norm_rope_back(ctypes.byref(a), ctypes.byref(b) if b is not None else None, d_kind,
-                                 kind, w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
+    rc = L.oop_qk_norm_rope_back(a, b, d_kind, kind, w_kind, pp, pf, D, n_rot, T, 1 if interleaved else 0, eps,
                                  pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_qk_norm_rope_back")
@@ -1277,19 +1307,17 @@ class GatedFfn(NamedTuple):
 
 
 def _ffn_weights(w_gate, w_up, w_type, K):
-    """(type, F, byte stride of a row) of the two projections."""
+    """(type, F, byte stride of a row, pointers) of the two projections."""
+    if w_gate.dtype != w_up.dtype or w_gate.shape != w_up.shape or w_gate.dim() != 2:
+        raise ValueError("w_gate and w_up must have two dimensions, one shape and type")
     if w_type is None:
         w_type = _plain_type(w_gate.dtype, "w_gate")
-    for w, name in ((w_gate, "w_gate"), (w_up, "w_up")):
-        if w.dim() != 2:
-            raise ValueError(f"{name} must have two dimensions")
-        _check_src0(w, w_type, name)
-    if w_gate.shape != w_up.shape or w_gate.dtype != w_up.dtype:
-        raise ValueError("w_gate and w_up must have one shape and type")
-    M, F, nb = _matrix(w_gate, "w_gate")
-    nb_up = _matrix(w_up, "w_up")[2]
-    if F > 1 and nb != nb_up:
-        raise ValueError("the rows of w_gate and w_up must lie at one stride")
+    else:
+        _check_src0(w_gate, w_type, "w_gate")
+    M, F, nb = _rows(w_gate, "w_gate")
+    if F > 1 and _rows(w_up, "w_up")[2] != nb or not w_up.is_cuda:
+        raise ValueError("w_gate and w_up must be CUDA tensors whose rows lie at one stride")
+    row = M if w_type in _BLOCKS else M * _size_of(w_gate)
     if w_type in _BLOCKS:
         qk, nbytes = _BLOCKS[w_type]
         if M % nbytes:
@@ -1297,12 +1325,8 @@ def _ffn_weights(w_gate, w_up, w_type, K):
         M = M // nbytes * qk
     if M != K:
         raise ValueError("x and the weights must have one row length")
-    return w_type, F, nb
-
-
-def _apart(t, nb):
-    """Whether rows start and step by multiples of 16 bytes and do not overlap."""
-    return t.data_ptr() % 16 == 0 and nb % 16 == 0 and nb >= t.shape[-1] * t.element_size()
+    pg, pu = w_gate.data_ptr(), w_up.data_ptr()
+    return w_type, F, nb, pg, pu, not ((pg | pu | nb) & 15) and nb >= row
 
 
 def _act_of(act):
@@ -1325,24 +1349,29 @@ def gated_ffn(x, w_gate, w_up, act="silu", keep=False, w_type=None, out=None, wo
     if stream is not None:
         return _on_stream(stream, lambda: gated_ffn(x, w_gate, w_up, act, keep, w_type, out,
                                                     workspace), x, w_gate, w_up, out, workspace)
-    K, T, nb_x = _matrix(x, "x")
-    kind = _plain_type(x.dtype, "x")
+    K, T, nb_x = _rows(x, "x")
+    dtype, device = x.dtype, x.device
+    kind = _plain_type(dtype, "x")
     a_kind = _act_of(act)
-    w_kind, F, nb_w = _ffn_weights(w_gate, w_up, w_type, K)
-    shape = tuple(x.shape[:-1]) + (F,)
-    h, nb_h = _output(out, shape, x.dtype, x.device)
-    gate = rt.empty(shape, dtype=x.dtype, device=x.device) if keep else None
-    up = rt.empty(shape, dtype=x.dtype, device=x.device) if keep else None
+    w_kind, F, nb_w, pg, pu, apart = _ffn_weights(w_gate, w_up, w_type, K)
+    size, px = _size_of(x), x.data_ptr()
+    shape = x.shape[:-1] + (F,)
+    if out is None:
+        h, nb_h = rt.empty(shape, dtype=dtype, device=device), F * size
+    else:
+        h, nb_h = _output(out, shape, dtype, device)
+    gate = up = p_gate = p_up = None
+    if keep:
+        gate = rt.empty(shape, dtype=dtype, device=device)
+        up = rt.empty_like(gate)
+        p_gate, p_up = gate.data_ptr(), up.data_ptr()
     st = _current_stream(x, w_gate, w_up)
     ne = _Three(K, F, T)
     L = rt.lib
-    aligned = _apart(x, nb_x) and _apart(w_gate, nb_w) and _apart(w_up, nb_w)
-    ws, pws, nws = _scratch(L.oop_gated_ffn_workspace_size(kind, w_kind, ne, aligned), x.device,
-                            workspace)
-    rc = L.oop_gated_ffn(x.data_ptr(), kind, nb_x, w_gate.data_ptr(), w_up.data_ptr(), w_kind, nb_w,
-                         h.data_ptr(), nb_h, gate.data_ptr() if keep else None,
-                         up.data_ptr() if keep else None, F * x.element_size(), ne, a_kind, pws,
-                         nws, st)
+    need = L.oop_gated_ffn_workspace_size(kind, w_kind, ne, apart and not ((px | nb_x) & 15) and nb_x >= K * size)
+    ws, pws, nws = _scratch(need, device, workspace) if need else (None, None, 0)
+    rc = L.oop_gated_ffn(px, kind, nb_x, pg, pu, w_kind, nb_w, h.data_ptr(), nb_h, p_gate, p_up, F * size, ne,
+                         a_kind, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_gated_ffn")
     return GatedFfn(h, gate, up)
@@ -1359,33 +1388,40 @@ def gated_ffn_back(dh, x, w_gate, w_up, gate, up, act="silu", want_dx=True, want
         return _on_stream(stream, lambda: gated_ffn_back(dh, x, w_gate, w_up, gate, up, act,
                                                          want_dx, want_dw, w_type, out, workspace),
                           dh, x, w_gate, w_up, gate, up, out, workspace)
-    K, T, nb_x = _matrix(x, "x")
-    kind, d_kind = _plain_type(x.dtype, "x"), _plain_type(dh.dtype, "dh")
+    K, T, nb_x = _rows(x, "x")
+    dtype, d_type, device = x.dtype, dh.dtype, x.device
+    kind, d_kind = _plain_type(dtype, "x"), _plain_type(d_type, "dh")
     a_kind = _act_of(act)
-    w_kind, F, nb_w = _ffn_weights(w_gate, w_up, w_type, K)
-    shape = tuple(x.shape[:-1]) + (F,)
-    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have the shape {shape}")
-    if gate.dtype != x.dtype or up.dtype != x.dtype:
+    w_kind, F, nb_w, pg, pu, apart = _ffn_weights(w_gate, w_up, w_type, K)
+    size, px = _size_of(x), x.data_ptr()
+    shape = x.shape[:-1] + (F,)
+    if dh.shape != shape or gate.shape != shape or up.shape != shape:
+        raise ValueError(f"dh, gate and up must have the shape {tuple(shape)}")
+    if gate.dtype != dtype or up.dtype != dtype:
         raise ValueError("gate and up must have x's type")
-    nb_dh, nb_gu = _matrix(dh, "dh")[2], _matrix(gate, "gate")[2]
-    if T > 1 and _matrix(up, "up")[2] != nb_gu:
+    nb_dh, nb_gu = _rows(dh, "dh")[2], _rows(gate, "gate")[2]
+    if _rows(up, "up")[2] != nb_gu and T > 1:
         raise ValueError("the rows of gate and up must lie at one stride")
-    dx, nb_dx = _output(out, tuple(x.shape), dh.dtype, x.device) if want_dx else (None, 0)
-    dwg = rt.empty((F, K), dtype=dh.dtype, device=x.device) if want_dw else None
-    dwu = rt.empty((F, K), dtype=dh.dtype, device=x.device) if want_dw else None
+    dx = dwg = dwu = p_dx = p_dwg = p_dwu = None
+    nb_dx, d_size = 0, _size_of(dh)
+    if want_dx:
+        if out is None:
+            dx, nb_dx = rt.empty(x.shape, dtype=d_type, device=device), K * d_size
+        else:
+            dx, nb_dx = _output(out, x.shape, d_type, device)
+        p_dx = dx.data_ptr()
+    if want_dw:
+        dwg = rt.empty((F, K), dtype=d_type, device=device)
+        dwu = rt.empty_like(dwg)
+        p_dwg, p_dwu = dwg.data_ptr(), dwu.data_ptr()
     st = _current_stream(dh, x, w_gate, w_up, gate, up)
     ne = _Three(K, F, T)
     L = rt.lib
-    aligned = _apart(x, nb_x) and _apart(w_gate, nb_w) and _apart(w_up, nb_w)
-    ws, pws, nws = _scratch(L.oop_gated_ffn_back_workspace_size(d_kind, kind, w_kind, ne, aligned),
-                            x.device, workspace)
-    rc = L.oop_gated_ffn_back(dh.data_ptr(), d_kind, nb_dh, x.data_ptr(), kind, nb_x,
-                              w_gate.data_ptr(), w_up.data_ptr(), w_kind, nb_w, gate.data_ptr(),
-                              up.data_ptr(), nb_gu, dx.data_ptr() if want_dx else None, nb_dx,
-                              dwg.data_ptr() if want_dw else None,
-                              dwu.data_ptr() if want_dw else None, K * dh.element_size(), ne,
+    need = L.oop_gated_ffn_back_workspace_size(d_kind, kind, w_kind, ne,
+                                               apart and not ((px | nb_x) & 15) and nb_x >= K * size)
+    ws, pws, nws = _scratch(need, device, workspace)
+    rc = L.oop_gated_ffn_back(dh.data_ptr(), d_kind, nb_dh, px, kind, nb_x, pg, pu, w_kind, nb_w,
+                              gate.data_ptr(), up.data_ptr(), nb_gu, p_dx, nb_dx, p_dwg, p_dwu, K * d_size, ne,
                               a_kind, pws, nws, st)
     if rc != OK:
         raise OopError(rc, "oop_gated_ffn_back")
@@ -1398,8 +1434,11 @@ def _matrices(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    shape, st, size = t.shape, t.stride(), t.element_size()
+    shape, size = t.shape, _size_of(t)
     M, N = shape[-2], shape[-1]
+    if t.is_contiguous():
+        return (N, M, t.numel() // (M * N) if M and N else shape[:-2].numel()), (N * size, M * N * size)
+    st = t.stride()
     if N > 1 and st[-1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
     B, step = 1, None
@@ -1413,6 +1452,21 @@ def _matrices(t, name):
         B *= n
     row = st[-2] if M > 1 else N
     return (N, M, B), (row * size, (M * row if step is None else step) * size)
+
+
+def _coefficients(coefs, steps):
+    """One triple, or one for each step, as floats for the library."""
+    flat = [float(v) for c in coefs for v in (c if hasattr(c, "__len__") else (c,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError("coefs must be one triple, or one for each step")
+    return _floats(max(1, len(flat)))(*flat)
+
+
+@functools.lru_cache(maxsize=64)
+def _floats(n):
+    return ctypes.c_float * n
 
 
 def orthogonalise(x, steps=5, coefs=None, eps=1e-7, scale=1.0, out_dtype=None, out=None,
@@ -1429,21 +1483,17 @@ def orthogonalise(x, steps=5, coefs=None, eps=1e-7, scale=1.0, out_dtype=None, o
                                                         workspace), x, out, workspace)
     ne, nb = _matrices(x, "x")
     kind = _plain_type(x.dtype, "x")
-    table = None
-    if coefs is not None:
-        flat = [float(v) for c in coefs for v in (c if hasattr(c, "__len__") else (c,))]
-        if len(flat) == 3:
-            flat = flat * steps
-        if len(flat) != 3 * steps:
-            raise ValueError("coefs must be one triple, or one for each step")
-        table = (ctypes.c_float * max(1, len(flat)))(*flat)
+    table = None if coefs is None else _coefficients(coefs, steps)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else x.dtype
     if out is None:
         out = rt.empty(x.shape, dtype=out_dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != out_dtype or out.device != x.device:
-        raise ValueError(f"out must be a {out_dtype} tensor of shape {tuple(x.shape)} on {x.device}")
-    nb_y = _matrices(out, "out")[1]
+        row = ne[0] * _size_of(out)
+        nb_y = (row, ne[1] * row)
+    else:
+        if out.shape != x.shape or out.dtype != out_dtype or out.device != x.device:
+            raise ValueError(f"out must be a {out_dtype} tensor of shape {tuple(x.shape)} on {x.device}")
+        nb_y = _matrices(out, "out")[1]
     st = _current_stream(x)
     ne = _Three(*ne)
     L = rt.lib
