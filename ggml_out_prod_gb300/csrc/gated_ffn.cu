@@ -503,71 +503,67 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
 }
 
 // Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the
-// waves (a narrow tile reads A as often as a wide one for half the sums).  The SMs are
-// a GB300's, so that sizes can be asked for without one.
-constexpr int64_t kPairs = 76;
-
+// waves (a narrow tile reads A as often as a wide one for half the sums).
 bool narrow_tiles(int64_t M, int64_t N, int64_t batches, int wide_cols) {
     auto waves = [&](int64_t cols) {
         const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
-        return (tiles + kPairs - 1) / kPairs;
+        return (tiles + pair::kPairs - 1) / pair::kPairs;
     };
     return waves(wide_cols / 2) * 23 < waves(wide_cols) * 40;
 }
 
-// Parts of k of a product whose tiles fill less than half of the SMs, each of eight
-// stages or more: 333 x 1001 x 3074 in f32 has 16 tiles, whose 50 stages would take 40 us.
-int parts_of_k(int64_t M, int64_t N, int64_t K, int64_t batches, int64_t segments) {
-    const int64_t cols = narrow_tiles(M, N, batches, 256) ? 128 : 256;
-    const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
-    const int64_t blocks = (K + pair::kDepth - 1) / pair::kDepth * segments;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / std::max<int64_t>(tiles, 1), blocks / 8, 16})));
-}
-size_t parts_bytes(int parts, int64_t M, int64_t N, int64_t batches) {
-    return parts > 1 ? round256(static_cast<size_t>(parts) * static_cast<size_t>(M * N * batches) * 4) : 0;
+// A gradient's product: narrow tiles or wide ones, and which go in parts of k.  333 x 1001
+// x 3074 in f32 has 16 tiles, whose 50 stages would take 40 us; 8192 x 2560 x 19456 fills four
+// waves and a fifth of the next, which as parts takes a quarter of its time.
+struct GradientPlan {
+    bool narrow;
+    pair::TileMap map;
+    size_t slots;
+};
+GradientPlan gradient_plan(int64_t M, int64_t N, int64_t K, int planes_a, int planes_b, int64_t batches, int64_t segments) {
+    GradientPlan p;
+    const int64_t stages = (K + pair::kDepth - 1) / pair::kDepth * segments;
+    p.narrow = narrow_tiles(M, N, batches, 256);
+    const int64_t cols = p.narrow ? 128 : 256;
+    p.map = pair::tile_map(M, N, cols, stages, pair::count_terms(planes_a, planes_b), batches, false, true);
+    p.slots = pair::slot_bytes(p.map, batches, cols);
+    return p;
 }
 
-// Sums of the parts {N, M} of each batch, in their order, to p0 (and p1: the second batch's).
-template <int TYPE>
-__global__ void __launch_bounds__(256) join_kernel(const float *parts, int count, int64_t M, int64_t N, char *p0, char *p1, int64_t nb) {
+// Sums of the parts to p0 (and p1: the second batch's).
+template <int TYPE, int BN>
+__global__ void __launch_bounds__(256) join_kernel(const pair::TileMap map, const float *slots, int64_t M, int64_t N, char *p0, char *p1,
+                                                   int64_t nb) {
     let_next_start();
     wait_previous();
-    const float *src = parts + blockIdx.y * count * M * N;
-    char *dst = blockIdx.y ? p1 : p0;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < M * N; i += gridDim.x * 256LL) {
-        float v = src[i];
-        for (int k = 1; k < count; ++k) v += src[k * M * N + i];
-        const int64_t r = i / N;
-        row_of<TYPE>(dst, nb, r)[i - r * N] = from_float<TYPE>(v);
-    }
+    pair::each_joined<BN>(map, slots, [&](int z, int64_t r, int64_t c, float4 v) {
+        if (r >= M) return;
+        auto *row = row_of<TYPE>(z ? p1 : p0, nb, r);
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < N) row[c + i] = from_float<TYPE>(f[i]);
+    });
 }
 
-template <int EPI, bool FOLD>
-cudaError_t product(const pair::Spec &s, int *status, cudaStream_t st) {
-    const int wide_cols = EPI == pair::kGate ? 128 : 256;
-    return narrow_tiles(s.M, s.N, s.batches, wide_cols) ? pair::launch<EPI, FOLD, 128>(s, status, st)
-                                                        : pair::launch<EPI, FOLD, 256>(s, status, st);
-}
-
-// A gradient's product, in parts of k where that fills the SMs.
-template <bool FOLD>
-cudaError_t gradient(pair::Spec s, void *workspace, int *status, cudaStream_t st) {
-    const int parts = parts_of_k(s.M, s.N, s.K, s.batches, s.segments);
-    if (parts == 1) return product<pair::kPlain, FOLD>(s, status, st);
-    const pair::Out out = s.out;
-    s.splits = parts;
-    s.out.p0 = workspace, s.out.p1 = nullptr;
-    s.out.nb0 = s.N * 4, s.out.batch = s.M * s.N * 4;
-    s.out.type = OOP_TYPE_F32;
-    s.out.wide = s.N % 4 == 0;
-    const cudaError_t e = product<pair::kPlain, FOLD>(s, status, st);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(blocks_of(s.M * s.N), static_cast<unsigned>(s.batches));
-    const float *p = static_cast<const float *>(workspace);
-    char *p0 = static_cast<char *>(out.p0), *p1 = static_cast<char *>(out.p1);
+template <int TYPE, int BN>
+cudaError_t launch_join(const pair::TileMap &m, const pair::Spec &s, cudaStream_t st) {
     ++g_kernel_launches;
-    return out.type == OOP_TYPE_F32 ? launch_dependent(join_kernel<OOP_TYPE_F32>, grid, 256, 0, st, p, parts, s.M, s.N, p0, p1, out.nb0)
-                                    : launch_dependent(join_kernel<OOP_TYPE_BF16>, grid, 256, 0, st, p, parts, s.M, s.N, p0, p1, out.nb0);
+    return launch_dependent(join_kernel<TYPE, BN>, dim3(static_cast<unsigned>(pair::kJoinCtas * pair::tiles_in_parts(m, s.batches))), 256, 0, st, m,
+                            static_cast<const float *>(s.out.slots), s.M, s.N, static_cast<char *>(s.out.p0),
+                            static_cast<char *>(s.out.p1), s.out.nb0);
+}
+
+template <bool FOLD>
+cudaError_t gradient(pair::Spec s, void *slots, int *status, cudaStream_t st) {
+    const GradientPlan p = gradient_plan(s.M, s.N, s.K, s.planes_a, s.planes_b, s.batches, s.segments);
+    s.in_parts = true;
+    s.out.slots = static_cast<float *>(slots);
+    const cudaError_t e = p.narrow ? pair::launch<pair::kPlain, FOLD, 128>(s, status, st) : pair::launch<pair::kPlain, FOLD, 256>(s, status, st);
+    if (e != cudaSuccess || p.map.parts == 1) return e;
+    if (s.out.type == OOP_TYPE_F32)
+        return p.narrow ? launch_join<OOP_TYPE_F32, 128>(p.map, s, st) : launch_join<OOP_TYPE_F32, 256>(p.map, s, st);
+    return p.narrow ? launch_join<OOP_TYPE_BF16, 128>(p.map, s, st) : launch_join<OOP_TYPE_BF16, 256>(p.map, s, st);
 }
 
 cudaError_t zero_rows(void *p, int64_t nb, int64_t row_bytes, int64_t rows, cudaStream_t st) {
@@ -631,7 +627,8 @@ size_t oop_gated_ffn_back_workspace_size(int dh_type, int x_type, int w_type, co
     const BackForms f = back_forms(dh_type, x_type, w_type, ne[2], aligned != 0);
     const int64_t K = ne[0], F = ne[1], T = ne[2];
     // the parts of the two products follow each other in one place
-    const size_t parts = std::max(parts_bytes(parts_of_k(T, K, F, 1, 2), T, K, 1), parts_bytes(parts_of_k(F, K, T, 2, 1), F, K, 2));
+    const size_t parts = std::max(gradient_plan(T, K, F, f.d.planes, f.w.planes, 1, 2).slots,
+                                  gradient_plan(F, K, T, f.d.planes, f.x.planes, 2, 1).slots);
     return form_bytes(f.d, F, 2 * T) + form_bytes(f.x, K, T) + 2 * form_bytes(f.w, K, F) + parts;
 }
 
@@ -688,7 +685,9 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     s.out.type = x_type, s.out.act = act;
     s.out.wide = F * size % 16 == 0 && rows_aligned(h, nb_h, T) &&
                  (!gate || (rows_aligned(gate, nb_gu, T) && rows_aligned(up, nb_gu, T)));
-    e = x_type == OOP_TYPE_F32 ? product<pair::kGate, true>(s, status, st) : product<pair::kGate, false>(s, status, st);
+    const bool narrow = narrow_tiles(T, F, 1, 128);
+    if (x_type == OOP_TYPE_F32) e = narrow ? pair::launch<pair::kGate, true, 128>(s, status, st) : pair::launch<pair::kGate, true, 256>(s, status, st);
+    else e = narrow ? pair::launch<pair::kGate, false, 128>(s, status, st) : pair::launch<pair::kGate, false, 256>(s, status, st);
     return cuda_status(e);
 }
 

@@ -506,19 +506,18 @@ size_t plane_pair_bytes(int64_t cols, int64_t rows, int64_t B) {
     return round256(static_cast<size_t>(2 * B * rows * round8(cols)) * 2);
 }
 
-constexpr int64_t kPairs = 76;                             // of SMs: sizes can be asked for without a GPU
-
-// Parts of k of A = X X' where its tiles fill less than half of the SMs (76 pairs), each of
-// eight stages or more: 200 x 2560 is one tile of 40 stages, 32 us.
-int parts_of_a(int64_t n, int64_t deep, int64_t B) {
-    const int64_t t = (n + 255) / 256, tiles = t * (t + 1) / 2 * B, blocks = (deep + pair::kDepth - 1) / pair::kDepth;
-    return blocks < 24 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, blocks / 8, 16})));
+// The tiles of A = X X': those that would leave SMs idle go in parts of k (200 x 2560 is one tile
+// of 40 stages, 32 us).
+pair::TileMap map_of_a(int64_t n, int64_t deep, int64_t B) {
+    return pair::tile_map(n, n, 256, (deep + pair::kDepth - 1) / pair::kDepth, 3, B, true, true);
 }
+
 // About the time of a product in microseconds: 9 for a launch, 0.8 for each stage of a wave of
 // tiles, 6 for the join of parts.
 double product_time(int64_t tiles, int64_t k, int parts) {
-    const int64_t blocks = (k + pair::kDepth - 1) / pair::kDepth, waves = (tiles * parts + kPairs - 1) / kPairs;
-    return 9.0 + 0.8 * static_cast<double>(waves * ((blocks + parts - 1) / parts)) + (parts > 1 ? 6.0 : 0.0);
+    const int64_t blocks = (k + pair::kDepth - 1) / pair::kDepth, waves = tiles / pair::kPairs;
+    const int64_t last = tiles % pair::kPairs ? (blocks + parts - 1) / parts : 0;
+    return 9.0 + 0.8 * static_cast<double>(waves * blocks + last) + (parts > 1 ? 6.0 : 0.0);
 }
 
 // B matrices of two planes: [2][B][rows][pitch].
@@ -560,32 +559,27 @@ double rounding_of_a(int steps, const float *coefs) {
 bool on_a_alone(int64_t n, int64_t deep, int64_t B, int steps, const float *coefs) {
     if (steps < 2 || rounding_of_a(steps, coefs) > 0x1p-9) return false;
     const int64_t t = (n + 255) / 256, half = t * (t + 1) / 2 * B, whole = t * ((deep + 255) / 256) * B;
-    const double first = product_time(half, deep, parts_of_a(n, deep, B)), square = product_time(half, n, 1), with_x = product_time(whole, n, 1);
+    const double first = product_time(half, deep, map_of_a(n, deep, B).parts), square = product_time(half, n, 1), with_x = product_time(whole, n, 1);
     return first + (4 * steps - 3) * square + with_x < steps * (first + square + with_x);
 }
 
-size_t parts_bytes(int64_t n, int64_t deep, int64_t B) {
-    const int parts = parts_of_a(n, deep, B);
-    return parts > 1 ? round256(static_cast<size_t>(parts) * static_cast<size_t>(B * n * n) * 4) : 0;
-}
-
-// The parts {n, n} of each matrix summed in their order, on and above the diagonal's tiles, scaled
-// and with the shift on the diagonal, as planes.
-__global__ void __launch_bounds__(256) join_kernel(const float *parts, int count, int64_t n, int64_t pitch, float alpha, float diag,
-                                                   __half *hi, __half *lo) {
+// The tiles of A in parts: summed, scaled, with the shift on the diagonal, as planes.
+__global__ void __launch_bounds__(256) join_kernel(const pair::TileMap map, const float *slots, int64_t n, int64_t pitch, float alpha,
+                                                   float diag, __half *hi, __half *lo) {
     let_next_start();
     wait_previous();
-    const float *src = parts + blockIdx.y * count * n * n;
-    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < n * n; i += gridDim.x * 256LL) {
-        const int64_t r = i / n, c = i - r * n;
-        if (c / pair::kTileM < r / pair::kTileM) continue;
-        float v = src[i];
-        for (int k = 1; k < count; ++k) v += src[k * n * n + i];
-        v = v * alpha + (r == c ? diag : 0.f);
-        const int64_t at = (blockIdx.y * n + r) * pitch + c;
-        hi[at] = __float2half_rn(v);
-        lo[at] = __float2half_rn(v - __half2float(hi[at]));
-    }
+    pair::each_joined<256>(map, slots, [&](int z, int64_t r, int64_t c, float4 v) {
+        if (r >= n) return;
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        const int64_t at = (z * n + r) * pitch + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (c + i >= n) continue;
+            const float one = f[i] * alpha + (r == c + i ? diag : 0.f);
+            hi[at + i] = __float2half_rn(one);
+            lo[at + i] = __float2half_rn(one - __half2float(hi[at + i]));
+        }
+    });
 }
 
 // A product of two such operands over all matrices.
@@ -623,7 +617,7 @@ size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     if (small_ctas(n, std::max(ne[0], ne[1]))) return 0;
     const size_t x = plane_pair_bytes(ne[0], ne[1], ne[2]), a = plane_pair_bytes(n, n, ne[2]);
     return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(Squares)) + std::max(2 * x + 2 * a, x + 5 * a) +
-           parts_bytes(n, std::max(ne[0], ne[1]), ne[2]);
+           pair::slot_bytes(map_of_a(n, std::max(ne[0], ne[1]), ne[2]), ne[2], 256);
 }
 
 int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y, int y_type, const int64_t nb_y[2],
@@ -688,30 +682,23 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     if (e == cudaSuccess) e = steps == 0 ? start(start_kernel<true>, nullptr, 0) : start(start_kernel<false>, X.hi(), X.pitch());
     g_kernel_launches = 2;
     // A = X X', or X' X, with a shift in its diagonal
-    float *parts_at = reinterpret_cast<float *>(
+    float *slots = reinterpret_cast<float *>(
         X.p + std::max(2 * plane_pair_bytes(N, M, B) + 2 * plane_pair_bytes(n, n, B), plane_pair_bytes(N, M, B) + 5 * plane_pair_bytes(n, n, B)));
-    const int k_parts = parts_of_a(n, deep, B);
+    const pair::TileMap map = map_of_a(n, deep, B);
     auto square_of = [&](const Planes &x_now, const Planes &d, double shift) {
+        constexpr float kAlpha = kScaleA / (kScaleX * kScaleX);
+        const float diag = static_cast<float>(shift * kScaleA);
         pair::Spec p = product_of(x_now, tall, x_now, tall, n, n, deep);
         p.symmetric = true;
-        if (k_parts == 1) {
-            to_planes(p, d, kScaleA / (kScaleX * kScaleX));
-            p.out.diag = static_cast<float>(shift * kScaleA);
-            return pair::launch<pair::kSplit, true, 256>(p, status, st);
-        }
-        p.splits = k_parts;
-        p.out.p0 = parts_at;
-        p.out.nb0 = n * 4;
-        p.out.batch = n * n * 4;
-        p.out.type = OOP_TYPE_F32;
-        p.out.alpha = 1.f;
-        p.out.wide = n % 4 == 0;
-        const cudaError_t err = pair::launch<pair::kPlain, true, 256>(p, status, st);
-        if (err != cudaSuccess) return err;
+        p.in_parts = true;
+        p.out.slots = slots;
+        to_planes(p, d, kAlpha);
+        p.out.diag = diag;
+        const cudaError_t err = pair::launch<pair::kSplit, true, 256>(p, status, st);
+        if (err != cudaSuccess || map.parts == 1) return err;
         ++g_kernel_launches;
-        return launch_dependent(join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n * n + 255) / 256, 1024)), nb), 256, 0, st,
-                                static_cast<const float *>(parts_at), k_parts, n, d.pitch(), kScaleA / (kScaleX * kScaleX),
-                                static_cast<float>(shift * kScaleA), d.hi(), d.lo());
+        return launch_dependent(join_kernel, dim3(static_cast<unsigned>(pair::kJoinCtas * pair::tiles_in_parts(map, B))), 256, 0, st, map,
+                                static_cast<const float *>(slots), n, d.pitch(), kAlpha, diag, d.hi(), d.lo());
     };
     auto last_product = [&](pair::Spec p, float alpha) {
         p.out.p0 = yp;

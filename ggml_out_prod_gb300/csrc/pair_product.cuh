@@ -24,6 +24,8 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "activation.cuh"
 #include "oop_internal.cuh"
 #include "rows.cuh"
@@ -49,6 +51,7 @@ enum Epilogue {
 struct Out {
     void *p0, *p1, *p2;            // matrix (p1: that of batch 1, or NULL); h, gate, up
     int64_t nb0, nb1, batch;       // bytes between rows of p0 (kSplit: of C), of p1 and p2; between batches of p0 (or C)
+    float *slots;                  // where the parts' sums go
     const __half *c_hi, *c_lo;     // kSplit: C's planes, laid out as the result's
     const float *row_scale;        // kGate with FOLD: factors of the rows, and of the gates' and
     const float *col_scale[2];     // the ups' columns, powers of two
@@ -58,6 +61,15 @@ struct Out {
     int wide;                      // 16-byte stores are allowed
 };
 
+// The tiles of a product.  Those from `whole` on are taken in parts of k, each an
+// item of its own whose sums go to a slot of 256 x BN floats for another kernel to join: all tiles where they are
+// few, else the last wave's where it would leave more than half of the SMs idle.
+struct TileMap {
+    int m_tiles, n_tiles, tiles;   // tiles of a batch
+    int symmetric;                 // only tiles on and above the diagonal
+    int whole, parts;
+};
+
 struct Job {
     CUtensorMap a, b[2];
     CUtensorMap a_turned, b_turned;   // a_half, b_half: the same matrix with its rows as k
@@ -65,16 +77,15 @@ struct Job {
     Out out;
     int *status;
     int64_t M, N;                  // kGate: N features, BN / 2 of them to a tile
-    int m_tiles, n_tiles, tiles, batches;   // tiles of a batch
+    TileMap map;
+    int items;                     // of the map
     int k_blocks, segments;        // stages of a segment; with two, b[s] and a's plane + s * a_seg
-    int splits;                    // parts of k, each a tile of its own, summed by another kernel
     int planes_a, planes_b, terms;
     int a_plane, a_batch, a_seg, b_plane, b_batch;   // third coordinates
     int term_a[kMaxTerms], term_b[kMaxTerms];
     int stages, stage_bytes;
     int sum_blocks;                // stages of one sum in tensor memory
     int a_rows, b_rows;            // the operand lies with its rows contiguous
-    int symmetric;                 // only tiles on and above the diagonal
     int a_half, b_half;            // the operand is a result of that kind
     uint32_t idesc;
 };
@@ -261,22 +272,25 @@ __device__ __forceinline__ void store_block(int type, uint8_t *stage, const floa
 
 struct Tile {
     int m, n, z;                   // z: batch
-    int part;                      // of k
+    int part, parts;               // of k
+    int slot;                      // of the part's sums; -1: a whole tile
 };
 
-// First stage of a part of k.
-__device__ __forceinline__ int part_start(const Job &j, int part) {
-    return static_cast<int>(static_cast<int64_t>(j.k_blocks) * j.segments * part / j.splits);
-}
-
-// Tile i: batches outermost, then bands of eight row tiles, so that the tiles of a
+// Item i: batches outermost, then bands of eight row tiles, so that the tiles of a
 // wave share their operands in L2.
-__device__ __forceinline__ Tile tile_of(const Job &j, int i) {
+__device__ __forceinline__ Tile tile_of(const TileMap &j, int i) {
     Tile t;
+    t.part = 0;
+    t.parts = 1;
+    t.slot = -1;
+    if (i >= j.whole) {
+        t.slot = i - j.whole;
+        t.part = t.slot % j.parts;
+        t.parts = j.parts;
+        i = j.whole + t.slot / j.parts;
+    }
     t.z = i / j.tiles;
     i -= t.z * j.tiles;
-    t.part = t.z % j.splits;
-    t.z /= j.splits;
     if (j.symmetric) {                                     // row tile m has n_tiles - m tiles
         t.m = 0;
         for (int left = j.n_tiles; i >= left; --left) {
@@ -291,6 +305,14 @@ __device__ __forceinline__ Tile tile_of(const Job &j, int i) {
     t.n = rest / rows;
     t.m = 8 * band + rest - t.n * rows;
     return t;
+}
+
+// First stage of a tile's part of k (end: of the next one).
+__device__ __forceinline__ int first_stage(const Job &j, const Tile &t) {
+    return static_cast<int>(static_cast<int64_t>(j.k_blocks) * j.segments * t.part / t.parts);
+}
+__device__ __forceinline__ int end_stage(const Job &j, const Tile &t) {
+    return static_cast<int>(static_cast<int64_t>(j.k_blocks) * j.segments * (t.part + 1) / t.parts);
 }
 
 // Whether a symmetric matrix of which only the tiles on and above the diagonal exist has to be
@@ -404,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     let_next_start();
     wait_previous();
     const uint32_t stage0 = ptx::smem_u32(smem) + kHeader;
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.tiles * j.batches * j.splits;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, total = j.items;
     // one second, and two microseconds for every product that a wait may be for
     const uint64_t limit = 1000000000ull + 2000ull * static_cast<uint64_t>(j.sum_blocks) * j.terms * 4;
     bool timed_out = false;
@@ -435,12 +457,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             int stage = 0;
             uint32_t phase = 0;
             for (int i = first; i < total; i += step) {
-                const Tile t = tile_of(j, i);
+                const Tile t = tile_of(j.map, i);
                 const int am = t.m * kTileM + static_cast<int>(rank) * 128;
                 const int bn = EPI == kGate ? t.n * (BN / 2) : t.n * BN + static_cast<int>(rank) * (BN / 2);
                 bool ok = true;
-                const int end = part_start(j, t.part + 1);
-                for (int kb = part_start(j, t.part); kb < end && ok; ++kb) {
+                const int end = end_stage(j, t);
+                for (int kb = first_stage(j, t); kb < end && ok; ++kb) {
                     ok = wait(&sh.empty[stage], phase ^ 1);
                     if (!ok) break;
                     const uint32_t bar = leader_addr(&sh.full[stage]);
@@ -484,10 +506,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
-                const Tile t = tile_of(j, i);
-                const int end = part_start(j, t.part + 1);
+                const Tile t = tile_of(j.map, i);
+                const int end = end_stage(j, t);
                 if constexpr (FOLD) {
-                    for (int kb = part_start(j, t.part); kb < end && ok; ++kb) {
+                    for (int kb = first_stage(j, t); kb < end && ok; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         const uint32_t sa = stage0 + stage * j.stage_bytes, sb = sa + j.planes_a * kPlaneBytes;
                         const int a_rows = j.a_rows | below(j.a_half, kb * kDepth, t.m);
@@ -522,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     if (!ok) break;
                     ptx::tc_fence_after();
                     uint32_t add = 0;
-                    for (int kb = part_start(j, t.part); kb < end; ++kb) {
+                    for (int kb = first_stage(j, t); kb < end; ++kb) {
                         ok = wait(&sh.full[stage], phase);
                         if (!ok) break;
                         ptx::tc_fence_after();
@@ -571,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         // The code from here to the stores is kept short: a tile runs it once, and unrolled for a
         // whole row and every type it took 28 us to be fetched, twice a small call's products.
         for (int i = first; i < total && ok; i += step) {
-            const Tile t = tile_of(j, i);
+            const Tile t = tile_of(j.map, i);
             const int64_t r0 = static_cast<int64_t>(t.m) * kTileM + rank * 128 + quarter * 32, rows = j.M - r0;
             // a gate's pieces: the gates and ups of 32 features
             auto gate = [&](float (&g)[32], float (&u)[32], int64_t f) {
@@ -610,13 +632,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
             };
             auto plain = [&](float (&v)[32], int64_t c) {
                 if (rows <= 0 || c >= j.N) return;
-                if constexpr (EPI == kSplit) {
+                if (t.slot >= 0) {
+                    if constexpr (EPI == kSplit) {
+                        if (lane == 0) ptx::bulk_wait_read();                  // the last tile's copies have left the stage
+                        __syncwarp();
+                    }
+                    const int r = rank * 128 + quarter * 32, at = static_cast<int>(c - static_cast<int64_t>(t.n) * BN);
+                    char *slot = reinterpret_cast<char *>(j.out.slots + (static_cast<int64_t>(t.slot) * kTileM + r) * BN + at);
+                    store_block<OOP_TYPE_F32>(stage_out, v, slot, BN * 4, 32, 32, 1);
+                } else if constexpr (EPI == kSplit) {
                     store_split(stage_out, &j.result, j.out, v, t.z, r0, c, j.M);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
-                    char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1)
-                                                 : static_cast<char *>(j.out.p0) + (t.z * j.splits + t.part) * j.out.batch;
+                    char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1) : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
                     store_block(j.out.type, stage_out, v, base + r0 * j.out.nb0 + c * element, j.out.nb0, rows, j.N - c, j.out.wide);
                 }
             };
@@ -624,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 uint64_t sums[kCols / 2];                  // of each half: 64 columns, or 32 gates and 32 ups
 #pragma unroll
                 for (int c = 0; c < kCols / 2; ++c) sums[c] = 0;
-                for (int kb = part_start(j, t.part); kb < part_start(j, t.part + 1) && ok; ++kb) {
+                for (int kb = first_stage(j, t); kb < end_stage(j, t) && ok; ++kb) {
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h) {
                         if (!sums_ready()) break;
@@ -688,7 +717,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                      : "memory");
 }
 
+// use(z, row, column, sum of the parts in their order) for every element of the tiles in parts, four
+// of a row at a time; a CTA of 256 threads to four rows (blockIdx.x = kJoinCtas * tile + rows).
+constexpr int kJoinCtas = kTileM / 4;
+
+template <int BN, class F>
+__device__ __forceinline__ void each_joined(const TileMap &map, const float *slots, F &&use) {
+    const Tile t = tile_of(map, map.whole + static_cast<int>(blockIdx.x / kJoinCtas) * map.parts);
+    const int i = threadIdx.x * 4;
+    if (i >= 4 * BN) return;
+    const int at = static_cast<int>(blockIdx.x % kJoinCtas) * 4 * BN + i;
+    const float *p = slots + static_cast<int64_t>(t.slot) * kTileM * BN + at;
+    float4 v = *reinterpret_cast<const float4 *>(p);
+#pragma unroll 4
+    for (int k = 1; k < map.parts; ++k) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(k) * kTileM * BN);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    use(t.z, static_cast<int64_t>(t.m) * kTileM + at / BN, static_cast<int64_t>(t.n) * BN + at % BN, v);
+}
+
 // ---- host -----------------------------------------------------------------
+
+constexpr int64_t kPairs = 76;                             // of SMs: sizes can be asked for without a GPU
+
+// The tiles of a product of so many stages and terms, and which of them go in parts of at least
+// eight stages: where the stages that saves (0.27 us for each term) outweigh the join's
+// launch (8 us) and the slots' traffic (0.1 us each).
+inline TileMap tile_map(int64_t M, int64_t N, int64_t cols, int64_t stages, int terms, int64_t batches, bool symmetric, bool in_parts) {
+    TileMap m = {};
+    const int64_t mt = (M + kTileM - 1) / kTileM, nt = (N + cols - 1) / cols;
+    m.m_tiles = static_cast<int>(mt);
+    m.n_tiles = static_cast<int>(nt);
+    m.tiles = static_cast<int>(symmetric ? nt * (nt + 1) / 2 : mt * nt);
+    m.symmetric = symmetric;
+    const int64_t all = m.tiles * batches, last = all % kPairs;
+    m.whole = static_cast<int>(all);
+    m.parts = 1;
+    if (in_parts && last > 0 && 2 * last <= kPairs && stages >= 16) {
+        const int64_t n = std::min<int64_t>({kPairs / last, stages / 8, 16});
+        const double saved = 0.27 * terms * static_cast<double>(stages - (stages + n - 1) / n);
+        if (saved > 8.0 + 0.1 * static_cast<double>(last * n)) m.whole = static_cast<int>(all - last), m.parts = static_cast<int>(n);
+    }
+    return m;
+}
+inline int64_t tiles_in_parts(const TileMap &m, int64_t batches) { return m.tiles * batches - m.whole; }
+inline size_t slot_bytes(const TileMap &m, int64_t batches, int64_t cols) {
+    return (static_cast<size_t>(tiles_in_parts(m, batches)) * m.parts * kTileM * cols * 4 + 255) / 256 * 256;
+}
 
 // One operand: `planes` planes of `batches` matrices of `rows` x `k`, their rows or their k contiguous.
 struct Operand {
@@ -719,7 +795,7 @@ struct Spec {
     Operand a, b[2];
     int64_t M, N, K;               // K of one segment
     int batches, segments, planes_a, planes_b;
-    int splits;                    // of k (0: 1); kPlain: each to a batch of its own, batch * splits + part
+    bool in_parts;                 // out.slots is there for the tiles that go in parts
     int a_plane, a_batch, a_seg, b_plane, b_batch;
     bool symmetric;
     bool a_half, b_half;           // FOLD and 256 columns only
@@ -741,6 +817,11 @@ inline int list_terms(int pa, int pb, int (&ta)[kMaxTerms], int (&tb)[kMaxTerms]
     return n;
 }
 
+inline int count_terms(int pa, int pb) {
+    int ta[kMaxTerms], tb[kMaxTerms];
+    return list_terms(pa, pb, ta, tb);
+}
+
 template <int EPI, bool FOLD, int BN>
 cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     Job j = {};
@@ -760,20 +841,16 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.M = s.M;
     j.N = s.N;
     constexpr int kTileN = EPI == kGate ? BN / 2 : BN;
-    const int64_t mt = (s.M + kTileM - 1) / kTileM, nt = (s.N + kTileN - 1) / kTileN;
-    const int64_t tiles = s.symmetric ? nt * (nt + 1) / 2 : mt * nt;
+    j.terms = list_terms(s.planes_a, s.planes_b, j.term_a, j.term_b);
     const int64_t blocks = (s.K + kDepth - 1) / kDepth;
-    j.splits = s.splits > 1 ? s.splits : 1;
-    if (tiles * s.batches * j.splits > 0x7fffffffLL || blocks * s.segments > 0x7fffffffLL) return cudaErrorInvalidValue;
-    j.m_tiles = static_cast<int>(mt);
-    j.n_tiles = static_cast<int>(nt);
-    j.tiles = static_cast<int>(tiles);
-    j.batches = s.batches;
+    const int64_t most = (s.M + kTileM - 1) / kTileM * ((s.N + kTileN - 1) / kTileN) * s.batches;
+    if (most * 16 > 0x7fffffffLL || blocks * s.segments > 0x7fffffffLL) return cudaErrorInvalidValue;
+    j.map = tile_map(s.M, s.N, kTileN, blocks * s.segments, j.terms, s.batches, s.symmetric, s.in_parts);
+    j.items = j.map.whole + static_cast<int>(tiles_in_parts(j.map, s.batches)) * j.map.parts;
     j.k_blocks = static_cast<int>(blocks);
     j.segments = s.segments;
     j.planes_a = s.planes_a;
     j.planes_b = s.planes_b;
-    j.terms = list_terms(s.planes_a, s.planes_b, j.term_a, j.term_b);
     j.a_plane = s.a_plane, j.a_batch = s.a_batch, j.a_seg = s.a_seg, j.b_plane = s.b_plane, j.b_batch = s.b_batch;
     j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
     j.stages = (kSmem - kHeader - kEpilogueWarps * kOutBytes) / j.stage_bytes;
@@ -781,13 +858,12 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.sum_blocks = FOLD ? 1 : static_cast<int>(blocks * s.segments);
     j.a_rows = s.a.rows_contiguous;
     j.b_rows = s.b[0].rows_contiguous;
-    j.symmetric = s.symmetric;
     const uint32_t kind = s.a.half ? 0u : 1u;
     j.idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>((FOLD ? 128 : BN) >> 3) << 17) |
               (static_cast<uint32_t>(kTileM >> 4) << 24);
     const int sms = device_sm_count();
     int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-    if (pairs > tiles * s.batches * j.splits) pairs = tiles * s.batches * j.splits;
+    if (pairs > j.items) pairs = j.items;
     cudaError_t e = allow_smem<product_kernel<EPI, FOLD, BN>>();
     if (e != cudaSuccess) return e;
     if (FOLD) {                                            // another split would wait forever for its registers
