@@ -719,6 +719,93 @@ def test_captured_and_replayed(op):
             assert all(torch.equal(g, v) for g, v in zip(r, w))
 
 
+def test_captured_over_two_streams(op):
+    """A capture that forks to another stream and joins it: the results of one stream's calls feed the other's."""
+    import torch
+    x, _ = _rand(1, (300, 128), "bf16")
+    wg, _ = _rand(2, (264, 128), "bf16", 0.1)
+    wu, _ = _rand(3, (264, 128), "bf16", 0.1)
+    m, _ = _rand(4, (96, 300), "f32")
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        a = op.orthogonalise(m)                                        # the longer one, on the first stream
+        b0 = op.gated_ffn(x, wg, wu, keep=True)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = op.gated_ffn_back(b0.h, x, wg, wu, b0.gate, b0.up)
+            c = op.gated_ffn(b[0], wg, wu)
+        d = op.orthogonalise(a)
+        main.wait_stream(side)
+        e = op.gated_ffn(c.h[:, :128].contiguous(), wg, wu)            # first in its call, after both
+        return [a, *b, c.h, d, e.h, op.orthogonalise(b[1].float())]
+
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_two_graphs_that_share_a_workspace(op):
+    """Captured with one workspace of the caller's and replayed in turn."""
+    import torch
+    x, _ = _rand(1, (300, 128), "f32")
+    w, _ = _rand(2, (264, 128), "f32", 0.1)
+    m, _ = _rand(3, (2, 200, 264), "f32")
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    calls = [lambda: op.gated_ffn(x, w, w, workspace=ws).h, lambda: op.orthogonalise(m, workspace=ws)]
+    want = [c().clone() for c in calls]
+    torch.cuda.synchronize()
+    graphs = []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = c()
+        graphs.append((g, r))
+    for _ in range(3):
+        for g, r in graphs:
+            r.fill_(float("nan"))
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(r, v) for (_, r), v in zip(graphs, want))
+
+
+def test_calls_from_two_threads(op):
+    """Host threads, each with a stream of its own."""
+    import threading
+    import torch
+    calls = _all_calls(op)
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                for c, w in zip(calls, want):
+                    got = c()
+                    s.synchronize()
+                    if not all(torch.equal(g, v) for g, v in zip(got, w)):
+                        wrong.append(c)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_offsets_beyond_32_bits(op):
     """Rows more than 2^32 bytes apart from the first."""
     import torch
