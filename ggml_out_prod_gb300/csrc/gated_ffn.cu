@@ -472,11 +472,14 @@ ForwardForms forward_forms(int x_type, int w_type, bool aligned) {
 struct BackForms {
     Form d, x, w;
 };
-// dgate and dup of few tokens keep 16 bits where dh has 8: reading the weights takes longer than
-// twice the products, and a gradient of few terms would show their rounding.
-BackForms back_forms(int dh_type, int x_type, int w_type, int64_t T, bool aligned) {
+// dgate and dup of small calls keep 16 bits where dh has 8: with few tokens reading the weights
+// takes longer than twice the products, in small products their launch does (2^31 elements:
+// 9 us), and a gradient of few terms would show their rounding.
+BackForms back_forms(int dh_type, int x_type, int w_type, const int64_t ne[3], bool aligned) {
     const bool precise = dh_type == OOP_TYPE_F32;
-    return {{precise ? 3 : T <= pair::kTileM ? 2 : 1, false, true, false}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
+    const double size = static_cast<double>(ne[0]) * static_cast<double>(ne[1]) * static_cast<double>(ne[2]);
+    const bool small = ne[2] <= pair::kTileM || size <= 0x1p31;
+    return {{precise ? 3 : small ? 2 : 1, false, true, false}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
 }
 
 // A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
@@ -624,7 +627,7 @@ size_t oop_gated_ffn_workspace_size(int x_type, int w_type, const int64_t ne[3],
 
 size_t oop_gated_ffn_back_workspace_size(int dh_type, int x_type, int w_type, const int64_t ne[3], int aligned) {
     if (!gradient_type(dh_type) || check_ffn(x_type, w_type, ne, 0) != OOP_OK) return 0;
-    const BackForms f = back_forms(dh_type, x_type, w_type, ne[2], aligned != 0);
+    const BackForms f = back_forms(dh_type, x_type, w_type, ne, aligned != 0);
     const int64_t K = ne[0], F = ne[1], T = ne[2];
     // the parts of the two products follow each other in one place
     const size_t parts = std::max(gradient_plan(T, K, F, f.d.planes, f.w.planes, 1, 2).slots,
@@ -733,7 +736,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
         if (want_dw && e == cudaSuccess) e = zero_rows(dw_up, nb_dw, K * d_size, F, st);
         return cuda_status(e);
     }
-    const BackForms f = back_forms(dh_type, x_type, w_type, T, aligned);
+    const BackForms f = back_forms(dh_type, x_type, w_type, ne, aligned);
     char *at = static_cast<char *>(workspace);
     const int64_t pitch = round8(F);
     // [plane][gate, up][T][pitch]

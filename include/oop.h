@@ -656,8 +656,8 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
  * dh {F, T} and every result: F32 or BF16, one type.  Operands that are not BF16 go
  * to the tensor cores as sums of bfloat16 terms: two for F16, else three (24 bits) where
  * dh is F32 and two (16 bits) where it is BF16.  Between the
- * products dgate and dup are held to 24 bits where dh is F32, to 16 where it is BF16 and T is
- * at most 256, else in BF16.  dx may be NULL,
+ * products dgate and dup are held to 24 bits where dh is F32, to 16 where it is BF16 and the
+ * call small (T at most 256, or K * F * T at most 2^31), else in BF16.  dx may be NULL,
  * and dw_gate and dw_up both (not computed); dw rows are nb_dw apart.  T == 0
  * writes zeros to dw_gate and dw_up.  No output may overlap an input.
  */

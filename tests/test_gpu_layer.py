@@ -438,10 +438,10 @@ def test_gated_ffn_of_few_tokens(op, T, kind, K, F):
             _close(got, want, t, "few tokens")
 
 
-@pytest.mark.parametrize("T,K,F", [(300, 200, 3000), (64, 136, 2048), (256, 96, 520), (257, 96, 520), (2100, 72, 80)])
+@pytest.mark.parametrize("T,K,F", [(300, 200, 3000), (64, 136, 2048), (256, 96, 520), (2100, 72, 80), (520, 1032, 4100)])
 @pytest.mark.parametrize("x_kind,d_kind", [("f32", "f32"), ("bf16", "bf16"), ("f16", "bf16")])
 def test_gated_ffn_back_in_parts(op, T, K, F, x_kind, d_kind):
-    """Long sums over few tiles, which are taken in parts, and the number of tokens where dgate's bits change."""
+    """Long sums over few tiles, which are taken in parts, and a call so large that dgate has dh's bits."""
     x, xv = _rand(T, (T, K), x_kind)
     wg, wgv = _rand(K, (F, K), x_kind, K ** -0.5)
     wu, wuv = _rand(F, (F, K), x_kind, K ** -0.5)
