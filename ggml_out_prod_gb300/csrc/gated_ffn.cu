@@ -295,16 +295,34 @@ cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
 // Rows of any type as P binary16 planes [P][rows][pitch] of a scaled value, hi + lo: a row is
 // scaled by the power of two that brings its largest magnitude to 2^13 .. 2^14, so nothing
 // overflows, what is above 2^-15 of the largest keeps 22 bits or more, and what is below is
-// off by 2^-39 of the largest, which is in every sum of the row.  factors: the inverse scales.  Two planes and
-// three terms do for the forward products of f32 what three bfloat16 planes and six terms do elsewhere, whose
-// sums run over other rows' scales.  A CTA takes a row, read once up to 8192 columns.
+// off by 2^-39 of the largest, which is in every sum of the row.  factors: the inverse
+// scales.  Two planes and three terms do for the forward products of f32 what three bfloat16
+// planes and six terms do elsewhere, whose sums run over other rows' scales.  A warp takes a
+// row, read once up to 2560 columns; up to three matrices of the same columns in a launch.
+struct Scaled {
+    const char *src;
+    int64_t nb, rows;
+    __half *dst;
+    float *factors;
+    int wide;
+};
+struct ScaledArgs {
+    Scaled m[3];
+    int count;
+    int64_t cols, pitch;
+};
+
 template <int TYPE, int P>
-__global__ void __launch_bounds__(256) halves_kernel(const char *src, int64_t nb, int64_t cols, int64_t rows, __half *dst, int64_t pitch,
-                                                     float *factors, int wide) {
-    constexpr int kHold = 4;
-    __shared__ float part[8];
+__global__ void __launch_bounds__(256) halves_kernel(const __grid_constant__ ScaledArgs a) {
+    constexpr int kHold = 10;
     let_next_start();
-    const char *row = src + blockIdx.x * nb;
+    const int lane = threadIdx.x & 31;
+    int64_t r = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    int which = 0;
+    while (which < a.count && r >= a.m[which].rows) r -= a.m[which++].rows;
+    if (which == a.count) return;
+    const Scaled &m = a.m[which];
+    const char *row = m.src + r * m.nb;
     float held[kHold][8], top = 0.f;
     auto largest = [&](const float (&v)[8]) {
 #pragma unroll
@@ -312,29 +330,26 @@ __global__ void __launch_bounds__(256) halves_kernel(const char *src, int64_t nb
     };
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
-        const int64_t c = (threadIdx.x + 256 * h) * 8;
-        if (c < cols) {
-            load8<TYPE>(row, c, cols, wide, held[h]);
-            largest(held[h]);
-        }
+        const int64_t c = (lane + 32 * h) * 8;
+        if (c < a.cols) load8<TYPE>(row, c, a.cols, m.wide, held[h]);
     }
-    for (int64_t c = (threadIdx.x + 256 * kHold) * 8; c < cols; c += 256 * 8) {
+#pragma unroll
+    for (int h = 0; h < kHold; ++h)
+        if ((lane + 32 * h) * 8 < a.cols) largest(held[h]);
+    for (int64_t c = (lane + 32 * kHold) * 8; c < a.cols; c += 32 * 8) {
         float v[8];
-        load8<TYPE>(row, c, cols, wide, v);
+        load8<TYPE>(row, c, a.cols, m.wide, v);
         largest(v);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, part[i]);
     // 13 - floor(log2 top), within a float's exponents; 0 for a row of zeros or one that is not finite
     const int exponent = static_cast<int>(__float_as_uint(top) >> 23);
     const int e = top > 0.f && exponent < 255 ? max(-126, min(126, 13 + 127 - exponent)) : 0;
     const float scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    if (threadIdx.x == 0) factors[blockIdx.x] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    __half *d = dst + blockIdx.x * pitch;
+    if (lane == 0) m.factors[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    __half *d = m.dst + r * a.pitch;
+    const int64_t plane = m.rows * a.pitch;
     auto put = [&](const float (&v)[8], int64_t c) {
         float left[8];
 #pragma unroll
@@ -349,38 +364,30 @@ __global__ void __launch_bounds__(256) halves_kernel(const char *src, int64_t nb
             }
             uint4 w;
             __builtin_memcpy(&w, h, 16);
-            *reinterpret_cast<uint4 *>(d + p * rows * pitch + c) = w;
+            *reinterpret_cast<uint4 *>(d + p * plane + c) = w;
         }
     };
 #pragma unroll
-    for (int h = 0; h < kHold; ++h) {
-        const int64_t c = (threadIdx.x + 256 * h) * 8;
-        if (c < cols) put(held[h], c);
-    }
-    for (int64_t c = (threadIdx.x + 256 * kHold) * 8; c < cols; c += 256 * 8) {
+    for (int h = 0; h < kHold; ++h)
+        if ((lane + 32 * h) * 8 < a.cols) put(held[h], (lane + 32 * h) * 8);
+    for (int64_t c = (lane + 32 * kHold) * 8; c < a.cols; c += 32 * 8) {
         float v[8];
-        load8<TYPE>(row, c, cols, wide, v);
+        load8<TYPE>(row, c, a.cols, m.wide, v);
         put(v, c);
     }
 }
 
-template <int P>
-cudaError_t launch_halves_of(const void *src, int type, int64_t nb, int64_t cols, int64_t rows, void *dst, int64_t pitch,
-                             float *factors, cudaStream_t st) {
-    const char *s = static_cast<const char *>(src);
-    auto *d = static_cast<__half *>(dst);
-    const int wide = is_aligned(src, 16) && nb % 16 == 0;
-    const unsigned g = static_cast<unsigned>(rows);
-#define OOP_CASE(T) \
-    case T: halves_kernel<T, P><<<g, 256, 0, st>>>(s, nb, cols, rows, d, pitch, factors, wide); break;
-    if constexpr (P == 1) {
-        switch (type) { OOP_CASE(OOP_TYPE_F16) OOP_CASE(OOP_TYPE_BF16) }
-    } else {
-        switch (type) {
-            OOP_CASE(OOP_TYPE_F32) OOP_CASE(OOP_TYPE_Q4_0) OOP_CASE(OOP_TYPE_Q4_1) OOP_CASE(OOP_TYPE_Q5_0) OOP_CASE(OOP_TYPE_Q5_1)
-            OOP_CASE(OOP_TYPE_Q8_0) OOP_CASE(OOP_TYPE_Q2_K) OOP_CASE(OOP_TYPE_Q3_K) OOP_CASE(OOP_TYPE_Q4_K) OOP_CASE(OOP_TYPE_Q5_K)
-            OOP_CASE(OOP_TYPE_Q6_K)
-        }
+cudaError_t launch_halves(const ScaledArgs &a, int type, cudaStream_t st) {
+    int64_t rows = 0;
+    for (int i = 0; i < a.count; ++i) rows += a.m[i].rows;
+    const unsigned g = static_cast<unsigned>((rows + 7) / 8);
+#define OOP_CASE(T, P) \
+    case T: halves_kernel<T, P><<<g, 256, 0, st>>>(a); break;
+    switch (type) {
+        OOP_CASE(OOP_TYPE_F16, 1) OOP_CASE(OOP_TYPE_BF16, 1) OOP_CASE(OOP_TYPE_F32, 2) OOP_CASE(OOP_TYPE_Q4_0, 2)
+        OOP_CASE(OOP_TYPE_Q4_1, 2) OOP_CASE(OOP_TYPE_Q5_0, 2) OOP_CASE(OOP_TYPE_Q5_1, 2) OOP_CASE(OOP_TYPE_Q8_0, 2)
+        OOP_CASE(OOP_TYPE_Q2_K, 2) OOP_CASE(OOP_TYPE_Q3_K, 2) OOP_CASE(OOP_TYPE_Q4_K, 2) OOP_CASE(OOP_TYPE_Q5_K, 2)
+        OOP_CASE(OOP_TYPE_Q6_K, 2)
     }
 #undef OOP_CASE
     ++g_kernel_launches;
@@ -485,7 +492,7 @@ BackForms back_forms(int dh_type, int x_type, int w_type, const int64_t ne[3], b
 // A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
 // that this call writes at `at`, which moves on.
 cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_t cols, int64_t rows, bool rows_contiguous,
-                    char *&at, pair::Operand &o, cudaStream_t st, const float **factors_at = nullptr) {
+                    char *&at, pair::Operand &o, cudaStream_t st) {
     o = {src, cols, rows, nb, 0, 1, rows_contiguous, f.half};
     if (!f.copy) return cudaSuccess;
     const int64_t pitch = round8(cols);
@@ -494,15 +501,19 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
     o.matrix_bytes = rows * pitch * 2;
     o.matrices = f.planes;
     at += form_bytes(f, cols, rows);
-    if (f.scaled) {
-        float *factors = reinterpret_cast<float *>(at - round256(static_cast<size_t>(rows) * 4));
-        if (factors_at) *factors_at = factors;
-        return f.planes == 1 ? launch_halves_of<1>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, factors, st)
-                             : launch_halves_of<2>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, factors, st);
-    }
     if (f.planes == 1) return launch_planes_of<0>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
     return f.planes == 2 ? launch_planes_of<2>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st)
                          : launch_planes_of<3>(src, type, nb, cols, rows, const_cast<void *>(o.p), pitch, st);
+}
+
+// The same for a matrix whose rows are scaled, k contiguous: what halves_kernel has to do.
+Scaled scaled_operand(const Form &f, const void *src, int64_t nb, int64_t cols, int64_t rows, char *&at, pair::Operand &o) {
+    const int64_t pitch = round8(cols);
+    o = {at, cols, rows, pitch * 2, rows * pitch * 2, f.planes, false, true};
+    Scaled m = {static_cast<const char *>(src), nb, rows, reinterpret_cast<__half *>(at), nullptr, is_aligned(src, 16) && nb % 16 == 0};
+    at += form_bytes(f, cols, rows);
+    m.factors = reinterpret_cast<float *>(at - round256(static_cast<size_t>(rows) * 4));
+    return m;
 }
 
 // Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the
@@ -675,9 +686,27 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     const ForwardForms f = forward_forms(x_type, w_type, aligned);
     char *at = static_cast<char *>(workspace);
     pair::Spec s = {};
-    cudaError_t e = operand(f.x, x, x_type, nb_x, K, T, false, at, s.a, st, &s.out.row_scale);
-    if (e == cudaSuccess) e = operand(f.w, w_gate, w_type, nb_w, K, F, false, at, s.b[0], st, &s.out.col_scale[0]);
-    if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, false, at, s.b[1], st, &s.out.col_scale[1]);
+    cudaError_t e = cudaSuccess;
+    if (f.x.scaled) {
+        ScaledArgs a = {};
+        a.cols = K, a.pitch = round8(K);
+        a.m[a.count++] = scaled_operand(f.x, x, nb_x, K, T, at, s.a);
+        s.out.row_scale = a.m[0].factors;
+        if (w_type != OOP_TYPE_F32) {                      // another type: a launch of its own
+            e = launch_halves(a, x_type, st);
+            a.count = 0;
+        }
+        const void *w[2] = {w_gate, w_up};
+        for (int i = 0; i < 2; ++i) {
+            a.m[a.count] = scaled_operand(f.w, w[i], nb_w, K, F, at, s.b[i]);
+            s.out.col_scale[i] = a.m[a.count++].factors;
+        }
+        if (e == cudaSuccess) e = launch_halves(a, w_type, st);
+    } else {
+        e = operand(f.x, x, x_type, nb_x, K, T, false, at, s.a, st);
+        if (e == cudaSuccess) e = operand(f.w, w_gate, w_type, nb_w, K, F, false, at, s.b[0], st);
+        if (e == cudaSuccess) e = operand(f.w, w_up, w_type, nb_w, K, F, false, at, s.b[1], st);
+    }
     if (e != cudaSuccess) return cuda_status(e);
     s.M = T, s.N = F, s.K = K;
     s.batches = s.segments = 1;
