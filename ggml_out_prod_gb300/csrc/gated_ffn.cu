@@ -13,8 +13,9 @@
 // lie as they are, with their rows or their k contiguous.
 //
 // Measured: bf16 8192 x 5120 x 17408, gate and up kept: 1.53 ms, 1.91 PFLOP/s (97% of the
-// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x 2560 x 9728: 1.10 ms, 1.48
-// PFLOP/s, of it 0.13 for dgate and dup and a last wave of dx that fills a fifth of the SMs.
+// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x 2560 x
+// 9728: 1.04 ms, 1.57 PFLOP/s, 0.13 of it for dgate and dup.  f32 512 x 2560 x 9728, kept: 167 us,
+// 60 of it for the planes of the weights, the rest two waves of tiles with their epilogues.
 #include <algorithm>
 #include <cmath>
 

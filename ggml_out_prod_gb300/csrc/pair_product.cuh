@@ -600,10 +600,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 if (rows <= 0 || f >= j.N) return;
                 if constexpr (FOLD) {
                     const float by = lane < rows ? j.out.row_scale[r0 + lane] : 0.f;
+                    const int64_t c = min(f + lane, j.N - 1);
+                    const float of_g = j.out.col_scale[0][c], of_u = j.out.col_scale[1][c];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const int64_t c = min(f + k, j.N - 1);
-                        const float bg = j.out.col_scale[0][c], bu = j.out.col_scale[1][c];
+                        const float bg = __shfl_sync(0xffffffffu, of_g, k), bu = __shfl_sync(0xffffffffu, of_u, k);
                         g[k] = g[k] * fminf(by, bg) * fmaxf(by, bg);       // the small one first: no step leaves fp32's
                         u[k] = u[k] * fminf(by, bu) * fmaxf(by, bu);       // range that the result does not leave
                     }
