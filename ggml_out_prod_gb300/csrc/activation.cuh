@@ -5,9 +5,9 @@
 
 namespace oop {
 
-// 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation.
-// exp is kept below 2^116: within the fast division's range (2 ulp), and the product of the
-// two is never Inf * 0.
+// 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation. exp is kept
+// below 2^116: within the fast division's range (2 ulp), and the product of the two is
+// never Inf * 0.
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + expf(fminf(-v, 80.f))); }
 __device__ __forceinline__ float logistic(float v, float &rest) {
     const float e = expf(fminf(-v, 80.f)), s = __fdividef(1.f, 1.f + e);

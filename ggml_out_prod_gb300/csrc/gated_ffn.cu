@@ -1,21 +1,22 @@
-// gated_ffn.cu -- the gated feed-forward block up to its last projection, and
-// its backward pass.
+// gated_ffn.cu -- the gated feed-forward block up to its last projection, and its backward
+// pass.
 //
 //   gate = x Wg',  up = x Wu',  h = act(gate) up
 //   dgate = dh up act'(gate),  dup = dh act(gate)
 //   dx = dgate Wg + dup Wu,  dWg = dgate' x,  dWu = dup' x
 //
 // Bound by the tensor cores from a few hundred tokens on.  Forward: one product whose
-// tiles take half their columns from each weight, so that a tile's epilogue holds the gates
-// and the ups of the same features and nothing goes to memory between.  Backward: one pass over dh, gate
-// and up writes dgate and dup (16 bits each where dh has 16), then dx as one product over
-// both weights' rows, and both weight gradients as one product of two batches; the operands
-// lie as they are, with their rows or their k contiguous.
+// tiles take half their columns from each weight, so that a tile's epilogue holds the
+// gates and the ups of the same features and nothing goes to memory between.  Backward:
+// one pass over dh, gate and up writes dgate and dup (16 bits each where dh has 16), then
+// dx as one product over both weights' rows, and both weight gradients as one product of
+// two batches; the operands lie as they are, with their rows or their k contiguous.
 //
 // Measured: bf16 8192 x 5120 x 17408, gate and up kept: 1.53 ms, 1.91 PFLOP/s (97% of the
-// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x 2560 x
-// 9728: 1.04 ms, 1.57 PFLOP/s, 0.13 of it for dgate and dup.  f32 512 x 2560 x 9728, kept: 167 us,
-// 60 of it for the planes of the weights, the rest two waves of tiles with their epilogues.
+// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x
+// 2560 x 9728: 1.04 ms, 1.57 PFLOP/s, 0.13 of it for dgate and dup.  f32 512 x 2560 x
+// 9728, kept: 167 us, 60 of it for the planes of the weights, the rest two waves of tiles
+// with their epilogues.
 #include <algorithm>
 #include <cmath>
 
@@ -44,8 +45,8 @@ __device__ __forceinline__ void split(float v, __nv_bfloat16 (&t)[P]) {
     }
 }
 
-// Eight aligned elements of a plain type as they lie in memory: the load alone, so
-// that several can be in flight.
+// Eight aligned elements of a plain type as they lie in memory: the load alone, so that
+// several can be in flight.
 template <int TYPE>
 struct Eight {
     static constexpr int E = 16 / plain_size(TYPE);
@@ -159,12 +160,13 @@ cudaError_t launch_planes_of(const void *src, int type, int64_t nb, int64_t cols
 
 // ---- few tokens -----------------------------------------------------------
 //
-// Up to eight tokens: the weights' bytes are all there is to do, and the tensor
-// cores' tiles of 256 tokens would only be waited for.  A warp takes a feature: its
-// gate and its up row, each read once in long runs (five or six 16-byte loads of each row in flight per lane),
-// against the tokens in shared memory as floats.  Sums in fp32 on the CUDA cores, which any
-// type of weight allows without a copy.  bf16, 1 x 2560 x 9728: 17.7 us,
-// 5.6 TB/s, 84% of the measured copy rate (one load of each row at a time: 48 us; on the tensor cores 44 us).
+// Up to eight tokens: the weights' bytes are all there is to do, and the tensor cores'
+// tiles of 256 tokens would only be waited for.  A warp takes a feature: its gate and its
+// up row, each read once in long runs (five or six 16-byte loads of each row in flight per
+// lane), against the tokens in shared memory as floats.  Sums in fp32 on the CUDA cores,
+// which any type of weight allows without a copy.  bf16, 1 x 2560 x 9728: 17.7 us, 5.6
+// TB/s, 84% of the measured copy rate (one load of each row at a time: 48 us; on the
+// tensor cores 44 us).
 constexpr int kFewThreads = 512, kFewTokens = 8;
 constexpr int64_t kFewBytes = 180 * 1024;
 
@@ -255,7 +257,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 }
 
 // Operands that the tensor cores take as they are go there from five tokens on (5120 x
-// 17408: 77 us for 4 tokens here, 131 for 8, 85 there), others have to be copied first (f32: 164, 597).
+// 17408: 77 us for 4 tokens here, 131 for 8, 85 there), others have to be copied first
+// (f32: 164, 597).
 bool few_tokens(int64_t T, int64_t K, int x_type, int w_type) {
     const int64_t nt = !plain_size(w_type) ? 8 : T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
     const bool native = x_type == w_type && plain_size(w_type) == 2;
@@ -293,13 +296,14 @@ cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
-// Rows of any type as P binary16 planes [P][rows][pitch] of a scaled value, hi + lo: a row is
-// scaled by the power of two that brings its largest magnitude to 2^13 .. 2^14, so nothing
-// overflows, what is above 2^-15 of the largest keeps 22 bits or more, and what is below is
-// off by 2^-39 of the largest, which is in every sum of the row.  factors: the inverse
-// scales.  Two planes and three terms do for the forward products of f32 what three bfloat16
-// planes and six terms do elsewhere, whose sums run over other rows' scales.  A warp takes a
-// row, read once up to 2560 columns; up to three matrices of the same columns in a launch.
+// Rows of any type as P binary16 planes [P][rows][pitch] of a scaled value, hi + lo: a row
+// is scaled by the power of two that brings its largest magnitude to 2^13 .. 2^14, so
+// nothing overflows, what is above 2^-15 of the largest keeps 22 bits or more, and what is
+// below is off by 2^-39 of the largest, which is in every sum of the row.  factors: the
+// inverse scales.  Two planes and three terms do for the forward products of f32 what
+// three bfloat16 planes and six terms do elsewhere, whose sums run over other rows'
+// scales.  A warp takes a row, read once up to 2560 columns; up to three matrices of the
+// same columns in a launch.
 struct Scaled {
     const char *src;
     int64_t nb, rows;
@@ -344,7 +348,8 @@ __global__ void __launch_bounds__(256) halves_kernel(const __grid_constant__ Sca
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 13 - floor(log2 top), within a float's exponents; 0 for a row of zeros or one that is not finite
+    // 13 - floor(log2 top), within a float's exponents; 0 for a row of zeros or one that is not
+    // finite
     const int exponent = static_cast<int>(__float_as_uint(top) >> 23);
     const int e = top > 0.f && exponent < 255 ? max(-126, min(126, 13 + 127 - exponent)) : 0;
     const float scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
@@ -446,15 +451,16 @@ void launch_gate_back(int x_type, const char *dh, int64_t nb_dh, const char *gat
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// How a matrix of a type goes to the tensor cores: as it is (0: not even copied), or
-// as so many 16-bit planes in the workspace.
+// How a matrix of a type goes to the tensor cores: as it is (0: not even copied), or as so
+// many 16-bit planes in the workspace.
 struct Form {
     int planes;        // terms of a value
     bool half, copy;   // binary16; in the workspace
     bool scaled;       // by rows
 };
 
-// `native`: the other operand has this 16-bit type too.  `precise`: the product is wanted to 24 bits.
+// `native`: the other operand has this 16-bit type too.  `precise`: the product is wanted
+// to 24 bits.
 Form form_of(int type, bool native, bool precise, bool aligned) {
     if (native) return {1, type == OOP_TYPE_F16, !aligned, false};
     if (type == OOP_TYPE_BF16) return {1, false, !aligned, false};
@@ -480,9 +486,9 @@ ForwardForms forward_forms(int x_type, int w_type, bool aligned) {
 struct BackForms {
     Form d, x, w;
 };
-// dgate and dup of small calls keep 16 bits where dh has 8: with few tokens reading the weights
-// takes longer than twice the products, in small products their launch does (2^31 elements:
-// 9 us), and a gradient of few terms would show their rounding.
+// dgate and dup of small calls keep 16 bits where dh has 8: with few tokens reading the
+// weights takes longer than twice the products, in small products their launch does (2^31
+// elements: 9 us), and a gradient of few terms would show their rounding.
 BackForms back_forms(int dh_type, int x_type, int w_type, const int64_t ne[3], bool aligned) {
     const bool precise = dh_type == OOP_TYPE_F32;
     const double size = static_cast<double>(ne[0]) * static_cast<double>(ne[1]) * static_cast<double>(ne[2]);
@@ -490,8 +496,8 @@ BackForms back_forms(int dh_type, int x_type, int w_type, const int64_t ne[3], b
     return {{precise ? 3 : small ? 2 : 1, false, true, false}, form_of(x_type, false, precise, aligned), form_of(w_type, false, precise, aligned)};
 }
 
-// A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's memory, or planes
-// that this call writes at `at`, which moves on.
+// A matrix {cols, rows} as an operand whose k (or rows) are contiguous: the caller's
+// memory, or planes that this call writes at `at`, which moves on.
 cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_t cols, int64_t rows, bool rows_contiguous,
                     char *&at, pair::Operand &o, cudaStream_t st) {
     o = {src, cols, rows, nb, 0, 1, rows_contiguous, f.half};
@@ -517,8 +523,8 @@ Scaled scaled_operand(const Form &f, const void *src, int64_t nb, int64_t cols, 
     return m;
 }
 
-// Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the
-// waves (a narrow tile reads A as often as a wide one for half the sums).
+// Tiles of 256 columns, or of 128 where those leave SMs idle: the time of the waves (a
+// narrow tile reads A as often as a wide one for half the sums).
 bool narrow_tiles(int64_t M, int64_t N, int64_t batches, int wide_cols) {
     auto waves = [&](int64_t cols) {
         const int64_t tiles = (M + pair::kTileM - 1) / pair::kTileM * ((N + cols - 1) / cols) * batches;
@@ -528,8 +534,8 @@ bool narrow_tiles(int64_t M, int64_t N, int64_t batches, int wide_cols) {
 }
 
 // A gradient's product: narrow tiles or wide ones, and which go in parts of k.  333 x 1001
-// x 3074 in f32 has 16 tiles, whose 50 stages would take 40 us; 8192 x 2560 x 19456 fills four
-// waves and a fifth of the next, which as parts takes a quarter of its time.
+// x 3074 in f32 has 16 tiles, whose 50 stages would take 40 us; 8192 x 2560 x 19456 fills
+// four waves and a fifth of the next, which as parts takes a quarter of its time.
 struct GradientPlan {
     bool narrow;
     pair::TileMap map;

@@ -1,14 +1,15 @@
-// orthogonalise.cu -- the update of a weight made nearly orthogonal by
-// Newton-Schulz steps, as the Muon optimiser does it.
+// orthogonalise.cu -- the update of a weight made nearly orthogonal by Newton-Schulz
+// steps, as the Muon optimiser does it.
 //
 //   X_0 = x / (|x|_F + eps),  X <- a X + (b A + c A A) X,  A = X X'
 //
-// A is taken on the smaller side: with M > N, X <- X (a + b X'X + c (X'X)^2) is
-// the same polynomial of the singular values.
+// A is taken on the smaller side: with M > N, X <- X (a + b X'X + c (X'X)^2) is the same
+// polynomial of the singular values.
 //
 // Bound by the tensor cores (three products of binary16 planes for one of 22 bits), whose
-// sums are folded every 64 k, and for few rows by launches.  f32, five steps: 8 x 2560
-// 13 to 15 us, 32 x 768 x 2048 1.63 ms, 9728 x 2560 to bf16 1.09 ms (1.97 with the steps on X itself).
+// sums are folded every 64 k, and for few rows by launches.  f32, five steps: 8 x 2560 13
+// to 15 us, 32 x 768 x 2048 1.63 ms, 9728 x 2560 to bf16 1.09 ms (1.97 with the steps on X
+// itself).
 #include <algorithm>
 #include <cmath>
 
@@ -22,11 +23,11 @@ namespace {
 constexpr int kMaxSteps = 64;
 constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// The matrices between the products are held as two binary16 planes, hi + lo, of a
-// scaled value: 22 bits or more, as many as a product of three terms keeps.  The
-// scales leave room for magnitudes of 8, 64 and 256 below binary16's largest, and keep
-// the planes of a 4096 x 4096 matrix (X's elements are about 2^-12) out of its
-// subnormals.  bfloat16 planes would need no scale, but three of them and six terms.
+// The matrices between the products are held as two binary16 planes, hi + lo, of a scaled
+// value: 22 bits or more, as many as a product of three terms keeps.  The scales leave
+// room for magnitudes of 8, 64 and 256 below binary16's largest, and keep the planes of a
+// 4096 x 4096 matrix (X's elements are about 2^-12) out of its subnormals.  bfloat16
+// planes would need no scale, but three of them and six terms.
 constexpr float kScaleX = 0x1p13f, kScaleA = 0x1p10f, kScaleQ = 0x1p8f;
 
 // Sums of squares: those of large, ordinary and small magnitudes apart, scaled so that
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(256) start_kernel(const char *x, int type, int
 
 // ---- few rows -------------------------------------------------------------
 //
-// A matrix whose smaller side n is at most 32 (an adapter's): all steps in one
-// launch.  A cluster of up to eight CTAs holds X in shared memory as floats, each CTA
-// a slice of the longer side; only the n x n partial products pass between them.
-// Bound by latency: per step one exchange over the cluster, three barriers, and
-// n^2 products per column, which the CUDA cores do faster than a tile of 256 rows
-// could be loaded.  8 x 2560 in one launch instead of seventeen.
+// A matrix whose smaller side n is at most 32 (an adapter's): all steps in one launch.  A
+// cluster of up to eight CTAs holds X in shared memory as floats, each CTA a slice of the
+// longer side; only the n x n partial products pass between them. Bound by latency: per
+// step one exchange over the cluster, three barriers, and n^2 products per column, which
+// the CUDA cores do faster than a tile of 256 rows could be loaded.  8 x 2560 in one
+// launch instead of seventeen.
 
 constexpr int kSmallCtas = 8;
 constexpr int kSmallThreads = 256;
@@ -236,8 +237,8 @@ struct SmallArgs {
     float coefs[3 * kMaxSteps];
 };
 
-// Floats between columns of the slice: 16-byte units in odd number, so that
-// neighbouring threads' columns lie in different banks.
+// Floats between columns of the slice: 16-byte units in odd number, so that neighbouring
+// threads' columns lie in different banks.
 __host__ __device__ constexpr int small_pitch(int nmax) { return nmax / 4 % 2 ? nmax : nmax + 4; }
 constexpr size_t small_fixed_bytes(int nmax) {
     // every CTA's partial products (two steps'), the warps' parts, A and Q
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
             for (int j = 0; j < NMAX; ++j) parts[warp * kSquare + j * NMAX + row] = acc[j];
         }
         __syncthreads();
-        // sent to every CTA as they are ready; two steps' apart, as a slow CTA may still read the last one's
+        // sent to every CTA as they are ready; two steps' apart, as a slow CTA may still read the
+        // last one's
         float *all = partial + (step & 1) * kSmallCtas * kSquare;
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
@@ -506,14 +508,14 @@ size_t plane_pair_bytes(int64_t cols, int64_t rows, int64_t B) {
     return round256(static_cast<size_t>(2 * B * rows * round8(cols)) * 2);
 }
 
-// The tiles of A = X X': those that would leave SMs idle go in parts of k (200 x 2560 is one tile
-// of 40 stages, 32 us).
+// The tiles of A = X X': those that would leave SMs idle go in parts of k (200 x 2560 is
+// one tile of 40 stages, 32 us).
 pair::TileMap map_of_a(int64_t n, int64_t deep, int64_t B) {
     return pair::tile_map(n, n, 256, (deep + pair::kDepth - 1) / pair::kDepth, 3, B, true, true);
 }
 
-// About the time of a product in microseconds: 9 for a launch, 0.8 for each stage of a wave of
-// tiles, 6 for the join of parts.
+// About the time of a product in microseconds: 9 for a launch, 0.8 for each stage of a
+// wave of tiles, 6 for the join of parts.
 double product_time(int64_t tiles, int64_t k, int parts) {
     const int64_t blocks = (k + pair::kDepth - 1) / pair::kDepth, waves = tiles / pair::kPairs;
     const int64_t last = tiles % pair::kPairs ? (blocks + parts - 1) / parts : 0;
@@ -543,13 +545,13 @@ double largest_q(const float *c) {
     return most;
 }
 
-// Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all products but the
-// first and the last are of the smaller side alone, 3 r + 4 s - 3 of them (in n^3, symmetric
-// results counted half) against s (3 r + 1) for a matrix r times as long as wide: fewer from r = 1.25 on,
-// but more launches.  What it costs is precision: a rounding of A grows by Q^2 at every step, where one of X grows by
-// Q, and reaches the last Q as this share of it.  So only results of 16 bits are
-// computed this way, and only where the share stays below their rounding (five
-// steps of the usual coefficients).
+// Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all
+// products but the first and the last are of the smaller side alone, 3 r + 4 s - 3 of them
+// (in n^3, symmetric results counted half) against s (3 r + 1) for a matrix r times as
+// long as wide: fewer from r = 1.25 on, but more launches.  What it costs is precision: a
+// rounding of A grows by Q^2 at every step, where one of X grows by Q, and reaches the
+// last Q as this share of it.  So only results of 16 bits are computed this way, and only
+// where the share stays below their rounding (five steps of the usual coefficients).
 double rounding_of_a(int steps, const float *coefs) {
     double grown = 0x1p-24;
     for (int i = 0; i + 1 < steps; ++i) grown *= std::pow(largest_q(coefs ? coefs + 3 * i : kDefault), 2);

@@ -1,25 +1,26 @@
-// pair_product.cuh -- the tensor-core matrix product inside the operators of a
-// layer's training step: D[m, n] = sum_k A[m, k] B[n, k], two SMs to a tile.
+// pair_product.cuh -- the tensor-core matrix product inside the operators of a layer's
+// training step: D[m, n] = sum_k A[m, k] B[n, k], two SMs to a tile.
 //
-// Operands are 16-bit planes (bfloat16, or binary16): a matrix of more precise
-// values is the sum of its planes, and the product the sum of the plane
-// products that matter (the terms), all in one accumulator.  Either operand may
-// lie with k or with its rows contiguous (the tensor core reads both from
-// shared memory), so no transpose is ever written.
+// Operands are 16-bit planes (bfloat16, or binary16): a matrix of more precise values is
+// the sum of its planes, and the product the sum of the plane products that matter (the
+// terms), all in one accumulator.  Either operand may lie with k or with its rows
+// contiguous (the tensor core reads both from shared memory), so no transpose is ever
+// written.
 //
 // A cluster of two CTAs owns a tile of 256 rows of A and BN rows of B
-// (tcgen05.mma.cta_group::2: each SM holds 128 rows of A, half of B's, and 128 x BN
-// sums in its tensor memory), so a byte of B that one SM loads is used by two.  The
-// grid is persistent.  In each CTA warp 0 loads (TMA, a ring of stages of 64 k, each
-// with every plane), warp 1 of the first CTA issues the products of both, and eight
-// warps take finished sums to the epilogue while the next tile's products run
-// (two buffers of BN columns of tensor memory).  Products of one plane run at 1.91 PFLOP/s
-// (8192 x 5120 x 34816, cuBLAS's measured burst is 1.96); stages of 128 k were no faster.
+// (tcgen05.mma.cta_group::2: each SM holds 128 rows of A, half of B's, and 128 x BN sums
+// in its tensor memory), so a byte of B that one SM loads is used by two.  The grid is
+// persistent.  In each CTA warp 0 loads (TMA, a ring of stages of 64 k, each with every
+// plane), warp 1 of the first CTA issues the products of both, and eight warps take
+// finished sums to the epilogue while the next tile's products run (two buffers of BN
+// columns of tensor memory).  Products of one plane run at 1.91 PFLOP/s (8192 x 5120 x
+// 34816, cuBLAS's measured burst is 1.96); stages of 128 k were no faster.
 //
-// With FOLD the sums of one stage (64 k, the small terms first) at a time are
-// added up in registers: the tensor core's additions cut off instead of rounding, which over a
-// whole row of f32 terms would cost more than the terms themselves keep.  The fold hides behind the products
-// (1557 of 1536 cycles a stage of three terms); the epilogue, on the same warps, does not.
+// With FOLD the sums of one stage (64 k, the small terms first) at a time are added up in
+// registers: the tensor core's additions cut off instead of rounding, which over a whole
+// row of f32 terms would cost more than the terms themselves keep.  The fold hides behind
+// the products (1557 of 1536 cycles a stage of three terms); the epilogue, on the same
+// warps, does not.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -61,9 +62,10 @@ struct Out {
     int wide;                      // 16-byte stores are allowed
 };
 
-// The tiles of a product.  Those from `whole` on are taken in parts of k, each an
-// item of its own whose sums go to a slot of 256 x BN floats for another kernel to join: all tiles where they are
-// few, else the last wave's where it would leave more than half of the SMs idle.
+// The tiles of a product.  Those from `whole` on are taken in parts of k, each an item of
+// its own whose sums go to a slot of 256 x BN floats for another kernel to join: all tiles
+// where they are few, else the last wave's where it would leave more than half of the SMs
+// idle.
 struct TileMap {
     int m_tiles, n_tiles, tiles;   // tiles of a batch
     int symmetric;                 // only tiles on and above the diagonal
@@ -106,8 +108,8 @@ __device__ __forceinline__ uint32_t leader_addr(const void *p) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(ptx::smem_u32(p)));
     return r;
 }
-// No memory is handed over with it (the tcgen05 fences order tensor memory), so the
-// plain form does: releasing to the cluster costs about a thousand cycles.
+// No memory is handed over with it (the tcgen05 fences order tensor memory), so the plain
+// form does: releasing to the cluster costs about a thousand cycles.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -134,8 +136,9 @@ __device__ __forceinline__ void commit_both(const void *bar) {
         : "memory");
 }
 // Shared-memory descriptor of a plane, 128-byte swizzle.  k contiguous: rows of 64 k,
-// groups of 8 rows 1024 bytes apart.  Rows contiguous: blocks of 64 rows by 64 k, 8 KB each (the leading offset),
-// in them one k every 128 bytes (groups of 8 k 1024 bytes apart).
+// groups of 8 rows 1024 bytes apart.  Rows contiguous: blocks of 64 rows by 64 k, 8 KB
+// each (the leading offset), in them one k every 128 bytes (groups of 8 k 1024 bytes
+// apart).
 __device__ __forceinline__ uint64_t plane_desc(uint32_t addr, int rows_contiguous) {
     uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(rows_contiguous ? 8192 >> 4 : 1) << 16;
@@ -219,8 +222,8 @@ __device__ __forceinline__ void take_sums(const uint64_t *sums, float (&v)[32]) 
     for (int i = 0; i < 16; ++i) ptx::unpack2(sums[i], v[2 * i], v[2 * i + 1]);
 }
 
-// 32 columns of the warp's 32 rows (a lane's row each) to memory: `row` is the first one's, from
-// column c on; `rows` and `cols` of them exist.  A lane's row goes through the
+// 32 columns of the warp's 32 rows (a lane's row each) to memory: `row` is the first
+// one's, from column c on; `rows` and `cols` of them exist.  A lane's row goes through the
 // warp's part of shared memory, so that a store covers whole 64- or 128-byte pieces of few
 // rows instead of 16 bytes of 32 (the XOR keeps both sides free of bank conflicts).
 template <int TYPE>
@@ -276,8 +279,8 @@ struct Tile {
     int slot;                      // of the part's sums; -1: a whole tile
 };
 
-// Item i: batches outermost, then bands of eight row tiles, so that the tiles of a
-// wave share their operands in L2.
+// Item i: batches outermost, then bands of eight row tiles, so that the tiles of a wave
+// share their operands in L2.
 __device__ __forceinline__ Tile tile_of(const TileMap &j, int i) {
     Tile t;
     t.part = 0;
@@ -315,15 +318,16 @@ __device__ __forceinline__ int end_stage(const Job &j, const Tile &t) {
     return static_cast<int>(static_cast<int64_t>(j.k_blocks) * j.segments * (t.part + 1) / t.parts);
 }
 
-// Whether a symmetric matrix of which only the tiles on and above the diagonal exist has to be
-// read as its transpose at k of row tile `tile`: then the tensor core takes the mirrored
-// tile with its rows contiguous, and nothing is ever mirrored in memory.
+// Whether a symmetric matrix of which only the tiles on and above the diagonal exist has
+// to be read as its transpose at k of row tile `tile`: then the tensor core takes the
+// mirrored tile with its rows contiguous, and nothing is ever mirrored in memory.
 __device__ __forceinline__ int below(int half, int k, int tile) { return half && k / kTileM < tile; }
 
-// 32 columns (from c) of the warp's rows (from r0) as two binary16 planes, each staged in its
-// half of the warp's shared memory (swizzled as TMA reads it: 64-byte rows) and copied from there while
-// the warp goes on: every tile of a wave ends at once, and plain stores held the products up for as long
-// as L2 took to swallow them all (32 x 768 x 2048: 290 of 1840 us).
+// 32 columns (from c) of the warp's rows (from r0) as two binary16 planes, each staged in
+// its half of the warp's shared memory (swizzled as TMA reads it: 64-byte rows) and copied
+// from there while the warp goes on: every tile of a wave ends at once, and plain stores
+// held the products up for as long as L2 took to swallow them all (32 x 768 x 2048: 290 of
+// 1840 us).
 __device__ __forceinline__ void store_split(uint8_t *stage, const CUtensorMap *map, const Out &o, float (&v)[32], int z, int64_t r0,
                                             int64_t c, int64_t M) {
     const int lane = threadIdx.x & 31;
@@ -395,9 +399,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     constexpr int kPlaneB = BN / 2 * kDepth * 2;
-    // Buffers of sums in tensor memory.  With FOLD a buffer is taken every 64 k, so four small
-    // ones hide the way from the tensor core to the registers and back better than two; a
-    // tile of 256 columns then fills two of them, from the halves of each CTA's rows of B.
+    // Buffers of sums in tensor memory.  With FOLD a buffer is taken every 64 k, so four small ones
+    // hide the way from the tensor core to the registers and back better than two; a tile of 256
+    // columns then fills two of them, from the halves of each CTA's rows of B.
     constexpr int kBufCols = FOLD ? 128 : BN, kBuffers = FOLD ? 4 : 2, kHalves = BN / kBufCols;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -446,8 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         }
     };
 
-    // With FOLD the epilogue's warps need more registers than an even share: the first
-    // warpgroup gives up its own (128 * 48 + 256 * 224 of the 384 * 168 at launch).
+    // With FOLD the epilogue's warps need more registers than an even share: the first warpgroup
+    // gives up its own (128 * 48 + 256 * 224 of the 384 * 168 at launch).
     if (warp < 4) {
         if constexpr (FOLD) ptx::setmaxnreg_dec<48>();
         if (warp == 0 && ptx::elect_one()) {
@@ -718,8 +722,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                      : "memory");
 }
 
-// use(z, row, column, sum of the parts in their order) for every element of the tiles in parts, four
-// of a row at a time; a CTA of 256 threads to four rows (blockIdx.x = kJoinCtas * tile + rows).
+// use(z, row, column, sum of the parts in their order) for every element of the tiles in
+// parts, four of a row at a time; a CTA of 256 threads to four rows (blockIdx.x =
+// kJoinCtas * tile + rows).
 constexpr int kJoinCtas = kTileM / 4;
 
 template <int BN, class F>
@@ -742,9 +747,9 @@ __device__ __forceinline__ void each_joined(const TileMap &map, const float *slo
 
 constexpr int64_t kPairs = 76;                             // of SMs: sizes can be asked for without a GPU
 
-// The tiles of a product of so many stages and terms, and which of them go in parts of at least
-// eight stages: where the stages that saves (0.27 us for each term) outweigh the join's
-// launch (8 us) and the slots' traffic (0.1 us each).
+// The tiles of a product of so many stages and terms, and which of them go in parts of at
+// least eight stages: where the stages that saves (0.27 us for each term) outweigh the
+// join's launch (8 us) and the slots' traffic (0.1 us each).
 inline TileMap tile_map(int64_t M, int64_t N, int64_t cols, int64_t stages, int terms, int64_t batches, bool symmetric, bool in_parts) {
     TileMap m = {};
     const int64_t mt = (M + kTileM - 1) / kTileM, nt = (N + cols - 1) / cols;
@@ -767,7 +772,8 @@ inline size_t slot_bytes(const TileMap &m, int64_t batches, int64_t cols) {
     return (static_cast<size_t>(tiles_in_parts(m, batches)) * m.parts * kTileM * cols * 4 + 255) / 256 * 256;
 }
 
-// One operand: `planes` planes of `batches` matrices of `rows` x `k`, their rows or their k contiguous.
+// One operand: `planes` planes of `batches` matrices of `rows` x `k`, their rows or their
+// k contiguous.
 struct Operand {
     const void *p;
     int64_t inner, outer, pitch_bytes;         // contiguous extent, the other one, bytes between its lines
@@ -804,8 +810,8 @@ struct Spec {
     Out out;
 };
 
-// The terms that matter: planes i and j with i + j below the larger number of
-// planes (each plane is 2^-8, or 2^-11, of the one before).
+// The terms that matter: planes i and j with i + j below the larger number of planes (each
+// plane is 2^-8, or 2^-11, of the one before).
 inline int list_terms(int pa, int pb, int (&ta)[kMaxTerms], int (&tb)[kMaxTerms]) {
     const int top = pa > pb ? pa : pb;
     int n = 0;

@@ -1,22 +1,22 @@
-// qk_norm_rope.cu -- RMS norm of every query and key head and the rotation by
-// the token's position, in one pass, and its backward pass.
+// qk_norm_rope.cu -- RMS norm of every query and key head and the rotation by the token's
+// position, in one pass, and its backward pass.
 //
 //   r = (sum_d x^2 / D + eps)^(-1/2),  n = x r w,  y = R(pos) n
 //   dn = R(-pos) dy,  g = dn w,  dx = r (g - x r^2 sum_d (g x) / D),
 //   dw = sum over tokens and heads of dn x r
 //
-// Bound by memory: x is read once and y written once, nothing else is of their
-// size.  bf16, 16384 tokens of 32 + 8 heads of 128: 63 us, 5.3 TB/s (80% of the measured
-// copy rate), backward 106 us, 4.7 TB/s (71%): half of the issue slots are taken, and 16 warps
-// per SM wait for their loads and shuffles.  A head is held by a group of 2, 4 .. 32 lanes.  A lane's unit is two
-// chunks of E elements that hold whole pairs: chunk j of the first half of the
-// rotated elements and its partner in the second half, or two neighbouring
-// chunks.  So a rotation needs no other lane, and a lane's frequencies and
+// Bound by memory: x is read once and y written once, nothing else is of their size.
+// bf16, 16384 tokens of 32 + 8 heads of 128: 63 us, 5.3 TB/s (80% of the measured copy
+// rate), backward 106 us, 4.7 TB/s (71%): half of the issue slots are taken, and 16 warps
+// per SM wait for their loads and shuffles.  A head is held by a group of 2, 4 .. 32
+// lanes.  A lane's unit is two chunks of E elements that hold whole pairs: chunk j of the
+// first half of the rotated elements and its partner in the second half, or two
+// neighbouring chunks.  So a rotation needs no other lane, and a lane's frequencies and
 // weights are the same for every head: they stay in registers.
 //
-// The angle pos * freq is held in turns as a 64-bit fraction: freq / 2 pi is
-// rounded once to 2^-64 turns, and the product with the integer position wraps
-// around as the angle does, so no position loses precision.
+// The angle pos * freq is held in turns as a 64-bit fraction: freq / 2 pi is rounded once
+// to 2^-64 turns, and the product with the integer position wraps around as the angle
+// does, so no position loses precision.
 #include <algorithm>
 #include <cmath>
 
@@ -48,9 +48,9 @@ struct Args {
     float eps, inv_d;
 };
 
-// freq / (2 pi) modulo 1 as a 64-bit fraction: the 24-bit significand times 128
-// bits of 1 / (2 pi), shifted by the exponent, in integers (64-bit floating point has
-// a sixtieth of the rate here).  Exact to 2^-64 for |freq| < 2^40.
+// freq / (2 pi) modulo 1 as a 64-bit fraction: the 24-bit significand times 128 bits of 1
+// / (2 pi), shifted by the exponent, in integers (64-bit floating point has a sixtieth of
+// the rate here).  Exact to 2^-64 for |freq| < 2^40.
 __device__ __forceinline__ uint64_t turns_of(float freq) {
     constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;   // 2^128 / (2 pi)
     const uint32_t bits = __float_as_uint(freq);
@@ -157,8 +157,8 @@ __device__ __forceinline__ void store_head(char *row, const Values<E, U> &v, con
     }
 }
 
-// cos and sin of the token's angles; 0 turns for what is not rotated.  FAST: for
-// results of 16 bits, the hardware's functions, off by 2^-21 on (-pi, pi).
+// cos and sin of the token's angles; 0 turns for what is not rotated.  FAST: for results
+// of 16 bits, the hardware's functions, off by 2^-21 on (-pi, pi).
 template <bool FAST, int E, int U>
 __device__ __forceinline__ void angles(float (&c)[U][E], float (&s)[U][E], int64_t pos,
                                        const Steps &steps, const Lane<E, U> &l) {
@@ -227,7 +227,8 @@ __device__ __forceinline__ void fill_weights(float *w, const Side &s, int type, 
 }
 
 // A warp takes whole tokens, or with few tokens a share of a token's heads: the queries'
-// and then the keys', its groups the heads in turn, kAhead turns' loads before the first is used.
+// and then the keys', its groups the heads in turn, kAhead turns' loads before the first
+// is used.
 template <int TYPE, int E, int U>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) forward_kernel(const __grid_constant__ Args a) {
     constexpr int kAhead = E * U <= 8 ? 4 : 1;
