@@ -880,3 +880,33 @@ def test_callers_workspace(op):
                  lambda: op.gated_ffn_back(d, x, w, w, r.gate, r.up, workspace=ws[:256])):
         with pytest.raises(op.OopError):
             call()
+
+
+def test_refused_by_the_binding(op):
+    """Shapes, types and layouts that do not go together raise before anything is enqueued."""
+    import torch
+    q, k = torch.zeros(5, 4, 32, device="cuda"), torch.zeros(5, 2, 32, device="cuda")
+    pos, freqs = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.zeros(16, device="cuda")
+    x, w = torch.zeros(6, 16, device="cuda"), torch.zeros(24, 16, device="cuda")
+    h = torch.zeros(6, 24, device="cuda")
+    wide = torch.zeros(24, 20, device="cuda")[:, :16]
+    for call in (lambda: op.qk_norm_rope(q, k[:4], pos, freqs), lambda: op.qk_norm_rope(q, k.half(), pos, freqs),
+                 lambda: op.qk_norm_rope(q, k, pos[:4], freqs), lambda: op.qk_norm_rope(q, k, pos.long(), freqs),
+                 lambda: op.qk_norm_rope(q, k, None, freqs), lambda: op.qk_norm_rope(q, k, pos, freqs, freqs),
+                 lambda: op.qk_norm_rope(q[:, :, ::2], None, None, None), lambda: op.qk_norm_rope(q, k, pos, freqs, out_q=q[:4]),
+                 lambda: op.qk_norm_rope(q.double(), None, None, None),
+                 lambda: op.qk_norm_rope_back(q, None, q, k, pos, freqs), lambda: op.qk_norm_rope_back(q[:4], k, q, k, pos, freqs),
+                 lambda: op.gated_ffn(x, w, w[:, :8]), lambda: op.gated_ffn(x, w, wide), lambda: op.gated_ffn(x, w, w, act="tanh"),
+                 lambda: op.gated_ffn(x[:, :8], w, w), lambda: op.gated_ffn(x, w.double(), w.double()),
+                 lambda: op.gated_ffn(x, w, w, out=h.half()), lambda: op.gated_ffn(x, w, w, w_type=op.TYPE_Q8_0),
+                 lambda: op.gated_ffn_back(h[:5], x, w, w, h, h), lambda: op.gated_ffn_back(h, x, w, w, h.half(), h),
+                 lambda: op.gated_ffn_back(h, x, w, w, h, torch.zeros(6, 30, device="cuda")[:, :24]),
+                 lambda: op.orthogonalise(x, coefs=(1.0, 2.0)), lambda: op.orthogonalise(x, steps=2, coefs=[(1, 2, 3)] * 3),
+                 lambda: op.orthogonalise(x.t()), lambda: op.orthogonalise(x, out=x[:5]), lambda: op.orthogonalise(x[0])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: op.qk_norm_rope_back(q.half(), None, q, None, pos, freqs), lambda: op.orthogonalise(x.half()),
+                 lambda: op.gated_ffn_back(h.half(), x, w, w, h, h), lambda: op.qk_norm_rope(q, k, pos, freqs, eps=-1.0),
+                 lambda: op.qk_norm_rope(q[..., :16], None, pos, freqs), lambda: op.orthogonalise(x, steps=65)):
+        with pytest.raises(op.OopError):
+            call()
