@@ -8,7 +8,7 @@
 //
 // Bound by the tensor cores (three products of binary16 planes for one of 22 bits), whose
 // sums are folded every 64 k, and for few rows by launches.  f32, five steps: 8 x 2560 13
-// to 15 us, 32 x 768 x 2048 1.63 ms, 9728 x 2560 to bf16 1.09 ms (1.97 with the steps on X
+// to 15 us, 32 x 768 x 2048 1.63 ms, 9728 x 2560 to bf16 1.28 ms (1.97 with the steps on X
 // itself).
 #include <algorithm>
 #include <cmath>
@@ -546,12 +546,17 @@ double largest_q(const float *c) {
 }
 
 // Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all
-// products but the first and the last are of the smaller side alone, 3 r + 4 s - 3 of them
+// products but the first and the last are of the smaller side alone, 3 r + 5 s - 4 of them
 // (in n^3, symmetric results counted half) against s (3 r + 1) for a matrix r times as
-// long as wide: fewer from r = 1.25 on, but more launches.  What it costs is precision: a
-// rounding of A grows by Q^2 at every step, where one of X grows by Q, and reaches the
-// last Q as this share of it.  So only results of 16 bits are computed this way, and only
-// where the share stays below their rounding (five steps of the usual coefficients).
+// long as wide: fewer from r = 4/3 on, but more launches.  Z is symmetric as a polynomial,
+// but not as computed, and is kept whole: Q's rounding meets the small singular values'
+// large factors on one side of Q Z alone, and half of it mirrored would bring them to the
+// leading ones (an update of rank one was off by 11%).  What is left is the loss of
+// precision in A: a rounding of it grows by Q^2 at every step, where one of X grows by Q,
+// and reaches the last Q as this share of it.  So only results of 16 bits are computed this
+// way, and only where the share stays below their rounding (five steps of the usual
+// coefficients: measured up to 4096 x 12288, 1.3e-3 of the result's norm for an update of
+// rank one, below 4e-4 for others; bfloat16's own rounding is 1.7e-3).
 double rounding_of_a(int steps, const float *coefs) {
     double grown = 0x1p-24;
     for (int i = 0; i + 1 < steps; ++i) grown *= std::pow(largest_q(coefs ? coefs + 3 * i : kDefault), 2);
@@ -562,7 +567,8 @@ bool on_a_alone(int64_t n, int64_t deep, int64_t B, int steps, const float *coef
     if (steps < 2 || rounding_of_a(steps, coefs) > 0x1p-9) return false;
     const int64_t t = (n + 255) / 256, half = t * (t + 1) / 2 * B, whole = t * ((deep + 255) / 256) * B;
     const double first = product_time(half, deep, map_of_a(n, deep, B).parts), square = product_time(half, n, 1), with_x = product_time(whole, n, 1);
-    return first + (4 * steps - 3) * square + with_x < steps * (first + square + with_x);
+    const double whole_z = product_time(t * t * B, n, 1);
+    return first + (3 * steps - 2) * square + (steps - 1) * whole_z + with_x < steps * (first + square + with_x);
 }
 
 // The tiles of A in parts: summed, scaled, with the shift on the diagonal, as planes.
@@ -747,7 +753,10 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
                 for (int k : free_ones)
                     if (k != z_at && k != q_at) to = k;
                 const double next_scale = std::exp2(std::floor(std::log2(32768.0 / std::max(z_bound, 1.0))));
-                symmetric(q, pool[z_at], pool[to], next_scale / (kScaleQ * z_scale));
+                s = product_of(q, false, pool[z_at], i > 1, n, n, n);              // whole from here on; the first was a Q
+                s.a_half = true;
+                s.b_half = i == 1;
+                to_planes(s, pool[to], static_cast<float>(next_scale / (kScaleQ * z_scale)));
                 e = pair::launch<pair::kSplit, true, 256>(s, status, st);
                 z_scale = next_scale;
                 z_at = to;
@@ -761,9 +770,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         }
         if (e != cudaSuccess) return cuda_status(e);
         Z = pool[z_at];
-        s = tall ? product_of(X, false, Z, false, M, N, N) : product_of(Z, false, X, true, M, N, M);
-        s.a_half = !tall;
-        s.b_half = tall;
+        s = tall ? product_of(X, false, Z, false, M, N, N) : product_of(Z, false, X, true, M, N, M);   // X_0 Z', or Z X_0
         return cuda_status(last_product(s, static_cast<float>(1.0 / (z_scale * kScaleX))));
     }
     for (int i = 0; i < steps && e == cudaSuccess; ++i) {

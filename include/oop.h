@@ -688,7 +688,9 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
  * bits: the products take each factor as two binary16 terms of a scaled value
  * (22 bits or more), and X_s has to stay below 8 in magnitude, X X' below 64
  * and a + b X X' + c (X X')^2 below 256, as they do for coefficients that
- * keep the singular values below 1.5; beyond that the matrix is not finite.  A
+ * keep the singular values below 1.5; beyond that the matrix is not finite.  A BF16 y of
+ * a matrix much longer than wide (or the reverse) may come from the steps of X X' alone and one
+ * product with X_0, which adds up to 2^-9 of its norm to its rounding.  A
  * matrix of zeros gives zeros (eps > 0), one with a value that is not finite
  * gives NaN.  steps 0 .. 64.  eps >= 0, scale and coefs finite.  workspace:
  * oop_orthogonalise_workspace_size(...) bytes, 256-byte aligned.

@@ -1,0 +1,65 @@
+"""GPU tests of the layer operators at the ends of their range and at the borders of their rules: values that
+their intermediate steps could lose, coefficients and scales beyond the usual ones, one row, outliers.  Tolerances are
+those of test_gpu_layer, or derived where they stand; all are written before any run."""
+
+import numpy as np
+import pytest
+
+from oracle import layer
+from test_gpu_layer import ACTS, FLOOR, PROD, TINY, U, UOUT, USUAL, _close, _dt, _np, _rand, _status, _y_tol, op  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# orthogonalised updates
+# ---------------------------------------------------------------------------
+
+def _growth(x, coefs, eps=1e-7):
+    """How far an error of 1 of each X_s relative to its norm (at least 1) reaches in the result, summed over the steps.
+    A step maps every singular value t to p(t) = t (a + b t^2 + c t^4); to first order the part of an error between two
+    singular vectors grows by a difference quotient of p at their values, (p(t) -+ p(u)) / (t -+ u)."""
+    t = np.linalg.svd(x, compute_uv=False)
+    t = t / (np.sqrt((t * t).sum()) + eps)
+    norms, factors = [np.sqrt((t * t).sum())], []
+    for a, b, c in coefs:
+        u, v = t[:, None], np.append(t, 0.0)[None, :]               # 0: what the longer side has beyond them
+        s = t * t
+        # the quotients as polynomials, without the division
+        minus = a + b * (u * u + u * v + v * v) + c * (u ** 4 + u ** 3 * v + u * u * v * v + u * v ** 3 + v ** 4)
+        plus = a + b * (u * u - u * v + v * v) + c * (u ** 4 - u ** 3 * v + u * u * v * v - u * v ** 3 + v ** 4)
+        factors.append(np.maximum(np.abs(minus), np.abs(plus)))
+        t = t * (a + b * s + c * s * s)
+        norms.append(np.sqrt((t * t).sum()))
+    total, reach = max(1.0, norms[-1]), np.ones_like(u * v)
+    for n, f in zip(norms[-2::-1], factors[::-1]):
+        reach = reach * f
+        total += max(1.0, n) * reach.max()
+    return total
+
+
+def _steps_tol(x, coefs, want, kind, scale=1.0):
+    """Every stage is off by a few 2^-22 of its matrix."""
+    return 8 * 2.0 ** -22 * abs(scale) * _growth(x, coefs) + UOUT[kind] * np.linalg.norm(want)
+
+
+def _spectrum(seed, M, N, rank, noise):
+    """A matrix of low rank with noise: f32 tensor and its values."""
+    import torch
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((M, rank)) @ rng.standard_normal((rank, N)) + noise * rng.standard_normal((M, N))).float()
+    return x.cuda(), x.double().numpy()
+
+
+@pytest.mark.parametrize("M,N", [(100, 12000), (300, 9000), (1600, 4800), (4800, 1600)])
+@pytest.mark.parametrize("rank,noise", [(1, 1e-5), (6, 1e-3), (40, 1e-2), (0, 1.0)])
+def test_orthogonalise_spectra_on_the_smaller_side(op, M, N, rank, noise):  # noqa: F811
+    """16-bit results of updates of low rank by the usual steps, which run on A alone where one side is much the smaller."""
+    x, xv = _spectrum(rank, min(M, N), max(M, N), rank, noise)
+    if M > N:
+        x = x.t().contiguous()
+    want = layer.orthogonalise(xv, 5, [USUAL] * 5, 1e-7)
+    y = op.orthogonalise(x, out_dtype=_dt("bf16"))
+    # a rounding of A that reaches the last step: below 2^-9 of the result
+    got = _np(y) if M <= N else _np(y).T
+    assert np.linalg.norm(got - want) <= _steps_tol(xv, [USUAL] * 5, want, "bf16") + 2.0 ** -9 * np.linalg.norm(want)
