@@ -5,14 +5,19 @@
 
 namespace oop {
 
-// 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation. exp is kept
-// below 2^116: within the fast division's range (2 ulp), and the product of the two is
-// never Inf * 0.
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + expf(fminf(-v, 80.f))); }
+// 1 / (1 + exp(-v)), and with REST its difference from 1 without cancellation.  Of the two
+// the one below 1/2 is taken from exp(-|v|), so it falls to 0 as it should, whatever is
+// multiplied with it (a limit on the argument would leave 2e-35, which a gate of -1e35 or
+// its square shows), and the divisor stays between 1 and 2, in the fast division's range
+// (2 ulp).
+__device__ __forceinline__ float logistic(float v) {
+    const float e = expf(-fabsf(v)), s = __fdividef(1.f, 1.f + e);
+    return v < 0.f ? e * s : s;
+}
 __device__ __forceinline__ float logistic(float v, float &rest) {
-    const float e = expf(fminf(-v, 80.f)), s = __fdividef(1.f, 1.f + e);
-    rest = e * s;
-    return v != v ? v : s;
+    const float e = expf(-fabsf(v)), s = __fdividef(1.f, 1.f + e);
+    rest = v < 0.f ? s : e * s;
+    return v < 0.f ? e * s : s;
 }
 
 constexpr float kGeluTwice = 1.5957691216057308f;          // 2 sqrt(2 / pi)
@@ -43,7 +48,8 @@ __device__ __forceinline__ float activation_and_slope(int act, float v, float &s
     if (act == OOP_ACT_GELU_TANH) {
         float rest;
         const float s = logistic(gelu_argument(v), rest);
-        slope = s + v * (s * rest) * (kGeluTwice * (1.f + 0.134145f * v * v));
+        const float both = s * rest;                       // 0 long before v * v overflows
+        slope = both == 0.f ? s : s + v * both * (kGeluTwice * (1.f + 0.134145f * v * v));
         return v * s;
     }
     if (act == OOP_ACT_GELU_ERF) {

@@ -63,3 +63,37 @@ def test_orthogonalise_spectra_on_the_smaller_side(op, M, N, rank, noise):  # no
     # a rounding of A that reaches the last step: below 2^-9 of the result
     got = _np(y) if M <= N else _np(y).T
     assert np.linalg.norm(got - want) <= _steps_tol(xv, [USUAL] * 5, want, "bf16") + 2.0 ** -9 * np.linalg.norm(want)
+
+
+# ---------------------------------------------------------------------------
+# activations of large projections
+# ---------------------------------------------------------------------------
+
+SIZES_OF_GATES = [1e2, 1e4, 1e10, 1e11, 1e12, 1e15, 1e18, 2.5e19, 1e30, 1e33, 1e35, 3e38]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [4, 40])
+@pytest.mark.parametrize("act", ACTS)
+def test_activations_of_large_gates(op, act, T, kind):  # noqa: F811
+    """Values and slopes from 1e2 to the largest, of both signs: what lies below zero goes to 0 however large the factors
+    beside it.  x is a unit matrix, so every sum has one term: gates within 2^-21, activations and slopes within 16 u of
+    themselves, and the result's rounding."""
+    import torch
+    g = torch.tensor([s * v for v in SIZES_OF_GATES for s in (-1.0, 1.0)], dtype=torch.float64).to(_dt(kind)).cuda()
+    F = len(g)
+    x = torch.eye(T, dtype=_dt(kind), device="cuda")
+    wg = g[:, None].expand(F, T).contiguous()
+    one = torch.ones_like(wg)
+    v = np.broadcast_to(_np(g), (T, F))
+    want, slope = layer.act(v, act), layer.act_slope(v, act)
+    r = op.gated_ffn(x, wg, one, act=act, keep=True)
+    near = 2.0 ** -20 + UOUT[kind]
+    _close(r.gate, v, near * np.abs(v), "gate")
+    _close(r.h, want, near * np.abs(want) + TINY, "h")
+    gate, up = g.expand(T, F).contiguous(), torch.ones(T, F, dtype=_dt(kind), device="cuda")
+    dx, dwg, dwu = op.gated_ffn_back(torch.ones_like(up), x, one, torch.zeros_like(one), gate, up, act=act)
+    _close(dwg, slope.T, near * np.abs(slope.T) + TINY, "slope")
+    _close(dwu, want.T, near * np.abs(want.T) + TINY, "activation")
+    total = slope.sum(1)[:, None] * np.ones((1, T))
+    _close(dx, total, 2 * near * np.abs(slope).sum(1)[:, None] + TINY, "dx")
