@@ -535,16 +535,6 @@ struct Planes {
     }
 };
 
-// The largest |a + b l + c l^2| for eigenvalues l of A from 0 to 1.5.
-double largest_q(const float *c) {
-    double most = 0.0;
-    for (int i = 0; i <= 48; ++i) {
-        const double l = i / 32.0;
-        most = std::max(most, std::fabs(c[0] + l * (c[1] + l * c[2])));
-    }
-    return most;
-}
-
 // Steps on A alone.  Q is a polynomial of A, so X_s = Z X_0 with Z <- Q Z, A <- Q A Q: all
 // products but the first and the last are of the smaller side alone, 3 r + 5 s - 4 of them
 // (in n^3, symmetric results counted half) against s (3 r + 1) for a matrix r times as
@@ -557,14 +547,34 @@ double largest_q(const float *c) {
 // way, and only where the share stays below their rounding (five steps of the usual
 // coefficients: measured up to 4096 x 12288, 1.3e-3 of the result's norm for an update of
 // rank one, below 4e-4 for others; bfloat16's own rounding is 1.7e-3).
-double rounding_of_a(int steps, const float *coefs) {
-    double grown = 0x1p-24;
-    for (int i = 0; i + 1 < steps; ++i) grown *= std::pow(largest_q(coefs ? coefs + 3 * i : kDefault), 2);
-    const float *last = coefs ? coefs + 3 * (steps - 1) : kDefault;
-    return grown * std::fabs(last[1]) / std::max(1e-3, std::fabs(static_cast<double>(last[0])));
-}
+//
+// The eigenvalues l of A start within 0 .. 1, and a step takes them to l q(l)^2, with q(l) =
+// a + b l + c l^2: the largest magnitudes of q and of its slope, and the slope of l q^2
+// (what a rounding grows by), are taken over the range that the steps so far can reach.
+struct Reach {
+    double top = 1.0, z = 1.0;     // of the eigenvalues, of Z's
+    double grown = 0x1p-24;        // a rounding of A
+    double share = 0.0;            // of the Qs so far
+    void step(const float *c) {
+        double q_most = 0.0, slope_most = 0.0, growth = 0.0, next = 0.0;
+        for (int i = 0; i <= 64; ++i) {
+            const double l = top * i / 64.0, q = c[0] + l * (c[1] + l * c[2]), slope = c[1] + 2.0 * l * c[2];
+            q_most = std::max(q_most, std::fabs(q));
+            slope_most = std::max(slope_most, std::fabs(slope));
+            growth = std::max({growth, q * q, std::fabs(q * q + 2.0 * l * q * slope)});
+            next = std::max(next, l * q * q);
+        }
+        share += grown * slope_most / std::max(1e-3, std::fabs(static_cast<double>(c[0])));
+        grown = std::max(grown * growth, 0x1p-24);
+        z *= q_most;
+        top = 1.01 * next;                                 // between the samples
+    }
+};
 bool on_a_alone(int64_t n, int64_t deep, int64_t B, int steps, const float *coefs) {
-    if (steps < 2 || rounding_of_a(steps, coefs) > 0x1p-9) return false;
+    if (steps < 2) return false;
+    Reach r;
+    for (int i = 0; i < steps; ++i) r.step(coefs ? coefs + 3 * i : kDefault);
+    if (!(r.share <= 0x1p-9 && r.z <= 0x1p20)) return false;               // and Z keeps 19 bits of its leading part
     const int64_t t = (n + 255) / 256, half = t * (t + 1) / 2 * B, whole = t * ((deep + 255) / 256) * B;
     const double first = product_time(half, deep, map_of_a(n, deep, B).parts), square = product_time(half, n, 1), with_x = product_time(whole, n, 1);
     const double whole_z = product_time(t * t * B, n, 1);
@@ -723,7 +733,8 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         const Planes G = {next.p, n, n, B};                // A
         int free_ones[3] = {1, 2, 3};                      // pool[0] is P's
         P = pool[0];
-        double z_scale = 1.0, z_bound = 1.0;
+        double z_scale = 1.0;
+        Reach reach;                                       // Z's planes leave room for what it can reach
         pair::Spec s;
         e = square_of(X, G, 0.0);
         auto symmetric = [&](const Planes &a, const Planes &b, const Planes &d, double alpha) {
@@ -744,7 +755,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
             s.out.beta = c[1] * (kScaleQ / kScaleA);
             s.out.diag = c[0] * kScaleQ;
             e = pair::launch<pair::kSplit, true, 256>(s, status, st);
-            z_bound *= largest_q(c);
+            reach.step(c);
             if (i == 0) {
                 z_at = q_at;
                 z_scale = kScaleQ;
@@ -752,7 +763,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
                 int to = -1;
                 for (int k : free_ones)
                     if (k != z_at && k != q_at) to = k;
-                const double next_scale = std::exp2(std::floor(std::log2(32768.0 / std::max(z_bound, 1.0))));
+                const double next_scale = std::exp2(std::floor(std::log2(32768.0 / std::max(reach.z, 1.0))));
                 s = product_of(q, false, pool[z_at], i > 1, n, n, n);              // whole from here on; the first was a Q
                 s.a_half = true;
                 s.b_half = i == 1;

@@ -65,6 +65,25 @@ def test_orthogonalise_spectra_on_the_smaller_side(op, M, N, rank, noise):  # no
     assert np.linalg.norm(got - want) <= _steps_tol(xv, [USUAL] * 5, want, "bf16") + 2.0 ** -9 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(100, 12000), (9000, 130)])
+def test_orthogonalise_beyond_the_usual_range(op, M, N, out):  # noqa: F811
+    """Steps that stay within what the header allows (|X| < 8, |X X'| < 64, |Q| < 256) but take singular values past
+    those that the usual coefficients reach, and many steps whose last one has no linear term."""
+    import torch
+    x, xv = _rand(1, (M, N), "f32", 1e-4)
+    x[7, 5], xv[7, 5] = 1e3, 1e3                                    # one singular value, in one place
+    for xs, xsv, coefs in ((x, xv, [(2.8, 0.0, 0.0), (0.2, 0.0, 0.04)]),
+                           (*_spectrum(2, M, N, 6, 1e-3), [(1.5, 0.0, -0.5)] * 25)):
+        coefs32 = np.float32(coefs).astype(np.float64).tolist()
+        want = layer.orthogonalise(xsv, len(coefs), coefs32, 1e-7) if M <= N else layer.orthogonalise(xsv.T, len(coefs), coefs32, 1e-7).T
+        y = op.orthogonalise(xs, steps=len(coefs), coefs=coefs, out_dtype=_dt(out))
+        assert torch.isfinite(y).all()
+        tol = _steps_tol(xsv if M <= N else xsv.T, coefs32, want, out)
+        assert tol < 0.1 * np.linalg.norm(want)
+        assert np.linalg.norm(_np(y) - want) <= tol
+
+
 # ---------------------------------------------------------------------------
 # activations of large projections
 # ---------------------------------------------------------------------------
