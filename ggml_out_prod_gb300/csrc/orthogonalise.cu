@@ -787,8 +787,9 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     for (int i = 0; i < steps && e == cudaSuccess; ++i) {
         const float *c = coefs ? coefs + 3 * i : kDefault;
         // a + b A + c A A = c (A + b / 2c)^2 + a - b^2 / 4c: with the shift in A's diagonal Q is
-        // one product, and A need not be read again.  The shift has to be of A's size.
-        const bool square = c[2] != 0.f && std::fabs(c[1]) <= 8.f * std::fabs(c[2]);
+        // one product, and A need not be read again.  The shift has to be of A's size, and to bring
+        // A's eigenvalues, which are not negative, closer to 0: A's planes have no room above 64.
+        const bool square = c[2] != 0.f && (c[1] == 0.f || (c[1] < 0.f) != (c[2] < 0.f)) && std::fabs(c[1]) <= 8.f * std::fabs(c[2]);
         const double shift = square ? 0.5 * c[1] / c[2] : 0.0;
         e = square_of(X, A, shift);
         if (e != cudaSuccess) break;

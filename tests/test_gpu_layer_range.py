@@ -84,6 +84,20 @@ def test_orthogonalise_beyond_the_usual_range(op, M, N, out):  # noqa: F811
         assert np.linalg.norm(_np(y) - want) <= tol
 
 
+@pytest.mark.parametrize("M,N", [(64, 64), (70, 300)])
+def test_orthogonalise_coefficients_of_one_sign(op, M, N):  # noqa: F811
+    """X X' of 62 and a polynomial whose square has its centre on the other side: nothing leaves the range on the way."""
+    import torch
+    x = torch.zeros(M, N, device="cuda")
+    x[3, 5] = 2.0
+    coefs = [(7.9, 0.0, 0.0), (0.1, 0.0008, 0.0002)]
+    coefs32 = np.float32(coefs).astype(np.float64).tolist()
+    want = layer.orthogonalise(_np(x), 2, coefs32, 1e-7)
+    assert 7 < np.abs(want).max() < 8
+    y = op.orthogonalise(x, steps=2, coefs=coefs)
+    assert np.linalg.norm(_np(y) - want) <= _steps_tol(_np(x), coefs32, want, "f32")
+
+
 # ---------------------------------------------------------------------------
 # activations of large projections
 # ---------------------------------------------------------------------------
