@@ -797,7 +797,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
         s.batches = 1, s.segments = 2;
         s.planes_a = f.d.planes, s.planes_b = f.w.planes;
         s.a_plane = 2, s.a_seg = 1, s.b_plane = 1;
-        s.out.p0 = dx, s.out.nb0 = nb_dx, s.out.type = dh_type, s.out.alpha = 1.f;
+        s.out.p0 = dx, s.out.nb0 = nb_dx, s.out.type = dh_type, s.out.alpha = s.out.beta = 1.f;
         s.out.wide = K * d_size % 16 == 0 && rows_aligned(dx, nb_dx, T);
         if (e == cudaSuccess) e = run(s);
     }
@@ -811,7 +811,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
         s.batches = 2, s.segments = 1;
         s.planes_a = f.d.planes, s.planes_b = f.x.planes;
         s.a_plane = 2, s.a_batch = 1, s.b_plane = 1;
-        s.out.p0 = dw_gate, s.out.p1 = dw_up, s.out.nb0 = nb_dw, s.out.type = dh_type, s.out.alpha = 1.f;
+        s.out.p0 = dw_gate, s.out.p1 = dw_up, s.out.nb0 = nb_dw, s.out.type = dh_type, s.out.alpha = s.out.beta = 1.f;
         s.out.wide = K * d_size % 16 == 0 && rows_aligned(dw_gate, nb_dw, F) && rows_aligned(dw_up, nb_dw, F);
         if (e == cudaSuccess) e = run(s);
     }

@@ -723,7 +723,8 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
         p.out.nb0 = nb_y[0];
         p.out.batch = nb_y[1];
         p.out.type = y_type;
-        p.out.alpha = scale * alpha;
+        p.out.alpha = alpha;                               // a power of two: its product with a small scale would lose bits
+        p.out.beta = scale;
         p.out.wide = N * ys % 16 == 0 && is_aligned(y, 16) && (M <= 1 || nb_y[0] % 16 == 0) && (B <= 1 || nb_y[1] % 16 == 0);
         return pair::launch<pair::kPlain, true, 256>(p, status, st);
     };

@@ -44,7 +44,7 @@ constexpr int kSmem = 227 * 1024;
 
 // Where finished sums go.
 enum Epilogue {
-    kPlain,      // alpha * sum, rounded once, to a matrix
+    kPlain,      // beta * (alpha * sum), rounded once, to a matrix
     kGate,       // act(gate) * up, and the two themselves if they are kept
     kSplit       // alpha * sum + beta * C + diag on the diagonal, as two binary16 planes
 };
@@ -649,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     store_split(stage_out, &j.result, j.out, v, t.z, r0, c, j.M);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha;
+                    for (int k = 0; k < 32; ++k) v[k] *= j.out.alpha, v[k] *= j.out.beta;
                     char *base = j.out.p1 && t.z ? static_cast<char *>(j.out.p1) : static_cast<char *>(j.out.p0) + t.z * j.out.batch;
                     store_block(j.out.type, stage_out, v, base + r0 * j.out.nb0 + c * element, j.out.nb0, rows, j.N - c, j.out.wide);
                 }

@@ -98,6 +98,18 @@ def test_orthogonalise_coefficients_of_one_sign(op, M, N):  # noqa: F811
     assert np.linalg.norm(_np(y) - want) <= _steps_tol(_np(x), coefs32, want, "f32")
 
 
+@pytest.mark.parametrize("M,N", [(12, 40), (96, 200)])
+@pytest.mark.parametrize("scale", [2e-38, -1e-33, 3e30])
+def test_orthogonalise_of_any_scale(op, M, N, scale):  # noqa: F811
+    """The factor of the result from the smallest to large ones."""
+    x, xv = _rand(3, (M, N), "f32")
+    scale = float(np.float32(scale))
+    for out in ("f32", "bf16"):
+        want = layer.orthogonalise(xv, 5, [USUAL] * 5, 1e-7, scale)
+        y = op.orthogonalise(x, scale=scale, out_dtype=_dt(out))
+        assert np.linalg.norm(_np(y) - want) <= _steps_tol(xv, [USUAL] * 5, want, out, scale) + M * N * FLOOR[out]
+
+
 # ---------------------------------------------------------------------------
 # activations of large projections
 # ---------------------------------------------------------------------------
