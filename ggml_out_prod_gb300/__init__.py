@@ -1315,8 +1315,8 @@ def _ffn_weights(w_gate, w_up, w_type, K):
     else:
         _check_src0(w_gate, w_type, "w_gate")
     M, F, nb = _rows(w_gate, "w_gate")
-    if F > 1 and _rows(w_up, "w_up")[2] != nb or not w_up.is_cuda:
-        raise ValueError("w_gate and w_up must be CUDA tensors whose rows lie at one stride")
+    if _rows(w_up, "w_up")[2] != nb and F > 1:
+        raise ValueError("the rows of w_gate and w_up must lie at one stride")
     row = M if w_type in _BLOCKS else M * _size_of(w_gate)
     if w_type in _BLOCKS:
         qk, nbytes = _BLOCKS[w_type]

@@ -142,3 +142,30 @@ def test_activations_of_large_gates(op, act, T, kind):  # noqa: F811
     _close(dwu, want.T, near * np.abs(want.T) + TINY, "activation")
     total = slope.sum(1)[:, None] * np.ones((1, T))
     _close(dx, total, 2 * near * np.abs(slope).sum(1)[:, None] + TINY, "dx")
+
+
+# ---------------------------------------------------------------------------
+# one row of weights
+# ---------------------------------------------------------------------------
+
+def test_gated_ffn_of_one_feature(op):  # noqa: F811
+    """F = 1: a row's place does not matter, but its elements have to be contiguous in either weight."""
+    import torch
+    x, _ = _rand(1, (20, 16), "f32")
+    wg, _ = _rand(2, (1, 16), "f32")
+    wu, _ = _rand(3, (1, 16), "f32")
+    r = op.gated_ffn(x, wg, wu, keep=True)
+    apart = torch.cat([wu, wg], 1)[:, :16]                          # a row of a wider matrix
+    assert torch.equal(op.gated_ffn(x, wg, apart).h, r.h) and torch.equal(op.gated_ffn(x, apart, wg).h, op.gated_ffn(x, wu, wg).h)
+    d = torch.ones_like(r.h)
+    for a, b in zip(op.gated_ffn_back(d, x, wg, apart, r.gate, r.up), op.gated_ffn_back(d, x, wg, wu, r.gate, r.up)):
+        assert torch.equal(a, b)
+    spread = wu.repeat_interleave(2, 1)[:, ::2]
+    assert torch.equal(spread, wu) and spread.stride(1) == 2
+    for a, b in ((wg, spread), (spread, wu)):
+        with pytest.raises(ValueError):
+            op.gated_ffn(x, a, b)
+        with pytest.raises(ValueError):
+            op.gated_ffn_back(d, x, a, b, r.gate, r.up)
+    with pytest.raises(ValueError):
+        op.gated_ffn(x, wg, wu.cpu())
