@@ -6,8 +6,8 @@
 //   dw = sum over tokens and heads of dn x r
 //
 // Bound by memory: x is read once and y written once, nothing else is of their size.
-// bf16, 16384 tokens of 32 + 8 heads of 128: 63 us, 5.3 TB/s (80% of the measured copy
-// rate), backward 106 us, 4.7 TB/s (71%): half of the issue slots are taken, and 16 warps
+// bf16, 16384 tokens of 32 + 8 heads of 128: 62 us, 5.4 TB/s (80% of the measured copy
+// rate), backward 108 us, 4.6 TB/s (69%): half of the issue slots are taken, and 16 warps
 // per SM wait for their loads and shuffles.  A head is held by a group of 2, 4 .. 32
 // lanes.  A lane's unit is two chunks of E elements that hold whole pairs: chunk j of the
 // first half of the rotated elements and its partner in the second half, or two
@@ -19,6 +19,7 @@
 // does, so no position loses precision.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "oop_internal.cuh"
 #include "rows.cuh"
@@ -46,6 +47,7 @@ struct Args {
     int64_t T;
     int D, half, interleaved, group_shift, units, w_type;
     float eps, inv_d;
+    float low;                       // sums of squares below it are taken again
 };
 
 // freq / (2 pi) modulo 1 as a 64-bit fraction: the 24-bit significand times 128 bits of 1
@@ -184,12 +186,14 @@ __device__ __forceinline__ void angles(float (&c)[U][E], float (&s)[U][E], int64
         }
 }
 
-// The lane's pairs turned; DIR = -1: back.
-template <int DIR, int E, int U>
+// The lane's pairs turned; DIR = -1: back.  Without INF what is not rotated is turned by 0:
+// nothing in it may be Inf.
+template <int DIR, bool INF, int E, int U>
 __device__ __forceinline__ void rotate(Values<E, U> &v, const float (&c)[U][E], const float (&s)[U][E],
-                                       bool interleaved) {
+                                       bool interleaved, const Lane<E, U> &l) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if (INF && l.freq[u] < 0) continue;
         if (E == 1 || !interleaved) {
 #pragma unroll
             for (int p = 0; p < E; ++p) turn(v.a[u][p], v.b[u][p], c[u][p], DIR * s[u][p]);
@@ -203,10 +207,11 @@ __device__ __forceinline__ void rotate(Values<E, U> &v, const float (&c)[U][E], 
     }
 }
 
-__device__ __forceinline__ float group_sum(float v, int group) {
-    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ float sum_in_group(float v, int group, unsigned lanes) {
+    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(lanes, v, o);
     return v;
 }
+__device__ __forceinline__ float group_sum(float v, int group) { return sum_in_group(v, group, 0xffffffffu); }
 
 template <int E, int U>
 __device__ __forceinline__ float dot(const Values<E, U> &v, const Values<E, U> &w) {
@@ -219,6 +224,42 @@ __device__ __forceinline__ float dot(const Values<E, U> &v, const Values<E, U> &
             z = fmaf(v.b[u][i], w.b[u][i], z);
         }
     return s + z;
+}
+
+// A head whose sum of squares has left fp32's range, or lost its bits below it.  Such heads
+// are rare: their loops leave them out and take them again, by themselves, where the sum is
+// that of the head times a power of two.
+__device__ __forceinline__ bool out_of_range(float sum, const Args &a) {
+    return !(sum >= a.low && sum < __int_as_float(0x7f800000));
+}
+
+__device__ __forceinline__ unsigned lanes_of_group(int group) {
+    return (0xffffffffu >> (32 - group)) << (threadIdx.x & 31 & ~(group - 1));
+}
+
+// r of such a head, which keeps the power of two that `scale` returns (r is that of the
+// scaled head).  One that is not finite, or 0 with eps = 0, stays as it is.  All lanes of a
+// group come here together.
+template <int E, int U>
+__device__ __forceinline__ float rescaled(Values<E, U> &v, const Args &a, float &scale) {
+    const int group = 1 << a.group_shift;
+    const unsigned lanes = lanes_of_group(group);
+    float top = sqrtf(a.eps);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) top = fmaxf(top, fmaxf(fabsf(v.a[u][i]), fabsf(v.b[u][i])));
+    for (int o = group >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
+    const int exponent = static_cast<int>(__float_as_uint(top) >> 23);
+    scale = top == 0.f || exponent == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(1, 254 - exponent)) << 23);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            v.a[u][i] *= scale;
+            v.b[u][i] *= scale;
+        }
+    return rsqrtf(sum_in_group(dot(v, v), group, lanes) * a.inv_d + a.eps * scale * scale);
 }
 
 // Weights of both sides in shared memory, as floats.
@@ -272,13 +313,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) forward_kernel(const
                         wv.a[u][i] = l.c0[u] < 0 ? 0.f : w[l.c0[u] + i];
                         wv.b[u][i] = l.c1[u] < 0 ? 0.f : w[l.c1[u] + i];
                     }
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    if (h0 + k * step >= s.heads) break;   // the same for the warp
-                    const int h = h0 + k * step + mine;
-                    Values<E, U> v;
-                    raw[k].get(v);
-                    const float r = rsqrtf(group_sum(dot(v, v), group) * a.inv_d + a.eps);
+                auto finish = [&](auto inf, Values<E, U> &v, float r, int h, bool stored) {
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -286,8 +321,33 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) forward_kernel(const
                             v.a[u][i] *= r * wv.a[u][i];
                             v.b[u][i] *= r * wv.b[u][i];
                         }
-                    rotate<1>(v, c, sn, a.interleaved);
-                    if (h < s.heads) store_head<TYPE>(y + h * s.out_head, v, l);
+                    rotate<1, inf>(v, c, sn, a.interleaved, l);
+                    if (stored) store_head<TYPE>(y + h * s.out_head, v, l);
+                };
+                unsigned again = 0;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (h0 + k * step >= s.heads) break;   // the same for the warp
+                    const int h = h0 + k * step + mine;
+                    Values<E, U> v;
+                    raw[k].get(v);
+                    const float sum = group_sum(dot(v, v), group);
+                    const bool out = out_of_range(sum, a);
+                    again |= out ? 1u << k : 0u;
+                    finish(std::false_type(), v, rsqrtf(sum * a.inv_d + a.eps), h, h < s.heads && !out);
+                }
+                if (!__any_sync(0xffffffffu, again)) continue;
+#pragma unroll 1
+                for (int k = 0; k < kAhead; ++k) {
+                    const int h = h0 + k * step + mine;
+                    if (!(again >> k & 1) || h >= s.heads) continue;       // the same for the group
+                    Raw<TYPE, E, U> one;
+                    Values<E, U> v;
+                    float scale;
+                    one.load(x + h * s.x_head, true, l);   // not stored to yet, if y is x
+                    one.get(v);
+                    const float r = rescaled(v, a, scale);
+                    finish(std::true_type(), v, r, h, true);
                 }
             }
         }
@@ -299,6 +359,8 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(cons
     constexpr int kAhead = E * U <= 4 ? 4 : E * U <= 8 ? 2 : 1;
     __shared__ Steps steps;
     __shared__ __align__(16) float weights[kMaxHead];
+    __shared__ int again[kThreads / 32];                   // a warp has left out heads
+    if (threadIdx.x < kThreads / 32) again[threadIdx.x] = 0;           // before the barriers below
     const int which = blockIdx.x >= static_cast<unsigned>(a.side[0].ctas);
     const Side &s = a.side[which];
     const int lane = threadIdx.x & 31, group = 1 << a.group_shift;
@@ -310,12 +372,37 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(cons
     Values<E, U> dw = {};
     const int64_t cta = static_cast<int64_t>(blockIdx.x) - (which ? a.side[0].ctas : 0);
     const int64_t warps = static_cast<int64_t>(s.ctas) * (kThreads / 32);
-    for (int64_t item = cta * (kThreads / 32) + (threadIdx.x >> 5); item < a.T * s.splits; item += warps) {
+    const int64_t first = cta * (kThreads / 32) + (threadIdx.x >> 5);
+    const int step = groups * s.splits;
+    float c[U][E], sn[U][E];
+    auto weigh = [&](auto inf, Values<E, U> &x, Values<E, U> &d, float r) {        // x becomes x r, d becomes g
+        rotate<-1, inf>(d, c, sn, a.interleaved, l);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                x.a[u][i] *= r;
+                x.b[u][i] *= r;
+                dw.a[u][i] = fmaf(d.a[u][i], x.a[u][i], dw.a[u][i]);
+                dw.b[u][i] = fmaf(d.b[u][i], x.b[u][i], dw.b[u][i]);
+                d.a[u][i] *= l.c0[u] < 0 ? 0.f : weights[l.c0[u] + i];
+                d.b[u][i] *= l.c1[u] < 0 ? 0.f : weights[l.c1[u] + i];
+            }
+    };
+    auto finish = [&](const Values<E, U> &x, Values<E, U> &d, float r, float m) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                d.a[u][i] = r * (d.a[u][i] - x.a[u][i] * m);
+                d.b[u][i] = r * (d.b[u][i] - x.b[u][i] * m);
+            }
+    };
+    for (int64_t item = first; item < a.T * s.splits; item += warps) {
         const int64_t t = item / s.splits;
-        const int share = static_cast<int>(item - t * s.splits), step = groups * s.splits;
+        const int share = static_cast<int>(item - t * s.splits);
         const char *xt = static_cast<const char *>(s.x) + t * s.x_tok, *dt = static_cast<const char *>(s.dy) + t * s.dy_tok;
         char *yt = static_cast<char *>(s.out) + t * s.out_tok;
-        float c[U][E], sn[U][E];
         for (int h0 = share * groups; h0 < s.heads; h0 += step * kAhead) {
             Raw<TYPE, E, U> raw_x[kAhead];
             Raw<DTYPE, E, U> raw_d[kAhead];
@@ -333,29 +420,47 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) backward_kernel(cons
                 Values<E, U> x, d;
                 raw_x[k].get(x);
                 raw_d[k].get(d);
-                float r = rsqrtf(group_sum(dot(x, x), group) * a.inv_d + a.eps);
-                if (h >= s.heads) r = 0.f;                 // eps = 0: not 0 * Inf
-                rotate<-1>(d, c, sn, a.interleaved);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {          // x becomes x r, d becomes g
-                        x.a[u][i] *= r;
-                        x.b[u][i] *= r;
-                        dw.a[u][i] = fmaf(d.a[u][i], x.a[u][i], dw.a[u][i]);
-                        dw.b[u][i] = fmaf(d.b[u][i], x.b[u][i], dw.b[u][i]);
-                        d.a[u][i] *= l.c0[u] < 0 ? 0.f : weights[l.c0[u] + i];
-                        d.b[u][i] *= l.c1[u] < 0 ? 0.f : weights[l.c1[u] + i];
-                    }
-                const float m = group_sum(dot(d, x), group) * a.inv_d;
+                const float sum = group_sum(dot(x, x), group);
+                const bool out = out_of_range(sum, a);
+                if (out) again[threadIdx.x >> 5] = 1;      // in shared memory: the registers are all taken
+                float r = rsqrtf(sum * a.inv_d + a.eps);
+                if (h >= s.heads || out) r = 0.f;          // adds nothing; eps = 0: not 0 * Inf
+                weigh(std::false_type(), x, d, r);
+                finish(x, d, r, group_sum(dot(d, x), group) * a.inv_d);
+                if (h < s.heads && !out) store_head<DTYPE>(yt + h * s.out_head, d, l);
+            }
+        }
+    }
+    __syncwarp();
+    if (again[threadIdx.x >> 5]) {                         // those left out, in a loop of their own for the same reason
+#pragma unroll 1
+        for (int64_t item = first; item < a.T * s.splits; item += warps) {
+            const int64_t t = item / s.splits;
+            const int share = static_cast<int>(item - t * s.splits);
+            angles<DTYPE != OOP_TYPE_F32>(c, sn, a.half ? a.pos[t] : 0, steps, l);
+#pragma unroll 1
+            for (int h0 = share * groups; h0 < s.heads; h0 += step) {
+                const int h = h0 + mine;
+                Raw<TYPE, E, U> raw_x;
+                Raw<DTYPE, E, U> raw_d;
+                Values<E, U> x, d;
+                raw_x.load(static_cast<const char *>(s.x) + t * s.x_tok + h * s.x_head, h < s.heads, l);
+                raw_x.get(x);
+                if (!out_of_range(group_sum(dot(x, x), group), a) || h >= s.heads) continue;       // the same for the group
+                raw_d.load(static_cast<const char *>(s.dy) + t * s.dy_tok + h * s.dy_head, true, l);       // not stored to, if dx is dy
+                raw_d.get(d);
+                float scale;
+                const float r = rescaled(x, a, scale);
+                weigh(std::true_type(), x, d, r);
+                finish(x, d, r, sum_in_group(dot(d, x), group, lanes_of_group(group)) * a.inv_d);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
-                        d.a[u][i] = r * (d.a[u][i] - x.a[u][i] * m);
-                        d.b[u][i] = r * (d.b[u][i] - x.b[u][i] * m);
+                        d.a[u][i] *= scale;
+                        d.b[u][i] *= scale;
                     }
-                if (h < s.heads) store_head<DTYPE>(yt + h * s.out_head, d, l);
+                store_head<DTYPE>(static_cast<char *>(s.out) + t * s.out_tok + h * s.out_head, d, l);
             }
         }
     }
@@ -435,6 +540,8 @@ void plan(Args &a, int e, int64_t D, int64_t n_rot, int64_t T, int sms, bool bac
     a.D = static_cast<int>(D);
     a.half = static_cast<int>(n_rot / 2);
     a.inv_d = 1.f / static_cast<float>(D);
+    // squares below 2^-126 lose bits: of up to 1024 they matter to a sum below 2^-100
+    a.low = static_cast<double>(a.eps) * static_cast<double>(D) < 0x1p-100 ? 0x1p-100f : 0.f;
     a.units = a.half / e + static_cast<int>((D - n_rot + 2 * e - 1) / (2 * e));
     a.group_shift = 0;
     while ((1 << a.group_shift) < a.units && a.group_shift < 5) ++a.group_shift;

@@ -564,7 +564,9 @@ int oop_preference_loss_back(const void *logits, int type, int64_t nb, const int
  * where the results have 16 bits.  freqs: device f32 {n_rot/2}, radians per position.
  * q and k may be slices of one buffer; k may be NULL (queries only).  D is 1 ..
  * 1024, n_rot even, 0 .. D (0: norm only, pos and freqs not used).  y may be x.
- * eps >= 0, finite.  A pair whose frequency is not finite is NaN.
+ * eps >= 0, finite.  A head may have any finite values: where its squares leave fp32's
+ * range they are taken of the head times a power of two (a head of zeros is NaN with
+ * eps = 0).  A pair whose frequency is not finite is NaN.
  */
 typedef struct {
     const void *x;      /* {D, n_head, T}: device, plain type */

@@ -169,3 +169,55 @@ def test_gated_ffn_of_one_feature(op):  # noqa: F811
             op.gated_ffn_back(d, x, a, b, r.gate, r.up)
     with pytest.raises(ValueError):
         op.gated_ffn(x, wg, wu.cpu())
+
+
+# ---------------------------------------------------------------------------
+# head norms of very large and very small heads
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D,rot", [(64, 64), (128, 96), (33, 32), (7, 4), (1024, 512), (1021, 64)])
+@pytest.mark.parametrize("kind,d_kind", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_qk_norm_rope_of_heads_of_all_scales(op, D, rot, kind, d_kind, eps):  # noqa: F811
+    """Heads from 2^-115 to 2^120 side by side: sums of their squares leave fp32's range."""
+    import torch
+    scales = 2.0 ** np.array([0, 120, -115, 63, -52, 64, -63, 100, -100, 0, 70, -75])
+    T, H = 3, len(scales)
+    x, _ = _rand(D, (T, H, D), kind)
+    x = (x.double() * torch.from_numpy(scales).cuda()[None, :, None]).to(x.dtype)
+    xv = _np(x)
+    w, wv = _rand(2, (D,), "f32", 0.3, 1.0)
+    d, dv = _rand(3, (T, H, D), d_kind)
+    pos = np.array([0, 17, 90001], dtype=np.int32)
+    freqs = (1e4 ** (-np.arange(rot // 2) / (rot // 2))).astype(np.float32)
+    tp, tf = torch.from_numpy(pos).cuda(), torch.from_numpy(freqs).cuda()
+    eps_v = float(np.float32(eps))
+    y, yk = op.qk_norm_rope(x, x[:, :5], tp, tf, w, w, eps=eps)
+    want = layer.norm_rope(xv, wv, pos, freqs, eps_v, False)
+    n = layer.norm_rope(xv, wv, pos, freqs[:0], eps_v, False)
+    _close(y, want, _y_tol(n, rot, False, kind, want), "y")
+    assert torch.equal(yk, y[:, :5])
+    gx, _, gw, _ = op.qk_norm_rope_back(d, None, x, None, tp, tf, w, eps=eps)
+    dx, dw = layer.norm_rope_back(dv, xv, wv, pos, freqs, eps_v, False)
+    # as in test_qk_norm_rope_back; |dn| is bounded by its pair's elements
+    a, b = layer.pairs(D, rot, False)
+    dn = np.abs(dv)
+    dn[..., a], dn[..., b] = dn[..., a] + np.abs(dv[..., b]), dn[..., b] + np.abs(dv[..., a])
+    r = 1 / np.sqrt((xv * xv).mean(-1, keepdims=True) + eps_v)
+    xr, wd = np.abs(xv) * r, np.abs(wv) * dn
+    tol = r * (50 * U * wd + xr * (wd * xr).mean(-1, keepdims=True) * 130 * U) + UOUT[d_kind] * np.abs(dx) + FLOOR[d_kind]
+    _close(gx, dx, tol, "dx")
+    _close(gw, dw, (45 + T * H + 400) * U * (dn * xr).sum((0, 1)) + TINY, "dw")
+
+
+def test_qk_norm_rope_of_heads_that_are_not_finite(op):  # noqa: F811
+    """A NaN makes its head NaN, an Inf its own element, as the formula has it; zeros stay zeros; the heads beside them are
+    untouched."""
+    import torch
+    x, _ = _rand(1, (2, 6, 64), "f32")
+    want = op.qk_norm_rope(x, None, None, None)[0]
+    x[0, 1, 5], x[1, 2, 7], x[0, 3] = float("nan"), float("inf"), 0.0
+    y = op.qk_norm_rope(x, None, None, None)[0]
+    assert torch.isnan(y[0, 1]).all() and torch.isnan(y[1, 2, 7]) and (y[1, 2, :7] == 0).all() and (y[0, 3] == 0).all()
+    for t, h in ((0, 0), (0, 2), (0, 4), (0, 5), (1, 0), (1, 1), (1, 3), (1, 4), (1, 5)):
+        assert torch.equal(y[t, h], want[t, h])
