@@ -298,12 +298,13 @@ cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
 
 // Rows of any type as P binary16 planes [P][rows][pitch] of a scaled value, hi + lo: a row
 // is scaled by the power of two that brings its largest magnitude to 2^13 .. 2^14, so
-// nothing overflows, what is above 2^-15 of the largest keeps 22 bits or more, and what is
-// below is off by 2^-39 of the largest, which is in every sum of the row.  factors: the
-// inverse scales.  Two planes and three terms do for the forward products of f32 what
-// three bfloat16 planes and six terms do elsewhere, whose sums run over other rows'
-// scales.  A warp takes a row, read once up to 2560 columns; up to three matrices of the
-// same columns in a launch.
+// nothing overflows, what is above 2^-16 of the largest keeps 22 bits or more, and what is
+// below is off by up to 2^-38 of the largest (half of binary16's smallest step, 2^-24, over
+// 2^13).  That is relative to the row, not to a sum's terms: where the other matrix is zero
+// under the largest, it shows in full.  factors: the inverse scales.  So two planes and three
+// terms do for the forward products of f32; elsewhere, where sums run over other rows'
+// scales, it takes three bfloat16 planes and six terms.  A warp takes a row, read once up to
+// 2560 columns; up to three matrices of the same columns in a launch.
 struct Scaled {
     const char *src;
     int64_t nb, rows;

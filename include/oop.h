@@ -623,9 +623,12 @@ int oop_qk_norm_rope_back(const oop_heads_grad *q, const oop_heads_grad *k, int 
  *                       may both be NULL (not kept)
  *
  * h is computed from the 32-bit sums and rounded once.  x and the weights of
- * one 16-bit type go to the tensor cores as they are.  Where x is F32, its rows and the
- * weights' go as two binary16 terms (one for 16-bit weights) scaled by a power of two for each
- * row: an element keeps 22 bits or more, or is off by 2^-39 of its row's largest.  Other
+ * one 16-bit type go to the tensor cores as they are.  Where x is F32 and T above 8 (or x
+ * too long for the form of few tokens), its rows and the weights' go as two binary16 terms
+ * (one for 16-bit weights) scaled by a power of two for each row: an element keeps 22 bits or
+ * more, or is off by 2^-38 of its row's largest, so a sum may be off by 2^-38 of max |x| *
+ * sum |w| + sum |x| * max |w| beside its roundings: an element of x 2^16 times as large as
+ * the others costs them bits, also where its own weight is 0.  Few tokens keep fp32.  Other
  * operands go as two bfloat16 terms, 16 bits.  Nothing overflows on the way that fp32 holds.
  * Magnitudes below 2^-110 may lose bits.  A non-finite operand gives non-finite
  * sums.  K == 0: sums of nothing, 0.

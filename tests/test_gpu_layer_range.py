@@ -221,3 +221,26 @@ def test_qk_norm_rope_of_heads_that_are_not_finite(op):  # noqa: F811
     assert torch.isnan(y[0, 1]).all() and torch.isnan(y[1, 2, 7]) and (y[1, 2, :7] == 0).all() and (y[0, 3] == 0).all()
     for t, h in ((0, 0), (0, 2), (0, 4), (0, 5), (1, 0), (1, 1), (1, 3), (1, 4), (1, 5)):
         assert torch.equal(y[t, h], want[t, h])
+
+
+# ---------------------------------------------------------------------------
+# outliers
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [8, 9, 130])
+def test_gated_ffn_outlier_that_no_weight_meets(op, T):  # noqa: F811
+    """f32: an element of 2^28 under a column of zeros.  Up to eight tokens keep fp32; more of them lose up to 2^-38 of
+    their row's largest element in each of the others, whatever weight that one meets."""
+    K, F = 256, 40
+    x, xv = _rand(T, (T, K), "f32")
+    wg, wgv = _rand(2, (F, K), "f32", K ** -0.5)
+    wu, wuv = _rand(3, (F, K), "f32", K ** -0.5)
+    x[2, 9], xv[2, 9] = 2.0 ** 28, 2.0 ** 28
+    wg[:, 9], wgv[:, 9], wu[:, 9], wuv[:, 9] = 0.0, 0.0, 0.0, 0.0
+    r = op.gated_ffn(x, wg, wu, keep=True)
+    for got, wv in ((r.gate, wgv), (r.up, wuv)):
+        ax, aw = np.abs(xv), np.abs(wv)
+        tol = PROD(K, "f32") * (ax @ aw.T)
+        if T > 8:
+            tol = tol + 2.0 ** -38 * (ax.max(1)[:, None] * aw.sum(1) + ax.sum(1)[:, None] * aw.max(1))
+        _close(got, xv @ wv.T, tol, "outlier")
