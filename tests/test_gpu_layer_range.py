@@ -244,3 +244,41 @@ def test_gated_ffn_outlier_that_no_weight_meets(op, T):  # noqa: F811
         if T > 8:
             tol = tol + 2.0 ** -38 * (ax.max(1)[:, None] * aw.sum(1) + ax.sum(1)[:, None] * aw.max(1))
         _close(got, xv @ wv.T, tol, "outlier")
+
+
+# ---------------------------------------------------------------------------
+# how much dgate and dup keep between the products
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,K,F", [(1, 96, 130), (16, 264, 24), (40, 72, 48), (256, 136, 72), (257, 2048, 4080), (257, 2048, 4088)])
+def test_gated_ffn_back_keeps_16_bits_in_small_calls(op, T, K, F):  # noqa: F811
+    """bf16: two bfloat16 terms of dgate and dup, 2^-16, where T is at most 256 or K * F * T at most 2^31; 2^-8 beyond.
+    Results that cancel show it: a result's own rounding is 2^-8 of itself, that of the terms of their magnitudes.
+    Exact products, sums of two (or one) terms for each of N elements: 2 N / 16 + 4 tensor-core additions."""
+    small = T <= 256 or K * F * T <= 2 ** 31
+    assert small == ((T, K, F) != (257, 2048, 4088))
+    x, xv = _rand(1, (T, K), "bf16")
+    wg, wgv = _rand(2, (F, K), "bf16", K ** -0.5)
+    wu, wuv = _rand(3, (F, K), "bf16", K ** -0.5)
+    gate, gv = _rand(4, (T, F), "bf16")
+    up, uv = _rand(5, (T, F), "bf16")
+    d, dv = _rand(6, (T, F), "bf16")
+    dx, dwg, dwu = op.gated_ffn_back(d, x, wg, wu, gate, up)
+    tokens, features = slice(0, min(T, 24)), slice(F - min(F, 72), F)
+    held = 2.0 ** -16 if small else 2.0 ** -8
+
+    def terms(rows, cols):
+        g, u, e = gv[rows, cols], uv[rows, cols], dv[rows, cols]
+        dg, du = e * u * layer.act_slope(g, "silu"), e * layer.act(g, "silu")
+        eg, eu = 20 * U * np.abs(e * u) * (1 + np.abs(g)) + held * np.abs(dg), 20 * U * np.abs(e) * (1 + np.abs(g)) + held * np.abs(du)
+        return dg, du, eg, eu
+
+    def check(got, want, errors, magnitudes, n, what):
+        tol = errors + (2 * n / 16 + 4) * 2.0 ** -23 * magnitudes + UOUT["bf16"] * np.abs(want) * 1.01 + FLOOR["bf16"]
+        _close(got, want, tol, what)
+
+    dg, du, eg, eu = terms(tokens, slice(None))
+    check(dx[tokens], dg @ wgv + du @ wuv, eg @ np.abs(wgv) + eu @ np.abs(wuv), np.abs(dg) @ np.abs(wgv) + np.abs(du) @ np.abs(wuv), 2 * F, "dx")
+    dg, du, eg, eu = terms(slice(None), features)
+    check(dwg[features], dg.T @ xv, eg.T @ np.abs(xv), np.abs(dg).T @ np.abs(xv), T, "dw_gate")
+    check(dwu[features], du.T @ xv, eu.T @ np.abs(xv), np.abs(du).T @ np.abs(xv), T, "dw_up")
