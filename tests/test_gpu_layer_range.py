@@ -84,6 +84,22 @@ def test_orthogonalise_beyond_the_usual_range(op, M, N, out):  # noqa: F811
         assert np.linalg.norm(_np(y) - want) <= tol
 
 
+# ---------------------------------------------------------------------------
+# how much the orthogonalised updates keep
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("steps", [1, 3, 5, 9])
+@pytest.mark.parametrize("M,N", [(12, 40), (40, 12), (100, 260), (200, 136), (300, 700)])
+def test_orthogonalise_keeps_22_bits(op, steps, M, N):  # noqa: F811
+    """Tolerances from the coefficients of the case: half of the bits missing anywhere would show."""
+    x, xv = _rand(steps, (M, N), "f32")
+    for coefs in ([(1.875 - 0.02 * i, -1.25, 0.375 + 0.01 * i) for i in range(steps)], [(1.5, -0.5, 0.0)] * steps, [USUAL] * steps):
+        coefs32 = np.float32(coefs).astype(np.float64).tolist()
+        want = layer.orthogonalise(xv, steps, coefs32, 1e-7)
+        y = op.orthogonalise(x, steps=steps, coefs=coefs)
+        assert np.linalg.norm(_np(y) - want) <= _steps_tol(xv, coefs32, want, "f32")
+
+
 @pytest.mark.parametrize("M,N", [(64, 64), (70, 300)])
 def test_orthogonalise_coefficients_of_one_sign(op, M, N):  # noqa: F811
     """X X' of 62 and a polynomial whose square has its centre on the other side: nothing leaves the range on the way."""
