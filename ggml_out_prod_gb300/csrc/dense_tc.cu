@@ -1840,6 +1840,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 void tc_set_inject(int v) { g_inject = v; }
+int tc_take_inject() { return g_inject.exchange(0); }
 void tc_set_schedule(int v) { g_schedule = v; }
 void tc_set_profile_events(cudaEvent_t before, cudaEvent_t after) {
     g_ev_before = before;
@@ -1907,7 +1908,7 @@ cudaError_t launch_dense_tc(const void *a, const float *b, float *dst, const Out
     p.num_kb = static_cast<int>((s.K + BK - 1) / BK);
     p.mtiles = static_cast<int>(mtiles);
     p.ntiles = static_cast<int>(ntiles);
-    p.inject = g_inject.exchange(0);
+    p.inject = tc_take_inject();
     const int64_t tiles = mtiles * ntiles * slices;
     p.ctas = tc_plan_ctas(s, device_sms(), workspace_bytes);
     p.iters = tiles * p.num_kb;

@@ -165,7 +165,8 @@ cudaError_t launch_b_gather(const float *b, const OutProdShape &s, float *out,
 // than tc_workspace_bytes the data-parallel schedule is used.
 size_t tc_workspace_bytes(const OutProdShape &s);
 size_t tc_workspace_min_bytes(const OutProdShape &s);
-void tc_set_inject(int v);   // test hook: the next tensor-core launch drops one TMA stage
+void tc_set_inject(int v);   // test hook: a wait of the next tensor-core launch runs out
+int tc_take_inject();        // whether it is this one
 void tc_set_schedule(int v); // test hook: 0 automatic, 1 data-parallel, 2 stream-K
 void tc_set_profile_events(cudaEvent_t before, cudaEvent_t after);
 // The tile kernel's schedule on a GPU with `sms` SMs and this much workspace

@@ -87,6 +87,7 @@ struct Job {
     int term_a[kMaxTerms], term_b[kMaxTerms];
     int stages, stage_bytes;
     int sum_blocks;                // stages of one sum in tensor memory
+    int inject;                    // test hook: the first stage waits for 16 bytes that no copy brings
     int a_rows, b_rows;            // the operand lies with its rows contiguous
     int a_half, b_half;            // the operand is a result of that kind
     uint32_t idesc;
@@ -470,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                     ok = wait(&sh.empty[stage], phase ^ 1);
                     if (!ok) break;
                     const uint32_t bar = leader_addr(&sh.full[stage]);
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * j.stage_bytes);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * j.stage_bytes + (i + kb == 0 ? j.inject * 16 : 0));
                     const int seg = kb >= j.k_blocks ? 1 : 0;
                     const int k = (kb - seg * j.k_blocks) * kDepth;
                     const bool a_turned = below(j.a_half, k, t.m), b_turned = below(j.b_half, k, t.n);
@@ -862,6 +863,7 @@ cudaError_t launch(const Spec &s, int *status, cudaStream_t st) {
     j.stage_bytes = s.planes_a * kPlaneBytes + s.planes_b * (BN / 2 * kDepth * 2);
     j.stages = (kSmem - kHeader - kEpilogueWarps * kOutBytes) / j.stage_bytes;
     if (j.stages > kMaxStages) j.stages = kMaxStages;
+    j.inject = tc_take_inject();
     j.sum_blocks = FOLD ? 1 : static_cast<int>(blocks * s.segments);
     j.a_rows = s.a.rows_contiguous;
     j.b_rows = s.b[0].rows_contiguous;

@@ -731,9 +731,9 @@ int oop_version(void);
 int oop_profile_main_kernel(void *before, void *after);
 
 /* Test hook for the device-side failure path (no counterpart on the pages).
- * With enable != 0, the NEXT tensor-core OUT_PROD launch on this process
- * skips one of its TMA copies, so its MMA thread's bounded wait runs out
- * (after about one second); the kernel then records OOP_ERR_DEVICE_TIMEOUT in
+ * With enable != 0, the NEXT tensor-core launch of OUT_PROD or of a layer operator
+ * (gated_ffn, orthogonalise) on this process waits for data that no TMA copy brings, so
+ * its MMA thread's bounded wait runs out (after about one second); the kernel then records OOP_ERR_DEVICE_TIMEOUT in
  * the device status word, releases its tensor memory and returns without
  * trapping.  dst is left unspecified by that call.  The flag is consumed by
  * that one launch.  Returns OOP_OK. */
