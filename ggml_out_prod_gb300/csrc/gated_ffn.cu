@@ -449,9 +449,6 @@ void launch_gate_back(int x_type, const char *dh, int64_t nb_dh, const char *gat
 
 // ---- operands -------------------------------------------------------------
 
-int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
 // How a matrix of a type goes to the tensor cores: as it is (0: not even copied), or as so
 // many 16-bit planes in the workspace.
 struct Form {
@@ -471,8 +468,8 @@ Form form_of(int type, bool native, bool precise, bool aligned) {
 
 size_t form_bytes(const Form &f, int64_t cols, int64_t rows) {
     if (!f.copy) return 0;
-    return round256(static_cast<size_t>(f.planes) * static_cast<size_t>(rows * round8(cols)) * 2) +
-           (f.scaled ? round256(static_cast<size_t>(rows) * 4) : 0);
+    return pair::round256(static_cast<size_t>(f.planes) * static_cast<size_t>(rows * pair::round8(cols)) * 2) +
+           (f.scaled ? pair::round256(static_cast<size_t>(rows) * 4) : 0);
 }
 
 struct ForwardForms {
@@ -503,7 +500,7 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
                     char *&at, pair::Operand &o, cudaStream_t st) {
     o = {src, cols, rows, nb, 0, 1, rows_contiguous, f.half};
     if (!f.copy) return cudaSuccess;
-    const int64_t pitch = round8(cols);
+    const int64_t pitch = pair::round8(cols);
     o.p = at;
     o.pitch_bytes = pitch * 2;
     o.matrix_bytes = rows * pitch * 2;
@@ -516,11 +513,11 @@ cudaError_t operand(const Form &f, const void *src, int type, int64_t nb, int64_
 
 // The same for a matrix whose rows are scaled, k contiguous: what halves_kernel has to do.
 Scaled scaled_operand(const Form &f, const void *src, int64_t nb, int64_t cols, int64_t rows, char *&at, pair::Operand &o) {
-    const int64_t pitch = round8(cols);
+    const int64_t pitch = pair::round8(cols);
     o = {at, cols, rows, pitch * 2, rows * pitch * 2, f.planes, false, true};
     Scaled m = {static_cast<const char *>(src), nb, rows, reinterpret_cast<__half *>(at), nullptr, is_aligned(src, 16) && nb % 16 == 0};
     at += form_bytes(f, cols, rows);
-    m.factors = reinterpret_cast<float *>(at - round256(static_cast<size_t>(rows) * 4));
+    m.factors = reinterpret_cast<float *>(at - pair::round256(static_cast<size_t>(rows) * 4));
     return m;
 }
 
@@ -697,7 +694,7 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
     cudaError_t e = cudaSuccess;
     if (f.x.scaled) {
         ScaledArgs a = {};
-        a.cols = K, a.pitch = round8(K);
+        a.cols = K, a.pitch = pair::round8(K);
         a.m[a.count++] = scaled_operand(f.x, x, nb_x, K, T, at, s.a);
         s.out.row_scale = a.m[0].factors;
         if (w_type != OOP_TYPE_F32) {                      // another type: a launch of its own
@@ -775,7 +772,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
     }
     const BackForms f = back_forms(dh_type, x_type, w_type, ne, aligned);
     char *at = static_cast<char *>(workspace);
-    const int64_t pitch = round8(F);
+    const int64_t pitch = pair::round8(F);
     // [plane][gate, up][T][pitch]
     pair::Operand d = {at, F, T, pitch * 2, T * pitch * 2, 2 * f.d.planes, false, false};
     const int wide = rows_aligned(dh, nb_dh, T) && rows_aligned(gate, nb_gu, T) && rows_aligned(up, nb_gu, T);

@@ -248,24 +248,6 @@ constexpr int small_columns(int nmax) {          // of a CTA, at most
     return static_cast<int>((kMostSmem - 2048 - small_fixed_bytes(nmax)) / (small_pitch(nmax) * 4));
 }
 
-__device__ __forceinline__ uint32_t cta_of_cluster() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t ctas_of_cluster() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void sync_cluster() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t address_in(const void *p, uint32_t cta) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(cta));
-    return r;
-}
 __device__ __forceinline__ float load_float(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -284,7 +266,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
     __shared__ float2 factors;
     float *partial = small_smem, *parts = partial + 2 * kSmallCtas * kSquare, *A = parts + kWarps * kSquare, *Q = A + NMAX * kLd;
     float *xs = Q + NMAX * kLd;
-    const uint32_t cta = cta_of_cluster(), ctas = ctas_of_cluster();
+    const uint32_t cta = pair::cluster_rank(), ctas = pair::cluster_ctas();
     const int64_t matrix = blockIdx.x / ctas;
     const int s0 = static_cast<int>(cta) * a.slice, cols = max(0, min(a.slice, a.deep - s0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -299,7 +281,6 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
         xs[s * kPitch + r] = v;
     };
     constexpr int kAhead = 8;                              // loads before the first is used
-    constexpr int kShare = kWarps > 8 ? kWarps / 8 : 1;    // warps of a row
     if (a.tall) {                                          // lanes along the rows, which are short
         const int total = cols * a.n;
         for (int i0 = tid; i0 < total; i0 += kSmallThreads * kAhead) {
@@ -315,9 +296,9 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
                 if (i < total) take(i - s * a.n, s, v[k]);
             }
         }
-    } else {                                               // a row to the warps of a share
-        for (int r = warp / kShare; r < a.n; r += kWarps / kShare)
-            for (int c0 = warp % kShare * 32 * kAhead + lane; c0 < cols; c0 += 32 * kAhead * kShare) {
+    } else {                                               // a row to a warp
+        for (int r = warp; r < a.n; r += kWarps)
+            for (int c0 = lane; c0 < cols; c0 += 32 * kAhead) {
                 float v[kAhead];
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
@@ -335,11 +316,11 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
         if (lane == 0) my_sum = sq;
     }
     if (ctas > 1) {
-        sync_cluster();
+        pair::cluster_sync();
         if (warp == 0) {                                   // a lane reads a CTA's
             Squares s;
             if (lane < ctas) {
-                const uint32_t at = address_in(&my_sum, lane);
+                const uint32_t at = pair::cluster_addr(&my_sum, lane);
                 s.big = load_float(at);
                 s.mid = load_float(at + 4);
                 s.small = load_float(at + 8);
@@ -390,9 +371,9 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
             float v = 0.f;
 #pragma unroll
             for (int p = 0; p < kWarps; ++p) v += parts[p * kSquare + e];
-            for (uint32_t c = 0; c < ctas; ++c) store_float(address_in(all + cta * kSquare + e, c), v);
+            for (uint32_t c = 0; c < ctas; ++c) store_float(pair::cluster_addr(all + cta * kSquare + e, c), v);
         }
-        if (ctas > 1) sync_cluster();
+        if (ctas > 1) pair::cluster_sync();
         else __syncthreads();
         for (int e = tid; e < kSquare; e += kSmallThreads) {
             float v = 0.f;
@@ -451,11 +432,11 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
             put(y + static_cast<int64_t>(s0 + s) * a.y_row, r, xs[s * kPitch + r]);
         }
     } else {
-        for (int r = warp / kShare; r < a.n; r += kWarps / kShare)
+        for (int r = warp; r < a.n; r += kWarps)
 #pragma unroll 4
-            for (int c = warp % kShare * 32 + lane; c < cols; c += 32 * kShare) put(y + r * a.y_row, s0 + c, xs[c * kPitch + r]);
+            for (int c = lane; c < cols; c += 32) put(y + r * a.y_row, s0 + c, xs[c * kPitch + r]);
     }
-    if (ctas > 1) sync_cluster();                          // no CTA ends while another reads its sums
+    if (ctas > 1) pair::cluster_sync();                          // no CTA ends while another reads its sums
 }
 
 // CTAs of a matrix's cluster, 0 where it has to go the other way: by its size alone.
@@ -501,11 +482,8 @@ int check_matrices(const int64_t nb[2], const int64_t ne[3], int size, bool outp
     return check_row_stride(bytes, ne[2], nb[1], size, output);
 }
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
-
 size_t plane_pair_bytes(int64_t cols, int64_t rows, int64_t B) {
-    return round256(static_cast<size_t>(2 * B * rows * round8(cols)) * 2);
+    return pair::round256(static_cast<size_t>(2 * B * rows * pair::round8(cols)) * 2);
 }
 
 // The tiles of A = X X': those that would leave SMs idle go in parts of k (200 x 2560 is
@@ -526,7 +504,7 @@ double product_time(int64_t tiles, int64_t k, int parts) {
 struct Planes {
     char *p;
     int64_t cols, rows, B;
-    int64_t pitch() const { return round8(cols); }
+    int64_t pitch() const { return pair::round8(cols); }
     int64_t matrix_bytes() const { return rows * pitch() * 2; }
     __half *hi() const { return reinterpret_cast<__half *>(p); }
     __half *lo() const { return reinterpret_cast<__half *>(p + B * matrix_bytes()); }
@@ -634,7 +612,7 @@ size_t oop_orthogonalise_workspace_size(const int64_t ne[3]) {
     const int64_t n = std::min(ne[0], ne[1]);
     if (small_ctas(n, std::max(ne[0], ne[1]))) return 0;
     const size_t x = plane_pair_bytes(ne[0], ne[1], ne[2]), a = plane_pair_bytes(n, n, ne[2]);
-    return round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(Squares)) + std::max(2 * x + 2 * a, x + 5 * a) +
+    return pair::round256(static_cast<size_t>(ne[2] * parts_of(ne[0] * ne[1])) * sizeof(Squares)) + std::max(2 * x + 2 * a, x + 5 * a) +
            pair::slot_bytes(map_of_a(n, std::max(ne[0], ne[1]), ne[2]), ne[2], 256);
 }
 
@@ -682,7 +660,7 @@ int oop_orthogonalise(const void *x, int x_type, const int64_t nb_x[2], void *y,
     }
     const int parts = static_cast<int>(parts_of(M * N));
     Squares *sums = static_cast<Squares *>(workspace);
-    char *at = static_cast<char *>(workspace) + round256(static_cast<size_t>(B * parts) * sizeof(Squares));
+    char *at = static_cast<char *>(workspace) + pair::round256(static_cast<size_t>(B * parts) * sizeof(Squares));
     Planes X = {at, N, M, B}, next = {at + plane_pair_bytes(N, M, B), N, M, B};
     const Planes A = {next.p + plane_pair_bytes(N, M, B), n, n, B}, Q = {A.p + plane_pair_bytes(n, n, B), n, n, B};
     const char *xp = static_cast<const char *>(x);

@@ -103,10 +103,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The shared address of the first CTA's copy of a variable.
-__device__ __forceinline__ uint32_t leader_addr(const void *p) {
+__device__ __forceinline__ uint32_t cluster_ctas() {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(ptx::smem_u32(p)));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// The shared address of a CTA's copy of a variable.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t cta) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_u32(p)), "r"(cta));
     return r;
 }
 // No memory is handed over with it (the tcgen05 fences order tensor memory), so the plain
@@ -470,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
                 for (int kb = first_stage(j, t); kb < end && ok; ++kb) {
                     ok = wait(&sh.empty[stage], phase ^ 1);
                     if (!ok) break;
-                    const uint32_t bar = leader_addr(&sh.full[stage]);
+                    const uint32_t bar = cluster_addr(&sh.full[stage], 0);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * j.stage_bytes + (i + kb == 0 ? j.inject * 16 : 0));
                     const int seg = kb >= j.k_blocks ? 1 : 0;
                     const int k = (kb - seg * j.k_blocks) * kDepth;
@@ -577,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) product
         if constexpr (FOLD) ptx::setmaxnreg_inc<224>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t empty_bar = leader_addr(&sh.sums_empty[0]);
+        const uint32_t empty_bar = cluster_addr(&sh.sums_empty[0], 0);
         uint8_t *stage_out = smem + kHeader + j.stages * j.stage_bytes + (warp - 4) * kOutBytes;
         const int element = plain_size(j.out.type);
         int buf = 0;
@@ -745,6 +750,10 @@ __device__ __forceinline__ void each_joined(const TileMap &map, const float *slo
 }
 
 // ---- host -----------------------------------------------------------------
+
+// Elements of a plane's row, which starts on 16 bytes, and bytes of a part of a workspace.
+inline int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t kPairs = 76;                             // of SMs: sizes can be asked for without a GPU
 
