@@ -65,6 +65,19 @@ def test_orthogonalise_spectra_on_the_smaller_side(op, M, N, rank, noise):  # no
     assert np.linalg.norm(got - want) <= _steps_tol(xv, [USUAL] * 5, want, "bf16") + 2.0 ** -9 * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("M,N", [(100, 12000), (300, 9000), (9000, 300)])
+def test_orthogonalise_spectra_of_a_batch(op, M, N):  # noqa: F811
+    """The same for matrices of different ranks in one call."""
+    import torch
+    made = [_spectrum(rank, min(M, N), max(M, N), rank, noise) for rank, noise in ((1, 1e-5), (0, 1.0), (6, 1e-3))]
+    x = torch.stack([t for t, _ in made])
+    y = op.orthogonalise(x if M <= N else x.transpose(1, 2).contiguous(), out_dtype=_dt("bf16"))
+    y = y if M <= N else y.transpose(1, 2)
+    for got, (_, xv) in zip(y, made):
+        want = layer.orthogonalise(xv, 5, [USUAL] * 5, 1e-7)
+        assert np.linalg.norm(_np(got) - want) <= _steps_tol(xv, [USUAL] * 5, want, "bf16") + 2.0 ** -9 * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N", [(100, 12000), (9000, 130)])
 def test_orthogonalise_beyond_the_usual_range(op, M, N, out):  # noqa: F811
