@@ -13,10 +13,10 @@
 // two batches; the operands lie as they are, with their rows or their k contiguous.
 //
 // Measured: bf16 8192 x 5120 x 17408, gate and up kept: 1.53 ms, 1.91 PFLOP/s (97% of the
-// measured burst of cuBLAS), 1.75 ms where the card's power limit holds; backward 8192 x
-// 2560 x 9728: 1.04 ms, 1.57 PFLOP/s, 0.13 of it for dgate and dup.  f32 512 x 2560 x
-// 9728, kept: 167 us, 60 of it for the planes of the weights, the rest two waves of tiles
-// with their epilogues.
+// measured burst of cuBLAS), 1.79 to 1.89 ms a call where the card's power limit holds;
+// backward 8192 x 2560 x 9728: 1.02 to 1.07 ms, 1.52 to 1.60 PFLOP/s, 0.13 or more of it for
+// dgate and dup.  f32 512 x 2560 x 9728, kept: 165 us, 60 of it for the planes of the weights, the
+// rest two waves of tiles with their epilogues.
 #include <algorithm>
 #include <cmath>
 
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     }
 }
 
-// Operands that the tensor cores take as they are go there from five tokens on (5120 x
-// 17408: 77 us for 4 tokens here, 131 for 8, 85 there), others have to be copied first
-// (f32: 164, 597).
+// Operands that the tensor cores take as they are go there from five tokens on (bf16 5120 x
+// 17408: 4 tokens 77 us here and 91 there, 5 tokens 126 and 83), others have to be copied
+// first (f32: 8 tokens 162 us here and 488 there).
 bool few_tokens(int64_t T, int64_t K, int x_type, int w_type) {
     const int64_t nt = !plain_size(w_type) ? 8 : T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
     const bool native = x_type == w_type && plain_size(w_type) == 2;
@@ -304,7 +304,10 @@ cudaError_t launch_few(const FewArgs &a, int w_type, cudaStream_t st) {
 // under the largest, it shows in full.  factors: the inverse scales.  So two planes and three
 // terms do for the forward products of f32; elsewhere, where sums run over other rows'
 // scales, it takes three bfloat16 planes and six terms.  A warp takes a row, read once up to
-// 2560 columns; up to three matrices of the same columns in a launch.
+// kHold * 256 columns; up to three matrices of the same columns in a launch.  512 tokens of
+// f32 with kHold of 5, 10 and 20: K = 1280, F = 9728 94, 95 and 124 us, K = 2560 189, 165 and
+// 182, K = 5120, F = 17408 681, 684 and 578: held rows cost registers, rows read twice
+// bandwidth.
 struct Scaled {
     const char *src;
     int64_t nb, rows;

@@ -26,8 +26,9 @@ constexpr float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
 // The matrices between the products are held as two binary16 planes, hi + lo, of a scaled
 // value: 22 bits or more, as many as a product of three terms keeps.  The scales leave
 // room for magnitudes of 8, 64 and 256 below binary16's largest, and keep the planes of a
-// 4096 x 4096 matrix (X's elements are about 2^-12) out of its subnormals.  bfloat16
-// planes would need no scale, but three of them and six terms.
+// 4096 x 4096 matrix (X's elements are about 2^-12) out of its subnormals; an element below
+// 2^-16 of X, 2^-13 of A or 2^-11 of Q is off by up to 2^-38, 2^-35 or 2^-33.  bfloat16 planes
+// would need no scale, but three of them and six terms.
 constexpr float kScaleX = 0x1p13f, kScaleA = 0x1p10f, kScaleQ = 0x1p8f;
 
 // Sums of squares: those of large, ordinary and small magnitudes apart, scaled so that

@@ -662,7 +662,8 @@ int oop_gated_ffn(const void *x, int x_type, int64_t nb_x, const void *w_gate, c
  * to the tensor cores as sums of bfloat16 terms: two for F16, else three (24 bits) where
  * dh is F32 and two (16 bits) where it is BF16.  Between the
  * products dgate and dup are held to 24 bits where dh is F32, to 16 where it is BF16 and the
- * call small (T at most 256, or K * F * T at most 2^31), else in BF16.  dx may be NULL,
+ * call small (T at most 256, or K * F * T at most 2^31), else in BF16: a caller who wants
+ * more of a large call gives dh in F32.  dx may be NULL,
  * and dw_gate and dw_up both (not computed); dw rows are nb_dw apart.  T == 0
  * writes zeros to dw_gate and dw_up.  No output may overlap an input.
  */
@@ -691,7 +692,7 @@ int oop_gated_ffn_back(const void *dh, int dh_type, int64_t nb_dh, const void *x
  *
  * The norm, the matrices between the products and their sums are held in 32
  * bits: the products take each factor as two binary16 terms of a scaled value
- * (22 bits or more), and X_s has to stay below 8 in magnitude, X X' below 64
+ * (22 bits, or 2^-38 for an element of X_s below 2^-16), and X_s has to stay below 8 in magnitude, X X' below 64
  * and a + b X X' + c (X X')^2 below 256, as they do for coefficients that
  * keep the singular values below 1.5; beyond that the matrix is not finite.  A BF16 y of
  * a matrix much longer than wide (or the reverse) may come from the steps of X X' alone and one
